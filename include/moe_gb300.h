@@ -84,7 +84,8 @@ typedef enum {
  * desc.down may have another type than gate and up).  They run on the GEMV kernels at every T
  * (moe_layer_path reports MOE_PATH_GEMV). */
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_Q8_0 = 2, MOE_Q4_K = 3, MOE_Q8_0_R = 4, MOE_Q5_K = 5,
-               MOE_Q6_K = 6, MOE_Q3_K = 7, MOE_MXFP4 = 8 } moe_dtype;
+               MOE_Q6_K = 6, MOE_Q3_K = 7, MOE_MXFP4 = 8,
+               MOE_F16 = 9 /* a value type of the grouped, 4-bit and norm calls only */ } moe_dtype;
 
 typedef enum { MOE_ROUTE_SOFTMAX = 0, MOE_ROUTE_SIGMOID_GROUP = 1 } moe_route_mode;
 
@@ -270,6 +271,136 @@ moe_status moe_combine(const float* y_pairs, const float* topk_w, const int32_t*
  */
 moe_status moe_rmsnorm_bf16(const float* x, const float* gamma, int T, int H, float eps, void* u,
                             moe_stream_t stream);
+
+/* ---------------------------------------------------------------- grouped products, unquantized experts */
+
+/*
+ * moe_grouped_matmul -- the rows of each expert times that expert's bf16 or fp16 matrix.
+ *   for sorted position i of expert e (offsets[e] <= i < offsets[e+1]) and its row
+ *   v = x[sorted_pairs[i] / k]  (sorted_pairs NULL: v = x[i]):
+ *     w_up NULL:  y[i, n] = sum_c W[e][n, c] * v[c]
+ *     w_up set :  y[i, n] = g / (1 + exp(-g)) * u,  g = W[e] v, u = W_up[e] v
+ *   with n < n_out, c < n_in; products exact, sums in fp32, one rounding to y_type at the end.
+ * With moe_route, moe_permute and moe_combine this is an MoE layer whose experts are stored
+ * unquantized: gate and up are one call (w_up set, rows gathered through sorted_pairs), down is a
+ * second one (sorted_pairs NULL, y_type MOE_F32, the y_pairs of moe_combine).
+ * Pages: routed experts run each over all of its tokens at once ("bloomery V4.1 README", feature
+ * list, "Batched prompts"); the pages' experts are GGUF blocks, this call serves the
+ * checkpoints whose experts are not.
+ *
+ * desc (host, read by plan_create):
+ *   type: MOE_BF16 or MOE_F16, the type of W, W_up and x;  y_type: MOE_F32, MOE_BF16 or MOE_F16;
+ *   order: MOE_W_OUT_IN (expert matrices [n_out][n_in]) or MOE_W_IN_OUT ([n_in][n_out]);
+ *   n_experts 1..1024, n_out and n_in 1..2^20, any value;
+ *   w, w_up (device, 16-byte aligned; w_up nullable): n_experts matrices of rows row_stride
+ *   elements apart (a multiple of 8, at least the row's length), expert_stride elements apart
+ *   (a multiple of 8, at least (rows - 1) * row_stride + the row's length; ignored for one expert).
+ * The plan keeps the pointers; the weights must outlive it and may change between calls.
+ *
+ * Call: x (device, 16-byte aligned) rows x_stride elements apart (a multiple of 8, >= n_in), T rows
+ *   with sorted_pairs, else T*k rows; offsets (device) int32 [n_experts + 1], non-decreasing within
+ *   0..T*k (NULL: one expert over all T*k rows); y (device, aligned to its type) rows y_stride >= n_out elements
+ *   apart.  Rows of y outside [offsets[0], offsets[n_experts]) are left as they were.  y must not
+ *   overlap x.  status (device int32, nullable, caller-owned, never cleared by the call) is
+ *   raised from MOE_OK to MOE_ERR_DEVICE_CHECK when an offset leaves 0..T*k or decreases (it is
+ *   clamped) or a pair leaves 0..T*k-1 (its row of y is undefined), and to MOE_ERR_TIMEOUT when a device-side wait ran out (y is
+ *   undefined).  T*k <= 2^30; T = 0 is a no-op.  Launches one kernel, allocates nothing, needs no
+ *   workspace, keeps nothing between calls: two calls may overlap on the GPU, and a captured call
+ *   replays with the bits of the eager one.
+ * Kernels (moe_grouped_path tells which): MOE_GROUPED_ROWS streams the weights of the experts that
+ *   have rows through the warps' matrix instructions; MOE_GROUPED_TENSOR tiles 256 weight rows
+ *   by up to 256 of an expert's rows on tcgen05.  Both sum in fp32, in a fixed order.
+ * Errors: MOE_ERR_INVALID_ARG (NULL, size, stride, alignment), MOE_ERR_UNSUPPORTED (a type),
+ *   MOE_ERR_CUDA (a launch failed).
+ */
+typedef enum { MOE_W_OUT_IN = 0, MOE_W_IN_OUT = 1 } moe_w_order;
+typedef struct {
+    moe_dtype type;              /* MOE_BF16 or MOE_F16: W, W_up and x */
+    moe_dtype y_type;            /* MOE_F32, MOE_BF16 or MOE_F16 */
+    moe_w_order order;
+    int n_experts, n_out, n_in;
+    const void* w;               /* (device) */
+    const void* w_up;            /* (device, nullable) */
+    int64_t row_stride, expert_stride;   /* elements */
+} moe_grouped_desc;
+typedef struct moe_grouped_plan moe_grouped_plan;
+#define MOE_GROUPED_ROWS 0
+#define MOE_GROUPED_TENSOR 1
+moe_status moe_grouped_plan_create(const moe_grouped_desc* desc, moe_grouped_plan** plan);
+moe_status moe_grouped_plan_destroy(moe_grouped_plan* plan);
+moe_status moe_grouped_path(const moe_grouped_plan* plan, int T, int k, int* path);
+moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64_t x_stride, int T, int k,
+                              const int32_t* sorted_pairs, const int32_t* offsets, void* y, int64_t y_stride,
+                              int32_t* status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit weights with group scales */
+
+/*
+ * moe_w4_matmul -- moe_grouped_matmul over 4-bit weights with one scale per group of weights:
+ *     W[e][n, c] = scale[e][n, c / group] * (q[e][n, c] - zero[e][n, c / group])
+ *   q: 4-bit codes 0..15, two to a byte (weight 2j in the low nibble of byte j, 2j+1 in the high),
+ *   rows dense: [n_experts][n_out][n_in / 2] bytes;  scales: fp16 or bf16 [n_experts][n_out][n_in / group];
+ *   zeros (nullable): uint8 [n_experts][n_out][n_in / group], values 0..15 (the low four bits are used);
+ *   NULL: every zero point is 8.  group: 32, 64 or 128;  n_in a multiple of group.
+ * The code minus its zero point is an exact small integer: it is multiplied with x exactly, a group's
+ * products are summed in fp32 and the scale is applied to that sum in fp32, so no weight is rounded.
+ * For a few rows an expert (decode): every active expert's codes are read once per 32 of its rows.
+ * Arguments, routing, y and status as moe_grouped_matmul; x of x_type MOE_BF16 or MOE_F16.
+ * q, q_up 16-byte aligned; scales and zeros aligned to their element.  One launch, no workspace.
+ * Pages: the card experts are 4-bit block types ("bloomery README 0.3.1", Status table, "Quant types"
+ * row) in GGUF super-blocks; this is the flat form, one scale (and zero point) a group.
+ */
+typedef struct {
+    moe_dtype x_type;            /* MOE_BF16 or MOE_F16 */
+    moe_dtype y_type;            /* MOE_F32, MOE_BF16 or MOE_F16 */
+    moe_dtype scale_type;        /* MOE_F16 or MOE_BF16 */
+    int group;                   /* 32, 64 or 128 */
+    int n_experts, n_out, n_in;
+    const void* q;               /* (device) */
+    const void* scales;          /* (device) */
+    const uint8_t* zeros;        /* (device, nullable) */
+    const void* q_up;            /* (device, nullable): the gated pair, as moe_grouped_desc.w_up */
+    const void* scales_up;       /* (device) set iff q_up is */
+    const uint8_t* zeros_up;     /* (device) set iff q_up and zeros are */
+} moe_w4_desc;
+typedef struct moe_w4_plan moe_w4_plan;
+moe_status moe_w4_plan_create(const moe_w4_desc* desc, moe_w4_plan** plan);
+moe_status moe_w4_plan_destroy(moe_w4_plan* plan);
+moe_status moe_w4_matmul(const moe_w4_plan* plan, const void* x, int64_t x_stride, int T, int k,
+                         const int32_t* sorted_pairs, const int32_t* offsets, void* y, int64_t y_stride,
+                         int32_t* status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- norms around a block */
+
+/*
+ * moe_norm_residual -- what stands between two blocks of a stack, in one pass over the rows:
+ *     n = gamma_post set ? y / sqrt(mean_h y^2 + eps) * gamma_post : y     (the norm behind the block)
+ *     r = res_scale * x + scale * gate * n                                 (its gate and residual scale)
+ *     x_out = r                                                            (the new residual stream)
+ *     u = r / sqrt(mean_h r^2 + eps) * gamma_pre                           (the norm before the next block)
+ *   y: the block's output (moe_combine's out, say); all arithmetic fp32, u computed from the
+ *   unrounded r, one rounding to each output's type.
+ * desc (host, read during the call): H 1..32768; x_type (x and x_out), y_type, u_type: MOE_F32,
+ *   MOE_BF16 or MOE_F16; gamma_post, gamma_pre (device fp32 [H], nullable); eps >= 0.
+ * gate (device fp32, nullable): element (t, h) at gate[t * gate_row + h * gate_col]; (0, 1) is one
+ *   gate per channel, (1, 0) one per token, (stride, 1) one per token and channel.
+ * x (nullable: taken as 0), y, x_out (nullable; may be x itself, with the same stride), u (nullable;
+ *   needs gamma_pre) (device): T rows, strides in elements, at least H.  x_out and u must not
+ *   overlap y, each other or the gate; u must not overlap x.  Any H, stride and element-aligned pointer is accepted; rows that start on 16-byte
+ *   boundaries with H a multiple of 8 are read 16 bytes at a time.
+ * One launch, no workspace; T = 0 is a no-op.  Pages: none of the normalisation is printed; these
+ * are the plain definitions.
+ */
+typedef struct {
+    int H;
+    moe_dtype x_type, y_type, u_type;
+    const float* gamma_post;     /* (device, nullable) */
+    const float* gamma_pre;      /* (device, nullable) */
+    float eps, res_scale, scale;
+} moe_norm_desc;
+moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x_stride, const void* y,
+                             int64_t y_stride, const float* gate, int64_t gate_row, int64_t gate_col, int T,
+                             void* x_out, int64_t x_out_stride, void* u, int64_t u_stride, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- fused layer */
 

@@ -18,7 +18,9 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_gb300.h")
 
 (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK,
  MOE_ERR_TIMEOUT) = range(7)
-MOE_F32, MOE_BF16, MOE_Q8_0, MOE_Q4_K, MOE_Q8_0_R, MOE_Q5_K, MOE_Q6_K, MOE_Q3_K, MOE_MXFP4 = range(9)
+MOE_F32, MOE_BF16, MOE_Q8_0, MOE_Q4_K, MOE_Q8_0_R, MOE_Q5_K, MOE_Q6_K, MOE_Q3_K, MOE_MXFP4, MOE_F16 = range(10)
+MOE_W_OUT_IN, MOE_W_IN_OUT = range(2)
+MOE_GROUPED_ROWS, MOE_GROUPED_TENSOR = range(2)
 MOE_ROUTE_SOFTMAX, MOE_ROUTE_SIGMOID_GROUP = range(2)
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -50,6 +52,25 @@ class moe_layer_desc(ctypes.Structure):
                 ("s_down", moe_qmat), ("accumulate", ctypes.c_int), ("tc_min_tokens", ctypes.c_int),
                 ("decode_chain_off", ctypes.c_int), ("norm_gamma", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
                 ("expert_counts", ctypes.c_void_p)]
+
+
+class moe_grouped_desc(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("y_type", ctypes.c_int), ("order", ctypes.c_int), ("n_experts", ctypes.c_int),
+                ("n_out", ctypes.c_int), ("n_in", ctypes.c_int), ("w", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("row_stride", ctypes.c_int64), ("expert_stride", ctypes.c_int64)]
+
+
+class moe_w4_desc(ctypes.Structure):
+    _fields_ = [("x_type", ctypes.c_int), ("y_type", ctypes.c_int), ("scale_type", ctypes.c_int),
+                ("group", ctypes.c_int), ("n_experts", ctypes.c_int), ("n_out", ctypes.c_int), ("n_in", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("q_up", ctypes.c_void_p), ("scales_up", ctypes.c_void_p), ("zeros_up", ctypes.c_void_p)]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("x_type", ctypes.c_int), ("y_type", ctypes.c_int), ("u_type", ctypes.c_int),
+                ("gamma_post", ctypes.c_void_p), ("gamma_pre", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -103,6 +124,14 @@ def _declare(lib):
         "moe_debug_set_stamps": [P, S],
         "moe_weights_prepare_size": [ctypes.POINTER(moe_qmat), I, PS],
         "moe_weights_prepare": [ctypes.POINTER(moe_qmat), I, P, S, P],
+        "moe_grouped_plan_create": [ctypes.POINTER(moe_grouped_desc), ctypes.POINTER(P)],
+        "moe_grouped_plan_destroy": [P],
+        "moe_grouped_path": [P, I, I, ctypes.POINTER(ctypes.c_int)],
+        "moe_grouped_matmul": [P, P, I64, I, I, P, P, P, I64, P, P],
+        "moe_w4_plan_create": [ctypes.POINTER(moe_w4_desc), ctypes.POINTER(P)],
+        "moe_w4_plan_destroy": [P],
+        "moe_w4_matmul": [P, P, I64, I, I, P, P, P, I64, P, P],
+        "moe_norm_residual": [ctypes.POINTER(moe_norm_desc), P, I64, P, I64, P, I64, I64, I, P, I64, P, I64, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -112,7 +141,6 @@ def _declare(lib):
     lib.moe_last_error.restype = ctypes.c_char_p
     lib.moe_version.argtypes = []
     lib.moe_version.restype = ctypes.c_char_p
-    del I64
     return lib
 
 
@@ -207,6 +235,49 @@ def moe_combine(y_pairs, topk_w, pair_pos, T, k, H, shared_out, accumulate, out,
 
 def moe_rmsnorm_bf16(x, gamma, T, H, eps, u, stream=None):
     _check(load().moe_rmsnorm_bf16(_p(x), _p(gamma), T, H, float(eps), _p(u), _stream(stream)))
+
+
+def moe_grouped_plan_create(desc: moe_grouped_desc) -> int:
+    h = ctypes.c_void_p(0)
+    _check(load().moe_grouped_plan_create(ctypes.byref(desc), ctypes.byref(h)))
+    return h.value
+
+
+def moe_grouped_plan_destroy(plan: int):
+    _check(load().moe_grouped_plan_destroy(plan))
+
+
+def moe_grouped_path(plan, T, k) -> int:
+    """Which kernel moe_grouped_matmul runs for T tokens of k experts: a MOE_GROUPED_* value."""
+    v = ctypes.c_int(-1)
+    _check(load().moe_grouped_path(plan, T, k, ctypes.byref(v)))
+    return v.value
+
+
+def moe_grouped_matmul(plan, x, x_stride, T, k, sorted_pairs, offsets, y, y_stride, status=None, stream=None):
+    _check(load().moe_grouped_matmul(plan, _p(x), x_stride, T, k, _p(sorted_pairs), _p(offsets), _p(y), y_stride,
+                                     _p(status), _stream(stream)))
+
+
+def moe_w4_plan_create(desc: moe_w4_desc) -> int:
+    h = ctypes.c_void_p(0)
+    _check(load().moe_w4_plan_create(ctypes.byref(desc), ctypes.byref(h)))
+    return h.value
+
+
+def moe_w4_plan_destroy(plan: int):
+    _check(load().moe_w4_plan_destroy(plan))
+
+
+def moe_w4_matmul(plan, x, x_stride, T, k, sorted_pairs, offsets, y, y_stride, status=None, stream=None):
+    _check(load().moe_w4_matmul(plan, _p(x), x_stride, T, k, _p(sorted_pairs), _p(offsets), _p(y), y_stride,
+                                _p(status), _stream(stream)))
+
+
+def moe_norm_residual(desc: moe_norm_desc, x, x_stride, y, y_stride, gate, gate_row, gate_col, T, x_out, x_out_stride,
+                      u, u_stride, stream=None):
+    _check(load().moe_norm_residual(ctypes.byref(desc), _p(x), x_stride, _p(y), y_stride, _p(gate), gate_row, gate_col,
+                                    T, _p(x_out), x_out_stride, _p(u), u_stride, _stream(stream)))
 
 
 def moe_layer_plan_create(desc: moe_layer_desc) -> int:

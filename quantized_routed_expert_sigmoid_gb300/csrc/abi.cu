@@ -278,7 +278,53 @@ moe_status run_ffn(const moe_qmat& gate, const moe_qmat& up, const moe_qmat& dow
     return MOE_OK;
 }
 
+bool is_16bit(int t) { return t == MOE_BF16 || t == MOE_F16; }
+bool is_value_type(int t) { return t == MOE_F32 || is_16bit(t); }
+size_t value_bytes(int t) { return t == MOE_F32 ? 4 : 2; }
+constexpr int kMaxDim = 1 << 20;
+
+moe_status check_product_shape(int E, int n_out, int n_in) {
+    if (E < 1 || E > kMaxExperts) return fail(MOE_ERR_INVALID_ARG, "n_experts %d outside 1..%d", E, kMaxExperts);
+    if (n_out < 1 || n_out > kMaxDim || n_in < 1 || n_in > kMaxDim)
+        return fail(MOE_ERR_INVALID_ARG, "n_out %d / n_in %d outside 1..%d", n_out, n_in, kMaxDim);
+    return MOE_OK;
+}
+
+// The rows of a product call (x, y, routing); *todo = false: nothing to launch.
+moe_status check_product_call(const moe::RowsArgs& a, int T, int k, bool* todo) {
+    *todo = false;
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", T);
+    if (k < 1 || k > kMaxTopK) return fail(MOE_ERR_INVALID_ARG, "k = %d outside 1..%d", k, kMaxTopK);
+    if (!a.offsets && a.E != 1) return fail(MOE_ERR_INVALID_ARG, "offsets may be NULL for one expert only");
+    if (T == 0) return MOE_OK;
+    if ((int64_t)T * k > (int64_t)1 << 30) return fail(MOE_ERR_INVALID_ARG, "T*k too large");
+    if (!a.x || !a.y) return fail(MOE_ERR_INVALID_ARG, "x / y are NULL");
+    if (!aligned(a.x, 16)) return fail(MOE_ERR_INVALID_ARG, "x not 16-byte aligned");
+    if (!aligned(a.y, value_bytes(a.y_type))) return fail(MOE_ERR_INVALID_ARG, "y not aligned to its type");
+    if (!aligned(a.sorted_pairs, 4) || !aligned(a.offsets, 4) || !aligned(a.status, 4))
+        return fail(MOE_ERR_INVALID_ARG, "sorted_pairs / offsets / status not 4-byte aligned");
+    if (a.x_stride < a.K || a.x_stride % 8)
+        return fail(MOE_ERR_INVALID_ARG, "x_stride %lld (need >= %d, a multiple of 8)", (long long)a.x_stride, a.K);
+    if (a.y_stride < a.N) return fail(MOE_ERR_INVALID_ARG, "y_stride %lld < n_out %d", (long long)a.y_stride, a.N);
+    const int64_t x_rows = a.sorted_pairs ? T : (int64_t)T * k, y_rows = (int64_t)T * k;
+    if (a.x_stride > ((int64_t)1 << 40) || a.y_stride > ((int64_t)1 << 40))
+        return fail(MOE_ERR_INVALID_ARG, "x_stride / y_stride too large");
+    const uintptr_t x0 = (uintptr_t)a.x, y0 = (uintptr_t)a.y;
+    const uintptr_t x1 = x0 + 2 * (uintptr_t)((x_rows - 1) * a.x_stride + a.K);
+    const uintptr_t y1 = y0 + value_bytes(a.y_type) * (uintptr_t)((y_rows - 1) * a.y_stride + a.N);
+    if (x0 < y1 && y0 < x1) return fail(MOE_ERR_INVALID_ARG, "y overlaps x");
+    *todo = true;
+    return MOE_OK;
+}
+
 }  // namespace
+
+struct moe_grouped_plan {
+    moe::RowsArgs a;             // the weights' side; a call fills in its own
+};
+struct moe_w4_plan {
+    moe::RowsArgs a;
+};
 
 extern "C" {
 
@@ -507,6 +553,174 @@ moe_status moe_rmsnorm_bf16(const float* x, const float* gamma, int T, int H, fl
     if (!(eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
     cudaError_t err = launch_rmsnorm_bf16(x, gamma, T, H, eps, u, reinterpret_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return cuda_fail(err, "rmsnorm kernel");
+    return MOE_OK;
+}
+
+moe_status moe_grouped_plan_create(const moe_grouped_desc* desc, moe_grouped_plan** plan) {
+    if (!desc || !plan) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    *plan = nullptr;
+    const moe_grouped_desc& d = *desc;
+    if (!is_16bit(d.type)) return fail(MOE_ERR_UNSUPPORTED, "type %d (supported: BF16, F16)", (int)d.type);
+    if (!is_value_type(d.y_type)) return fail(MOE_ERR_UNSUPPORTED, "y_type %d (supported: F32, BF16, F16)", (int)d.y_type);
+    if (d.order != MOE_W_OUT_IN && d.order != MOE_W_IN_OUT) return fail(MOE_ERR_INVALID_ARG, "unknown order %d", (int)d.order);
+    moe_status st = check_product_shape(d.n_experts, d.n_out, d.n_in);
+    if (st) return st;
+    if (!d.w) return fail(MOE_ERR_INVALID_ARG, "w is NULL");
+    if (!aligned(d.w, 16) || !aligned(d.w_up, 16)) return fail(MOE_ERR_INVALID_ARG, "w / w_up not 16-byte aligned");
+    const int64_t rows = d.order == MOE_W_OUT_IN ? d.n_out : d.n_in, cols = d.order == MOE_W_OUT_IN ? d.n_in : d.n_out;
+    if (d.row_stride < cols || d.row_stride % 8 || d.row_stride > ((int64_t)1 << 32))
+        return fail(MOE_ERR_INVALID_ARG, "row_stride %lld (need >= %lld, a multiple of 8)", (long long)d.row_stride,
+                    (long long)cols);
+    if (d.n_experts > 1 && (d.expert_stride < (rows - 1) * d.row_stride + cols || d.expert_stride % 8 ||
+                            d.expert_stride > ((int64_t)1 << 38)))
+        return fail(MOE_ERR_INVALID_ARG, "expert_stride %lld (need >= %lld, a multiple of 8)", (long long)d.expert_stride,
+                    (long long)((rows - 1) * d.row_stride + cols));
+    moe_grouped_plan* p = new (std::nothrow) moe_grouped_plan();
+    if (!p) return fail(MOE_ERR_INVALID_ARG, "out of host memory");
+    RowsArgs& a = p->a;
+    a.E = d.n_experts; a.N = d.n_out; a.K = d.n_in;
+    a.bf16 = d.type == MOE_BF16;
+    a.w0 = d.w; a.w1 = d.w_up;
+    a.row_stride = d.row_stride;
+    a.expert_stride = d.n_experts > 1 ? d.expert_stride : 0;
+    a.in_out = d.order == MOE_W_IN_OUT;
+    a.y_type = d.y_type;
+    *plan = p;
+    return MOE_OK;
+}
+
+moe_status moe_grouped_plan_destroy(moe_grouped_plan* plan) {
+    delete plan;
+    return MOE_OK;
+}
+
+moe_status moe_grouped_path(const moe_grouped_plan* plan, int T, int k, int* path) {
+    if (!plan || !path) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    if (T < 1 || k < 1) return fail(MOE_ERR_INVALID_ARG, "T = %d, k = %d", T, k);
+    *path = MOE_GROUPED_ROWS;
+    return MOE_OK;
+}
+
+moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64_t x_stride, int T, int k,
+                              const int32_t* sorted_pairs, const int32_t* offsets, void* y, int64_t y_stride,
+                              int32_t* status, moe_stream_t stream) {
+    if (!plan) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
+    RowsArgs a = plan->a;
+    a.x = x; a.x_stride = x_stride; a.k = k; a.sorted_pairs = sorted_pairs; a.offsets = offsets;
+    a.y = y; a.y_stride = y_stride; a.status = status;
+    bool todo;
+    moe_status st = check_product_call(a, T, k, &todo);
+    if (st || !todo) return st;
+    a.P = T * k;
+    cudaError_t err = launch_rows(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "grouped product kernel");
+    return MOE_OK;
+}
+
+moe_status moe_w4_plan_create(const moe_w4_desc* desc, moe_w4_plan** plan) {
+    if (!desc || !plan) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    *plan = nullptr;
+    const moe_w4_desc& d = *desc;
+    if (!is_16bit(d.x_type)) return fail(MOE_ERR_UNSUPPORTED, "x_type %d (supported: BF16, F16)", (int)d.x_type);
+    if (!is_value_type(d.y_type)) return fail(MOE_ERR_UNSUPPORTED, "y_type %d (supported: F32, BF16, F16)", (int)d.y_type);
+    if (!is_16bit(d.scale_type)) return fail(MOE_ERR_UNSUPPORTED, "scale_type %d (supported: F16, BF16)", (int)d.scale_type);
+    if (d.group != 32 && d.group != 64 && d.group != 128)
+        return fail(MOE_ERR_UNSUPPORTED, "group %d (supported: 32, 64, 128)", d.group);
+    moe_status st = check_product_shape(d.n_experts, d.n_out, d.n_in);
+    if (st) return st;
+    if (d.n_in % d.group) return fail(MOE_ERR_INVALID_ARG, "n_in %d not a multiple of the group %d", d.n_in, d.group);
+    if (!d.q || !d.scales) return fail(MOE_ERR_INVALID_ARG, "q / scales are NULL");
+    if ((d.q_up != nullptr) != (d.scales_up != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "q_up and scales_up must both be set or both be NULL");
+    if ((d.zeros_up != nullptr) != (d.q_up != nullptr && d.zeros != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "zeros_up must be set exactly when q_up and zeros are");
+    if (!aligned(d.q, 16) || !aligned(d.q_up, 16)) return fail(MOE_ERR_INVALID_ARG, "q / q_up not 16-byte aligned");
+    if (!aligned(d.scales, 2) || !aligned(d.scales_up, 2)) return fail(MOE_ERR_INVALID_ARG, "scales not 2-byte aligned");
+    moe_w4_plan* p = new (std::nothrow) moe_w4_plan();
+    if (!p) return fail(MOE_ERR_INVALID_ARG, "out of host memory");
+    RowsArgs& a = p->a;
+    a.E = d.n_experts; a.N = d.n_out; a.K = d.n_in;
+    a.bf16 = d.x_type == MOE_BF16;
+    a.w0 = d.q; a.w1 = d.q_up;
+    a.group = d.group;
+    a.s0 = d.scales; a.s1 = d.scales_up; a.z0 = d.zeros; a.z1 = d.zeros_up;
+    a.s_bf16 = d.scale_type == MOE_BF16;
+    a.y_type = d.y_type;
+    *plan = p;
+    return MOE_OK;
+}
+
+moe_status moe_w4_plan_destroy(moe_w4_plan* plan) {
+    delete plan;
+    return MOE_OK;
+}
+
+moe_status moe_w4_matmul(const moe_w4_plan* plan, const void* x, int64_t x_stride, int T, int k,
+                         const int32_t* sorted_pairs, const int32_t* offsets, void* y, int64_t y_stride,
+                         int32_t* status, moe_stream_t stream) {
+    if (!plan) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
+    RowsArgs a = plan->a;
+    a.x = x; a.x_stride = x_stride; a.k = k; a.sorted_pairs = sorted_pairs; a.offsets = offsets;
+    a.y = y; a.y_stride = y_stride; a.status = status;
+    bool todo;
+    moe_status st = check_product_call(a, T, k, &todo);
+    if (st || !todo) return st;
+    a.P = T * k;
+    cudaError_t err = launch_rows(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "4-bit product kernel");
+    return MOE_OK;
+}
+
+moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x_stride, const void* y,
+                             int64_t y_stride, const float* gate, int64_t gate_row, int64_t gate_col, int T,
+                             void* x_out, int64_t x_out_stride, void* u, int64_t u_stride, moe_stream_t stream) {
+    if (!desc) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+    const moe_norm_desc& d = *desc;
+    if (!is_value_type(d.x_type) || !is_value_type(d.y_type) || !is_value_type(d.u_type))
+        return fail(MOE_ERR_UNSUPPORTED, "types %d / %d / %d (supported: F32, BF16, F16)", (int)d.x_type, (int)d.y_type,
+                    (int)d.u_type);
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", T);
+    if (d.H < 1 || d.H > 32768) return fail(MOE_ERR_INVALID_ARG, "H = %d outside 1..32768", d.H);
+    if (!(d.eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    if (u && !d.gamma_pre) return fail(MOE_ERR_INVALID_ARG, "u needs gamma_pre");
+    if (!u && !x_out) return fail(MOE_ERR_INVALID_ARG, "neither x_out nor u is asked for");
+    if (T == 0) return MOE_OK;
+    if (!y) return fail(MOE_ERR_INVALID_ARG, "y is NULL");
+    const int64_t most = (int64_t)1 << 32;
+    auto bad_stride = [&](const void* p, int64_t st) { return p && (st < d.H || st > most); };
+    if (bad_stride(x, x_stride) || bad_stride(y, y_stride) || bad_stride(x_out, x_out_stride) || bad_stride(u, u_stride))
+        return fail(MOE_ERR_INVALID_ARG, "a row stride is smaller than H = %d (or too large)", d.H);
+    if (gate && (gate_row < 0 || gate_col < 0 || gate_row > most || gate_col > most))
+        return fail(MOE_ERR_INVALID_ARG, "gate strides %lld / %lld", (long long)gate_row, (long long)gate_col);
+    if (!aligned(x, value_bytes(d.x_type)) || !aligned(x_out, value_bytes(d.x_type)) || !aligned(y, value_bytes(d.y_type)) ||
+        !aligned(u, value_bytes(d.u_type)) || !aligned(gate, 4) || !aligned(d.gamma_post, 4) || !aligned(d.gamma_pre, 4))
+        return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+    // what is written must not overlap what other threads still read (x_out == x with one stride may)
+    struct Span { uintptr_t lo, hi; };
+    auto span = [&](const void* p, int type, int64_t st) {
+        const uintptr_t b = (uintptr_t)p;
+        return Span{b, p ? b + value_bytes(type) * (uintptr_t)((int64_t)(T - 1) * st + d.H) : b};
+    };
+    auto meet = [](const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; };
+    const Span sx = span(x, d.x_type, x_stride), sy = span(y, d.y_type, y_stride),
+               so = span(x_out, d.x_type, x_out_stride), su = span(u, d.u_type, u_stride);
+    Span sg{(uintptr_t)gate, (uintptr_t)gate};
+    if (gate) sg.hi += 4 * (uintptr_t)((int64_t)(T - 1) * gate_row + (int64_t)(d.H - 1) * gate_col + 1);
+    const bool in_place = x && x == x_out && x_stride == x_out_stride;
+    if (meet(so, sy) || meet(su, sy) || meet(so, su) || meet(su, sx) || meet(so, sg) || meet(su, sg) ||
+        (!in_place && meet(so, sx)))
+        return fail(MOE_ERR_INVALID_ARG, "x_out / u overlap an input or each other");
+    NormPairArgs a{};
+    a.T = T; a.H = d.H;
+    a.x = x; a.x_type = d.x_type; a.x_stride = x_stride;
+    a.y = y; a.y_type = d.y_type; a.y_stride = y_stride;
+    a.gate = gate; a.gate_row = gate_row; a.gate_col = gate_col;
+    a.gamma_post = d.gamma_post; a.gamma_pre = d.gamma_pre;
+    a.eps = d.eps; a.res_scale = d.res_scale; a.scale = d.scale;
+    a.x_out = x_out; a.x_out_stride = x_out_stride;
+    a.u = u; a.u_type = d.u_type; a.u_stride = u_stride;
+    cudaError_t err = launch_norm_pair(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "norm kernel");
     return MOE_OK;
 }
 

@@ -131,3 +131,203 @@ class MoeLayer:
                 self.plan = None
         except Exception:
             pass
+
+
+_VT = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16, torch.float16: N.MOE_F16}
+
+
+def _cuda(t, name, dtypes=None, dim=None):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, not {t.dtype}")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+
+
+def _row_stride(t, name):
+    """Elements between the rows of a 2-D tensor whose rows are dense."""
+    n, width = t.shape
+    row, col = t.stride()
+    if col != 1 and width != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    return row if n > 1 else (width + 7) // 8 * 8        # (one row: its stride is never used)
+
+
+class _Products:
+    """What GroupedExperts and W4Experts share: the rows of a call, checked and passed on."""
+
+    plan = None
+
+    def __call__(self, x: torch.Tensor, offsets: torch.Tensor | None = None, sorted_pairs: torch.Tensor | None = None,
+                 k: int = 1, out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+        """y [T*k, n_out]: row i is the product of sorted position i's row of x with its expert's matrix.
+
+        With sorted_pairs (int32 [T*k], moe_permute's) x holds the T tokens, row i being that of token
+        sorted_pairs[i] // k; without, x holds the T*k rows in sorted order.  offsets (int32 [E+1], moe_permute's) may
+        be left out for one expert.  status: int32 [1], raised when a device-side check fails.
+        """
+        n, width = x.shape
+        T = n if sorted_pairs is not None else n // k
+        P = T * k
+        if x.dtype is not self.x_dtype or width != self.n_in or not x.is_cuda:
+            raise ValueError(f"x must be a {self.x_dtype} CUDA tensor [rows, {self.n_in}]")
+        if sorted_pairs is None and P != n:
+            raise ValueError(f"{n} rows of x are not a multiple of k = {k}")
+        if sorted_pairs is not None and (sorted_pairs.dtype is not torch.int32 or sorted_pairs.numel() != P
+                                         or not sorted_pairs.is_contiguous() or not sorted_pairs.is_cuda):
+            raise ValueError(f"sorted_pairs must be a dense int32 CUDA tensor of {P} entries")
+        if offsets is not None and (offsets.dtype is not torch.int32 or offsets.numel() != self.n_experts + 1
+                                    or not offsets.is_contiguous() or not offsets.is_cuda):
+            raise ValueError(f"offsets must be a dense int32 CUDA tensor of {self.n_experts + 1} entries")
+        if status is not None and (status.dtype is not torch.int32 or status.numel() < 1 or not status.is_cuda):
+            raise ValueError("status must be an int32 CUDA tensor")
+        if out is None:
+            out = torch.empty((P, self.n_out), dtype=self.y_dtype, device=x.device)
+        elif out.dtype is not self.y_dtype or out.shape != (P, self.n_out) or not out.is_cuda:
+            raise ValueError(f"out must be a {self.y_dtype} CUDA tensor [{P}, {self.n_out}]")
+        self._matmul(self.plan, x, _row_stride(x, "x"), T, k, sorted_pairs, offsets, out, _row_stride(out, "out"), status,
+                     stream)
+        return out
+
+    def __del__(self):
+        try:
+            if self.plan:
+                self._destroy(self.plan)
+                self.plan = None
+        except Exception:
+            pass
+
+
+class GroupedExperts(_Products):
+    """Products of each expert's rows with its bf16 / fp16 matrix (moe_grouped_matmul).
+
+    w: [E, n_out, n_in] (order "out_in") or [E, n_in, n_out] ("in_out") on the GPU, last dimension dense, the
+    other strides multiples of 8 elements; w_up (same shape and strides): the call gives
+    silu(w x) * (w_up x).  y_dtype: fp32 (what moe_combine reads), bf16 or fp16.
+    """
+
+    _matmul = staticmethod(N.moe_grouped_matmul)
+    _destroy = staticmethod(N.moe_grouped_plan_destroy)
+
+    def __init__(self, w: torch.Tensor, w_up: torch.Tensor | None = None, *, order: str = "out_in",
+                 y_dtype: torch.dtype = torch.float32):
+        if order not in ("out_in", "in_out"):
+            raise ValueError(f"order must be 'out_in' or 'in_out', not {order!r}")
+        if y_dtype not in _VT:
+            raise ValueError(f"y_dtype must be one of {[str(d) for d in _VT]}")
+        _cuda(w, "w", (torch.bfloat16, torch.float16), 3)
+        if w.stride(2) != 1 and w.shape[2] != 1:
+            raise ValueError("the last dimension of w must be dense")
+        if w_up is not None:
+            _cuda(w_up, "w_up", (w.dtype,), 3)
+            if w_up.shape != w.shape or w_up.stride() != w.stride():
+                raise ValueError("w_up must have w's shape and strides")
+        self.n_experts = w.shape[0]
+        self.n_out, self.n_in = (w.shape[1], w.shape[2]) if order == "out_in" else (w.shape[2], w.shape[1])
+        self.x_dtype, self.y_dtype = w.dtype, y_dtype
+        self._keep = (w, w_up)
+        self.plan = N.moe_grouped_plan_create(N.moe_grouped_desc(
+            _VT[w.dtype], _VT[y_dtype], N.MOE_W_OUT_IN if order == "out_in" else N.MOE_W_IN_OUT, self.n_experts,
+            self.n_out, self.n_in, w.data_ptr(), w_up.data_ptr() if w_up is not None else None,
+            _row_stride(w[0], "w"), w.stride(0)))
+
+    def path(self, T: int, k: int = 1) -> str:
+        """Which kernel a call with T tokens of k experts runs: "rows" or "tensor"."""
+        return ("rows", "tensor")[N.moe_grouped_path(self.plan, T, k)]
+
+
+class W4Experts(_Products):
+    """The same products over 4-bit weights with group scales (moe_w4_matmul).
+
+    q: uint8 [E, n_out, n_in // 2] (weight 2j in the low nibble of byte j), scales: fp16 or bf16
+    [E, n_out, n_in // group], zeros: uint8 like scales, or None for 8 everywhere; up: (q, scales, zeros) of
+    the gated pair's other matrix.  All dense, on the GPU.
+    """
+
+    _matmul = staticmethod(N.moe_w4_matmul)
+    _destroy = staticmethod(N.moe_w4_plan_destroy)
+
+    def __init__(self, q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, *, up=None,
+                 group: int = 128, x_dtype: torch.dtype = torch.bfloat16, y_dtype: torch.dtype = torch.float32):
+        if x_dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("x_dtype must be torch.bfloat16 or torch.float16")
+        if y_dtype not in _VT:
+            raise ValueError(f"y_dtype must be one of {[str(d) for d in _VT]}")
+        if group not in (32, 64, 128):
+            raise ValueError(f"group must be 32, 64 or 128, not {group}")
+        up = (None, None, None) if up is None else tuple(up) + (None,) * (3 - len(up))
+        if (up[0] is not None) and (up[2] is None) != (zeros is None):
+            raise ValueError("both matrices have zero points, or neither")
+        _cuda(q, "q", (torch.uint8,), 3)
+        E, n_out, n_in = q.shape[0], q.shape[1], 2 * q.shape[2]
+        if n_in % group:
+            raise ValueError(f"n_in = {n_in} is not a multiple of the group {group}")
+        for name, t, dtypes, width in (("scales", scales, (torch.float16, torch.bfloat16), n_in // group),
+                                       ("zeros", zeros, (torch.uint8,), n_in // group),
+                                       ("q_up", up[0], (torch.uint8,), n_in // 2),
+                                       ("scales_up", up[1], (scales.dtype,), n_in // group),
+                                       ("zeros_up", up[2], (torch.uint8,), n_in // group), ("q", q, None, n_in // 2)):
+            if t is None:
+                if name in ("scales",) or (name == "scales_up" and up[0] is not None):
+                    raise ValueError(f"{name} is missing")
+                continue
+            _cuda(t, name, dtypes, 3)
+            if tuple(t.shape) != (E, n_out, width) or not t.is_contiguous():
+                raise ValueError(f"{name} must be dense [{E}, {n_out}, {width}]")
+        self.n_experts, self.n_out, self.n_in = E, n_out, n_in
+        self.x_dtype, self.y_dtype = x_dtype, y_dtype
+        self._keep = (q, scales, zeros, up)
+        p = [t.data_ptr() if t is not None else None for t in (q, scales, zeros) + up]
+        self.plan = N.moe_w4_plan_create(N.moe_w4_desc(_VT[x_dtype], _VT[y_dtype], _VT[scales.dtype], group, E, n_out,
+                                                       n_in, *p))
+
+
+class NormResidual:
+    """The norm behind a block, its gate and residual scale, and the next block's norm (moe_norm_residual).
+
+    gamma_post, gamma_pre: fp32 [H] on the GPU (gamma_post None: no norm behind the block; gamma_pre None: no u).
+    """
+
+    def __init__(self, H: int, *, gamma_post: torch.Tensor | None = None, gamma_pre: torch.Tensor | None = None,
+                 eps: float = 1e-6, res_scale: float = 1.0, scale: float = 1.0):
+        for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
+            if g is not None:
+                _cuda(g, name, (torch.float32,), 1)
+                if g.numel() != H or not g.is_contiguous():
+                    raise ValueError(f"{name} must be dense [{H}]")
+        self.H = H
+        self._keep = (gamma_post, gamma_pre)
+        self.desc = N.moe_norm_desc(H, 0, 0, 0, *(g.data_ptr() if g is not None else None for g in self._keep), eps,
+                                    res_scale, scale)
+
+    def __call__(self, x: torch.Tensor | None, y: torch.Tensor, gate: torch.Tensor | None = None,
+                 x_out: torch.Tensor | None = None, u: torch.Tensor | None = None, stream=None):
+        """(x_out, u): the residual stream behind the block (in x's type; x_out may be x) and its norm.
+
+        x (None: 0), y: [T, H].  gate: fp32, broadcastable to [T, H] ([H], [1, H], [T, 1] or [T, H]).
+        Outputs that are not given are made: x_out like x (or y), u in bf16 when gamma_pre was given.
+        """
+        T, H = y.shape
+        d = self.desc
+        if H != self.H or (x is not None and x.shape != y.shape):
+            raise ValueError(f"x and y must be [T, {self.H}]")
+        if x_out is None:
+            x_out = torch.empty((T, H), dtype=(x if x is not None else y).dtype, device=y.device)
+        if u is None and self._keep[1] is not None:
+            u = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+        for name, t in (("x", x), ("y", y), ("x_out", x_out), ("u", u)):
+            if t is not None and (t.dtype not in _VT or not t.is_cuda or t.shape != y.shape):
+                raise ValueError(f"{name} must be an fp32, bf16 or fp16 CUDA tensor [{T}, {self.H}]")
+        if x is not None and x.dtype is not x_out.dtype:
+            raise ValueError("x_out must have x's type")
+        gate_row = gate_col = 0
+        if gate is not None:
+            _cuda(gate, "gate", (torch.float32,))
+            gate_row, gate_col = gate.broadcast_to(T, H).stride()
+        d = N.moe_norm_desc(H, _VT[x_out.dtype], _VT[y.dtype], _VT[u.dtype] if u is not None else N.MOE_F32,
+                            d.gamma_post, d.gamma_pre, d.eps, d.res_scale, d.scale)
+        N.moe_norm_residual(d, x, _row_stride(x, "x") if x is not None else 0, y, _row_stride(y, "y"), gate, gate_row,
+                            gate_col, T, x_out, _row_stride(x_out, "x_out"), u, _row_stride(u, "u") if u is not None else 0,
+                            stream)
+        return x_out, u
