@@ -319,6 +319,9 @@ moe_status check_product_call(const moe::RowsArgs& a, int T, int k, bool* todo) 
 
 }  // namespace
 
+// Which kernel runs P rows of E experts: see moe_grouped_path.
+static bool grouped_tensor(const moe::RowsArgs& a, int64_t P) { return P > 64; }
+
 struct moe_grouped_plan {
     moe::RowsArgs a;             // the weights' side; a call fills in its own
 };
@@ -597,7 +600,7 @@ moe_status moe_grouped_plan_destroy(moe_grouped_plan* plan) {
 moe_status moe_grouped_path(const moe_grouped_plan* plan, int T, int k, int* path) {
     if (!plan || !path) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
     if (T < 1 || k < 1) return fail(MOE_ERR_INVALID_ARG, "T = %d, k = %d", T, k);
-    *path = MOE_GROUPED_ROWS;
+    *path = grouped_tensor(plan->a, (int64_t)T * k) ? MOE_GROUPED_TENSOR : MOE_GROUPED_ROWS;
     return MOE_OK;
 }
 
@@ -612,7 +615,8 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
     moe_status st = check_product_call(a, T, k, &todo);
     if (st || !todo) return st;
     a.P = T * k;
-    cudaError_t err = launch_rows(a, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err = grouped_tensor(a, a.P) ? launch_grouped_dense(a, s) : launch_rows(a, s);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product kernel");
     return MOE_OK;
 }

@@ -175,7 +175,8 @@ struct RowsArgs {
     int64_t y_stride;
     int32_t* status;             // nullable
 };
-cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);            // streams the weights (rows.cu)
+cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s);   // tcgen05, dense weights (ggemm_dense.cu)
 
 // ---------------------------------------------------------------- decode layer (T <= 4)
 // The whole layer for a few tokens: shapes, weights and workspace buffers.
