@@ -72,29 +72,19 @@ __device__ __forceinline__ uint32_t in_peer(uint32_t a) {
     return r;
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
-}
-__device__ __forceinline__ bool test_cluster(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, "
-        "p;\n}\n"
-        : "=r"(ok)
-        : "r"(su32(b)), "r"(parity), "r"(100000u)
-        : "memory");
-    return ok != 0;
 }
 // Bounded wait of a whole warp on a barrier that either CTA of the pair arrives on: false on every lane
 // after limit_ns (raising abort_flag) or when another warp of this CTA has raised it.
 __device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-    bool ok = test_cluster(b, parity);
+    bool ok = mbar_test(b, parity);
     if (!ok) {
         const uint64_t t0 = gtime();
-        while (!(ok = test_cluster(b, parity))) {
+        while (!(ok = mbar_test(b, parity))) {
             if (*abort_flag) break;
             if (gtime() - t0 > limit_ns) { *abort_flag = 1; break; }
         }
@@ -103,7 +93,7 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, volat
 }
 __device__ __forceinline__ void drain_wait(uint64_t* b, uint32_t parity, uint64_t limit_ns) {
     const uint64_t t0 = gtime();
-    while (!test_cluster(b, parity))
+    while (!mbar_test(b, parity))
         if (gtime() - t0 > limit_ns) return;
 }
 
