@@ -16,9 +16,11 @@
 // [in][out] weights enter as an MN-major operand (the descriptor's transpose bit): the same boxes
 // with their axes exchanged, no transposed copy.
 //
-// Warps: 0 loads (TMA: two 64 x 64 weight boxes; the x rows as 16-row boxes, or as four-row gathers
-// through the pairs), 1 issues the MMAs (in the first CTA of the pair) and owns TMEM, 4..11 are the epilogue
-// (two accumulators of 256 columns: one is read out while the next tile runs).  Persistent:
+// Warps: 0 loads (TMA: two 64 x 64 weight boxes, and the x rows in place as 16-row boxes), 1 issues the
+// MMAs (in the first CTA of the pair) and owns TMEM, 2 and 3 copy the x rows that the pairs name (cp.async,
+// 16 bytes a thread, four steps in flight; TMA's four-row gathers took 70 clocks each, 594 us for the
+// gated half of 4096 tokens), 4..11 are the epilogue (two accumulators of 256 columns: one is
+// read out while the next tile runs).  Persistent:
 // a pair takes every (pairs of CTAs)-th tile of the list that the offsets define, each warp role finding its
 // tiles by itself.  Every wait is bounded; a wait that runs out is reported (MOE_ERR_TIMEOUT), the copies in flight
 // are waited for (bounded), TMEM is freed and the kernel returns.
@@ -33,13 +35,17 @@ namespace {
 
 constexpr int kStages = 6, kStepK = 64, kMaxN = 256;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
-constexpr int kThreads = 384, kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kThreads = 384, kGatherWarp0 = 2, kGatherWarps = 2, kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kGatherAhead = 4;                          // steps a gathering thread has in flight
+constexpr int kGatherRows = 128 / (4 * kGatherWarps);    // rows of a step a gathering thread copies 16 bytes of
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
 
 struct DenseParams {
     CUtensorMap tw0, tw1;        // W, W_up: [E][rows][cols], boxes of 64 x 64
-    CUtensorMap tx;              // x rows: boxes of 64 x 16, or 64 x 1 for the four-row gathers
+    CUtensorMap tx;              // x rows in place: boxes of 64 x 16
+    const uint16_t* x;           // x rows for the gather
+    int64_t x_stride;
     const int32_t* sorted_pairs; // NULL: rows in place
     const int32_t* offsets;      // NULL: one expert over all P rows
     int E, k, P, N, K;
@@ -60,6 +66,9 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The pair's barriers order copies and MMAs, which carry their own ordering; no plain loads or stores
+// pass from CTA to CTA through them.  So their operations take the default scope: with release and
+// acquire at cluster scope every step of the pipeline waited about 0.5 us for its arrival.
 // Shared address of the pair's first CTA (the one that issues the MMAs) for an address of this one.
 __device__ __forceinline__ uint32_t in_leader(uint32_t a) {
     uint32_t r;
@@ -109,13 +118,6 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
         "[%4];" ::"r"(dst),
         "l"(m), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, int x, const int (&r)[4], uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(m), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -203,20 +205,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     uint64_t* never = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* issued = reinterpret_cast<int*>(tmem_slot + 2); // steps whose copies this CTA has issued
-    int* scan = reinterpret_cast<int*>(tmem_slot + 4);   // [16]
+    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // steps that warps 0, 2 and 3 have arrived for
+    int* scan = reinterpret_cast<int*>(tmem_slot + 6);   // [16]
     int* off = scan + 16;                                // [E + 1] offsets, clamped and in order
     int* tb0 = off + p.E + 1;                            // [E + 1] blocks of rows before each expert
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t cta = cta_rank();
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 2 + 2 * kGatherWarps : 2); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kEpiWarps); }
         mbar_init(drain, 1);
         mbar_init(never, 1);
         *abort_flag = 0;
-        *issued = 0;
+        for (int i = 0; i < 1 + kGatherWarps; ++i) done[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -270,19 +272,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         bool ok = true;
         Tile ti;
         for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
-            int rows[4] = {0, 0, 0, 0};
             const int c0 = ti.tok0 + (int)cta * ti.nh;   // this CTA's first column, as a sorted position
-            if (p.sorted_pairs && 4 * lane < ti.nh) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pair = __ldg(p.sorted_pairs + min(c0 + 4 * lane + i, ti.tok0 + ti.ntok - 1));
-                    const bool in = pair >= 0 && pair < p.P;
-                    bad |= !in;
-                    rows[i] = in ? pair / p.k : 0;
-                }
-            }
             const int r0 = ti.mb * kRowsTile + (int)cta * (kRowsTile / 2);
-            const uint32_t bytes = kABytes + ti.nh * 128;
+            const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : ti.nh * 128);
             for (int kb = 0; kb < nk; ++kb, ++g) {
                 const int s = g % kStages;
                 if (g >= kStages && !wait_cluster(&empty[s], (g / kStages - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
@@ -298,13 +290,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                         tma_3d(a, &p.tw0, c, r0, ti.e, bar);
                         tma_3d(a + 8192, UP ? &p.tw1 : &p.tw0, c, UP ? r0 : r0 + 64, ti.e, bar);
                     }
-                    *issued = (int)g + 1;
+                    done[0] = (int)g + 1;
                 }
-                if (p.sorted_pairs) {
-                    if (4 * lane < ti.nh) tma_gather4(b + 512 * lane, &p.tx, kb * kStepK, rows, bar);
-                } else if (16 * lane < ti.nh) {
+                if (!p.sorted_pairs && 16 * lane < ti.nh)
                     tma_2d(b + 2048 * lane, &p.tx, kb * kStepK, c0 + 16 * lane, bar);
-                }
                 __syncwarp();
             }
         }
@@ -348,6 +337,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                              : "memory");
             __syncwarp();
             drain_wait(drain, 0, p.wait_ns);
+        }
+    } else if (warp >= kGatherWarp0 && warp < kEpiWarp0) {
+        // ======================= gathered rows of x =======================
+        if (p.sorted_pairs) {
+            // thread u copies chunk u % 8 of rows u / 8 + 8 * kGatherWarps * j of a step into the swizzled layout
+            const int u = tid - 32 * kGatherWarp0, ch = u & 7, w = warp - kGatherWarp0;
+            constexpr int kRowStep = 4 * kGatherWarps;
+            const uint32_t full0 = in_leader(su32(full));
+            uint32_t g = 0, arrived = 0;
+            bool ok = true;
+            Tile ti;
+            for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
+                const int c0 = (int)cta * ti.nh, nc = min(ti.nh, ti.ntok - c0);   // columns of this CTA that hold rows
+                int row[kGatherRows];
+#pragma unroll
+                for (int j = 0; j < kGatherRows; ++j) {
+                    const int r = (u >> 3) + kRowStep * j;
+                    row[j] = 0;
+                    if (r < nc) {
+                        const int pair = __ldg(p.sorted_pairs + ti.tok0 + c0 + r);
+                        const bool in = pair >= 0 && pair < p.P;
+                        bad |= !in;
+                        row[j] = in ? pair / p.k : 0;
+                    }
+                }
+                for (int kb = 0; kb < nk; ++kb, ++g) {
+                    const int s = g % kStages;
+                    if (g >= kStages && !wait_cluster(&empty[s], (g / kStages - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                    const int c = kb * kStepK + 8 * ch;
+                    const uint32_t bytes = (uint32_t)min(max(2 * (p.K - c), 0), 16);   // zeros past the row's end
+                    uint8_t* dst = smem + s * kStageBytes + kABytes;
+#pragma unroll
+                    for (int j = 0; j < kGatherRows; ++j) {
+                        const int r = (u >> 3) + kRowStep * j;
+                        if (r < nc) cp_async16(dst + swz(r, ch), p.x + row[j] * p.x_stride + (bytes ? c : 0), bytes);
+                    }
+                    cp_commit();
+                    if (g >= kGatherAhead) {
+                        cp_wait<kGatherAhead>();
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(full0 + 8 * ((g - kGatherAhead) % kStages));
+                        arrived = g - kGatherAhead + 1;
+                    }
+                }
+            }
+            cp_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            for (; ok && arrived < g; ++arrived)
+                if (lane == 0) arrive_cluster(full0 + 8 * (arrived % kStages));
+            if (lane == 0) done[1 + w] = (int)arrived;
         }
     } else if (warp >= kEpiWarp0) {
         // ======================= epilogue =======================
@@ -413,20 +454,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     __syncwarp();
     cluster_sync();                                      // both CTAs' roles have left their loops
     if (cta == 0 && tid == 0) {
-        // after a timeout copies may still be in flight: complete the phases of the steps that only
-        // one CTA has issued (on behalf of the other) and wait, within the limit, for the bytes
-        const int mine = *issued;
-        int theirs;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(theirs) : "r"(in_peer(su32(issued))) : "memory");
+        // after a timeout copies may still be in flight: complete the phases of the steps that some
+        // warps have arrived for (on behalf of the others) and wait, within the limit, for the bytes
         int peer_abort;
         asm volatile("ld.volatile.shared::cluster.u32 %0, [%1];"
                      : "=r"(peer_abort)
                      : "r"(in_peer(su32(const_cast<int*>(abort_flag))))
                      : "memory");
         if (*abort_flag || peer_abort) {
-            const int last = max(mine, theirs);
-            for (int s = mine; s < last; ++s) mbar_arrive(&full[s % kStages]);
-            for (int s = theirs; s < last; ++s) mbar_arrive(&full[s % kStages]);
+            const int warps = p.sorted_pairs ? 1 + kGatherWarps : 1;
+            int of[2][1 + kGatherWarps], last = 0;
+            for (int i = 0; i < warps; ++i) {
+                of[0][i] = done[i];
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(of[1][i]) : "r"(in_peer(su32(done + i))) : "memory");
+                last = max(last, max(of[0][i], of[1][i]));
+            }
+            for (int c = 0; c < 2; ++c)
+                for (int i = 0; i < warps; ++i)
+                    for (int s = of[c][i]; s < last; ++s) mbar_arrive(&full[s % kStages]);
             for (int s = max(0, last - kStages); s < last; ++s) drain_wait(&full[s % kStages], (s / kStages) & 1, p.wait_ns);
             if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
         }
@@ -469,7 +514,7 @@ bool encode(CUtensorMap* m, bool bf16, int rank, const void* base, const cuuint6
 }
 
 size_t smem_bytes(int E) {
-    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 16 + 64 + 2 * (size_t)(E + 1) * 4;
+    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 24 + 64 + 2 * (size_t)(E + 1) * 4;
 }
 
 }  // namespace
@@ -481,11 +526,13 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     const cuuint64_t wd[3] = {cols, rows, (cuuint64_t)a.E};
     const cuuint64_t ws[2] = {(cuuint64_t)a.row_stride * 2, a.E > 1 ? (cuuint64_t)a.expert_stride * 2
                                                                     : (cuuint64_t)a.row_stride * rows * 2};
-    const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)(a.sorted_pairs ? a.P / a.k : a.P), 1};
+    const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.P, 1};
     const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
     if (!encode(&p.tw0, a.bf16, 3, a.w0, wd, ws, 64) || (a.w1 && !encode(&p.tw1, a.bf16, 3, a.w1, wd, ws, 64)) ||
-        !encode(&p.tx, a.bf16, 2, a.x, xd, xs, a.sorted_pairs ? 1 : 16))
+        (!a.sorted_pairs && !encode(&p.tx, a.bf16, 2, a.x, xd, xs, 16)))
         return cudaErrorInvalidValue;
+    p.x = static_cast<const uint16_t*>(a.x);
+    p.x_stride = a.x_stride;
     p.sorted_pairs = a.sorted_pairs; p.offsets = a.offsets;
     p.E = a.E; p.k = a.k; p.P = a.P; p.N = a.N; p.K = a.K;
     p.bf16 = a.bf16; p.in_out = a.in_out;

@@ -380,3 +380,24 @@ def test_w4_nan_and_inf_stay_in_their_row():
     assert not bool(torch.isfinite(bad[3:, 7]).any())
     cols = [c for c in range(N_) if c != 7]
     assert torch.equal(bad[3:, cols], good[3:, cols])
+
+
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_wait_that_runs_out_is_reported(gather):
+    """The test setting's stalled wait: the call returns, says so, and the next call gives the bits of the one before."""
+    T, k, E, K, N_ = 200, 2, 3, 1024, 300
+    _, off, pairs, x, w, _ = _dense_case(T, k, E, K, N_, False, gather, BF, F32, "out_in")
+    op = moe.GroupedExperts(w)
+    assert op.path(T, k) == "tensor"
+    p = pairs if gather else None
+    ref = op(x, off, p, k=k).clone()
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        N.moe_debug_set_waits(2_000_000, 1)
+        op(x, off, p, k=k, status=status)
+        torch.cuda.synchronize()
+    finally:
+        N.moe_debug_set_waits(0, 0)
+    assert status.item() == N.MOE_ERR_TIMEOUT
+    assert torch.equal(op(x, off, p, k=k), ref)
