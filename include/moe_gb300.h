@@ -304,7 +304,7 @@ moe_status moe_rmsnorm_bf16(const float* x, const float* gamma, int T, int H, fl
  *   overlap x.  status (device int32, nullable, caller-owned, never cleared by the call) is
  *   raised from MOE_OK to MOE_ERR_DEVICE_CHECK when an offset leaves 0..T*k or decreases (it is
  *   clamped) or a pair leaves 0..T*k-1 (its row of y is undefined), and to MOE_ERR_TIMEOUT when a device-side wait ran out (y is
- *   undefined).  T*k <= 2^30; T = 0 is a no-op.  Launches one kernel, allocates nothing, needs no
+ *   undefined).  T*k <= 2^30; T * x_stride <= 2^35 with sorted_pairs; T = 0 is a no-op.  Launches one kernel, allocates nothing, needs no
  *   workspace, keeps nothing between calls: two calls may overlap on the GPU, and a captured call
  *   replays with the bits of the eager one.
  * Kernels (moe_grouped_path tells which): MOE_GROUPED_ROWS streams the weights of the experts that

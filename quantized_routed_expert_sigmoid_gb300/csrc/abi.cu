@@ -615,6 +615,8 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
     moe_status st = check_product_call(a, T, k, &todo);
     if (st || !todo) return st;
     a.P = T * k;
+    if (sorted_pairs && (int64_t)T * x_stride > (int64_t)1 << 35)
+        return fail(MOE_ERR_INVALID_ARG, "T * x_stride above 2^35 elements with gathered rows");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err = grouped_tensor(a, a.P) ? launch_grouped_dense(a, s) : launch_rows(a, s);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product kernel");

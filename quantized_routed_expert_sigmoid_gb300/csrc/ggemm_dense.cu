@@ -16,10 +16,10 @@
 // [in][out] weights enter as an MN-major operand (the descriptor's transpose bit): the same boxes
 // with their axes exchanged, no transposed copy.
 //
-// Warps: 0 loads (TMA: two 64 x 64 weight boxes, and the x rows in place as 16-row boxes), 1 issues the
-// MMAs (in the first CTA of the pair) and owns TMEM, 2 and 3 copy the x rows that the pairs name (cp.async,
-// 16 bytes a thread, four steps in flight; TMA's four-row gathers took 70 clocks each, 594 us for the
-// gated half of 4096 tokens), 4..11 are the epilogue (two accumulators of 256 columns: one is
+// Warps: 0 loads (TMA, as few boxes as there can be: issuing one takes about 100 clocks of the
+// thread), 1 issues the MMAs (in the first CTA of the pair) and owns TMEM, 2, 3, 12 and 13 copy the x rows that
+// the pairs name, a step each in turn (cp.async, 16 bytes a thread; TMA's four-row gathers, 32 a step,
+// took longer than the step's MMAs), 4..11 are the epilogue (two accumulators of 256 columns: one is
 // read out while the next tile runs).  Persistent:
 // a pair takes every (pairs of CTAs)-th tile of the list that the offsets define, each warp role finding its
 // tiles by itself.  Every wait is bounded; a wait that runs out is reported (MOE_ERR_TIMEOUT), the copies in flight
@@ -35,21 +35,22 @@ namespace {
 
 constexpr int kStages = 6, kStepK = 64, kMaxN = 256;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
-constexpr int kThreads = 384, kGatherWarp0 = 2, kGatherWarps = 2, kEpiWarp0 = 4, kEpiWarps = 8;
-constexpr int kGatherAhead = 4;                          // steps a gathering thread has in flight
-constexpr int kGatherRows = 128 / (4 * kGatherWarps);    // rows of a step a gathering thread copies 16 bytes of
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;              // (a warp reads the TMEM lanes 32 (warp % 4)..)
+constexpr int kGatherWarps = 4;                          // warps 2, 3, 12, 13
+constexpr int kThreads = 32 * (2 + kEpiWarps + kGatherWarps);
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
+constexpr int kSpins = 64;                               // tests of a barrier before a wait looks at the clock
 
 struct DenseParams {
     CUtensorMap tw0, tw1;        // W, W_up: [E][rows][cols], boxes of 64 x 64
-    CUtensorMap tx;              // x rows in place: boxes of 64 x 16
+    CUtensorMap tx[4];           // x rows in place: boxes of 64 x 16, 32, 64, 128
     const uint16_t* x;           // x rows for the gather
     int64_t x_stride;
     const int32_t* sorted_pairs; // NULL: rows in place
     const int32_t* offsets;      // NULL: one expert over all P rows
     int E, k, P, N, K;
-    bool bf16, in_out;
+    bool bf16;
     void* y;
     int y_type;
     int64_t y_stride;
@@ -87,19 +88,30 @@ __device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) 
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-// Bounded wait of a whole warp on a barrier that either CTA of the pair arrives on: false on every lane
-// after limit_ns (raising abort_flag) or when another warp of this CTA has raised it.
-__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-    bool ok = mbar_test(b, parity);
-    if (!ok) {
-        const uint64_t t0 = gtime();
-        while (!(ok = mbar_test(b, parity))) {
-            if (*abort_flag) break;
-            if (gtime() - t0 > limit_ns) { *abort_flag = 1; break; }
-        }
+// Bounded wait on a barrier that either CTA of the pair arrives on: false after limit_ns (raising
+// abort_flag) or when another warp of this CTA has raised it.
+__device__ __forceinline__ bool wait_one(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+    for (int i = 0; i < kSpins; ++i)
+        if (mbar_test(b, parity)) return true;
+    const uint64_t t0 = gtime();                         // (reading the clock takes long: not before the spins)
+    while (!mbar_test(b, parity)) {
+        if (*abort_flag) return false;
+        if (gtime() - t0 > limit_ns) { *abort_flag = 1; return false; }
     }
-    return __all_sync(0xffffffffu, ok);
+    return true;
 }
+// The same for a whole warp: the answer is that of all its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, wait_one(b, parity, abort_flag, limit_ns));
+}
+// A position in the ring of stages and the parity of its round.
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == kStages) { s = 0; ph ^= 1; }
+    }
+};
 __device__ __forceinline__ void drain_wait(uint64_t* b, uint32_t parity, uint64_t limit_ns) {
     const uint64_t t0 = gtime();
     while (!mbar_test(b, parity))
@@ -163,12 +175,6 @@ __device__ __forceinline__ void named_sync(int barrier, int threads) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ void store_out(void* y, int type, int64_t i, float v) {
-    if (type == MOE_F32) reinterpret_cast<float*>(y)[i] = v;
-    else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
-    else reinterpret_cast<__half*>(y)[i] = __float2half_rn(v);
-}
-
 struct Tile {
     int e, mb, tok0, ntok, nh;   // expert, block of M rows, first sorted position, rows, columns per CTA
 };
@@ -192,7 +198,85 @@ __device__ __forceinline__ bool tile_at(const int* off, const int* tb0, int E, i
     return true;
 }
 
-template <bool UP>
+template <typename T> __device__ __forceinline__ T to_out(float v);
+template <> __device__ __forceinline__ float to_out<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half to_out<__half>(float v) { return __float2half_rn(v); }
+
+// An epilogue warp: warp w reads TMEM lanes 32 (w % 4).. (weight rows) and every other group of columns
+// (rows of x) of each tile, and stores 32 neighbouring outputs of one row at a time.
+template <bool UP, typename T>
+__device__ __forceinline__ void epilogue(const DenseParams& p, const int* off, const int* tb0, int n_mb, int first, int n_pairs,
+                                         int cta, uint32_t tmem, float* exch, uint64_t* accf, uint64_t* accr,
+                                         volatile int* abort_flag) {
+    constexpr int kRowsTile = UP ? 128 : 256;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
+    const uint32_t accr0 = in_leader(su32(accr));
+    const int pairbar = 1 + side * 2 + (q & 1);          // gated: warps q and q + 2 trade columns
+    int j = 0, turn = 0;
+    Tile ti;
+    for (int t = first; tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
+        const int b = j & 1;
+        bool ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
+        // (the two warps of a trade leave together, or one would wait for the other for ever)
+        if constexpr (UP) ok = all_of(pairbar, 64, ok);
+        if (!ok) break;
+        tc_after();
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)b * kMaxN;
+        if constexpr (UP) {
+            const int row = ti.mb * kRowsTile + cta * 64 + (q & 1) * 32 + lane;
+            const bool is_up = q >= 2;
+            // the W warp keeps columns 0..7 of 16 and gives 8..15, the W_up warp the other way round
+            float* const buf = exch + (pairbar - 1) * 1024 + lane;
+            T* y = static_cast<T*>(p.y) + (int64_t)(ti.tok0 + 16 * side + (is_up ? 8 : 0)) * p.y_stride + row;
+            for (int c0 = 16 * side; c0 < ti.ntok; c0 += 32, ++turn, y += 32 * p.y_stride) {
+                uint32_t r[16];
+                tmem_ld16(acc + c0, r);
+                tmem_ld_wait();
+                float* mine = buf + (turn & 1) * 512 + (is_up ? 256 : 0);
+                const float* theirs = buf + (turn & 1) * 512 + (is_up ? 0 : 256);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mine[i * 32] = __uint_as_float(is_up ? r[i] : r[8 + i]);
+                named_sync(pairbar, 64);
+                const int n = row < p.N ? ti.ntok - c0 - (is_up ? 8 : 0) : 0;
+                T* at = y;
+#pragma unroll
+                for (int i = 0; i < 8; ++i, at += p.y_stride) {
+                    const float other = theirs[i * 32];
+                    const float gv = is_up ? other : __uint_as_float(r[i]);
+                    const float uv = is_up ? __uint_as_float(r[8 + i]) : other;
+                    // (the approximate division is off by at most two units; its 0 for a divisor above
+                    // 2^126 is what the exact one rounds to)
+                    if (i < n) *at = to_out<T>(__fdividef(gv, 1.0f + expf(-gv)) * uv);
+                }
+            }
+        } else {
+            const int row = ti.mb * kRowsTile + cta * 128 + q * 32 + lane;
+            T* y = static_cast<T*>(p.y) + (int64_t)(ti.tok0 + 32 * side) * p.y_stride + row;
+            for (int c0 = 32 * side; c0 < ti.ntok; c0 += 64, y += 64 * p.y_stride) {
+                uint32_t r[32];
+                tmem_ld32(acc + c0, r);
+                tmem_ld_wait();
+                const int n = row < p.N ? ti.ntok - c0 : 0;
+                T* at = y;
+                if (n >= 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i, at += p.y_stride) *at = to_out<T>(__uint_as_float(r[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i, at += p.y_stride)
+                        if (i < n) *at = to_out<T>(__uint_as_float(r[i]));
+                }
+            }
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(accr0 + 8 * b);
+    }
+}
+
+template <bool UP, bool IN_OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped_dense_kernel(const __grid_constant__ DenseParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -205,20 +289,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     uint64_t* never = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // steps that warps 0, 2 and 3 have arrived for
-    int* scan = reinterpret_cast<int*>(tmem_slot + 6);   // [16]
+    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [5] last step + 1 that warp 0 / each gathering warp arrived for
+    int* scan = reinterpret_cast<int*>(tmem_slot + 8);   // [16]
     int* off = scan + 16;                                // [E + 1] offsets, clamped and in order
     int* tb0 = off + p.E + 1;                            // [E + 1] blocks of rows before each expert
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t cta = cta_rank();
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 2 + 2 * kGatherWarps : 2); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 4 : 2); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kEpiWarps); }
         mbar_init(drain, 1);
         mbar_init(never, 1);
         *abort_flag = 0;
-        for (int i = 0; i < 1 + kGatherWarps; ++i) done[i] = 0;
+        for (int i = 0; i <= kGatherWarps; ++i) done[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -266,188 +350,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     const int nk = (p.K + kStepK - 1) / kStepK;
 
     if (warp == 0) {
-        // ======================= loads =======================
-        const uint32_t full0 = in_leader(su32(full));
-        uint32_t g = 0;
-        bool ok = true;
-        Tile ti;
-        for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
-            const int c0 = ti.tok0 + (int)cta * ti.nh;   // this CTA's first column, as a sorted position
-            const int r0 = ti.mb * kRowsTile + (int)cta * (kRowsTile / 2);
-            const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : ti.nh * 128);
-            for (int kb = 0; kb < nk; ++kb, ++g) {
-                const int s = g % kStages;
-                if (g >= kStages && !wait_cluster(&empty[s], (g / kStages - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
-                const uint32_t bar = full0 + 8 * s;
-                const uint32_t a = su32(smem + s * kStageBytes), b = a + kABytes;
-                if (lane == 0) {
+        // ======================= loads (one thread) =======================
+        if (lane == 0) {
+            const uint32_t full0 = in_leader(su32(full)), stage0 = su32(smem);
+            int g = 0;
+            Ring ring;
+            bool ok = true;
+            Tile ti;
+            for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
+                const int c0 = ti.tok0 + (int)cta * ti.nh;   // this CTA's first column, as a sorted position
+                const int r0 = ti.mb * kRowsTile + (int)cta * (kRowsTile / 2);
+                const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : ti.nh * 128);
+                for (int c = 0; c < nk * kStepK; c += kStepK, ring.next()) {
+                    if (!wait_one(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                    const uint32_t bar = full0 + 8 * ring.s, a = stage0 + ring.s * kStageBytes;
                     arrive_tx_cluster(bar, bytes);
-                    const int c = kb * kStepK;
-                    if (p.in_out) {
+                    if constexpr (IN_OUT) {
                         tma_3d(a, &p.tw0, r0, c, ti.e, bar);
                         tma_3d(a + 8192, UP ? &p.tw1 : &p.tw0, UP ? r0 : r0 + 64, c, ti.e, bar);
                     } else {
-                        tma_3d(a, &p.tw0, c, r0, ti.e, bar);
-                        tma_3d(a + 8192, UP ? &p.tw1 : &p.tw0, c, UP ? r0 : r0 + 64, ti.e, bar);
+                        tma_3d(a, &p.tw0, c, r0, ti.e, bar);     // (128 rows at once unless gated)
+                        if constexpr (UP) tma_3d(a + 8192, &p.tw1, c, r0, ti.e, bar);
                     }
-                    done[0] = (int)g + 1;
+                    if (!p.sorted_pairs) {
+                        // the rows as at most four boxes, the largest first: one for each bit of nh / 16
+                        const uint32_t b = a + kABytes;
+                        if (ti.nh == 128) {
+                            tma_2d(b, &p.tx[3], c, c0, bar);
+                        } else {
+#pragma unroll
+                            for (int i = 2; i >= 0; --i) {
+                                const int box = 16 << i, at = ti.nh & ~(2 * box - 1);
+                                if (ti.nh & box) tma_2d(b + 128 * at, &p.tx[i], c, c0 + at, bar);
+                            }
+                        }
+                    }
+                    ++g;
                 }
-                if (!p.sorted_pairs && 16 * lane < ti.nh)
-                    tma_2d(b + 2048 * lane, &p.tx, kb * kStepK, c0 + 16 * lane, bar);
-                __syncwarp();
             }
+            done[0] = g;
+            // the last steps' arrivals on this CTA's barriers have landed before it may leave
+            if (g < kStages) ring = Ring{0, 1};
+            for (int i = 0; ok && i < min(g, kStages); ++i, ring.next())
+                ok = wait_one(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns);
         }
-        // the last steps' arrivals on this CTA's barriers have landed before it may leave
-        if (ok)
-            for (uint32_t s = g > kStages ? g - kStages : 0; s < g; ++s)
-                if (!wait_cluster(&empty[s % kStages], (s / kStages) & 1, abort_flag, p.wait_ns)) break;
-    } else if (warp == 1 && cta == 0) {
-        // ======================= MMA issue =======================
-        uint32_t g = 0;
-        int j = 0;
-        bool ok = true;
-        Tile ti;
-        for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
-            const uint32_t idesc = idesc_mma(256, 2 * ti.nh, p.bf16) | (p.in_out ? 1u << 15 : 0u);
-            const int b = j & 1;
-            if (j >= 2 && !wait_cluster(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
-            tc_after();
-            const uint32_t acc = tmem + (uint32_t)b * kMaxN;
-            for (int kb = 0; kb < nk; ++kb, ++g) {
-                const int s = g % kStages;
-                uint64_t* fb = p.stall && g == 0 ? never : &full[s];         // (test stall)
-                if (!wait_cluster(fb, fb == never ? 0u : (g / kStages) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
+    } else if (warp == 1) {
+        // ======================= MMA issue (one thread of the first CTA) =======================
+        if (cta == 0 && lane == 0) {
+            // a step's descriptors: the address field of the first stage's, plus the step's offset / 16
+            const uint32_t a0 = su32(smem);
+            const uint64_t da0 = IN_OUT ? sdesc_mn(a0) : sdesc(a0), db0 = sdesc(a0 + kABytes);
+            constexpr uint32_t kAdvA = (IN_OUT ? 2048 : 32) >> 4, kAdvB = 32 >> 4;
+            Ring ring;
+            int j = 0;
+            bool ok = true, any = false;
+            Tile ti;
+            for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
+                const uint32_t idesc = idesc_mma(256, 2 * ti.nh, p.bf16) | (IN_OUT ? 1u << 15 : 0u);
+                const int b = j & 1;
+                if (j >= 2 && !wait_one(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
                 tc_after();
-                if (lane == 0) {
-                    const uint32_t a0 = su32(smem + s * kStageBytes), b0 = a0 + kABytes;
+                const uint32_t acc = tmem + (uint32_t)b * kMaxN;
+                for (int kb = 0; kb < nk; ++kb, ring.next()) {
+                    const bool stalled = p.stall && !any;            // (test setting)
+                    if (!wait_one(stalled ? never : &full[ring.s], stalled ? 0u : ring.ph, abort_flag, p.wait_ns)) { ok = false; break; }
+                    tc_after();
+                    const uint32_t adv = (uint32_t)ring.s * (kStageBytes >> 4);
+                    const uint64_t da = da0 + adv, db = db0 + adv;
 #pragma unroll
                     for (int kk = 0; kk < kStepK / 16; ++kk)
-                        mma_pair(acc, p.in_out ? sdesc_mn(a0 + 2048 * kk) : sdesc(a0 + 32 * kk), sdesc(b0 + 32 * kk), idesc,
-                                 (kb | kk) != 0);
-                    commit_pair(&empty[s]);
-                    if (kb == nk - 1) commit_pair(&accf[b]);
+                        mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 ? 1u : (uint32_t)(kb > 0));
+                    commit_pair(&empty[ring.s]);
+                    any = true;
                 }
-                __syncwarp();
+                if (ok) commit_pair(&accf[b]);
             }
-        }
-        // every MMA issued has completed before TMEM is freed
-        if (g > 0) {
-            if (lane == 0)
+            // every MMA issued has completed before TMEM is freed
+            if (any) {
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(drain))
                              : "memory");
-            __syncwarp();
-            drain_wait(drain, 0, p.wait_ns);
+                drain_wait(drain, 0, p.wait_ns);
+            }
         }
-    } else if (warp >= kGatherWarp0 && warp < kEpiWarp0) {
+    } else if (warp < kEpiWarp0 || warp >= kEpiWarp0 + kEpiWarps) {
         // ======================= gathered rows of x =======================
         if (p.sorted_pairs) {
-            // thread u copies chunk u % 8 of rows u / 8 + 8 * kGatherWarps * j of a step into the swizzled layout
-            const int u = tid - 32 * kGatherWarp0, ch = u & 7, w = warp - kGatherWarp0;
-            constexpr int kRowStep = 4 * kGatherWarps;
+            // warp w takes the steps w, w + 4, ..: lane u copies chunk u % 8 of rows u / 8 + 4 j of the
+            // step into the swizzled layout and waits for them; the other warps' steps overlap that
+            const int w = warp < kEpiWarp0 ? warp - 2 : warp - kEpiWarps - 2, ch = lane & 7, r0 = lane >> 3;
             const uint32_t full0 = in_leader(su32(full));
-            uint32_t g = 0, arrived = 0;
+            const uint32_t d0 = su32(smem) + kABytes + swz(r0, ch), d1 = su32(smem) + kABytes + swz(r0 + 4, ch);
+            int g = 0;
+            Ring ring;
             bool ok = true;
             Tile ti;
             for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
                 const int c0 = (int)cta * ti.nh, nc = min(ti.nh, ti.ntok - c0);   // columns of this CTA that hold rows
-                int row[kGatherRows];
+                uint32_t row[32];                        // where the rows start, in 16 bytes
 #pragma unroll
-                for (int j = 0; j < kGatherRows; ++j) {
-                    const int r = (u >> 3) + kRowStep * j;
+                for (int j = 0; j < 32; ++j) {
+                    const int r = r0 + 4 * j;
                     row[j] = 0;
                     if (r < nc) {
                         const int pair = __ldg(p.sorted_pairs + ti.tok0 + c0 + r);
                         const bool in = pair >= 0 && pair < p.P;
                         bad |= !in;
-                        row[j] = in ? pair / p.k : 0;
+                        row[j] = in ? (uint32_t)(pair / p.k) * (uint32_t)(p.x_stride >> 3) : 0u;
                     }
                 }
-                for (int kb = 0; kb < nk; ++kb, ++g) {
-                    const int s = g % kStages;
-                    if (g >= kStages && !wait_cluster(&empty[s], (g / kStages - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                const int nj = nc > r0 ? (nc - r0 + 3) >> 2 : 0;     // rows of this lane
+                for (int kb = 0; kb < nk; ++kb, ++g, ring.next()) {
+                    if (g % kGatherWarps != w) continue;
+                    if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
                     const int c = kb * kStepK + 8 * ch;
                     const uint32_t bytes = (uint32_t)min(max(2 * (p.K - c), 0), 16);   // zeros past the row's end
-                    uint8_t* dst = smem + s * kStageBytes + kABytes;
+                    const uint16_t* src = p.x + (bytes ? c : 0);
+                    const uint32_t so = ring.s * kStageBytes;
+                    auto copy = [&](int j) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((j & 1 ? d1 : d0) + so + (j >> 1) * 1024),
+                                     "l"(src + 8 * (uint64_t)row[j]), "r"(bytes)
+                                     : "memory");
+                    };
+                    if (nj == 32) {
 #pragma unroll
-                    for (int j = 0; j < kGatherRows; ++j) {
-                        const int r = (u >> 3) + kRowStep * j;
-                        if (r < nc) cp_async16(dst + swz(r, ch), p.x + row[j] * p.x_stride + (bytes ? c : 0), bytes);
+                        for (int j = 0; j < 32; ++j) copy(j);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < nj) copy(j);
                     }
-                    cp_commit();
-                    if (g >= kGatherAhead) {
-                        cp_wait<kGatherAhead>();
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(full0 + 8 * ((g - kGatherAhead) % kStages));
-                        arrived = g - kGatherAhead + 1;
+                    cp_wait_all();
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive_cluster(full0 + 8 * ring.s);
+                        done[1 + w] = g + 1;
                     }
                 }
             }
-            cp_wait_all();
-            fence_async_smem();
-            __syncwarp();
-            for (; ok && arrived < g; ++arrived)
-                if (lane == 0) arrive_cluster(full0 + 8 * (arrived % kStages));
-            if (lane == 0) done[1 + w] = (int)arrived;
         }
-    } else if (warp >= kEpiWarp0) {
+    } else {
         // ======================= epilogue =======================
-        // warp w reads TMEM lanes 32 (w % 4).. and half of the columns (groups of 32, every other one)
-        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
-        const uint32_t accr0 = in_leader(su32(accr));
-        const int pairbar = 1 + side * 2 + (q & 1);      // gated: warps q and q + 2 trade columns
-        int j = 0, turn = 0;
-        Tile ti;
-        for (int t = first; tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
-            const int b = j & 1;
-            bool ok = wait_cluster(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
-            // (the two warps of a trade leave together, or one would wait for the other for ever)
-            if constexpr (UP) ok = all_of(pairbar, 64, ok);
-            if (!ok) break;
-            tc_after();
-            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)b * kMaxN;
-            if constexpr (UP) {
-                const int row = ti.mb * kRowsTile + (int)cta * 64 + (q & 1) * 32 + lane;
-                const bool is_up = q >= 2;
-                for (int c0 = 16 * side; c0 < ti.ntok; c0 += 32, ++turn) {
-                    uint32_t r[16];
-                    tmem_ld16(acc + c0, r);
-                    tmem_ld_wait();
-                    // the W warp keeps columns 0..7 and gives 8..15, the W_up warp the other way round
-                    float* buf = exch + (((pairbar - 1) * 2 + (turn & 1)) * 2) * 256;
-                    float* mine = buf + (is_up ? 256 : 0);
-                    const float* theirs = buf + (is_up ? 0 : 256);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mine[i * 32 + lane] = __uint_as_float(is_up ? r[i] : r[8 + i]);
-                    named_sync(pairbar, 64);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float other = theirs[i * 32 + lane];
-                        const float gv = is_up ? other : __uint_as_float(r[i]);
-                        const float uv = is_up ? __uint_as_float(r[8 + i]) : other;
-                        const int col = c0 + (is_up ? 8 : 0) + i;
-                        if (col < ti.ntok && row < p.N)
-                            store_out(p.y, p.y_type, (int64_t)(ti.tok0 + col) * p.y_stride + row, gv / (1.0f + expf(-gv)) * uv);
-                    }
-                }
-            } else {
-                const int row = ti.mb * kRowsTile + (int)cta * 128 + q * 32 + lane;
-                for (int c0 = 32 * side; c0 < ti.ntok; c0 += 64) {
-                    uint32_t r[32];
-                    tmem_ld32(acc + c0, r);
-                    tmem_ld_wait();
-                    if (row < p.N) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c0 + i < ti.ntok)
-                                store_out(p.y, p.y_type, (int64_t)(ti.tok0 + c0 + i) * p.y_stride + row, __uint_as_float(r[i]));
-                    }
-                }
-            }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(accr0 + 8 * b);
-        }
+        if (p.y_type == MOE_F32) epilogue<UP, float>(p, off, tb0, n_mb, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
+        else if (p.y_type == MOE_BF16)
+            epilogue<UP, __nv_bfloat16>(p, off, tb0, n_mb, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
+        else epilogue<UP, __half>(p, off, tb0, n_mb, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
     }
     if (bad && p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
     tc_before();
@@ -462,16 +509,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                      : "r"(in_peer(su32(const_cast<int*>(abort_flag))))
                      : "memory");
         if (*abort_flag || peer_abort) {
-            const int warps = p.sorted_pairs ? 1 + kGatherWarps : 1;
             int of[2][1 + kGatherWarps], last = 0;
-            for (int i = 0; i < warps; ++i) {
+            for (int i = 0; i <= kGatherWarps; ++i) {
                 of[0][i] = done[i];
                 asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(of[1][i]) : "r"(in_peer(su32(done + i))) : "memory");
                 last = max(last, max(of[0][i], of[1][i]));
             }
-            for (int c = 0; c < 2; ++c)
-                for (int i = 0; i < warps; ++i)
-                    for (int s = of[c][i]; s < last; ++s) mbar_arrive(&full[s % kStages]);
+            for (int s = max(0, last - kStages); s < last; ++s)
+                for (int c = 0; c < 2; ++c) {
+                    if (of[c][0] <= s) mbar_arrive(&full[s % kStages]);
+                    if (p.sorted_pairs && of[c][1 + s % kGatherWarps] <= s) mbar_arrive(&full[s % kStages]);
+                }
             for (int s = max(0, last - kStages); s < last; ++s) drain_wait(&full[s % kStages], (s / kStages) & 1, p.wait_ns);
             if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
         }
@@ -514,7 +562,7 @@ bool encode(CUtensorMap* m, bool bf16, int rank, const void* base, const cuuint6
 }
 
 size_t smem_bytes(int E) {
-    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 24 + 64 + 2 * (size_t)(E + 1) * 4;
+    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 32 + 64 + 2 * (size_t)(E + 1) * 4;
 }
 
 }  // namespace
@@ -528,14 +576,17 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
                                                                     : (cuuint64_t)a.row_stride * rows * 2};
     const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.P, 1};
     const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
-    if (!encode(&p.tw0, a.bf16, 3, a.w0, wd, ws, 64) || (a.w1 && !encode(&p.tw1, a.bf16, 3, a.w1, wd, ws, 64)) ||
-        (!a.sorted_pairs && !encode(&p.tx, a.bf16, 2, a.x, xd, xs, 16)))
+    if (!encode(&p.tw0, a.bf16, 3, a.w0, wd, ws, a.in_out || a.w1 ? 64 : 128) ||
+        (a.w1 && !encode(&p.tw1, a.bf16, 3, a.w1, wd, ws, 64)))
         return cudaErrorInvalidValue;
+    if (!a.sorted_pairs)
+        for (int i = 0; i < 4; ++i)
+            if (!encode(&p.tx[i], a.bf16, 2, a.x, xd, xs, 16 << i)) return cudaErrorInvalidValue;
     p.x = static_cast<const uint16_t*>(a.x);
     p.x_stride = a.x_stride;
     p.sorted_pairs = a.sorted_pairs; p.offsets = a.offsets;
     p.E = a.E; p.k = a.k; p.P = a.P; p.N = a.N; p.K = a.K;
-    p.bf16 = a.bf16; p.in_out = a.in_out;
+    p.bf16 = a.bf16;
     p.y = a.y; p.y_type = a.y_type; p.y_stride = a.y_stride; p.status = a.status;
     const WaitCfg wc = wait_cfg();
     p.wait_ns = wc.limit_ns; p.stall = wc.stall;
@@ -543,13 +594,17 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
     if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
-    const void* fn = a.w1 ? (const void*)grouped_dense_kernel<true> : (const void*)grouped_dense_kernel<false>;
-    static std::atomic<uint64_t> ready[2];               // devices whose function attribute is set
+    const int v = (a.w1 ? 2 : 0) + (a.in_out ? 1 : 0);
+    const void* fn = v == 3   ? (const void*)grouped_dense_kernel<true, true>
+                     : v == 2 ? (const void*)grouped_dense_kernel<true, false>
+                     : v == 1 ? (const void*)grouped_dense_kernel<false, true>
+                              : (const void*)grouped_dense_kernel<false, false>;
+    static std::atomic<uint64_t> ready[4];               // devices whose function attribute is set
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!bit || !(ready[a.w1 != nullptr].load(std::memory_order_acquire) & bit)) {
+    if (!bit || !(ready[v].load(std::memory_order_acquire) & bit)) {
         if ((err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kMaxExperts))) != cudaSuccess)
             return err;
-        ready[a.w1 != nullptr].fetch_or(bit, std::memory_order_release);
+        ready[v].fetch_or(bit, std::memory_order_release);
     }
     // one pair per two SMs, and no more pairs than there can be tiles
     const int64_t n_mb = (a.N + (a.w1 ? 127 : 255)) / (a.w1 ? 128 : 256);
