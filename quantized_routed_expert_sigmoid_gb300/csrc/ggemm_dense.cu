@@ -444,20 +444,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             Ring ring;
             bool ok = true;
             Tile ti;
+            int pair[4];
+            auto pairs_of = [&](int t) {
+                Tile n;
+                const bool any = tile_at(off, tb0, p.E, n_mb, t, n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = lane + 32 * i, c = (int)cta * n.nh + r;
+                    pair[i] = any && r < n.nh && c < n.ntok ? __ldg(p.sorted_pairs + n.tok0 + c) : 0;
+                }
+            };
+            pairs_of(first);
             for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
                 const int c0 = (int)cta * ti.nh, nc = min(ti.nh, ti.ntok - c0);   // columns of this CTA that hold rows
+                // lane u has read the pairs of columns u, u + 32, .. (before the tile before this one ended)
+                uint32_t at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = (uint32_t)pair[i] < (uint32_t)p.P;
+                    bad |= !in;
+                    at[i] = in ? (uint32_t)(pair[i] / p.k) * (uint32_t)(p.x_stride >> 3) : 0u;
+                }
                 uint32_t row[32];                        // where the rows start, in 16 bytes
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int r = r0 + 4 * j;
-                    row[j] = 0;
-                    if (r < nc) {
-                        const int pair = __ldg(p.sorted_pairs + ti.tok0 + c0 + r);
-                        const bool in = pair >= 0 && pair < p.P;
-                        bad |= !in;
-                        row[j] = in ? (uint32_t)(pair / p.k) * (uint32_t)(p.x_stride >> 3) : 0u;
-                    }
-                }
+                for (int j = 0; j < 32; ++j) row[j] = __shfl_sync(0xffffffffu, at[j >> 3], (r0 + 4 * j) & 31);
+                pairs_of(t + n_pairs);
                 const int nj = nc > r0 ? (nc - r0 + 3) >> 2 : 0;     // rows of this lane
                 for (int kb = 0; kb < nk; ++kb, ++g, ring.next()) {
                     if (g % kGatherWarps != w) continue;
