@@ -360,7 +360,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
                 const int c0 = ti.tok0 + (int)cta * ti.nh;   // this CTA's first column, as a sorted position
                 const int r0 = ti.mb * kRowsTile + (int)cta * (kRowsTile / 2);
-                const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : ti.nh * 128);
+                // one box for the rows, of 16, 32, 64 or 128: what it reads past this block's is not used
+                const int box = ti.nh > 64 ? 3 : ti.nh > 32 ? 2 : ti.nh > 16 ? 1 : 0;
+                const CUtensorMap* xmap = &p.tx[box];
+                const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : 2048 << box);
                 for (int c = 0; c < nk * kStepK; c += kStepK, ring.next()) {
                     if (!wait_one(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
                     const uint32_t bar = full0 + 8 * ring.s, a = stage0 + ring.s * kStageBytes;
@@ -372,19 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                         tma_3d(a, &p.tw0, c, r0, ti.e, bar);     // (128 rows at once unless gated)
                         if constexpr (UP) tma_3d(a + 8192, &p.tw1, c, r0, ti.e, bar);
                     }
-                    if (!p.sorted_pairs) {
-                        // the rows as at most four boxes, the largest first: one for each bit of nh / 16
-                        const uint32_t b = a + kABytes;
-                        if (ti.nh == 128) {
-                            tma_2d(b, &p.tx[3], c, c0, bar);
-                        } else {
-#pragma unroll
-                            for (int i = 2; i >= 0; --i) {
-                                const int box = 16 << i, at = ti.nh & ~(2 * box - 1);
-                                if (ti.nh & box) tma_2d(b + 128 * at, &p.tx[i], c, c0 + at, bar);
-                            }
-                        }
-                    }
+                    if (!p.sorted_pairs) tma_2d(a + kABytes, xmap, c, c0, bar);
                     ++g;
                 }
             }
