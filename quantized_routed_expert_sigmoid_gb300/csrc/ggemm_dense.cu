@@ -17,7 +17,7 @@
 // with their axes exchanged, no transposed copy.
 //
 // Warps: 0 loads (TMA, as few boxes as there can be: issuing one takes about 100 clocks of the
-// thread), 1 issues the MMAs (in the first CTA of the pair) and owns TMEM, 2, 3, 12 and 13 copy the x rows that
+// thread), 1 issues the MMAs (in the first CTA of the pair) and owns TMEM, 2, 3 and 12..15 copy the x rows that
 // the pairs name, a step each in turn (cp.async, 16 bytes a thread; TMA's four-row gathers, 32 a step,
 // took longer than the step's MMAs), 4..11 are the epilogue (two accumulators of 256 columns: one is
 // read out while the next tile runs).  Persistent:
@@ -36,7 +36,7 @@ namespace {
 constexpr int kStages = 6, kStepK = 64, kMaxN = 256;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;              // (a warp reads the TMEM lanes 32 (warp % 4)..)
-constexpr int kGatherWarps = 4;                          // warps 2, 3, 12, 13
+constexpr int kGatherWarps = kStages;                    // warps 2, 3, 12..15: one for each stage of the ring
 constexpr int kThreads = 32 * (2 + kEpiWarps + kGatherWarps);
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
@@ -103,6 +103,15 @@ __device__ __forceinline__ bool wait_one(uint64_t* b, uint32_t parity, volatile 
 // The same for a whole warp: the answer is that of all its lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
     return __all_sync(0xffffffffu, wait_one(b, parity, abort_flag, limit_ns));
+}
+// The same value on every lane, for the compiler to know it.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// True on one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 // A position in the ring of stages and the parity of its round.
 struct Ring {
@@ -289,8 +298,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     uint64_t* never = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [5] last step + 1 that warp 0 / each gathering warp arrived for
-    int* scan = reinterpret_cast<int*>(tmem_slot + 8);   // [16]
+    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [7] last step + 1 that warp 0 / each gathering warp arrived for
+    int* scan = reinterpret_cast<int*>(tmem_slot + 10);  // [16]
     int* off = scan + 16;                                // [E + 1] offsets, clamped and in order
     int* tb0 = off + p.E + 1;                            // [E + 1] blocks of rows before each expert
 
@@ -350,44 +359,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     const int nk = (p.K + kStepK - 1) / kStepK;
 
     if (warp == 0) {
-        // ======================= loads (one thread) =======================
-        if (lane == 0) {
-            const uint32_t full0 = in_leader(su32(full)), stage0 = su32(smem);
-            int g = 0;
-            Ring ring;
-            bool ok = true;
-            Tile ti;
-            for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
-                const int c0 = ti.tok0 + (int)cta * ti.nh;   // this CTA's first column, as a sorted position
-                const int r0 = ti.mb * kRowsTile + (int)cta * (kRowsTile / 2);
-                // one box for the rows, of 16, 32, 64 or 128: what it reads past this block's is not used
-                const int box = ti.nh > 64 ? 3 : ti.nh > 32 ? 2 : ti.nh > 16 ? 1 : 0;
-                const CUtensorMap* xmap = &p.tx[box];
-                const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : 2048 << box);
-                for (int c = 0; c < nk * kStepK; c += kStepK, ring.next()) {
-                    if (!wait_one(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
-                    const uint32_t bar = full0 + 8 * ring.s, a = stage0 + ring.s * kStageBytes;
+        // ======================= loads =======================
+        // (the whole warp keeps step, so that what one lane issues lies in uniform registers)
+        const uint32_t full0 = in_leader(su32(full)), stage0 = su32(smem);
+        int g = 0;
+        Ring ring;
+        bool ok = true;
+        Tile ti;
+        for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
+            const int c0 = uniform(ti.tok0 + (int)cta * ti.nh);  // this CTA's first column, as a sorted position
+            const int r0 = uniform(ti.mb * kRowsTile + (int)cta * (kRowsTile / 2)), e = uniform(ti.e);
+            // one box for the rows, of 16, 32, 64 or 128: what it reads past this block's is not used
+            const int box = uniform(ti.nh > 64 ? 3 : ti.nh > 32 ? 2 : ti.nh > 16 ? 1 : 0);
+            const CUtensorMap* xmap = &p.tx[box];
+            const uint32_t bytes = kABytes + (p.sorted_pairs ? 0 : 2048 << box);
+            for (int c = 0; c < nk * kStepK; c += kStepK, ++g, ring.next()) {
+                if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                const uint32_t bar = full0 + 8 * ring.s, a = stage0 + ring.s * kStageBytes;
+                if (elect_one()) {
                     arrive_tx_cluster(bar, bytes);
                     if constexpr (IN_OUT) {
-                        tma_3d(a, &p.tw0, r0, c, ti.e, bar);
-                        tma_3d(a + 8192, UP ? &p.tw1 : &p.tw0, UP ? r0 : r0 + 64, c, ti.e, bar);
+                        tma_3d(a, &p.tw0, r0, c, e, bar);
+                        tma_3d(a + 8192, UP ? &p.tw1 : &p.tw0, UP ? r0 : r0 + 64, c, e, bar);
                     } else {
-                        tma_3d(a, &p.tw0, c, r0, ti.e, bar);     // (128 rows at once unless gated)
-                        if constexpr (UP) tma_3d(a + 8192, &p.tw1, c, r0, ti.e, bar);
+                        tma_3d(a, &p.tw0, c, r0, e, bar);        // (128 rows at once unless gated)
+                        if constexpr (UP) tma_3d(a + 8192, &p.tw1, c, r0, e, bar);
                     }
                     if (!p.sorted_pairs) tma_2d(a + kABytes, xmap, c, c0, bar);
-                    ++g;
                 }
+                __syncwarp();
             }
-            done[0] = g;
-            // the last steps' arrivals on this CTA's barriers have landed before it may leave
-            if (g < kStages) ring = Ring{0, 1};
-            for (int i = 0; ok && i < min(g, kStages); ++i, ring.next())
-                ok = wait_one(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns);
         }
+        if (lane == 0) done[0] = g;
+        // the last steps' arrivals on this CTA's barriers have landed before it may leave
+        if (g < kStages) ring = Ring{0, 1};
+        for (int i = 0; ok && i < min(g, kStages); ++i, ring.next())
+            ok = wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns);
     } else if (warp == 1) {
-        // ======================= MMA issue (one thread of the first CTA) =======================
-        if (cta == 0 && lane == 0) {
+        // ======================= MMA issue (in the first CTA) =======================
+        if (cta == 0) {
             // a step's descriptors: the address field of the first stage's, plus the step's offset / 16
             const uint32_t a0 = su32(smem);
             const uint64_t da0 = IN_OUT ? sdesc_mn(a0) : sdesc(a0), db0 = sdesc(a0 + kABytes);
@@ -397,37 +407,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             bool ok = true, any = false;
             Tile ti;
             for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
-                const uint32_t idesc = idesc_mma(256, 2 * ti.nh, p.bf16) | (IN_OUT ? 1u << 15 : 0u);
+                const uint32_t idesc = uniform(idesc_mma(256, 2 * ti.nh, p.bf16) | (IN_OUT ? 1u << 15 : 0u));
                 const int b = j & 1;
-                if (j >= 2 && !wait_one(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
+                if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
                 tc_after();
-                const uint32_t acc = tmem + (uint32_t)b * kMaxN;
+                const uint32_t acc = uniform(tmem + (uint32_t)b * kMaxN);
                 for (int kb = 0; kb < nk; ++kb, ring.next()) {
                     const bool stalled = p.stall && !any;            // (test setting)
-                    if (!wait_one(stalled ? never : &full[ring.s], stalled ? 0u : ring.ph, abort_flag, p.wait_ns)) { ok = false; break; }
+                    if (!wait_warp(stalled ? never : &full[ring.s], stalled ? 0u : ring.ph, abort_flag, p.wait_ns)) { ok = false; break; }
                     tc_after();
                     const uint32_t adv = (uint32_t)ring.s * (kStageBytes >> 4);
                     const uint64_t da = da0 + adv, db = db0 + adv;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kStepK / 16; ++kk)
-                        mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 ? 1u : (uint32_t)(kb > 0));
-                    commit_pair(&empty[ring.s]);
+                        for (int kk = 0; kk < kStepK / 16; ++kk)
+                            mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 ? 1u : (uint32_t)(kb > 0));
+                        commit_pair(&empty[ring.s]);
+                        if (kb == nk - 1) commit_pair(&accf[b]);
+                    }
+                    __syncwarp();
                     any = true;
                 }
-                if (ok) commit_pair(&accf[b]);
             }
             // every MMA issued has completed before TMEM is freed
             if (any) {
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(drain))
-                             : "memory");
+                if (elect_one())
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(drain))
+                                 : "memory");
+                __syncwarp();
                 drain_wait(drain, 0, p.wait_ns);
             }
         }
     } else if (warp < kEpiWarp0 || warp >= kEpiWarp0 + kEpiWarps) {
         // ======================= gathered rows of x =======================
         if (p.sorted_pairs) {
-            // warp w takes the steps w, w + 4, ..: lane u copies chunk u % 8 of rows u / 8 + 4 j of the
-            // step into the swizzled layout and waits for them; the other warps' steps overlap that
+            // warp w fills stage w: lane u copies chunk u % 8 of rows u / 8 + 4 j of a step into the
+            // swizzled layout and waits for them; the other warps' steps overlap that
             const int w = warp < kEpiWarp0 ? warp - 2 : warp - kEpiWarps - 2, ch = lane & 7, r0 = lane >> 3;
             const uint32_t full0 = in_leader(su32(full));
             const uint32_t d0 = su32(smem) + kABytes + swz(r0, ch), d1 = su32(smem) + kABytes + swz(r0 + 4, ch);
@@ -462,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 pairs_of(t + n_pairs);
                 const int nj = nc > r0 ? (nc - r0 + 3) >> 2 : 0;     // rows of this lane
                 for (int kb = 0; kb < nk; ++kb, ++g, ring.next()) {
-                    if (g % kGatherWarps != w) continue;
+                    if (ring.s != w) continue;
                     if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
                     const int c = kb * kStepK + 8 * ch;
                     const uint32_t bytes = (uint32_t)min(max(2 * (p.K - c), 0), 16);   // zeros past the row's end
@@ -520,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             for (int s = max(0, last - kStages); s < last; ++s)
                 for (int c = 0; c < 2; ++c) {
                     if (of[c][0] <= s) mbar_arrive(&full[s % kStages]);
-                    if (p.sorted_pairs && of[c][1 + s % kGatherWarps] <= s) mbar_arrive(&full[s % kStages]);
+                    if (p.sorted_pairs && of[c][1 + s % kStages] <= s) mbar_arrive(&full[s % kStages]);
                 }
             for (int s = max(0, last - kStages); s < last; ++s) drain_wait(&full[s % kStages], (s / kStages) & 1, p.wait_ns);
             if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
@@ -564,7 +579,7 @@ bool encode(CUtensorMap* m, bool bf16, int rank, const void* base, const cuuint6
 }
 
 size_t smem_bytes(int E) {
-    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 32 + 64 + 2 * (size_t)(E + 1) * 4;
+    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 40 + 64 + 2 * (size_t)(E + 1) * 4;
 }
 
 }  // namespace
