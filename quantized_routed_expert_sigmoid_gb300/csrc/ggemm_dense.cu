@@ -187,24 +187,53 @@ __device__ __forceinline__ void named_sync(int barrier, int threads) {
 struct Tile {
     int e, mb, tok0, ntok, nh;   // expert, block of M rows, first sorted position, rows, columns per CTA
 };
-// Tile t of the list: experts in order, their rows in even blocks of at most 256, blocks of M rows fastest
-// (the pairs that run at one time share the rows of x and walk through one expert's weights).
-__device__ __forceinline__ bool tile_at(const int* off, const int* tb0, int E, int n_mb, int t, Tile& ti) {
-    const int tb = t / n_mb;
-    if (tb >= tb0[E]) return false;
-    int lo = 0, hi = E;                                  // tb0[lo] <= tb < tb0[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tb0[mid] <= tb) lo = mid; else hi = mid;
+// The order of the tiles, in shared memory.  An expert's rows are cut into even blocks of at most 256.
+// Experts with several blocks (whose weights are read from memory once and then found in L2: bound by
+// the tensor cores) and experts with one block (bound by memory) are spread evenly among each other, so that both are
+// busy all the time; in each of the two sequences the experts with the largest blocks come first, so that
+// what the pairs of CTAs are left with at the end are small tiles.  Blocks of M rows are fastest:
+// the pairs that run at one time share the rows of x and walk through one expert's weights.
+struct Order {
+    const int* off;              // [E + 1] offsets, clamped and in order
+    const int* tb0;              // [n_big + 1] blocks before the i-th expert of several blocks
+    const uint16_t* expert;      // experts of several blocks, then those of one
+    int n_big, n_blocks, n_mb;
+    uint32_t ratio;              // 2^32 * (blocks of the first sequence) / n_blocks, rounded up (0: all of them)
+
+    // blocks of the first sequence among the first i of all
+    __device__ __forceinline__ int big_before(int i) const { return ratio ? (int)__umulhi((uint32_t)i, ratio) : min(i, tb0[n_big]); }
+    __device__ __forceinline__ bool at(int t, Tile& ti) const {
+        const int tb = t / n_mb;
+        if (tb >= n_blocks) return false;
+        const int nl = big_before(tb);
+        int i, nb = 1, blk = 0;
+        if (big_before(tb + 1) > nl) {
+            int hi = n_big;                              // tb0[i] <= nl < tb0[hi]
+            for (i = 0; hi - i > 1;) {
+                const int mid = (i + hi) >> 1;
+                if (tb0[mid] <= nl) i = mid; else hi = mid;
+            }
+            nb = tb0[i + 1] - tb0[i];
+            blk = nl - tb0[i];
+        } else {
+            i = n_big + tb - nl;
+        }
+        const int e = expert[i], cnt = off[e + 1] - off[e];
+        const int per = ((cnt + nb - 1) / nb + 31) & ~31;    // (nb - 1) * per < cnt, as per <= 256 < cnt / (nb - 1)
+        ti.e = e;
+        ti.mb = t - tb * n_mb;
+        ti.tok0 = off[e] + blk * per;
+        ti.ntok = min(per, cnt - blk * per);
+        ti.nh = ((ti.ntok + 31) & ~31) >> 1;
+        return true;
     }
-    const int cnt = off[lo + 1] - off[lo], nb = tb0[lo + 1] - tb0[lo], blk = tb - tb0[lo];
-    const int per = ((cnt + nb - 1) / nb + 31) & ~31;    // (nb - 1) * per < cnt, as per <= 256 < cnt / (nb - 1)
-    ti.e = lo;
-    ti.mb = t - tb * n_mb;
-    ti.tok0 = off[lo] + blk * per;
-    ti.ntok = min(per, cnt - blk * per);
-    ti.nh = ((ti.ntok + 31) & ~31) >> 1;
-    return true;
+};
+constexpr int kBuckets = 16;     // by columns of a block, 256 first: 8 for several blocks, 8 for one
+__device__ __forceinline__ int blocks_of(int cnt) { return (cnt + kMaxN - 1) / kMaxN; }
+__device__ __forceinline__ int bucket_of(int cnt) {
+    if (cnt <= 0) return kBuckets;                       // no rows, no tiles
+    const int nb = blocks_of(cnt), cols = ((cnt + nb - 1) / nb + 31) >> 5;
+    return (nb > 1 ? 0 : 8) + 8 - cols;
 }
 
 template <typename T> __device__ __forceinline__ T to_out(float v);
@@ -215,8 +244,7 @@ template <> __device__ __forceinline__ __half to_out<__half>(float v) { return _
 // An epilogue warp: warp w reads TMEM lanes 32 (w % 4).. (weight rows) and every other group of columns
 // (rows of x) of each tile, and stores 32 neighbouring outputs of one row at a time.
 template <bool UP, typename T>
-__device__ __forceinline__ void epilogue(const DenseParams& p, const int* off, const int* tb0, int n_mb, int first, int n_pairs,
-                                         int cta, uint32_t tmem, float* exch, uint64_t* accf, uint64_t* accr,
+__device__ __forceinline__ void epilogue(const DenseParams& p, const Order& order, int first, int n_pairs, int cta, uint32_t tmem, float* exch, uint64_t* accf, uint64_t* accr,
                                          volatile int* abort_flag) {
     constexpr int kRowsTile = UP ? 128 : 256;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -225,7 +253,7 @@ __device__ __forceinline__ void epilogue(const DenseParams& p, const int* off, c
     const int pairbar = 1 + side * 2 + (q & 1);          // gated: warps q and q + 2 trade columns
     int j = 0, turn = 0;
     Tile ti;
-    for (int t = first; tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
+    for (int t = first; order.at(t, ti); t += n_pairs, ++j) {
         const int b = j & 1;
         bool ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
         // (the two warps of a trade leave together, or one would wait for the other for ever)
@@ -300,8 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [7] last step + 1 that warp 0 / each gathering warp arrived for
     int* scan = reinterpret_cast<int*>(tmem_slot + 10);  // [16]
-    int* off = scan + 16;                                // [E + 1] offsets, clamped and in order
-    int* tb0 = off + p.E + 1;                            // [E + 1] blocks of rows before each expert
+    int* totals = scan + 16;                             // [2] experts of several blocks, experts with rows
+    int* off = totals + 2;                               // [E + 1]
+    int* tb0 = off + p.E + 1;                            // [E + 1]
+    uint16_t* expert = reinterpret_cast<uint16_t*>(tb0 + p.E + 1);   // [E]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t cta = cta_rank();
@@ -319,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    // ---- the list of row blocks, from the offsets (clamped into 0..P and into order)
+    // ---- the order of the tiles, from the offsets (clamped into 0..P and into order)
     bool bad = false;
     for (int i = tid; i <= p.E; i += kThreads) {
         const int o = p.offsets ? __ldg(p.offsets + i) : (i ? p.P : 0);
@@ -327,11 +357,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         off[i] = min(max(o, 0), p.P);
     }
     __syncthreads();
-    {
-        // thread t: experts t * per .. of a scan over the whole block
-        const int per = (p.E + kThreads - 1) / kThreads, e0 = tid * per;
+    // experts sorted by bucket, stably (every CTA finds the same order): counts per 32 experts and
+    // bucket, their running sums over the buckets, ranks
+    int* hist = reinterpret_cast<int*>(exch);            // [E / 32][kBuckets], before its use by the epilogue
+    const int n_chunks = (p.E + 31) / 32;
+    for (int c = warp; c < n_chunks; c += kThreads / 32) {
+        const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
+        if (lane < kBuckets) hist[c * kBuckets + lane] = 0;
+        __syncwarp();
+        const unsigned same = __match_any_sync(0xffffffffu, k);
+        if (k < kBuckets && (same & ((1u << lane) - 1u)) == 0) hist[c * kBuckets + k] = __popc(same);
+    }
+    __syncthreads();
+    if (warp == 0) {
         int sum = 0;
-        for (int i = e0; i < min(e0 + per, p.E); ++i) sum += (max(off[i + 1] - off[i], 0) + kMaxN - 1) / kMaxN;
+        if (lane < kBuckets)
+            for (int c = 0; c < n_chunks; ++c) {
+                const int n = hist[c * kBuckets + lane];
+                hist[c * kBuckets + lane] = sum;
+                sum += n;
+            }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 7) totals[0] = inc;
+        if (lane == 31) totals[1] = inc;
+        if (lane < kBuckets) scan[lane] = inc - sum;     // first place of the bucket
+    }
+    __syncthreads();
+    for (int c = warp; c < n_chunks; c += kThreads / 32) {
+        const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
+        const unsigned same = __match_any_sync(0xffffffffu, k);
+        if (k < kBuckets) expert[scan[k] + hist[c * kBuckets + k] + __popc(same & ((1u << lane) - 1u))] = (uint16_t)e;
+    }
+    __syncthreads();
+    const int n_big = totals[0];
+    {
+        // thread t: places t * per .. of a scan of the block counts over the whole CTA
+        const int per = (n_big + kThreads - 1) / kThreads, i0 = tid * per;
+        auto blocks_at = [&](int i) { return blocks_of(off[expert[i] + 1] - off[expert[i]]); };
+        int sum = 0;
+        for (int i = i0; i < min(i0 + per, n_big); ++i) sum += blocks_at(i);
         int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -342,11 +411,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         __syncthreads();
         int base = inc - sum;
         for (int w = 0; w < warp; ++w) base += scan[w];
-        for (int i = e0; i < min(e0 + per, p.E); ++i) {
+        for (int i = i0; i < min(i0 + per, n_big); ++i) {
             tb0[i] = base;
-            base += (max(off[i + 1] - off[i], 0) + kMaxN - 1) / kMaxN;
-            if (i == p.E - 1) tb0[p.E] = base;
+            base += blocks_at(i);
         }
+        if (tid == kThreads - 1) tb0[n_big] = base;
     }
     tc_before();
     __syncthreads();
@@ -354,7 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     tc_after();
     const uint32_t tmem = *tmem_slot;
     constexpr int kRowsTile = UP ? 128 : 256;            // outputs of a tile of the pair
-    const int n_mb = (p.N + kRowsTile - 1) / kRowsTile;
+    Order order{off, tb0, expert, n_big, tb0[n_big] + totals[1] - n_big, (p.N + kRowsTile - 1) / kRowsTile, 0u};
+    if (tb0[n_big] < order.n_blocks)
+        order.ratio = (uint32_t)((((uint64_t)tb0[n_big] << 32) + order.n_blocks - 1) / order.n_blocks);
     const int n_pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
     const int nk = (p.K + kStepK - 1) / kStepK;
 
@@ -366,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         Ring ring;
         bool ok = true;
         Tile ti;
-        for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
+        for (int t = first; ok && order.at(t, ti); t += n_pairs) {
             const int c0 = uniform(ti.tok0 + (int)cta * ti.nh);  // this CTA's first column, as a sorted position
             const int r0 = uniform(ti.mb * kRowsTile + (int)cta * (kRowsTile / 2)), e = uniform(ti.e);
             // one box for the rows, of 16, 32, 64 or 128: what it reads past this block's is not used
@@ -406,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             int j = 0;
             bool ok = true, any = false;
             Tile ti;
-            for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs, ++j) {
+            for (int t = first; ok && order.at(t, ti); t += n_pairs, ++j) {
                 const uint32_t idesc = uniform(idesc_mma(256, 2 * ti.nh, p.bf16) | (IN_OUT ? 1u << 15 : 0u));
                 const int b = j & 1;
                 if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
@@ -453,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             int pair[4];
             auto pairs_of = [&](int t) {
                 Tile n;
-                const bool any = tile_at(off, tb0, p.E, n_mb, t, n);
+                const bool any = order.at(t, n);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = lane + 32 * i, c = (int)cta * n.nh + r;
@@ -461,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 }
             };
             pairs_of(first);
-            for (int t = first; ok && tile_at(off, tb0, p.E, n_mb, t, ti); t += n_pairs) {
+            for (int t = first; ok && order.at(t, ti); t += n_pairs) {
                 const int c0 = (int)cta * ti.nh, nc = min(ti.nh, ti.ntok - c0);   // columns of this CTA that hold rows
                 // lane u has read the pairs of columns u, u + 32, .. (before the tile before this one ended)
                 uint32_t at[4];
@@ -508,10 +579,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         }
     } else {
         // ======================= epilogue =======================
-        if (p.y_type == MOE_F32) epilogue<UP, float>(p, off, tb0, n_mb, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
+        if (p.y_type == MOE_F32) epilogue<UP, float>(p, order, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
         else if (p.y_type == MOE_BF16)
-            epilogue<UP, __nv_bfloat16>(p, off, tb0, n_mb, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
-        else epilogue<UP, __half>(p, off, tb0, n_mb, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
+            epilogue<UP, __nv_bfloat16>(p, order, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
+        else epilogue<UP, __half>(p, order, first, n_pairs, (int)cta, tmem, exch, accf, accr, abort_flag);
     }
     if (bad && p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
     tc_before();
@@ -579,7 +650,7 @@ bool encode(CUtensorMap* m, bool bf16, int rank, const void* base, const cuuint6
 }
 
 size_t smem_bytes(int E) {
-    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 40 + 64 + 2 * (size_t)(E + 1) * 4;
+    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 40 + 72 + 2 * (size_t)(E + 1) * 4 + 2 * (size_t)E;
 }
 
 }  // namespace
