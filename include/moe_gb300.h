@@ -341,10 +341,12 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
  *   q: 4-bit codes 0..15, two to a byte (weight 2j in the low nibble of byte j, 2j+1 in the high),
  *   rows dense: [n_experts][n_out][n_in / 2] bytes;  scales: fp16 or bf16 [n_experts][n_out][n_in / group];
  *   zeros (nullable): uint8 [n_experts][n_out][n_in / group], values 0..15 (the low four bits are used);
- *   NULL: every zero point is 8.  group: 32, 64 or 128;  n_in a multiple of group.
- * The code minus its zero point is an exact small integer: it is multiplied with x exactly, a group's
- * products are summed in fp32 and the scale is applied to that sum in fp32, so no weight is rounded.
- * For a few rows an expert (decode): every active expert's codes are read once per 32 of its rows.
+ *   NULL: every zero point is 8.  group: 32, 64 or 128;  n_in a multiple of group,
+ *   at most 32768.
+ * A group's products of codes and x are exact and summed in fp32, the zero point is taken off that sum
+ * and the scale applied to it in fp32: no weight is rounded.  x is held as fp16 scaled by a power of two
+ * of its row's largest magnitude: exact down to 2^-27 of that (a row with an infinity gives infinities or NaN).
+ * For a few rows an expert (decode): an active expert's codes are read once per 8 or 16 of its rows.
  * Arguments, routing, y and status as moe_grouped_matmul; x of x_type MOE_BF16 or MOE_F16.
  * q, q_up 16-byte aligned; scales and zeros aligned to their element.  One launch, no workspace.
  * Pages: the card experts are 4-bit block types ("bloomery README 0.3.1", Status table, "Quant types"

@@ -634,6 +634,7 @@ moe_status moe_w4_plan_create(const moe_w4_desc* desc, moe_w4_plan** plan) {
         return fail(MOE_ERR_UNSUPPORTED, "group %d (supported: 32, 64, 128)", d.group);
     moe_status st = check_product_shape(d.n_experts, d.n_out, d.n_in);
     if (st) return st;
+    if (d.n_in > kMaxW4In) return fail(MOE_ERR_UNSUPPORTED, "n_in %d above %d", d.n_in, kMaxW4In);
     if (d.n_in % d.group) return fail(MOE_ERR_INVALID_ARG, "n_in %d not a multiple of the group %d", d.n_in, d.group);
     if (!d.q || !d.scales) return fail(MOE_ERR_INVALID_ARG, "q / scales are NULL");
     if ((d.q_up != nullptr) != (d.scales_up != nullptr))
@@ -672,7 +673,7 @@ moe_status moe_w4_matmul(const moe_w4_plan* plan, const void* x, int64_t x_strid
     moe_status st = check_product_call(a, T, k, &todo);
     if (st || !todo) return st;
     a.P = T * k;
-    cudaError_t err = launch_rows(a, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t err = launch_w4(a, reinterpret_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return cuda_fail(err, "4-bit product kernel");
     return MOE_OK;
 }

@@ -24,11 +24,9 @@
 // a pair takes every (pairs of CTAs)-th tile of the list that the offsets define, each warp role finding its
 // tiles by itself.  Every wait is bounded; a wait that runs out is reported (MOE_ERR_TIMEOUT), the copies in flight
 // are waited for (bounded), TMEM is freed and the kernel returns.
-#include <atomic>
-#include <cuda.h>   // CUtensorMap and its enums (the encoder is fetched from the driver at run time)
-
 #include "internal.cuh"
 #include "tc_ptx.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -619,36 +617,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-    static std::atomic<EncodeTiledFn> fn{nullptr};
-    EncodeTiledFn got = fn.load(std::memory_order_acquire);
-    if (!got) {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess) {
-            got = reinterpret_cast<EncodeTiledFn>(f);
-            fn.store(got, std::memory_order_release);
-        }
-    }
-    return got;
-}
-
-// 16-bit elements, boxes of 64 x box1 (x 1), 128-byte swizzle, zeros outside.
-bool encode(CUtensorMap* m, bool bf16, int rank, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-            int box1) {
-    EncodeTiledFn fn = encode_tiled();
-    if (!fn) return false;
-    const cuuint32_t box[3] = {64u, (cuuint32_t)box1, 1u}, one[3] = {1u, 1u, 1u};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-              const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t smem_bytes(int E) {
     return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 40 + 72 + 2 * (size_t)(E + 1) * 4 + 2 * (size_t)E;
 }
@@ -664,12 +632,13 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
                                                                     : (cuuint64_t)a.row_stride * rows * 2};
     const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.P, 1};
     const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
-    if (!encode(&p.tw0, a.bf16, 3, a.w0, wd, ws, a.in_out || a.w1 ? 64 : 128) ||
-        (a.w1 && !encode(&p.tw1, a.bf16, 3, a.w1, wd, ws, 64)))
+    const CUtensorMapDataType type = a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (!encode_map(&p.tw0, type, 3, a.w0, wd, ws, 64, a.in_out || a.w1 ? 64 : 128) ||
+        (a.w1 && !encode_map(&p.tw1, type, 3, a.w1, wd, ws, 64, 64)))
         return cudaErrorInvalidValue;
     if (!a.sorted_pairs)
         for (int i = 0; i < 4; ++i)
-            if (!encode(&p.tx[i], a.bf16, 2, a.x, xd, xs, 16 << i)) return cudaErrorInvalidValue;
+            if (!encode_map(&p.tx[i], type, 2, a.x, xd, xs, 64, 16 << i)) return cudaErrorInvalidValue;
     p.x = static_cast<const uint16_t*>(a.x);
     p.x_stride = a.x_stride;
     p.sorted_pairs = a.sorted_pairs; p.offsets = a.offsets;
@@ -678,22 +647,15 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     p.y = a.y; p.y_type = a.y_type; p.y_stride = a.y_stride; p.status = a.status;
     const WaitCfg wc = wait_cfg();
     p.wait_ns = wc.limit_ns; p.stall = wc.stall;
-    int dev = 0, sms = 0;
-    cudaError_t err;
-    if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
-    if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
     const int v = (a.w1 ? 2 : 0) + (a.in_out ? 1 : 0);
     const void* fn = v == 3   ? (const void*)grouped_dense_kernel<true, true>
                      : v == 2 ? (const void*)grouped_dense_kernel<true, false>
                      : v == 1 ? (const void*)grouped_dense_kernel<false, true>
                               : (const void*)grouped_dense_kernel<false, false>;
-    static std::atomic<uint64_t> ready[4];               // devices whose function attribute is set
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!bit || !(ready[v].load(std::memory_order_acquire) & bit)) {
-        if ((err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kMaxExperts))) != cudaSuccess)
-            return err;
-        ready[v].fetch_or(bit, std::memory_order_release);
-    }
+    static std::atomic<uint64_t> ready[4];
+    int sms = 0;
+    cudaError_t err = prepare_kernel(fn, (int)smem_bytes(kMaxExperts), ready[v], &sms);
+    if (err != cudaSuccess) return err;
     // one pair per two SMs, and no more pairs than there can be tiles
     const int64_t n_mb = (a.N + (a.w1 ? 127 : 255)) / (a.w1 ? 128 : 256);
     const int64_t most = ((int64_t)a.P / kMaxN + (a.E < a.P ? a.E : a.P)) * n_mb;

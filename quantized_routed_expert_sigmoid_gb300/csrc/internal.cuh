@@ -176,6 +176,8 @@ struct RowsArgs {
     int32_t* status;             // nullable
 };
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);            // streams the weights (rows.cu)
+cudaError_t launch_w4(const RowsArgs& a, cudaStream_t s);              // 4-bit weights (w4.cu)
+constexpr int kMaxW4In = 32768;      // n_in of 4-bit weights: one staged row of x has to fit beside the ring
 cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s);   // tcgen05, dense weights (ggemm_dense.cu)
 
 // ---------------------------------------------------------------- decode layer (T <= 4)

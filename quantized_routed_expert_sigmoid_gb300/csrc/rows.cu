@@ -1,5 +1,5 @@
-// rows.cu -- products of a few rows per expert with bf16 / fp16 weights or 4-bit weights with
-// group scales: the weights of the experts that have rows are streamed once through registers.
+// rows.cu -- products of a few rows per expert with bf16 / fp16 weights: the weights of the
+// experts that have rows are streamed once through registers.
 //
 //   y[i, n] = sum_c W[e][n, c] v_i[c],  or  silu(W v) * (W_up v),   v_i = x[sorted_pairs[i] / k] or x[i]
 //
@@ -220,138 +220,6 @@ struct InOut {
     }
 };
 
-// 4-bit weights [out][in]: warps take chunks of 128 c (128 / G groups); lane (g, t) holds, of rows g
-// and g + 8, the t-th quarter of each group (16, 8 or 4 bytes), so that the k slots of one
-// instruction never mix groups.  A word's nibbles (j, j + 4) fall out as 16-bit pairs of one mask;
-// under the exponent of 128 (bf16) or 1024 (fp16) such a nibble reads as that number plus q, and one
-// exact subtraction of that number plus the zero point leaves the integer q - z.  x is paired the same way by byte
-// permutes.  The group's sum is scaled in fp32.
-template <bool BF16, bool UP, int NT, int G>
-struct Q4 {
-    static constexpr int kMats = UP ? 2 : 1, kTiles = UP ? 1 : 2, kRows = 16 * kTiles;
-    static constexpr int kGroups = 128 / G, kWords = G / 32;      // groups a chunk; words a lane and group
-    __device__ static __forceinline__ int row(int tile, int g, int half) { return 16 * tile + g + 8 * half; }
-
-    __device__ static __forceinline__ uint32_t sub2(uint32_t q, uint32_t z) {
-        if constexpr (BF16) {
-            __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&q), *reinterpret_cast<__nv_bfloat162*>(&z));
-            return *reinterpret_cast<uint32_t*>(&v);
-        } else {
-            __half2 v = __hsub2(*reinterpret_cast<__half2*>(&q), *reinterpret_cast<__half2*>(&z));
-            return *reinterpret_cast<uint32_t*>(&v);
-        }
-    }
-    // the four 16-bit pairs (j, j + 4) of a word, minus the zero point (zz: offset + z, twice)
-    __device__ static __forceinline__ void codes(uint32_t w, uint32_t zz, uint32_t (&q)[4]) {
-        constexpr uint32_t kOff = BF16 ? 0x43004300u : 0x64006400u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = sub2(((w >> (4 * j)) & 0x000F000Fu) | kOff, zz);
-    }
-
-    __device__ static __forceinline__ void run(const RowsArgs& a, int e, int r0, const uint16_t* const (&xr)[NT],
-                                               int nt, float (&acc)[kMats][kTiles][NT][4]) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-        const int n_groups = a.K / G, n_chunks = (a.K + 127) / 128;
-        int64_t at[2][2];                                // this lane's rows, as row indices over all experts
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                at[j][h] = (int64_t)e * a.N + min(r0 + row(UP ? 0 : j, g, h), a.N - 1);
-        constexpr int U = 2;                             // chunks in flight
-        for (int c0 = warp; c0 < n_chunks; c0 += U * kWarps) {
-            uint32_t w[U][2][2][4];
-            uint16_t sc[U][2][2][kGroups];
-            uint8_t zp[U][2][2][kGroups];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * kWarps;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint8_t* q = static_cast<const uint8_t*>(UP && j ? a.w1 : a.w0) + at[j][h] * (a.K / 2);
-                        const uint16_t* s = static_cast<const uint16_t*>(UP && j ? a.s1 : a.s0) + at[j][h] * n_groups;
-                        const uint8_t* z = (UP && j ? a.z1 : a.z0);
-#pragma unroll
-                        for (int p = 0; p < kGroups; ++p) {
-                            const int gi = c * kGroups + p;
-                            const bool in = gi < n_groups;
-                            const uint8_t* src = q + (int64_t)gi * (G / 2) + t * (G / 8);
-                            if constexpr (G == 128) {
-                                const uint4 v = in ? ld_stream16(src) : make_uint4(0u, 0u, 0u, 0u);
-                                w[u][j][h][0] = v.x; w[u][j][h][1] = v.y; w[u][j][h][2] = v.z; w[u][j][h][3] = v.w;
-                            } else if constexpr (G == 64) {
-                                const uint2 v = in ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
-                                w[u][j][h][2 * p] = v.x; w[u][j][h][2 * p + 1] = v.y;
-                            } else {
-                                w[u][j][h][p] = in ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
-                            }
-                            sc[u][j][h][p] = in ? __ldg(s + gi) : (uint16_t)0;
-                            zp[u][j][h][p] = in && z ? __ldg(z + at[j][h] * n_groups + gi) & 15 : 8;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int p = 0; p < kGroups; ++p) {
-                    const int gi = (c0 + u * kWarps) * kGroups + p;
-                    if (gi >= n_groups) break;
-                    float part[2][NT][4];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) part[j][n][i] = 0.f;
-                    uint32_t zz[2][2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            zz[j][h] = (BF16 ? 0x43004300u : 0x64006400u) + (uint32_t)zp[u][j][h][p] * 0x00010001u;
-#pragma unroll
-                    for (int k = 0; k < kWords; ++k) {
-                        uint32_t q[2][2][4];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) codes(w[u][j][h][p * kWords + k], zz[j][h], q[j][h]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (n >= nt) break;
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (xr[n]) v = __ldg(reinterpret_cast<const uint4*>(xr[n] + gi * G + t * (G / 4) + 8 * k));
-                            const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
-                            const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                mma16816<BF16>(part[j][n], q[j][0][0], q[j][1][0], q[j][0][1], q[j][1][1], b0, b1);
-                                mma16816<BF16>(part[j][n], q[j][0][2], q[j][1][2], q[j][0][3], q[j][1][3], b2, b3);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint16_t sb = sc[u][j][h][p];
-                            const float s = a.s_bf16 ? __uint_as_float((uint32_t)sb << 16)
-                                                     : __half2float(__ushort_as_half(sb));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float(&c)[4] = acc[UP ? j : 0][UP ? 0 : j][n];
-                                c[2 * h] = fmaf(s, part[j][n][2 * h], c[2 * h]);
-                                c[2 * h + 1] = fmaf(s, part[j][n][2 * h + 1], c[2 * h + 1]);
-                            }
-                        }
-                }
-            }
-        }
-    }
-};
-
 template <class W, int NT>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowsArgs a) {
     constexpr int kMats = W::kMats, kTiles = W::kTiles, kFrag = kTiles * 4;
@@ -418,9 +286,6 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
 }
 template <bool BF16, bool UP, int NT>
 cudaError_t launch_w(const RowsArgs& a, cudaStream_t s) {
-    if (a.group == 128) return launch<Q4<BF16, UP, NT, 128>, NT>(a, s);
-    if (a.group == 64) return launch<Q4<BF16, UP, NT, 64>, NT>(a, s);
-    if (a.group == 32) return launch<Q4<BF16, UP, NT, 32>, NT>(a, s);
     if (a.in_out) {
         // (gated [in][out] tiles hold 32 accumulators a column tile: two of them at most)
         constexpr int M = NT > 2 ? 2 : NT;

@@ -401,3 +401,51 @@ def test_grouped_wait_that_runs_out_is_reported(gather):
         N.moe_debug_set_waits(0, 0)
     assert status.item() == N.MOE_ERR_TIMEOUT
     assert torch.equal(op(x, off, p, k=k), ref)
+
+
+@pytest.mark.parametrize("K", [128, 32768])
+def test_w4_longest_and_shortest_rows(K):
+    """The longest n_in leaves room for one staged row at a time; rows of 128 are half a stage."""
+    E, N_, T = 2, 70, 5
+    gen = _gen(K)
+    a = _quantize(torch.randn(E, N_, K, generator=gen, device="cuda") * 0.02, 32, True)
+    x = torch.randn(T, K, generator=gen, device="cuda").to(BF)
+    off = torch.tensor([0, 4, 5], dtype=torch.int32, device="cuda")
+    y = moe.W4Experts(*a, group=32)(x, off)
+    g, ga, _, _ = _expected(x, _dequant(*a, 32), None, off.tolist(), torch.arange(T, device="cuda"))
+    want, tol = _finish(g, ga, None, None, K // 16 + K // 32 + 40)
+    _close(y, want, tol, F32)
+
+
+def test_w4_rows_of_very_different_magnitudes():
+    """Rows of x are scaled one by one: from 2^-100 to 2^100, and one of zeros."""
+    E, N_, K = 1, 48, 256
+    gen = _gen(21)
+    a = _quantize(torch.randn(E, N_, K, generator=gen, device="cuda") * 0.02, 64, True)
+    x = torch.randn(6, K, generator=gen, device="cuda")
+    x *= torch.tensor([2.0 ** -100, 2.0 ** -20, 1.0, 2.0 ** 20, 2.0 ** 100, 0.0], device="cuda")[:, None]
+    x = x.to(BF)
+    y = moe.W4Experts(*a, group=64)(x)
+    g, ga, _, _ = _expected(x, _dequant(*a, 64), None, [0, 6], torch.arange(6, device="cuda"))
+    want, tol = _finish(g, ga, None, None, K // 16 + K // 64 + 40)
+    _close(y, want, tol, F32)
+    assert bool((y[5] == 0).all())
+
+
+def test_w4_wait_that_runs_out_is_reported():
+    T, E, K, N_ = 3, 4, 512, 200
+    a = _quantize(torch.randn(E, N_, K, generator=_gen(4), device="cuda") * 0.02, 128, False)
+    x = torch.randn(T, K, generator=_gen(5), device="cuda").to(BF)
+    off = torch.tensor([0, 1, 1, 2, 3], dtype=torch.int32, device="cuda")
+    op = moe.W4Experts(*a, group=128)
+    ref = op(x, off).clone()
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        N.moe_debug_set_waits(2_000_000, 1)
+        op(x, off, status=status)
+        torch.cuda.synchronize()
+    finally:
+        N.moe_debug_set_waits(0, 0)
+    assert status.item() == N.MOE_ERR_TIMEOUT
+    assert torch.equal(op(x, off), ref)
