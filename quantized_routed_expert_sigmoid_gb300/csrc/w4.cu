@@ -20,8 +20,11 @@
 // - x is staged once per expert: scaled by a power of two of its row's largest magnitude into fp16 (a
 //   value keeps all its bits down to 2^-27 of the largest; what is lost below is less than the
 //   rounding of the fp32 sum), in the word order of the codes, with the sums of each group.
-// 8 computing warps of 16 weight rows each, one loading warp; a CTA per SM takes an even share of the
-// (expert, 128 rows) units.
+// 16 computing warps (8 sets of 16 weight rows; every other stage each, joined at the end of a
+// unit: with 8 warps the latency of a warp's chain of reads, masks, products and scales showed, and with
+// half of every stage a warp the cost of waiting, arriving and scale addresses), one loading warp; a CTA per SM takes an even share of the (expert, 128 rows) units.
+#include <type_traits>
+
 #include "internal.cuh"
 #include "tc_ptx.cuh"
 #include "tmap.cuh"
@@ -29,7 +32,7 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);
+constexpr int kRowWarps = 8, kWarps = 2 * kRowWarps, kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 6, kStageBytes = 128 * 128, kStageK = 256;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -50,6 +53,30 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto zero.
+__device__ __forceinline__ void mma_f16_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Reads of shared memory by 32-bit address.
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ void store_y(void* y, int type, int64_t i, float v) {
     if (type == MOE_F32) reinterpret_cast<float*>(y)[i] = v;
     else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
@@ -57,48 +84,34 @@ __device__ __forceinline__ void store_y(void* y, int type, int64_t i, float v) {
 }
 __device__ __forceinline__ void computing_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
-// A stage's share of a row's scales and zero points, 256 / G of each.
+// Bytes of a row's scales and zero points in a stage (a copy has at least 4 bytes: with groups of 128 the two
+// zero points are copied with the two before or after them).
 template <int G>
-struct Scales {
-    static constexpr int kN = kStageK / G;
-    uint32_t s[kN / 2], z[(kN + 3) / 4];
-};
-// Those of groups g0 .. of row `row` (of all experts' rows); zeros past the row's end.  vec: rows hold a
-// whole number of stages and start on their size.
+__host__ __device__ constexpr int scale_bytes() { return kStageK / G * 2; }
 template <int G>
-__device__ __forceinline__ void load_scales(Scales<G>& o, const void* s, const uint8_t* z, int64_t row, int g0, int n_groups,
-                                            bool vec) {
-    constexpr int kN = Scales<G>::kN;
-    const uint16_t* sp = static_cast<const uint16_t*>(s) + row * n_groups + g0;
-    const uint8_t* zp = z ? z + row * n_groups + g0 : nullptr;
-#pragma unroll
-    for (int i = 0; i < (kN + 3) / 4; ++i) o.z[i] = 0x08080808u;
-    if (vec) {
-        if constexpr (G == 32) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
-            o.s[0] = v.x; o.s[1] = v.y; o.s[2] = v.z; o.s[3] = v.w;
-            if (zp) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(zp));
-                o.z[0] = w.x; o.z[1] = w.y;
-            }
-        } else if constexpr (G == 64) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
-            o.s[0] = v.x; o.s[1] = v.y;
-            if (zp) o.z[0] = __ldg(reinterpret_cast<const uint32_t*>(zp));
-        } else {
-            o.s[0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
-            if (zp) o.z[0] = __ldg(reinterpret_cast<const uint16_t*>(zp));
-        }
-        return;
+__host__ __device__ constexpr int zero_bytes() { return G == 128 ? 4 : kStageK / G; }
+template <int G>
+__host__ __device__ constexpr int stage_scales() { return 128 * (scale_bytes<G>() + zero_bytes<G>()); }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+// BYTES of shared memory as words.
+template <int BYTES>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t* v) {
+    if constexpr (BYTES == 16) {
+        const uint4 w = lds16(a);
+        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    } else if constexpr (BYTES == 8) {
+        const uint2 w = lds8(a);
+        v[0] = w.x; v[1] = w.y;
+    } else {
+        v[0] = lds4(a);
     }
-#pragma unroll
-    for (int i = 0; i < kN / 2; ++i) o.s[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-        if (g0 + i < n_groups) {
-            o.s[i >> 1] |= (uint32_t)__ldg(sp + i) << (16 * (i & 1));
-            if (zp) o.z[i >> 2] = (o.z[i >> 2] & ~(0xFFu << (8 * (i & 3)))) | (uint32_t)__ldg(zp + i) << (8 * (i & 3));
-        }
 }
 
 template <int G, bool UP, int NT>
@@ -109,20 +122,23 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int n_groups = a.K / G, n_ks = (a.K + kStageK - 1) / kStageK;
-    uint8_t* xs = ring_base + kStages * kStageBytes;       // staged x: p.cols rows, p.x_stride bytes apart
+    uint8_t* scales = ring_base + kStages * kStageBytes;   // [stages] scales, then zero points, of 128 rows
+    uint8_t* xs = scales + kStages * stage_scales<G>();    // staged x: p.cols rows, p.x_stride bytes apart
     float* sums = reinterpret_cast<float*>(xs + (size_t)p.cols * p.x_stride);   // [n_ks * kGroups][kCols]
     float* unscale = sums + (size_t)n_ks * kGroups * kCols;                     // [kCols] the rows' powers of two
-    uint64_t* full = reinterpret_cast<uint64_t*>(unscale + kCols);
+    float* join = unscale + kCols;                         // [2][4 * NT][32 * kRowWarps] one of two warps' sums
+    float* largest = join + 2 * 4 * NT * 32 * kRowWarps;   // [kWarps]
+    uint64_t* full = reinterpret_cast<uint64_t*>(largest + kWarps);
     uint64_t* empty = full + kStages;
     uint64_t* never = empty + kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
-    int* cnt = reinterpret_cast<int*>(never + 2);          // [16]
-    int* off = cnt + 16;                                   // [E + 1]
+    int* cnt = reinterpret_cast<int*>(never + 2);          // [kWarps + 1]
+    int* off = cnt + 20;                                   // [E + 1]
     uint16_t* expert = reinterpret_cast<uint16_t*>(off + a.E + 1);   // [E] those with rows
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], kWarps); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1 + 32); mbar_init(&empty[i], kRowWarps); }
         mbar_init(never, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -167,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
             if (gtime() - t0 > p.wait_ns) { *abort_flag = 1; return; }
         }
     };
-    int s = 0, n_issued = 0;
+    int s = 0, n_issued = 0, step = 0;
     uint32_t ph = 0;
     for (int64_t u = u0; u < u1;) {
         // the units of one expert
@@ -178,37 +194,80 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
         for (int base = 0; base < rows; base += p.cols) {
             if (warp == kWarps) {
                 // ======================= loads =======================
-                for (int b = b0; b < b1; ++b)
+                for (int b = b0; b < b1; ++b) {
+                    // lane u brings the scales of rows u, u + 32, ..
+                    int64_t at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = ((int64_t)e * a.N + min(b * kUnit + (UP ? (32 * i + lane) & 63 : 32 * i + lane), a.N - 1)) * n_groups;
                     for (int ks = 0; ks < n_ks; ++ks) {
                         wait(&empty[s], ph ^ 1);
                         __syncwarp();
-                        if (lane == 0 && !*abort_flag) {
-                            mbar_expect_tx(&full[s], kStageBytes);
-                            uint8_t* dst = ring_base + s * kStageBytes;
-                            const int row = e * a.N + b * kUnit;
-                            tma_load_2d(dst, &p.tw0, ks * 128, row, &full[s]);
-                            if constexpr (UP) tma_load_2d(dst + 8192, &p.tw1, ks * 128, row, &full[s]);
-                            mbar_arrive(&full[s]);
+                        if (!__any_sync(0xffffffffu, *abort_flag)) {
+                            if (lane == 0) {
+                                mbar_expect_tx(&full[s], kStageBytes);
+                                uint8_t* dst = ring_base + s * kStageBytes;
+                                const int row = e * a.N + b * kUnit;
+                                tma_load_2d(dst, &p.tw0, ks * 128, row, &full[s]);
+                                if constexpr (UP) tma_load_2d(dst + 8192, &p.tw1, ks * 128, row, &full[s]);
+                                mbar_arrive(&full[s]);
+                            }
+                            uint8_t* to = scales + s * stage_scales<G>();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint16_t* sp = static_cast<const uint16_t*>(UP && i >= 2 ? a.s1 : a.s0) + at[i] + ks * kGroups;
+                                const uint8_t* zp = (UP && i >= 2 ? a.z1 : a.z0) + at[i] + ks * kGroups;
+                                uint8_t* ts = to + (32 * i + lane) * scale_bytes<G>();
+                                uint8_t* tz = to + 128 * scale_bytes<G>() + (32 * i + lane) * zero_bytes<G>();
+                                if (p.vec) {
+                                    copy_async<scale_bytes<G>()>(su32(ts), sp);
+                                    if (a.z0) {
+                                        if constexpr (G == 128) copy_async<4>(su32(tz), reinterpret_cast<const void*>((uintptr_t)zp & ~(uintptr_t)3));
+                                        else copy_async<zero_bytes<G>()>(su32(tz), zp);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < kGroups; ++q) {
+                                        const bool in = ks * kGroups + q < n_groups;
+                                        reinterpret_cast<uint16_t*>(ts)[q] = in ? __ldg(sp + q) : (uint16_t)0;
+                                        if (a.z0) tz[q] = in ? __ldg(zp + q) : (uint8_t)0;
+                                    }
+                                }
+                            }
+                            if (p.vec) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(&full[s])) : "memory");
+                            else mbar_arrive(&full[s]);
                             ++n_issued;
                         }
                         if (++s == kStages) { s = 0; ph ^= 1; }
                     }
+                }
+                cp_wait_all();
                 continue;
             }
             // ======================= staging of x =======================
             const int nc = min(p.cols, rows - base);
             computing_sync();                            // the rows before have been used
-            for (int c = warp; c < nc; c += kWarps) {
-                int64_t row = lo + base + c;
-                if (a.sorted_pairs) {
-                    const int pair = __ldg(a.sorted_pairs + row);
-                    const bool in = (uint32_t)pair < (uint32_t)a.P;
-                    bad |= !in;
-                    row = in ? pair / a.k : 0;
+            // a set of wc warps a row: all 16 for one row, one each for 16
+            int wc = kWarps;
+            while (wc > 1 && wc * nc > kWarps) wc >>= 1;
+            for (int c0 = 0; c0 < nc; c0 += kWarps / wc) {
+                const int c = c0 + warp / wc, sub = warp % wc;
+                const int step = 256 * wc, i0 = 8 * (32 * sub + lane);
+                const uint16_t* src = static_cast<const uint16_t*>(a.x);
+                if (c < nc) {
+                    int64_t row = lo + base + c;
+                    if (a.sorted_pairs) {
+                        const int pair = __ldg(a.sorted_pairs + row);
+                        const bool in = (uint32_t)pair < (uint32_t)a.P;
+                        bad |= !in;
+                        row = in ? pair / a.k : 0;
+                    }
+                    src += row * a.x_stride;
                 }
-                const uint16_t* src = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
-                auto load = [&](int i, float (&v)[8]) {
-                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + i));
+                auto load = [&](int i) {
+                    return c < nc && i < a.K ? __ldg(reinterpret_cast<const uint4*>(src + i)) : make_uint4(0u, 0u, 0u, 0u);
+                };
+                auto values = [&](const uint4& w, float (&v)[8]) {
                     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -222,142 +281,213 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                         }
                     }
                 };
+                constexpr int kHold = 4;                 // reads a thread has in flight (and keeps, if they are all)
+                uint4 held[kHold];
                 float most = 0.f;
-                for (int i = 8 * lane; i < a.K; i += 256) {
-                    float v[8];
-                    load(i, v);
+                for (int i = i0; i < a.K; i += kHold * step) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
+                    for (int h = 0; h < kHold; ++h) held[h] = load(i + h * step);
+#pragma unroll
+                    for (int h = 0; h < kHold; ++h) {
+                        float v[8];
+                        values(held[h], v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
+                    }
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                if (wc > 1) {
+                    if (lane == 0) largest[warp] = most;
+                    computing_sync();
+                    for (int w = 0; w < wc; ++w) most = fmaxf(most, largest[warp - sub + w]);
+                }
                 // the largest becomes 2^14 .. 2^15 (a row of zeros, and one that is not finite, stay)
                 const int mexp = (int)(__float_as_uint(most) >> 23);
                 const int ex = mexp == 0 || mexp == 255 ? 0 : min(max(mexp - 127 - 14, -120), 113);
                 const float scale = __int_as_float((127 - ex) << 23);
-                if (lane == 0) unscale[c] = __int_as_float((127 + ex) << 23);
-                for (int i = 8 * lane; i < n_ks * kStageK; i += 256) {
-                    float v[8] = {};
-                    if (i < a.K) load(i, v);
-                    float sum = 0.f;
+                if (c < nc && sub == 0 && lane == 0) unscale[c] = __int_as_float((127 + ex) << 23);
+                const bool kept = kHold * step >= a.K;
+                for (int i = i0; i - 8 * lane < n_ks * kStageK; i += kHold * step) {
+                    if (!kept) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[j] *= scale;
-                        sum += v[j];
+                        for (int h = 0; h < kHold; ++h) held[h] = load(i + h * step);
+                    } else if (i0 >= a.K) {
+#pragma unroll
+                        for (int h = 0; h < kHold; ++h) held[h] = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    const __half2 h0 = __floats2half2_rn(v[0], v[4]), h1 = __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f);
-                    const __half2 h2 = __floats2half2_rn(v[2], v[6]), h3 = __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f);
-                    *reinterpret_cast<uint4*>(xs + (size_t)c * p.x_stride + 2 * i) =
-                        make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
-                                   *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
 #pragma unroll
-                    for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane % (G / 8) == 0) sums[(i / G) * kCols + c] = sum;
+                    for (int h = 0; h < kHold; ++h) {
+                        const int at = i + h * step;
+                        float v[8], sum = 0.f;
+                        values(held[h], v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            v[j] *= scale;
+                            sum += v[j];
+                        }
+                        const __half2 h0 = __floats2half2_rn(v[0], v[4]), h1 = __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f);
+                        const __half2 h2 = __floats2half2_rn(v[2], v[6]), h3 = __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f);
+#pragma unroll
+                        for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                        if (c < nc && at < n_ks * kStageK) {
+                            *reinterpret_cast<uint4*>(xs + (size_t)c * p.x_stride + 2 * at) =
+                                make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                                           *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
+                            if (lane % (G / 8) == 0) sums[(at / G) * kCols + c] = sum;
+                        }
+                    }
                 }
+                if (wc > 1 && c0 + kWarps / wc < nc) computing_sync();       // (largest is used again)
             }
             computing_sync();
             // ======================= products =======================
-            const int nt = (nc + 7) / 8;
-            const uint8_t* xc[NT];
+            const int rw = warp % kRowWarps, kh = warp / kRowWarps, nt = (nc + 7) / 8;
+            const uint32_t xs0 = su32(xs) + t * (G / 2);   // (t * G / 4 elements)
+            uint32_t xc[NT];                             // (columns past the last repeat it: their sums are not stored)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) xc[n] = 8 * n + g < nc ? xs + (size_t)(8 * n + g) * p.x_stride : nullptr;
-            const int ra = UP ? 8 * warp + g : 16 * warp + g, rb = UP ? 64 + 8 * warp + g : 16 * warp + 8 + g;   // in the stage
+            for (int n = 0; n < NT; ++n) xc[n] = xs0 + (uint32_t)(min(8 * n + g, nc - 1) * p.x_stride);
+            const uint32_t sums0 = su32(sums) + (uint32_t)(2 * t * 4);
+            const int ra = UP ? 8 * rw + g : 16 * rw + g, rb = UP ? 64 + 8 * rw + g : 16 * rw + 8 + g;   // in the stage
             const int ya = ra, yb = UP ? ra : rb;          // outputs of the two rows, in the unit
-            // scales of the two rows, two stages ahead
-            Scales<G> sa[3], sb[3];
-            int pb = b0, pk = 0;
-            auto ahead = [&](Scales<G>& qa, Scales<G>& qb) {
-                if (pb < b1) {
-                    const int64_t r0 = (int64_t)e * a.N + min(pb * kUnit + ya, a.N - 1);
-                    const int64_t r1 = (int64_t)e * a.N + min(pb * kUnit + yb, a.N - 1);
-                    load_scales<G>(qa, a.s0, a.z0, r0, pk * kGroups, n_groups, p.vec);
-                    load_scales<G>(qb, UP ? a.s1 : a.s0, UP ? a.z1 : a.z0, r1, pk * kGroups, n_groups, p.vec);
-                    if (++pk == n_ks) { pk = 0; ++pb; }
-                }
-            };
-            ahead(sa[0], sb[0]);
-            ahead(sa[1], sb[1]);
-            for (int b = b0; b < b1; ++b) {
+            const uint32_t wa0 = su32(ring_base) + ra * 128, wb0 = su32(ring_base) + rb * 128;
+            const uint32_t sa0 = su32(scales) + ra * scale_bytes<G>(), sb0 = su32(scales) + rb * scale_bytes<G>();
+            const uint32_t za0 = su32(scales) + 128 * scale_bytes<G>() + ra * zero_bytes<G>();
+            const uint32_t zb0 = su32(scales) + 128 * scale_bytes<G>() + rb * zero_bytes<G>();
+            int turn = 0;
+            for (int b = b0; b < b1; ++b, turn ^= 1) {
                 float acc[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
                 for (int ks = 0; ks < n_ks; ++ks) {
-                    ahead(sa[2], sb[2]);
+                    const bool mine = ((step + kh) & 1) == 0;
+                    ++step;
+                    if (!mine) {
+                        if (++s == kStages) { s = 0; ph ^= 1; }
+                        continue;
+                    }
                     const bool stalled = p.stall && u - b1 + b == u0 && ks == 0;      // (test setting)
                     wait(stalled ? never : &full[s], stalled ? 0u : ph);
-                    const uint8_t* wa = ring_base + s * kStageBytes + ra * 128;
-                    const uint8_t* wb = ring_base + s * kStageBytes + rb * 128;
-                    const int left = min(kGroups, n_groups - ks * kGroups);
+                    const uint32_t wa = wa0 + s * kStageBytes, wb = wb0 + s * kStageBytes;
+                    const uint32_t xk = (uint32_t)(ks * kStageK * 2), sk = sums0 + (uint32_t)(ks * kGroups * kCols * 4);
+                    // the two rows' scales and zero points
+                    constexpr int kZ = zero_bytes<G>() / 4;
+                    uint32_t fs_a[scale_bytes<G>() / 4], fs_b[scale_bytes<G>() / 4], z_a[kZ], z_b[kZ];
+                    const uint32_t so = s * stage_scales<G>();
+                    lds_words<scale_bytes<G>()>(sa0 + so, fs_a);
+                    lds_words<scale_bytes<G>()>(sb0 + so, fs_b);
 #pragma unroll
-                    for (int q = 0; q < kGroups; ++q) {
-                        if (q >= left) break;
+                    for (int i = 0; i < kZ; ++i) z_a[i] = z_b[i] = 0x08080808u;
+                    if (a.z0) {
+                        lds_words<zero_bytes<G>()>(za0 + so, z_a);
+                        lds_words<zero_bytes<G>()>(zb0 + so, z_b);
+                        if (G == 128 && p.vec) {         // (which half of the four was meant)
+                            const uintptr_t ga = (uintptr_t)a.z0 + ((size_t)e * a.N + min(b * kUnit + ya, a.N - 1)) * n_groups;
+                            const uintptr_t gb = (uintptr_t)(UP ? a.z1 : a.z0) + ((size_t)e * a.N + min(b * kUnit + yb, a.N - 1)) * n_groups;
+                            z_a[0] >>= 8 * ((ga + ks * kGroups) & 2);
+                            z_b[0] >>= 8 * ((gb + ks * kGroups) & 2);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kZ; ++i) {
+                            z_a[i] &= 0x0F0F0F0Fu;
+                            z_b[i] &= 0x0F0F0F0Fu;
+                        }
+                    }
+                    // one group of the stage.  kind: 0 for a single row of x, else column tiles
+                    auto group = [&](int q, auto kind) {
+                        constexpr int kKind = decltype(kind)::value, NA = kKind == 0 ? 1 : kKind, kWords = G / 32;
                         // this lane's quarter of the group's codes, of both rows
-                        constexpr int kWords = G / 32;
                         uint32_t va[kWords], vb[kWords];
                         const int byte = q * (G / 2) + t * (G / 8);
-                        const int o = (((byte >> 4) ^ g) << 4) + (byte & 15);
+                        const uint32_t o = (((byte >> 4) ^ g) << 4) + (byte & 15);
                         if constexpr (G == 128) {
-                            const uint4 x0 = *reinterpret_cast<const uint4*>(wa + o), x1 = *reinterpret_cast<const uint4*>(wb + o);
+                            const uint4 x0 = lds16(wa + o), x1 = lds16(wb + o);
                             va[0] = x0.x; va[1] = x0.y; va[2] = x0.z; va[3] = x0.w;
                             vb[0] = x1.x; vb[1] = x1.y; vb[2] = x1.z; vb[3] = x1.w;
                         } else if constexpr (G == 64) {
-                            const uint2 x0 = *reinterpret_cast<const uint2*>(wa + o), x1 = *reinterpret_cast<const uint2*>(wb + o);
+                            const uint2 x0 = lds8(wa + o), x1 = lds8(wb + o);
                             va[0] = x0.x; va[1] = x0.y;
                             vb[0] = x1.x; vb[1] = x1.y;
                         } else {
-                            va[0] = *reinterpret_cast<const uint32_t*>(wa + o);
-                            vb[0] = *reinterpret_cast<const uint32_t*>(wb + o);
+                            va[0] = lds4(wa + o);
+                            vb[0] = lds4(wb + o);
                         }
-                        float part[NT][4];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
+                        float part[NA][4];
 #pragma unroll
                         for (int w = 0; w < kWords; ++w) {
                             const uint32_t a8 = va[w] >> 8, b8 = vb[w] >> 8;
-                            const int xo = 2 * (ks * kStageK + q * G + t * (G / 4) + 8 * w);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                if (n >= nt) break;
-                                const uint4 x = xc[n] ? *reinterpret_cast<const uint4*>(xc[n] + xo) : make_uint4(0u, 0u, 0u, 0u);
-                                mma_f16_16816(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
-                                              vb[w] & 0x00F000F0u, x.x, x.y);
+                            for (int n = 0; n < NA; ++n) {
+                                const uint4 x = lds16(xc[n] + xk + 2 * (q * G + 8 * w));
+                                if (w == 0)
+                                    mma_f16_16816_first(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
+                                                        vb[w] & 0x00F000F0u, x.x, x.y);
+                                else
+                                    mma_f16_16816(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
+                                                  vb[w] & 0x00F000F0u, x.x, x.y);
                                 mma_f16_16816(part[n], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
                                               x.z, x.w);
                             }
                         }
-                        const uint32_t ha = sa[0].s[q >> 1] >> (16 * (q & 1)), hb = sb[0].s[q >> 1] >> (16 * (q & 1));
                         float fa, fb;
                         if (a.s_bf16) {
-                            fa = __uint_as_float(ha << 16);
-                            fb = __uint_as_float(hb << 16);
+                            fa = __uint_as_float(q & 1 ? fs_a[q >> 1] & 0xFFFF0000u : fs_a[q >> 1] << 16);
+                            fb = __uint_as_float(q & 1 ? fs_b[q >> 1] & 0xFFFF0000u : fs_b[q >> 1] << 16);
                         } else {
-                            fa = __half2float(__ushort_as_half((unsigned short)ha));
-                            fb = __half2float(__ushort_as_half((unsigned short)hb));
+                            const __half2 ha = *reinterpret_cast<const __half2*>(&fs_a[q >> 1]);
+                            const __half2 hb = *reinterpret_cast<const __half2*>(&fs_b[q >> 1]);
+                            fa = q & 1 ? __high2float(ha) : __low2float(ha);
+                            fb = q & 1 ? __high2float(hb) : __low2float(hb);
                         }
                         // -z * 2^-24, exactly: 2^23 + z as a float's bits, times -2^-24, plus 1/2
-                        const float za = fmaf(__uint_as_float(0x4B000000u | ((sa[0].z[q >> 2] >> (8 * (q & 3))) & 15u)), -0x1p-24f, 0.5f);
-                        const float zb = fmaf(__uint_as_float(0x4B000000u | ((sb[0].z[q >> 2] >> (8 * (q & 3))) & 15u)), -0x1p-24f, 0.5f);
+                        const float za = fmaf(__uint_as_float(__byte_perm(z_a[q >> 2], 0x4B000000u, 0x7650u | (q & 3))), -0x1p-24f, 0.5f);
+                        const float zb = fmaf(__uint_as_float(__byte_perm(z_b[q >> 2], 0x4B000000u, 0x7650u | (q & 3))), -0x1p-24f, 0.5f);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (n >= nt) break;
-                            const float2 xsum = *reinterpret_cast<const float2*>(sums + (size_t)(ks * kGroups + q) * kCols + 8 * n + 2 * t);
-                            acc[n][0] = fmaf(fa, fmaf(za, xsum.x, part[n][0]), acc[n][0]);
-                            acc[n][1] = fmaf(fa, fmaf(za, xsum.y, part[n][1]), acc[n][1]);
-                            acc[n][2] = fmaf(fb, fmaf(zb, xsum.x, part[n][2]), acc[n][2]);
-                            acc[n][3] = fmaf(fb, fmaf(zb, xsum.y, part[n][3]), acc[n][3]);
+                        for (int n = 0; n < NA; ++n) {
+                            const uint32_t xa = sk + (uint32_t)((q * kCols + 8 * n) * 4);
+                            if constexpr (kKind == 0) {
+                                const float xs1 = __uint_as_float(lds4(xa));
+                                acc[0][0] = fmaf(fa, fmaf(za, xs1, part[0][0]), acc[0][0]);
+                                acc[0][2] = fmaf(fb, fmaf(zb, xs1, part[0][2]), acc[0][2]);
+                            } else {
+                                const uint2 xw = lds8(xa);
+                                const float x0 = __uint_as_float(xw.x), x1 = __uint_as_float(xw.y);
+                                acc[n][0] = fmaf(fa, fmaf(za, x0, part[n][0]), acc[n][0]);
+                                acc[n][1] = fmaf(fa, fmaf(za, x1, part[n][1]), acc[n][1]);
+                                acc[n][2] = fmaf(fb, fmaf(zb, x0, part[n][2]), acc[n][2]);
+                                acc[n][3] = fmaf(fb, fmaf(zb, x1, part[n][3]), acc[n][3]);
+                            }
                         }
-                    }
+                    };
+                    auto groups = [&](auto kind) {
+                        const int left = n_groups - ks * kGroups;
+                        if (left >= kGroups) {
+#pragma unroll
+                            for (int q = 0; q < kGroups; ++q) group(q, kind);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < kGroups; ++q)
+                                if (q < left) group(q, kind);
+                        }
+                    };
+                    if (nc == 1) groups(std::integral_constant<int, 0>{});
+                    else if (NT == 1 || nt == 1) groups(std::integral_constant<int, 1>{});
+                    else groups(std::integral_constant<int, NT>{});
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[s]);
                     if (++s == kStages) { s = 0; ph ^= 1; }
-                    sa[0] = sa[1]; sb[0] = sb[1];
-                    sa[1] = sa[2]; sb[1] = sb[2];
                 }
-                if (*abort_flag) continue;
+                // join the two sets of stages: one gives its sums (two buffers, so one barrier a unit)
+                float* mine = join + turn * 4 * NT * 32 * kRowWarps + 32 * rw + lane;
+                if (kh == 1)
+#pragma unroll
+                    for (int i = 0; i < 4 * NT; ++i) mine[i * 32 * kRowWarps] = acc[i >> 2][i & 3];
+                computing_sync();
+                if (kh == 1 || *abort_flag) continue;
+#pragma unroll
+                for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += mine[i * 32 * kRowWarps];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -392,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 
 template <int G, bool UP, int NT>
 size_t fixed_bytes(const RowsArgs& a, int n_ks) {
-    return 1024 + (size_t)kStages * kStageBytes + (size_t)n_ks * (kStageK / G) * 8 * NT * 4 + 8 * NT * 4 + (2 * kStages + 2) * 8 + 64 +
+    return 1024 + (size_t)kStages * (kStageBytes + stage_scales<G>()) + (size_t)n_ks * (kStageK / G) * 8 * NT * 4 + 8 * NT * 4 + 2 * 4 * NT * 32 * kRowWarps * 4 +
+           kWarps * 4 + (2 * kStages + 2) * 8 + 80 +
            (size_t)(a.E + 1) * 4 + (size_t)a.E * 2;
 }
 
@@ -412,7 +543,8 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
     if (!encode_map(&p.tw0, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w0, dims, strides, 128, UP ? 64 : 128) ||
         (UP && !encode_map(&p.tw1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w1, dims, strides, 128, 64)))
         return cudaErrorInvalidValue;
-    p.vec = a.K % kStageK == 0 && (((uintptr_t)a.s0 | (uintptr_t)a.s1) & 15) == 0 && (((uintptr_t)a.z0 | (uintptr_t)a.z1) & 7) == 0;
+    p.vec = a.K % kStageK == 0 && (((uintptr_t)a.s0 | (uintptr_t)a.s1) & 15) == 0 && (((uintptr_t)a.z0 | (uintptr_t)a.z1) & 7) == 0 &&
+            (G < 128 || (int64_t)a.E * a.N * (a.K / G) % 4 == 0);    // (copies of 4 zero points stay inside)
     const WaitCfg wc = wait_cfg();
     p.wait_ns = wc.limit_ns; p.stall = wc.stall;
     static std::atomic<uint64_t> ready;
