@@ -298,8 +298,8 @@ class NormResidual:
                     raise ValueError(f"{name} must be dense [{H}]")
         self.H = H
         self._keep = (gamma_post, gamma_pre)
-        self.desc = N.moe_norm_desc(H, 0, 0, 0, *(g.data_ptr() if g is not None else None for g in self._keep), eps,
-                                    res_scale, scale)
+        self._scales = (eps, res_scale, scale)
+        self._desc = {}                  # the call's description, by the types of its tensors
 
     def __call__(self, x: torch.Tensor | None, y: torch.Tensor, gate: torch.Tensor | None = None,
                  x_out: torch.Tensor | None = None, u: torch.Tensor | None = None, stream=None):
@@ -308,26 +308,43 @@ class NormResidual:
         x (None: 0), y: [T, H].  gate: fp32, broadcastable to [T, H] ([H], [1, H], [T, 1] or [T, H]).
         Outputs that are not given are made: x_out like x (or y), u in bf16 when gamma_pre was given.
         """
-        T, H = y.shape
-        d = self.desc
-        if H != self.H or (x is not None and x.shape != y.shape):
-            raise ValueError(f"x and y must be [T, {self.H}]")
+        shape = y.shape
+        T, H = shape
+        if H != self.H:
+            raise ValueError(f"y must be [T, {self.H}]")
         if x_out is None:
             x_out = torch.empty((T, H), dtype=(x if x is not None else y).dtype, device=y.device)
         if u is None and self._keep[1] is not None:
             u = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-        for name, t in (("x", x), ("y", y), ("x_out", x_out), ("u", u)):
-            if t is not None and (t.dtype not in _VT or not t.is_cuda or t.shape != y.shape):
-                raise ValueError(f"{name} must be an fp32, bf16 or fp16 CUDA tensor [{T}, {self.H}]")
-        if x is not None and x.dtype is not x_out.dtype:
-            raise ValueError("x_out must have x's type")
-        gate_row = gate_col = 0
+        xs = us = gate_row = gate_col = 0
+        ys = self._rows(y, "y", shape)
+        os = self._rows(x_out, "x_out", shape)
+        if x is not None:
+            xs = self._rows(x, "x", shape)
+            if x.dtype is not x_out.dtype:
+                raise ValueError("x_out must have x's type")
+        if u is not None:
+            us = self._rows(u, "u", shape)
         if gate is not None:
-            _cuda(gate, "gate", (torch.float32,))
-            gate_row, gate_col = gate.broadcast_to(T, H).stride()
-        d = N.moe_norm_desc(H, _VT[x_out.dtype], _VT[y.dtype], _VT[u.dtype] if u is not None else N.MOE_F32,
-                            d.gamma_post, d.gamma_pre, d.eps, d.res_scale, d.scale)
-        N.moe_norm_residual(d, x, _row_stride(x, "x") if x is not None else 0, y, _row_stride(y, "y"), gate, gate_row,
-                            gate_col, T, x_out, _row_stride(x_out, "x_out"), u, _row_stride(u, "u") if u is not None else 0,
-                            stream)
+            gs, st = gate.shape, gate.stride()
+            if len(gs) == 1:
+                gs, st = (1,) + tuple(gs), (0,) + st
+            if gate.dtype is not torch.float32 or not gate.is_cuda or len(gs) != 2 or gs[0] not in (1, T) or gs[1] not in (1, H):
+                raise ValueError(f"gate must be an fp32 CUDA tensor broadcastable to [{T}, {H}]")
+            gate_row, gate_col = st[0] if gs[0] != 1 else 0, st[1] if gs[1] != 1 else 0
+        types = (x_out.dtype, y.dtype, u.dtype if u is not None else torch.float32)
+        desc = self._desc.get(types)
+        if desc is None:
+            g = [t.data_ptr() if t is not None else None for t in self._keep]
+            desc = self._desc[types] = N.moe_norm_desc(H, *(_VT[t] for t in types), *g, *self._scales)
+        N.moe_norm_residual(desc, x, xs, y, ys, gate, gate_row, gate_col, T, x_out, os, u, us, stream)
         return x_out, u
+
+    def _rows(self, t, name, shape):
+        """Elements between the rows of t, a [T, H] tensor of the call."""
+        if t.shape != shape or t.dtype not in _VT or not t.is_cuda:
+            raise ValueError(f"{name} must be an fp32, bf16 or fp16 CUDA tensor {list(shape)}")
+        row, col = t.stride()
+        if col != 1 and shape[1] != 1:
+            raise ValueError(f"the last dimension of {name} must be dense")
+        return row if shape[0] > 1 else (shape[1] + 7) // 8 * 8
