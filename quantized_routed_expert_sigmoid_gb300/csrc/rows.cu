@@ -126,7 +126,7 @@ __device__ __forceinline__ int64_t x_row(const RowsArgs& a, int i) {
 // [out][in] weights: warps take chunks of 32 c, lane (g, t) 8 of them of rows g and g + 8.
 template <bool BF16, bool UP, int NT>
 struct OutIn {
-    static constexpr int kMats = UP ? 2 : 1, kTiles = UP ? 1 : 2, kRows = 16 * kTiles;
+    static constexpr int kMats = UP ? 2 : 1, kTiles = UP ? 1 : 2, kRows = 16 * kTiles, kCtas = 3;
     __device__ static __forceinline__ int row(int tile, int g, int half) { return 16 * tile + g + 8 * half; }
     __device__ static __forceinline__ void run(const RowsArgs& a, int e, int r0, const uint16_t* const (&xr)[NT],
                                                int nt, float (&acc)[kMats][kTiles][NT][4]) {
@@ -140,7 +140,7 @@ struct OutIn {
                 wr[j][h] = static_cast<const uint16_t*>(UP && j == 1 ? a.w1 : a.w0) + (int64_t)e * a.expert_stride +
                            (int64_t)r * a.row_stride;
             }
-        constexpr int U = 4;                            // chunks in flight
+        constexpr int U = NT == 1 ? 2 : 4;              // chunks in flight
         const int n_chunks = (a.K + 31) / 32;
         for (int c0 = warp; c0 < n_chunks; c0 += U * kWarps) {
             uint4 w[U][2][2];
@@ -175,7 +175,7 @@ struct OutIn {
 // 4t + 3, and byte permutes pair the c of one output.  Output 8g + 2 tile + half is row g + 8 half.
 template <bool BF16, bool UP, int NT>
 struct InOut {
-    static constexpr int kMats = UP ? 2 : 1, kTiles = 4, kRows = 64;
+    static constexpr int kMats = UP ? 2 : 1, kTiles = 4, kRows = 64, kCtas = 2;
     __device__ static __forceinline__ int row(int tile, int g, int half) { return 8 * g + 2 * tile + half; }
     __device__ static __forceinline__ void run(const RowsArgs& a, int e, int r0, const uint16_t* const (&xr)[NT],
                                                int nt, float (&acc)[kMats][kTiles][NT][4]) {
@@ -221,7 +221,7 @@ struct InOut {
 };
 
 template <class W, int NT>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? W::kCtas : 1) rows_kernel(const __grid_constant__ RowsArgs a) {
     constexpr int kMats = W::kMats, kTiles = W::kTiles, kFrag = kTiles * 4;
     __shared__ float red[kWarps][kMats * kFrag][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2;

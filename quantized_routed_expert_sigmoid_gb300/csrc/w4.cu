@@ -114,7 +114,7 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t* v) {
     }
 }
 
-template <int G, bool UP, int NT>
+template <int G, bool UP, int NT, bool SCALE_BF16>
 __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__ W4Params p) {
     constexpr int kCols = 8 * NT, kUnit = UP ? 64 : 128;   // outputs of a unit
     constexpr int kGroups = kStageK / G;                   // groups of a stage
@@ -350,7 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
             const uint32_t sums0 = su32(sums) + (uint32_t)(2 * t * 4);
             const int ra = UP ? 8 * rw + g : 16 * rw + g, rb = UP ? 64 + 8 * rw + g : 16 * rw + 8 + g;   // in the stage
             const int ya = ra, yb = UP ? ra : rb;          // outputs of the two rows, in the unit
-            const uint32_t wa0 = su32(ring_base) + ra * 128, wb0 = su32(ring_base) + rb * 128;
+            // this lane's 16 (8, 4) bytes of a row's group q lie at (this address) xor (q * G / 2): the swizzle
+            // exchanges 16-byte chunks by the row's last three bits, which are g
+            const uint32_t wl = (((t * (G / 8)) >> 4 ^ g) << 4) + ((t * (G / 8)) & 15);
+            const uint32_t wa0 = su32(ring_base) + ra * 128 + wl, wb0 = su32(ring_base) + rb * 128 + wl;
             const uint32_t sa0 = su32(scales) + ra * scale_bytes<G>(), sb0 = su32(scales) + rb * scale_bytes<G>();
             const uint32_t za0 = su32(scales) + 128 * scale_bytes<G>() + ra * zero_bytes<G>();
             const uint32_t zb0 = su32(scales) + 128 * scale_bytes<G>() + rb * zero_bytes<G>();
@@ -400,19 +403,18 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                         constexpr int kKind = decltype(kind)::value, NA = kKind == 0 ? 1 : kKind, kWords = G / 32;
                         // this lane's quarter of the group's codes, of both rows
                         uint32_t va[kWords], vb[kWords];
-                        const int byte = q * (G / 2) + t * (G / 8);
-                        const uint32_t o = (((byte >> 4) ^ g) << 4) + (byte & 15);
+                        const uint32_t oa = wa ^ (uint32_t)(q * (G / 2)), ob = wb ^ (uint32_t)(q * (G / 2));
                         if constexpr (G == 128) {
-                            const uint4 x0 = lds16(wa + o), x1 = lds16(wb + o);
+                            const uint4 x0 = lds16(oa), x1 = lds16(ob);
                             va[0] = x0.x; va[1] = x0.y; va[2] = x0.z; va[3] = x0.w;
                             vb[0] = x1.x; vb[1] = x1.y; vb[2] = x1.z; vb[3] = x1.w;
                         } else if constexpr (G == 64) {
-                            const uint2 x0 = lds8(wa + o), x1 = lds8(wb + o);
+                            const uint2 x0 = lds8(oa), x1 = lds8(ob);
                             va[0] = x0.x; va[1] = x0.y;
                             vb[0] = x1.x; vb[1] = x1.y;
                         } else {
-                            va[0] = lds4(wa + o);
-                            vb[0] = lds4(wb + o);
+                            va[0] = lds4(oa);
+                            vb[0] = lds4(ob);
                         }
                         float part[NA][4];
 #pragma unroll
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                             }
                         }
                         float fa, fb;
-                        if (a.s_bf16) {
+                        if constexpr (SCALE_BF16) {
                             fa = __uint_as_float(q & 1 ? fs_a[q >> 1] & 0xFFFF0000u : fs_a[q >> 1] << 16);
                             fb = __uint_as_float(q & 1 ? fs_b[q >> 1] & 0xFFFF0000u : fs_b[q >> 1] << 16);
                         } else {
@@ -527,8 +529,8 @@ size_t fixed_bytes(const RowsArgs& a, int n_ks) {
            (size_t)(a.E + 1) * 4 + (size_t)a.E * 2;
 }
 
-template <int G, bool UP, int NT>
-cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
+template <int G, bool UP, int NT, bool SCALE_BF16>
+cudaError_t launch_as(const RowsArgs& a, cudaStream_t s) {
     W4Params p{};
     p.a = a;
     const int n_ks = (a.K + kStageK - 1) / kStageK;
@@ -549,7 +551,7 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
     p.wait_ns = wc.limit_ns; p.stall = wc.stall;
     static std::atomic<uint64_t> ready;
     int sms = 0;
-    const void* fn = (const void*)w4_kernel<G, UP, NT>;
+    const void* fn = (const void*)w4_kernel<G, UP, NT, SCALE_BF16>;
     cudaError_t err = prepare_kernel(fn, kSmemMax, ready, &sms);
     if (err != cudaSuccess) return err;
     constexpr int kUnit = UP ? 64 : 128;
@@ -558,6 +560,11 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
     const size_t smem = fixed + (size_t)p.cols * p.x_stride;
     err = cudaLaunchKernel(fn, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads), args, smem, s);
     return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int G, bool UP, int NT>
+cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
+    return a.s_bf16 ? launch_as<G, UP, NT, true>(a, s) : launch_as<G, UP, NT, false>(a, s);
 }
 
 template <int G>
