@@ -32,7 +32,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRowWarps = 8, kWarps = 2 * kRowWarps, kThreads = 32 * (kWarps + 1);
+constexpr int kRowWarps = 8, kWarps = 2 * kRowWarps, kScaleWarps = 3, kAllWarps = kWarps + 1 + kScaleWarps, kThreads = 32 * kAllWarps;
 constexpr int kStages = 6, kStageBytes = 128 * 128, kStageK = 256;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -48,16 +48,14 @@ struct W4Params {
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // The same onto zero.
 __device__ __forceinline__ void mma_f16_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                     uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
@@ -132,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     uint64_t* empty = full + kStages;
     uint64_t* never = empty + kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
-    int* cnt = reinterpret_cast<int*>(never + 2);          // [kWarps + 1]
+    int* cnt = reinterpret_cast<int*>(never + 2);          // [kAllWarps]
     int* off = cnt + 20;                                   // [E + 1]
     uint16_t* expert = reinterpret_cast<uint16_t*>(off + a.E + 1);   // [E] those with rows
 
@@ -158,17 +156,21 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
         const unsigned m = __ballot_sync(0xffffffffu, has);
         if (lane == 0) cnt[warp] = __popc(m);
         __syncthreads();
-        int base = n_active;
-        for (int w = 0; w <= kWarps; ++w) {
-            if (w < warp) base += cnt[w];
-            n_active += cnt[w];
+        int inc = lane < kAllWarps ? cnt[lane] : 0;
+        const int own = inc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
         }
+        const int base = n_active + __shfl_sync(0xffffffffu, inc - own, warp);
+        n_active += __shfl_sync(0xffffffffu, inc, 31);
         if (has) expert[base + __popc(m & ((1u << lane) - 1u))] = (uint16_t)e;
         __syncthreads();
     }
-    const int n_blk = (a.N + kUnit - 1) / kUnit;
-    const int64_t units = (int64_t)n_active * n_blk;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    // this CTA's units (at most 2^10 experts x 2^14 blocks, x 152 CTAs: 32 bits hold the products)
+    const uint32_t n_blk = (uint32_t)(a.N + kUnit - 1) / kUnit, units = n_active * n_blk;
+    const uint32_t u0 = (uint32_t)((uint64_t)units * blockIdx.x / gridDim.x), u1 = (uint32_t)((uint64_t)units * (blockIdx.x + 1) / gridDim.x);
 
     // Bounded wait; after a wait has run out every wait returns at once and the loops run to their
     // ends without waiting, loading or storing, so that the CTA's barriers stay matched.
@@ -185,21 +187,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     };
     int s = 0, n_issued = 0, step = 0;
     uint32_t ph = 0;
-    for (int64_t u = u0; u < u1;) {
+    for (uint32_t u = u0; u < u1;) {
         // the units of one expert
-        const int e = expert[u / n_blk], b0 = (int)(u % n_blk);
-        const int b1 = (int)min((int64_t)n_blk, b0 + (u1 - u));
+        const int nth = u / n_blk, e = expert[nth], b0 = (int)(u - nth * n_blk);
+        const int b1 = (int)min(n_blk, b0 + (u1 - u));
         const int lo = off[e], rows = off[e + 1] - lo;
         u += b1 - b0;
         for (int base = 0; base < rows; base += p.cols) {
             if (warp == kWarps) {
-                // ======================= loads =======================
-                for (int b = b0; b < b1; ++b) {
-                    // lane u brings the scales of rows u, u + 32, ..
-                    int64_t at[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        at[i] = ((int64_t)e * a.N + min(b * kUnit + (UP ? (32 * i + lane) & 63 : 32 * i + lane), a.N - 1)) * n_groups;
+                // ======================= codes =======================
+                for (int b = b0; b < b1; ++b)
                     for (int ks = 0; ks < n_ks; ++ks) {
                         wait(&empty[s], ph ^ 1);
                         __syncwarp();
@@ -212,6 +209,25 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                                 if constexpr (UP) tma_load_2d(dst + 8192, &p.tw1, ks * 128, row, &full[s]);
                                 mbar_arrive(&full[s]);
                             }
+                            ++n_issued;
+                        }
+                        if (++s == kStages) { s = 0; ph ^= 1; }
+                    }
+                continue;
+            }
+            if (warp > kWarps) {
+                // ======================= scales and zero points =======================
+                for (int b = b0; b < b1; ++b) {
+                    // lane u brings the scales of rows u, u + 32, ..
+                    int64_t at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = ((int64_t)e * a.N + min(b * kUnit + (UP ? (32 * i + lane) & 63 : 32 * i + lane), a.N - 1)) * n_groups;
+                    for (int ks = 0; ks < n_ks; ++ks) {
+                        const bool mine = step % kScaleWarps == warp - kWarps - 1;
+                        ++step;
+                        if (mine) {
+                            wait(&empty[s], ph ^ 1);
                             uint8_t* to = scales + s * stage_scales<G>();
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -236,7 +252,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                             }
                             if (p.vec) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(&full[s])) : "memory");
                             else mbar_arrive(&full[s]);
-                            ++n_issued;
                         }
                         if (++s == kStages) { s = 0; ph ^= 1; }
                     }
@@ -319,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 #pragma unroll
                     for (int h = 0; h < kHold; ++h) {
                         const int at = i + h * step;
+                        if (at - 8 * lane >= n_ks * kStageK) break;          // (the same for the whole warp)
                         float v[8], sum = 0.f;
                         values(held[h], v);
 #pragma unroll
@@ -416,23 +432,35 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                             va[0] = lds4(oa);
                             vb[0] = lds4(ob);
                         }
-                        float part[NA][4];
+                        // (two chains of products, of the low and of the high halves of the words)
+                        float part[NA][4], high[NA][4];
 #pragma unroll
                         for (int w = 0; w < kWords; ++w) {
                             const uint32_t a8 = va[w] >> 8, b8 = vb[w] >> 8;
 #pragma unroll
                             for (int n = 0; n < NA; ++n) {
                                 const uint4 x = lds16(xc[n] + xk + 2 * (q * G + 8 * w));
-                                if (w == 0)
+                                if (w == 0) {
                                     mma_f16_16816_first(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
                                                         vb[w] & 0x00F000F0u, x.x, x.y);
-                                else
+                                    if constexpr (kWords > 1) {
+                                        mma_f16_16816_first(high[n], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                                                            b8 & 0x00F000F0u, x.z, x.w);
+                                        continue;
+                                    }
+                                } else {
                                     mma_f16_16816(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
                                                   vb[w] & 0x00F000F0u, x.x, x.y);
-                                mma_f16_16816(part[n], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
-                                              x.z, x.w);
+                                }
+                                mma_f16_16816(kWords > 1 ? high[n] : part[n], a8 & 0x000F000Fu, b8 & 0x000F000Fu,
+                                              a8 & 0x00F000F0u, b8 & 0x00F000F0u, x.z, x.w);
                             }
                         }
+                        if constexpr (kWords > 1)
+#pragma unroll
+                            for (int n = 0; n < NA; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) part[n][i] += high[n][i];
                         float fa, fb;
                         if constexpr (SCALE_BF16) {
                             fa = __uint_as_float(q & 1 ? fs_a[q >> 1] & 0xFFFF0000u : fs_a[q >> 1] << 16);
@@ -511,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     if (bad && a.status) atomicCAS(a.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
     __syncthreads();
     if (tid == kWarps * 32 && *abort_flag) {
-        // copies that no warp waited for may still be in flight: wait (within the limit) for their stages
+        // codes that no warp waited for may still be in flight: wait (within the limit) for their stages
+        // (the other warps have waited for their own copies and arrived)
         for (int i = 0; i < min(n_issued, kStages); ++i) {
             const int step = n_issued - 1 - i;
             const uint64_t t0 = gtime();
