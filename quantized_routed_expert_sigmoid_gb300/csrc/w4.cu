@@ -32,7 +32,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRowWarps = 8, kWarps = 2 * kRowWarps, kScaleWarps = 3, kAllWarps = kWarps + 1 + kScaleWarps, kThreads = 32 * kAllWarps;
+constexpr int kRowWarps = 4, kWarps = 2 * kRowWarps, kTiles = 2, kScaleWarps = 3, kAllWarps = kWarps + 1 + kScaleWarps, kThreads = 32 * kAllWarps;
 constexpr int kStages = 6, kStageBytes = 128 * 128, kStageK = 256;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -116,6 +116,7 @@ template <int G, bool UP, int NT, bool SCALE_BF16>
 __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__ W4Params p) {
     constexpr int kCols = 8 * NT, kUnit = UP ? 64 : 128;   // outputs of a unit
     constexpr int kGroups = kStageK / G;                   // groups of a stage
+    constexpr int kJoin = kTiles * 4 * NT * 32 * kRowWarps;
     const RowsArgs& a = p.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -124,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     uint8_t* xs = scales + kStages * stage_scales<G>();    // staged x: p.cols rows, p.x_stride bytes apart
     float* sums = reinterpret_cast<float*>(xs + (size_t)p.cols * p.x_stride);   // [n_ks * kGroups][kCols]
     float* unscale = sums + (size_t)n_ks * kGroups * kCols;                     // [kCols] the rows' powers of two
-    float* join = unscale + kCols;                         // [2][4 * NT][32 * kRowWarps] one of two warps' sums
-    float* largest = join + 2 * 4 * NT * 32 * kRowWarps;   // [kWarps]
+    float* join = unscale + kCols;                         // [2][kTiles * 4 * NT][32 * kRowWarps] one of two warps' sums
+    float* largest = join + 2 * kJoin;                     // [kWarps]
     uint64_t* full = reinterpret_cast<uint64_t*>(largest + kWarps);
     uint64_t* empty = full + kStages;
     uint64_t* never = empty + kStages;
@@ -364,22 +365,29 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 #pragma unroll
             for (int n = 0; n < NT; ++n) xc[n] = xs0 + (uint32_t)(min(8 * n + g, nc - 1) * p.x_stride);
             const uint32_t sums0 = su32(sums) + (uint32_t)(2 * t * 4);
-            const int ra = UP ? 8 * rw + g : 16 * rw + g, rb = UP ? 64 + 8 * rw + g : 16 * rw + 8 + g;   // in the stage
-            const int ya = ra, yb = UP ? ra : rb;          // outputs of the two rows, in the unit
+            // tile j of this warp: the rows of W (and W_up) 16 (8) apart that lie at rows ra[j], rb[j] of the stage
+            int ra[kTiles], rb[kTiles];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                const int tile = kTiles * rw + j;
+                ra[j] = UP ? 8 * tile + g : 16 * tile + g;
+                rb[j] = UP ? 64 + ra[j] : ra[j] + 8;
+            }
             // this lane's 16 (8, 4) bytes of a row's group q lie at (this address) xor (q * G / 2): the swizzle
             // exchanges 16-byte chunks by the row's last three bits, which are g
-            const uint32_t wl = (((t * (G / 8)) >> 4 ^ g) << 4) + ((t * (G / 8)) & 15);
-            const uint32_t wa0 = su32(ring_base) + ra * 128 + wl, wb0 = su32(ring_base) + rb * 128 + wl;
-            const uint32_t sa0 = su32(scales) + ra * scale_bytes<G>(), sb0 = su32(scales) + rb * scale_bytes<G>();
-            const uint32_t za0 = su32(scales) + 128 * scale_bytes<G>() + ra * zero_bytes<G>();
-            const uint32_t zb0 = su32(scales) + 128 * scale_bytes<G>() + rb * zero_bytes<G>();
+            const uint32_t ring0 = su32(ring_base) + ra[0] * 128 + (((t * (G / 8)) >> 4 ^ g) << 4) + ((t * (G / 8)) & 15);
+            const uint32_t scales0 = su32(scales) + ra[0] * scale_bytes<G>();
+            const uint32_t zeros0 = su32(scales) + 128 * scale_bytes<G>() + ra[0] * zero_bytes<G>();
+            constexpr int kTileStep = UP ? 8 : 16, kHalfStep = UP ? 64 : 8;       // rows between tiles and halves
             int turn = 0;
             for (int b = b0; b < b1; ++b, turn ^= 1) {
-                float acc[NT][4];
+                float acc[kTiles][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[j][n][i] = 0.f;
                 for (int ks = 0; ks < n_ks; ++ks) {
                     const bool mine = ((step + kh) & 1) == 0;
                     ++step;
@@ -389,106 +397,96 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     }
                     const bool stalled = p.stall && u - b1 + b == u0 && ks == 0;      // (test setting)
                     wait(stalled ? never : &full[s], stalled ? 0u : ph);
-                    const uint32_t wa = wa0 + s * kStageBytes, wb = wb0 + s * kStageBytes;
+                    const uint32_t codes = ring0 + s * kStageBytes;
                     const uint32_t xk = (uint32_t)(ks * kStageK * 2), sk = sums0 + (uint32_t)(ks * kGroups * kCols * 4);
-                    // the two rows' scales and zero points
-                    constexpr int kZ = zero_bytes<G>() / 4;
-                    uint32_t fs_a[scale_bytes<G>() / 4], fs_b[scale_bytes<G>() / 4], z_a[kZ], z_b[kZ];
+                    // the rows' scales and zero points: [tile][half]
+                    constexpr int kS = scale_bytes<G>() / 4, kZ = zero_bytes<G>() / 4;
+                    uint32_t fs[kTiles][2][kS], fz[kTiles][2][kZ];
                     const uint32_t so = s * stage_scales<G>();
-                    lds_words<scale_bytes<G>()>(sa0 + so, fs_a);
-                    lds_words<scale_bytes<G>()>(sb0 + so, fs_b);
 #pragma unroll
-                    for (int i = 0; i < kZ; ++i) z_a[i] = z_b[i] = 0x08080808u;
-                    if (a.z0) {
-                        lds_words<zero_bytes<G>()>(za0 + so, z_a);
-                        lds_words<zero_bytes<G>()>(zb0 + so, z_b);
-                        if (G == 128 && p.vec) {         // (which half of the four was meant)
-                            const uintptr_t ga = (uintptr_t)a.z0 + ((size_t)e * a.N + min(b * kUnit + ya, a.N - 1)) * n_groups;
-                            const uintptr_t gb = (uintptr_t)(UP ? a.z1 : a.z0) + ((size_t)e * a.N + min(b * kUnit + yb, a.N - 1)) * n_groups;
-                            z_a[0] >>= 8 * ((ga + ks * kGroups) & 2);
-                            z_b[0] >>= 8 * ((gb + ks * kGroups) & 2);
-                        }
+                    for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                        for (int i = 0; i < kZ; ++i) {
-                            z_a[i] &= 0x0F0F0F0Fu;
-                            z_b[i] &= 0x0F0F0F0Fu;
+                        for (int h = 0; h < 2; ++h) {
+                            lds_words<scale_bytes<G>()>(scales0 + so + (j * kTileStep + h * kHalfStep) * scale_bytes<G>(), fs[j][h]);
+#pragma unroll
+                            for (int i = 0; i < kZ; ++i) fz[j][h][i] = 0x08080808u;
+                            if (a.z0) {
+                                lds_words<zero_bytes<G>()>(zeros0 + so + (j * kTileStep + h * kHalfStep) * zero_bytes<G>(), fz[j][h]);
+                                if (G == 128 && p.vec) { // (which half of the four was meant)
+                                    const int row = min(b * kUnit + (UP ? ra[j] : ra[j] + 8 * h), a.N - 1);
+                                    const uintptr_t at = (uintptr_t)(UP && h ? a.z1 : a.z0) + ((size_t)e * a.N + row) * n_groups;
+                                    fz[j][h][0] >>= 8 * ((at + ks * kGroups) & 2);
+                                }
+#pragma unroll
+                                for (int i = 0; i < kZ; ++i) fz[j][h][i] &= 0x0F0F0F0Fu;
+                            }
                         }
-                    }
                     // one group of the stage.  kind: 0 for a single row of x, else column tiles
                     auto group = [&](int q, auto kind) {
                         constexpr int kKind = decltype(kind)::value, NA = kKind == 0 ? 1 : kKind, kWords = G / 32;
-                        // this lane's quarter of the group's codes, of both rows
-                        uint32_t va[kWords], vb[kWords];
-                        const uint32_t oa = wa ^ (uint32_t)(q * (G / 2)), ob = wb ^ (uint32_t)(q * (G / 2));
-                        if constexpr (G == 128) {
-                            const uint4 x0 = lds16(oa), x1 = lds16(ob);
-                            va[0] = x0.x; va[1] = x0.y; va[2] = x0.z; va[3] = x0.w;
-                            vb[0] = x1.x; vb[1] = x1.y; vb[2] = x1.z; vb[3] = x1.w;
-                        } else if constexpr (G == 64) {
-                            const uint2 x0 = lds8(oa), x1 = lds8(ob);
-                            va[0] = x0.x; va[1] = x0.y;
-                            vb[0] = x1.x; vb[1] = x1.y;
-                        } else {
-                            va[0] = lds4(oa);
-                            vb[0] = lds4(ob);
-                        }
-                        // (two chains of products, of the low and of the high halves of the words)
-                        float part[NA][4], high[NA][4];
+                        // this lane's quarter of the group's codes, of every row
+                        uint32_t v[kTiles][2][kWords];
 #pragma unroll
-                        for (int w = 0; w < kWords; ++w) {
-                            const uint32_t a8 = va[w] >> 8, b8 = vb[w] >> 8;
+                        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                lds_words<G / 8>((codes ^ (uint32_t)(q * (G / 2))) + (j * kTileStep + h * kHalfStep) * 128, v[j][h]);
+                        // (two chains of products, of the low and of the high halves of the words)
+                        float part[kTiles][NA][4], high[kTiles][NA][4];
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w)
 #pragma unroll
                             for (int n = 0; n < NA; ++n) {
                                 const uint4 x = lds16(xc[n] + xk + 2 * (q * G + 8 * w));
-                                if (w == 0) {
-                                    mma_f16_16816_first(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
-                                                        vb[w] & 0x00F000F0u, x.x, x.y);
-                                    if constexpr (kWords > 1) {
-                                        mma_f16_16816_first(high[n], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
-                                                            b8 & 0x00F000F0u, x.z, x.w);
-                                        continue;
-                                    }
-                                } else {
-                                    mma_f16_16816(part[n], va[w] & 0x000F000Fu, vb[w] & 0x000F000Fu, va[w] & 0x00F000F0u,
-                                                  vb[w] & 0x00F000F0u, x.x, x.y);
+#pragma unroll
+                                for (int j = 0; j < kTiles; ++j) {
+                                    const uint32_t va = v[j][0][w], vb = v[j][1][w], a8 = va >> 8, b8 = vb >> 8;
+                                    float(&lo)[4] = part[j][n];
+                                    float(&hi)[4] = kWords > 1 ? high[j][n] : part[j][n];
+                                    if (w == 0)
+                                        mma_f16_16816_first(lo, va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u,
+                                                            x.x, x.y);
+                                    else
+                                        mma_f16_16816(lo, va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, x.x,
+                                                      x.y);
+                                    if (w == 0 && kWords > 1)
+                                        mma_f16_16816_first(hi, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
+                                                            x.z, x.w);
+                                    else
+                                        mma_f16_16816(hi, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, x.z,
+                                                      x.w);
                                 }
-                                mma_f16_16816(kWords > 1 ? high[n] : part[n], a8 & 0x000F000Fu, b8 & 0x000F000Fu,
-                                              a8 & 0x00F000F0u, b8 & 0x00F000F0u, x.z, x.w);
                             }
-                        }
-                        if constexpr (kWords > 1)
-#pragma unroll
-                            for (int n = 0; n < NA; ++n)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) part[n][i] += high[n][i];
-                        float fa, fb;
-                        if constexpr (SCALE_BF16) {
-                            fa = __uint_as_float(q & 1 ? fs_a[q >> 1] & 0xFFFF0000u : fs_a[q >> 1] << 16);
-                            fb = __uint_as_float(q & 1 ? fs_b[q >> 1] & 0xFFFF0000u : fs_b[q >> 1] << 16);
-                        } else {
-                            const __half2 ha = *reinterpret_cast<const __half2*>(&fs_a[q >> 1]);
-                            const __half2 hb = *reinterpret_cast<const __half2*>(&fs_b[q >> 1]);
-                            fa = q & 1 ? __high2float(ha) : __low2float(ha);
-                            fb = q & 1 ? __high2float(hb) : __low2float(hb);
-                        }
-                        // -z * 2^-24, exactly: 2^23 + z as a float's bits, times -2^-24, plus 1/2
-                        const float za = fmaf(__uint_as_float(__byte_perm(z_a[q >> 2], 0x4B000000u, 0x7650u | (q & 3))), -0x1p-24f, 0.5f);
-                        const float zb = fmaf(__uint_as_float(__byte_perm(z_b[q >> 2], 0x4B000000u, 0x7650u | (q & 3))), -0x1p-24f, 0.5f);
 #pragma unroll
                         for (int n = 0; n < NA; ++n) {
                             const uint32_t xa = sk + (uint32_t)((q * kCols + 8 * n) * 4);
-                            if constexpr (kKind == 0) {
-                                const float xs1 = __uint_as_float(lds4(xa));
-                                acc[0][0] = fmaf(fa, fmaf(za, xs1, part[0][0]), acc[0][0]);
-                                acc[0][2] = fmaf(fb, fmaf(zb, xs1, part[0][2]), acc[0][2]);
-                            } else {
-                                const uint2 xw = lds8(xa);
-                                const float x0 = __uint_as_float(xw.x), x1 = __uint_as_float(xw.y);
-                                acc[n][0] = fmaf(fa, fmaf(za, x0, part[n][0]), acc[n][0]);
-                                acc[n][1] = fmaf(fa, fmaf(za, x1, part[n][1]), acc[n][1]);
-                                acc[n][2] = fmaf(fb, fmaf(zb, x0, part[n][2]), acc[n][2]);
-                                acc[n][3] = fmaf(fb, fmaf(zb, x1, part[n][3]), acc[n][3]);
-                            }
+                            uint2 xw;
+                            if constexpr (kKind == 0) xw.x = xw.y = lds4(xa);
+                            else xw = lds8(xa);
+                            const float x0 = __uint_as_float(xw.x), x1 = __uint_as_float(xw.y);
+#pragma unroll
+                            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t sw = fs[j][h][q >> 1];
+                                    float f;
+                                    if constexpr (SCALE_BF16) {
+                                        f = __uint_as_float(q & 1 ? sw & 0xFFFF0000u : sw << 16);
+                                    } else {
+                                        const __half2 hw = *reinterpret_cast<const __half2*>(&sw);
+                                        f = q & 1 ? __high2float(hw) : __low2float(hw);
+                                    }
+                                    // -z * 2^-24, exactly: 2^23 + z as a float's bits, times -2^-24, plus 1/2
+                                    const float z = fmaf(__uint_as_float(__byte_perm(fz[j][h][q >> 2], 0x4B000000u, 0x7650u | (q & 3))),
+                                                         -0x1p-24f, 0.5f);
+                                    float p0 = part[j][n][2 * h], p1 = part[j][n][2 * h + 1];
+                                    if constexpr (kWords > 1) {
+                                        p0 += high[j][n][2 * h];
+                                        p1 += high[j][n][2 * h + 1];
+                                    }
+                                    acc[j][n][2 * h] = fmaf(f, fmaf(z, x0, p0), acc[j][n][2 * h]);
+                                    if constexpr (kKind != 0) acc[j][n][2 * h + 1] = fmaf(f, fmaf(z, x1, p1), acc[j][n][2 * h + 1]);
+                                }
                         }
                     };
                     auto groups = [&](auto kind) {
@@ -510,29 +508,31 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     if (++s == kStages) { s = 0; ph ^= 1; }
                 }
                 // join the two sets of stages: one gives its sums (two buffers, so one barrier a unit)
-                float* mine = join + turn * 4 * NT * 32 * kRowWarps + 32 * rw + lane;
+                float* sums_of = join + turn * kJoin + 32 * rw + lane;
                 if (kh == 1)
 #pragma unroll
-                    for (int i = 0; i < 4 * NT; ++i) mine[i * 32 * kRowWarps] = acc[i >> 2][i & 3];
+                    for (int i = 0; i < kTiles * 4 * NT; ++i) sums_of[i * 32 * kRowWarps] = acc[i / (4 * NT)][(i >> 2) % NT][i & 3];
                 computing_sync();
                 if (kh == 1 || *abort_flag) continue;
 #pragma unroll
-                for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += mine[i * 32 * kRowWarps];
+                for (int i = 0; i < kTiles * 4 * NT; ++i) acc[i / (4 * NT)][(i >> 2) % NT][i & 3] += sums_of[i * 32 * kRowWarps];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = 8 * n + 2 * t + i;
-                        if (c >= nc) continue;
-                        const float v0 = acc[n][i] * 0x1p24f * unscale[c], v1 = acc[n][2 + i] * 0x1p24f * unscale[c];
-                        const int64_t at = (int64_t)(lo + base + c) * a.y_stride + b * kUnit;
-                        if constexpr (UP) {
-                            if (b * kUnit + ya < a.N) store_y(a.y, a.y_type, at + ya, v0 / (1.0f + expf(-v0)) * v1);
-                        } else {
-                            if (b * kUnit + ya < a.N) store_y(a.y, a.y_type, at + ya, v0);
-                            if (b * kUnit + yb < a.N) store_y(a.y, a.y_type, at + yb, v1);
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = 8 * n + 2 * t + i, ya = b * kUnit + ra[j];
+                            if (c >= nc) continue;
+                            const float v0 = acc[j][n][i] * 0x1p24f * unscale[c], v1 = acc[j][n][2 + i] * 0x1p24f * unscale[c];
+                            const int64_t at = (int64_t)(lo + base + c) * a.y_stride + ya;
+                            if constexpr (UP) {
+                                if (ya < a.N) store_y(a.y, a.y_type, at, v0 / (1.0f + expf(-v0)) * v1);
+                            } else {
+                                if (ya < a.N) store_y(a.y, a.y_type, at, v0);
+                                if (ya + 8 < a.N) store_y(a.y, a.y_type, at + 8, v1);
+                            }
                         }
-                    }
             }
         }
     }
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 
 template <int G, bool UP, int NT>
 size_t fixed_bytes(const RowsArgs& a, int n_ks) {
-    return 1024 + (size_t)kStages * (kStageBytes + stage_scales<G>()) + (size_t)n_ks * (kStageK / G) * 8 * NT * 4 + 8 * NT * 4 + 2 * 4 * NT * 32 * kRowWarps * 4 +
+    return 1024 + (size_t)kStages * (kStageBytes + stage_scales<G>()) + (size_t)n_ks * (kStageK / G) * 8 * NT * 4 + 8 * NT * 4 + 2 * kTiles * 4 * NT * 32 * kRowWarps * 4 +
            kWarps * 4 + (2 * kStages + 2) * 8 + 80 +
            (size_t)(a.E + 1) * 4 + (size_t)a.E * 2;
 }
