@@ -65,6 +65,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
+// 16 bytes where `on` holds, else v stays as it was.
+__device__ __forceinline__ void lds16_if(uint4& v, uint32_t a, bool on) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n}\n"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "r"(a), "r"((uint32_t)on));
+}
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -169,9 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
         if (has) expert[base + __popc(m & ((1u << lane) - 1u))] = (uint16_t)e;
         __syncthreads();
     }
-    // this CTA's units (at most 2^10 experts x 2^14 blocks, x 152 CTAs: 32 bits hold the products)
+    // this CTA's units: an even share (at most 2^10 experts x 2^14 blocks in all)
     const uint32_t n_blk = (uint32_t)(a.N + kUnit - 1) / kUnit, units = n_active * n_blk;
-    const uint32_t u0 = (uint32_t)((uint64_t)units * blockIdx.x / gridDim.x), u1 = (uint32_t)((uint64_t)units * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t share = units / gridDim.x, more = units - share * gridDim.x;
+    const uint32_t u0 = share * blockIdx.x + min(blockIdx.x, more), u1 = u0 + share + (blockIdx.x < more ? 1 : 0);
 
     // Bounded wait; after a wait has run out every wait returns at once and the loops run to their
     // ends without waiting, loading or storing, so that the CTA's barriers stay matched.
@@ -305,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     for (int h = 0; h < kHold; ++h) held[h] = load(i + h * step);
 #pragma unroll
                     for (int h = 0; h < kHold; ++h) {
+                        if (i + h * step - 8 * lane >= a.K) break;           // (the same for the whole warp)
                         float v[8];
                         values(held[h], v);
 #pragma unroll
@@ -361,21 +369,24 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
             // ======================= products =======================
             const int rw = warp % kRowWarps, kh = warp / kRowWarps, nt = (nc + 7) / 8;
             const uint32_t xs0 = su32(xs) + t * (G / 2);   // (t * G / 4 elements)
-            uint32_t xc[NT];                             // (columns past the last repeat it: their sums are not stored)
+            uint32_t xc[NT];                             // this lane's rows of x (columns without one are not read: their
+            bool has[NT];                                // sums are not stored)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) xc[n] = xs0 + (uint32_t)(min(8 * n + g, nc - 1) * p.x_stride);
-            const uint32_t sums0 = su32(sums) + (uint32_t)(2 * t * 4);
-            // tile j of this warp: the rows of W (and W_up) 16 (8) apart that lie at rows ra[j], rb[j] of the stage
-            int ra[kTiles], rb[kTiles];
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
-                const int tile = kTiles * rw + j;
-                ra[j] = UP ? 8 * tile + g : 16 * tile + g;
-                rb[j] = UP ? 64 + ra[j] : ra[j] + 8;
+            for (int n = 0; n < NT; ++n) {
+                has[n] = 8 * n + g < nc;
+                xc[n] = xs0 + (uint32_t)(min(8 * n + g, nc - 1) * p.x_stride);
             }
+            const uint32_t sums0 = su32(sums) + (uint32_t)(2 * t * 4);
+            // Lane g's row of eight: the lanes whose reads go out together (8 lanes of 16 bytes, 16 of 8, 32 of 4) need
+            // rows whose swizzles keep them in different banks: two rows that differ in bit 2, four in bits 1 and 2.
+            const int gr = G == 128 ? (g & 1) << 2 | g >> 1 : G == 64 ? (g & 3) << 1 | g >> 2 : g;
+            // tile j of this warp: the row of W at ra[j] of the stage, and that of W_up (or the one 8 further)
+            int ra[kTiles];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) ra[j] = (UP ? 8 : 16) * (kTiles * rw + j) + gr;
             // this lane's 16 (8, 4) bytes of a row's group q lie at (this address) xor (q * G / 2): the swizzle
-            // exchanges 16-byte chunks by the row's last three bits, which are g
-            const uint32_t ring0 = su32(ring_base) + ra[0] * 128 + (((t * (G / 8)) >> 4 ^ g) << 4) + ((t * (G / 8)) & 15);
+            // exchanges 16-byte chunks by the row's last three bits, which are gr
+            const uint32_t ring0 = su32(ring_base) + ra[0] * 128 + (((t * (G / 8)) >> 4 ^ gr) << 4) + ((t * (G / 8)) & 15);
             const uint32_t scales0 = su32(scales) + ra[0] * scale_bytes<G>();
             const uint32_t zeros0 = su32(scales) + 128 * scale_bytes<G>() + ra[0] * zero_bytes<G>();
             constexpr int kTileStep = UP ? 8 : 16, kHalfStep = UP ? 64 : 8;       // rows between tiles and halves
@@ -424,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     // one group of the stage.  kind: 0 for a single row of x, else column tiles
                     auto group = [&](int q, auto kind) {
                         constexpr int kKind = decltype(kind)::value, NA = kKind == 0 ? 1 : kKind, kWords = G / 32;
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
                         // this lane's quarter of the group's codes, of every row
                         uint32_t v[kTiles][2][kWords];
 #pragma unroll
@@ -437,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                         for (int w = 0; w < kWords; ++w)
 #pragma unroll
                             for (int n = 0; n < NA; ++n) {
-                                const uint4 x = lds16(xc[n] + xk + 2 * (q * G + 8 * w));
+                                lds16_if(x, xc[n] + xk + 2 * (q * G + 8 * w), has[n]);
 #pragma unroll
                                 for (int j = 0; j < kTiles; ++j) {
                                     const uint32_t va = v[j][0][w], vb = v[j][1][w], a8 = va >> 8, b8 = vb >> 8;
