@@ -34,7 +34,7 @@ namespace {
 constexpr int kStages = 6, kStepK = 64, kMaxN = 256;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;              // (a warp reads the TMEM lanes 32 (warp % 4)..)
-constexpr int kGatherWarps = kStages;                    // warps 2, 3, 12..15: one for each stage of the ring
+constexpr int kGatherWarps = 4;                          // warps 2, 3, 12, 13
 constexpr int kThreads = 32 * (2 + kEpiWarps + kGatherWarps);
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
@@ -43,8 +43,7 @@ constexpr int kSpins = 64;                               // tests of a barrier b
 struct DenseParams {
     CUtensorMap tw0, tw1;        // W, W_up: [E][rows][cols], boxes of 64 x 64
     CUtensorMap tx[4];           // x rows in place: boxes of 64 x 16, 32, 64, 128
-    const uint16_t* x;           // x rows for the gather
-    int64_t x_stride;
+    CUtensorMap tg;              // x rows for the gathers: boxes of 64 x 1
     const int32_t* sorted_pairs; // NULL: rows in place
     const int32_t* offsets;      // NULL: one expert over all P rows
     int E, k, P, N, K;
@@ -137,6 +136,13 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
         "[%4];" ::"r"(dst),
         "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, int x, int r0, int r1, int r2, int r3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -324,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     uint64_t* never = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [7] last step + 1 that warp 0 / each gathering warp arrived for
+    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [5] steps that warp 0 / each gathering warp has arrived for
     int* scan = reinterpret_cast<int*>(tmem_slot + 10);  // [16]
     int* totals = scan + 16;                             // [2] experts of several blocks, experts with rows
     int* off = totals + 2;                               // [E + 1]
@@ -334,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t cta = cta_rank();
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 4 : 2); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 2 + 2 * kGatherWarps : 2); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kEpiWarps); }
         mbar_init(drain, 1);
         mbar_init(never, 1);
@@ -510,70 +516,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     } else if (warp < kEpiWarp0 || warp >= kEpiWarp0 + kEpiWarps) {
         // ======================= gathered rows of x =======================
         if (p.sorted_pairs) {
-            // warp w fills stage w: lane u copies chunk u % 8 of rows u / 8 + 4 j of a step into the
-            // swizzled layout and waits for them; the other warps' steps overlap that
-            const int w = warp < kEpiWarp0 ? warp - 2 : warp - kEpiWarps - 2, ch = lane & 7, r0 = lane >> 3;
-            const uint32_t full0 = in_leader(su32(full));
-            const uint32_t d0 = su32(smem) + kABytes + swz(r0, ch), d1 = su32(smem) + kABytes + swz(r0 + 4, ch);
+            // warp w brings rows 32 w .. of a step, four to a copy
+            const int w = warp < kEpiWarp0 ? warp - 2 : warp - kEpiWarps - 2;
+            const uint32_t full0 = in_leader(su32(full)), dst0 = su32(smem) + kABytes + w * 4096;
             int g = 0;
             Ring ring;
             bool ok = true;
             Tile ti;
-            int pair[4];
-            auto pairs_of = [&](int t) {
+            int pair = 0;                                // of row 32 w + lane, read a tile ahead
+            auto pair_of = [&](int t) {
                 Tile n;
                 const bool any = order.at(t, n);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = lane + 32 * i, c = (int)cta * n.nh + r;
-                    pair[i] = any && r < n.nh && c < n.ntok ? __ldg(p.sorted_pairs + n.tok0 + c) : 0;
-                }
+                const int r = 32 * w + lane, c = (int)cta * n.nh + r;
+                pair = any && r < n.nh && c < n.ntok ? __ldg(p.sorted_pairs + n.tok0 + c) : 0;
             };
-            pairs_of(first);
+            pair_of(first);
             for (int t = first; ok && order.at(t, ti); t += n_pairs) {
-                const int c0 = (int)cta * ti.nh, nc = min(ti.nh, ti.ntok - c0);   // columns of this CTA that hold rows
-                // lane u has read the pairs of columns u, u + 32, .. (before the tile before this one ended)
-                uint32_t at[4];
+                const bool in = (uint32_t)pair < (uint32_t)p.P;
+                bad |= !in;
+                const int row = in ? pair / p.k : 0;
+                int r[32];                               // (the same on every lane)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = (uint32_t)pair[i] < (uint32_t)p.P;
-                    bad |= !in;
-                    at[i] = in ? (uint32_t)(pair[i] / p.k) * (uint32_t)(p.x_stride >> 3) : 0u;
-                }
-                uint32_t row[32];                        // where the rows start, in 16 bytes
-#pragma unroll
-                for (int j = 0; j < 32; ++j) row[j] = __shfl_sync(0xffffffffu, at[j >> 3], (r0 + 4 * j) & 31);
-                pairs_of(t + n_pairs);
-                const int nj = nc > r0 ? (nc - r0 + 3) >> 2 : 0;     // rows of this lane
-                for (int kb = 0; kb < nk; ++kb, ++g, ring.next()) {
-                    if (ring.s != w) continue;
+                for (int i = 0; i < 32; ++i) r[i] = __shfl_sync(0xffffffffu, row, i);
+                pair_of(t + n_pairs);
+                const int mine = uniform(min(max(ti.nh - 32 * w, 0), 32));   // rows: 0, 16 or 32
+                for (int c = 0; c < nk * kStepK; c += kStepK, ++g, ring.next()) {
                     if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
-                    const int c = kb * kStepK + 8 * ch;
-                    const uint32_t bytes = (uint32_t)min(max(2 * (p.K - c), 0), 16);   // zeros past the row's end
-                    const uint16_t* src = p.x + (bytes ? c : 0);
-                    const uint32_t so = ring.s * kStageBytes;
-                    auto copy = [&](int j) {
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((j & 1 ? d1 : d0) + so + (j >> 1) * 1024),
-                                     "l"(src + 8 * (uint64_t)row[j]), "r"(bytes)
-                                     : "memory");
-                    };
-                    if (nj == 32) {
+                    const uint32_t bar = full0 + 8 * ring.s, dst = dst0 + ring.s * kStageBytes;
+                    if (elect_one()) {
+                        arrive_tx_cluster(bar, mine * 128);
+                        if (mine >= 16) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) copy(j);
-                    } else {
+                            for (int i = 0; i < 16; i += 4) tma_gather4(dst + i * 128, &p.tg, c, r[i], r[i + 1], r[i + 2], r[i + 3], bar);
+                        }
+                        if (mine == 32) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < nj) copy(j);
+                            for (int i = 16; i < 32; i += 4) tma_gather4(dst + i * 128, &p.tg, c, r[i], r[i + 1], r[i + 2], r[i + 3], bar);
+                        }
                     }
-                    cp_wait_all();
-                    fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        arrive_cluster(full0 + 8 * ring.s);
-                        done[1 + w] = g + 1;
-                    }
                 }
             }
+            if (lane == 0) done[1 + w] = g;
         }
     } else {
         // ======================= epilogue =======================
@@ -604,7 +588,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             for (int s = max(0, last - kStages); s < last; ++s)
                 for (int c = 0; c < 2; ++c) {
                     if (of[c][0] <= s) mbar_arrive(&full[s % kStages]);
-                    if (p.sorted_pairs && of[c][1 + s % kStages] <= s) mbar_arrive(&full[s % kStages]);
+                    for (int i = 1; p.sorted_pairs && i <= kGatherWarps; ++i)
+                        if (of[c][i] <= s) mbar_arrive(&full[s % kStages]);
                 }
             for (int s = max(0, last - kStages); s < last; ++s) drain_wait(&full[s % kStages], (s / kStages) & 1, p.wait_ns);
             if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
@@ -630,17 +615,18 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     const cuuint64_t wd[3] = {cols, rows, (cuuint64_t)a.E};
     const cuuint64_t ws[2] = {(cuuint64_t)a.row_stride * 2, a.E > 1 ? (cuuint64_t)a.expert_stride * 2
                                                                     : (cuuint64_t)a.row_stride * rows * 2};
-    const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.P, 1};
+    const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)(a.sorted_pairs ? a.P / a.k : a.P), 1};
     const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
     const CUtensorMapDataType type = a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (!encode_map(&p.tw0, type, 3, a.w0, wd, ws, 64, a.in_out || a.w1 ? 64 : 128) ||
         (a.w1 && !encode_map(&p.tw1, type, 3, a.w1, wd, ws, 64, 64)))
         return cudaErrorInvalidValue;
-    if (!a.sorted_pairs)
+    if (a.sorted_pairs) {
+        if (!encode_map(&p.tg, type, 2, a.x, xd, xs, 64, 1)) return cudaErrorInvalidValue;
+    } else {
         for (int i = 0; i < 4; ++i)
             if (!encode_map(&p.tx[i], type, 2, a.x, xd, xs, 64, 16 << i)) return cudaErrorInvalidValue;
-    p.x = static_cast<const uint16_t*>(a.x);
-    p.x_stride = a.x_stride;
+    }
     p.sorted_pairs = a.sorted_pairs; p.offsets = a.offsets;
     p.E = a.E; p.k = a.k; p.P = a.P; p.N = a.N; p.K = a.K;
     p.bf16 = a.bf16;
