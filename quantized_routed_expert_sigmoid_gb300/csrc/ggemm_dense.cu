@@ -61,9 +61,13 @@ __device__ __forceinline__ uint32_t cta_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
 // The pair's barriers order copies and MMAs, which carry their own ordering; no plain loads or stores
 // pass from CTA to CTA through them.  So their operations take the default scope: with release and
 // acquire at cluster scope every step of the pipeline waited about 0.5 us for its arrival.
@@ -268,29 +272,52 @@ __device__ __forceinline__ void epilogue(const DenseParams& p, const Order& orde
         if constexpr (UP) {
             const int row = ti.mb * kRowsTile + cta * 64 + (q & 1) * 32 + lane;
             const bool is_up = q >= 2;
-            // the W warp keeps columns 0..7 of 16 and gives 8..15, the W_up warp the other way round
+            // Of 16 columns the W warp keeps 0..7 and gives 8..15, the W_up warp the other way round.  The next
+            // 16 are read and given before these are computed, so that their latencies overlap.
             float* const buf = exch + (pairbar - 1) * 1024 + lane;
             T* y = static_cast<T*>(p.y) + (int64_t)(ti.tok0 + 16 * side + (is_up ? 8 : 0)) * p.y_stride + row;
-            for (int c0 = 16 * side; c0 < ti.ntok; c0 += 32, ++turn, y += 32 * p.y_stride) {
-                uint32_t r[16];
-                tmem_ld16(acc + c0, r);
-                tmem_ld_wait();
+            float keep[8], next[8];
+            auto give = [&](const uint32_t (&r)[16], float (&kept)[8]) {
                 float* mine = buf + (turn & 1) * 512 + (is_up ? 256 : 0);
-                const float* theirs = buf + (turn & 1) * 512 + (is_up ? 0 : 256);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mine[i * 32] = __uint_as_float(is_up ? r[i] : r[8 + i]);
+                for (int i = 0; i < 8; ++i) {
+                    mine[i * 32] = __uint_as_float(is_up ? r[i] : r[8 + i]);
+                    kept[i] = __uint_as_float(is_up ? r[8 + i] : r[i]);
+                }
+                ++turn;
+            };
+            uint32_t r[16];
+            if (16 * side < ti.ntok) {
+                tmem_ld16(acc + 16 * side, r);
+                tmem_ld_wait();
+                give(r, keep);
+            }
+            for (int c0 = 16 * side; c0 < ti.ntok; c0 += 32, y += 32 * p.y_stride) {
+                const bool more = c0 + 32 < ti.ntok;
+                if (more) tmem_ld16(acc + c0 + 32, r);
                 named_sync(pairbar, 64);
+                const float* theirs = buf + ((turn - 1) & 1) * 512 + (is_up ? 0 : 256);
+                float other[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) other[i] = theirs[i * 32];
+                if (more) {
+                    // (the other buffer: its last reader has passed the barrier above)
+                    tmem_ld_wait();
+                    give(r, next);
+                }
                 const int n = row < p.N ? ti.ntok - c0 - (is_up ? 8 : 0) : 0;
                 T* at = y;
 #pragma unroll
                 for (int i = 0; i < 8; ++i, at += p.y_stride) {
-                    const float other = theirs[i * 32];
-                    const float gv = is_up ? other : __uint_as_float(r[i]);
-                    const float uv = is_up ? __uint_as_float(r[8 + i]) : other;
-                    // (the approximate division is off by at most two units; its 0 for a divisor above
-                    // 2^126 is what the exact one rounds to)
-                    if (i < n) *at = to_out<T>(__fdividef(gv, 1.0f + expf(-gv)) * uv);
+                    const float gv = is_up ? other[i] : keep[i], uv = is_up ? keep[i] : other[i];
+                    // (the approximate division is off by at most two units; its 0 for a divisor above 2^126
+                    // is what the exact one rounds to.  __expf is off by 2^-21 at most for the |g| whose
+                    // exponential matters beside 1, far below a 16-bit output's half step)
+                    const float ex = sizeof(T) == 2 ? __expf(-gv) : expf(-gv);
+                    if (i < n) *at = to_out<T>(__fdividef(gv, 1.0f + ex) * uv);
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) keep[i] = next[i];
             }
         } else {
             const int row = ti.mb * kRowsTile + cta * 128 + q * 32 + lane;
@@ -347,12 +374,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         *abort_flag = 0;
         for (int i = 0; i <= kGatherWarps; ++i) done[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tw0);
+        if (UP) prefetch_map(&p.tw1);
+        if (p.sorted_pairs) prefetch_map(&p.tg);
+        else
+            for (int i = 0; i < 4; ++i) prefetch_map(&p.tx[i]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "n"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    __syncwarp();
+    cluster_arrive();                                    // (barriers and TMEM are ready; waited for below)
     // ---- the order of the tiles, from the offsets (clamped into 0..P and into order)
     bool bad = false;
     for (int i = tid; i <= p.E; i += kThreads) {
@@ -360,73 +394,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         bad |= o < 0 || o > p.P || (i > 0 && p.offsets && __ldg(p.offsets + i - 1) > o);
         off[i] = min(max(o, 0), p.P);
     }
+    bool big = false;
     __syncthreads();
-    // experts sorted by bucket, stably (every CTA finds the same order): counts per 32 experts and
-    // bucket, their running sums over the buckets, ranks
-    int* hist = reinterpret_cast<int*>(exch);            // [E / 32][kBuckets], before its use by the epilogue
+    for (int i = tid; i < p.E; i += kThreads) big |= off[i + 1] - off[i] > kMaxN;
+    big = __syncthreads_or(big);
+    int* hist = reinterpret_cast<int*>(exch);            // (before its use by the epilogue)
     const int n_chunks = (p.E + 31) / 32;
-    for (int c = warp; c < n_chunks; c += kThreads / 32) {
-        const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
-        if (lane < kBuckets) hist[c * kBuckets + lane] = 0;
-        __syncwarp();
-        const unsigned same = __match_any_sync(0xffffffffu, k);
-        if (k < kBuckets && (same & ((1u << lane) - 1u)) == 0) hist[c * kBuckets + k] = __popc(same);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int sum = 0;
-        if (lane < kBuckets)
-            for (int c = 0; c < n_chunks; ++c) {
-                const int n = hist[c * kBuckets + lane];
-                hist[c * kBuckets + lane] = sum;
-                sum += n;
-            }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
+    if (!big) {
+        // one block an expert at most: those with rows, as they come (the sort below takes 1.5 us more, and
+        // only pays where many tiles of different cost follow one another)
+        for (int c = warp; c < n_chunks; c += kThreads / 32) {
+            const int e = 32 * c + lane;
+            const unsigned m = __ballot_sync(0xffffffffu, e < p.E && off[e + 1] > off[e]);
+            if (lane == 0) hist[c] = __popc(m);
         }
-        if (lane == 7) totals[0] = inc;
-        if (lane == 31) totals[1] = inc;
-        if (lane < kBuckets) scan[lane] = inc - sum;     // first place of the bucket
-    }
-    __syncthreads();
-    for (int c = warp; c < n_chunks; c += kThreads / 32) {
-        const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
-        const unsigned same = __match_any_sync(0xffffffffu, k);
-        if (k < kBuckets) expert[scan[k] + hist[c * kBuckets + k] + __popc(same & ((1u << lane) - 1u))] = (uint16_t)e;
-    }
-    __syncthreads();
-    const int n_big = totals[0];
-    {
-        // thread t: places t * per .. of a scan of the block counts over the whole CTA
-        const int per = (n_big + kThreads - 1) / kThreads, i0 = tid * per;
-        auto blocks_at = [&](int i) { return blocks_of(off[expert[i] + 1] - off[expert[i]]); };
-        int sum = 0;
-        for (int i = i0; i < min(i0 + per, n_big); ++i) sum += blocks_at(i);
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) scan[warp] = inc;
         __syncthreads();
-        int base = inc - sum;
-        for (int w = 0; w < warp; ++w) base += scan[w];
-        for (int i = i0; i < min(i0 + per, n_big); ++i) {
-            tb0[i] = base;
-            base += blocks_at(i);
+        int inc = lane < n_chunks ? hist[lane] : 0;
+        const int own = inc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
         }
-        if (tid == kThreads - 1) tb0[n_big] = base;
+        for (int c = warp; c < n_chunks; c += kThreads / 32) {
+            const int e = 32 * c + lane, base = __shfl_sync(0xffffffffu, inc - own, c);
+            const bool has = e < p.E && off[e + 1] > off[e];
+            const unsigned m = __ballot_sync(0xffffffffu, has);
+            if (has) expert[base + __popc(m & ((1u << lane) - 1u))] = (uint16_t)e;
+        }
+        if (tid == 0) { totals[0] = 0; tb0[0] = 0; }
+        if (tid == 31) totals[1] = inc;
+    } else {
+        // experts sorted by bucket, stably (every CTA finds the same order): counts per 32 experts and
+        // bucket, their running sums over the buckets, ranks
+        for (int c = warp; c < n_chunks; c += kThreads / 32) {
+            const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
+            if (lane < kBuckets) hist[c * kBuckets + lane] = 0;
+            __syncwarp();
+            const unsigned same = __match_any_sync(0xffffffffu, k);
+            if (k < kBuckets && (same & ((1u << lane) - 1u)) == 0) hist[c * kBuckets + k] = __popc(same);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int sum = 0;
+            if (lane < kBuckets)
+                for (int c = 0; c < n_chunks; ++c) {
+                    const int n = hist[c * kBuckets + lane];
+                    hist[c * kBuckets + lane] = sum;
+                    sum += n;
+                }
+            int inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 7) totals[0] = inc;
+            if (lane == 31) totals[1] = inc;
+            if (lane < kBuckets) scan[lane] = inc - sum;     // first place of the bucket
+        }
+        __syncthreads();
+        for (int c = warp; c < n_chunks; c += kThreads / 32) {
+            const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
+            const unsigned same = __match_any_sync(0xffffffffu, k);
+            if (k < kBuckets) expert[scan[k] + hist[c * kBuckets + k] + __popc(same & ((1u << lane) - 1u))] = (uint16_t)e;
+        }
+        __syncthreads();
+        const int n_big = totals[0];
+        {
+            // thread t: places t * per .. of a scan of the block counts over the whole CTA
+            const int per = (n_big + kThreads - 1) / kThreads, i0 = tid * per;
+            auto blocks_at = [&](int i) { return blocks_of(off[expert[i] + 1] - off[expert[i]]); };
+            int sum = 0;
+            for (int i = i0; i < min(i0 + per, n_big); ++i) sum += blocks_at(i);
+            int inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            int base = inc - sum;
+            for (int w = 0; w < warp; ++w) base += scan[w];
+            for (int i = i0; i < min(i0 + per, n_big); ++i) {
+                tb0[i] = base;
+                base += blocks_at(i);
+            }
+            if (tid == kThreads - 1) tb0[n_big] = base;
+        }
     }
     tc_before();
     __syncthreads();
-    cluster_sync();
+    cluster_wait();
     tc_after();
     const uint32_t tmem = *tmem_slot;
     constexpr int kRowsTile = UP ? 128 : 256;            // outputs of a tile of the pair
+    const int n_big = totals[0];
     Order order{off, tb0, expert, n_big, tb0[n_big] + totals[1] - n_big, (p.N + kRowsTile - 1) / kRowsTile, 0u};
     if (tb0[n_big] < order.n_blocks)
         order.ratio = (uint32_t)((((uint64_t)tb0[n_big] << 32) + order.n_blocks - 1) / order.n_blocks);
