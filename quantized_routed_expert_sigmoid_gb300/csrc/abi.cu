@@ -319,8 +319,15 @@ moe_status check_product_call(const moe::RowsArgs& a, int T, int k, bool* todo) 
 
 }  // namespace
 
-// Which kernel runs P rows of E experts: see moe_grouped_path.
-static bool grouped_tensor(const moe::RowsArgs& a, int64_t P) { return P > 64; }
+// Which kernel runs T tokens of k experts each: the streaming one while its few columns hold an expert's rows
+// (16) and the start of the tensor-core kernel (about 5 us) shows.  Measured, rows / tensor, hidden 2048,
+// intermediate 768, 128 experts: gated T*k = 8: 11.8 / 15.8 us, 32: 33.4 / 37.2, 64: 56.5 / 57.0; down 64: 38.4 / 30.9; one
+// expert of 2048 x 2048, T = 16: 7.3 / 11.3, 64: 21.1 / 11.5.  [in][out] weights, which the streaming kernel
+// reads in narrower strips: gated T*k = 8: 20.2 / 15.6.
+static bool grouped_tensor(const moe::RowsArgs& a, int T, int k) {
+    const int64_t P = (int64_t)T * k;
+    return a.in_out ? P >= 8 : P > 32 || T > 16;
+}
 
 struct moe_grouped_plan {
     moe::RowsArgs a;             // the weights' side; a call fills in its own
@@ -600,7 +607,7 @@ moe_status moe_grouped_plan_destroy(moe_grouped_plan* plan) {
 moe_status moe_grouped_path(const moe_grouped_plan* plan, int T, int k, int* path) {
     if (!plan || !path) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
     if (T < 1 || k < 1) return fail(MOE_ERR_INVALID_ARG, "T = %d, k = %d", T, k);
-    *path = grouped_tensor(plan->a, (int64_t)T * k) ? MOE_GROUPED_TENSOR : MOE_GROUPED_ROWS;
+    *path = grouped_tensor(plan->a, T, k) ? MOE_GROUPED_TENSOR : MOE_GROUPED_ROWS;
     return MOE_OK;
 }
 
@@ -618,7 +625,7 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
     if (sorted_pairs && (int64_t)T * x_stride > (int64_t)1 << 35)
         return fail(MOE_ERR_INVALID_ARG, "T * x_stride above 2^35 elements with gathered rows");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t err = grouped_tensor(a, a.P) ? launch_grouped_dense(a, s) : launch_rows(a, s);
+    cudaError_t err = grouped_tensor(a, T, k) ? launch_grouped_dense(a, s) : launch_rows(a, s);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product kernel");
     return MOE_OK;
 }

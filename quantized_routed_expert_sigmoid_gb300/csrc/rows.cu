@@ -284,31 +284,22 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
     rows_kernel<W, NT><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
-template <bool BF16, bool UP, int NT>
-cudaError_t launch_w(const RowsArgs& a, cudaStream_t s) {
-    if (a.in_out) {
-        // (gated [in][out] tiles hold 32 accumulators a column tile: two of them at most)
-        constexpr int M = NT > 2 ? 2 : NT;
-        return launch<InOut<BF16, UP, M>, M>(a, s);
-    }
-    return launch<OutIn<BF16, UP, NT>, NT>(a, s);
-}
 template <bool BF16, bool UP>
-cudaError_t launch_nt(const RowsArgs& a, cudaStream_t s) {
-    // columns held at once: what an expert can have at most, up to 32 (a token asks for an expert
-    // once, so T rows; more rows than that are taken in passes)
+cudaError_t launch_w(const RowsArgs& a, cudaStream_t s) {
+    // columns held at once: what an expert can have at most (a token asks for an expert once, so T rows;
+    // more than the columns are taken in passes).  [in][out] weights come here with less than 8 rows in all.
     const int most = a.offsets ? a.P / a.k : a.P;
-    if (most <= 8) return launch_w<BF16, UP, 1>(a, s);
-    if (most <= 16) return launch_w<BF16, UP, 2>(a, s);
-    return launch_w<BF16, UP, 4>(a, s);
+    if (a.in_out) return launch<InOut<BF16, UP, 1>, 1>(a, s);
+    if (most <= 8) return launch<OutIn<BF16, UP, 1>, 1>(a, s);
+    return launch<OutIn<BF16, UP, 2>, 2>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
     if (a.P <= 0) return cudaSuccess;
-    if (a.bf16) return a.w1 ? launch_nt<true, true>(a, s) : launch_nt<true, false>(a, s);
-    return a.w1 ? launch_nt<false, true>(a, s) : launch_nt<false, false>(a, s);
+    if (a.bf16) return a.w1 ? launch_w<true, true>(a, s) : launch_w<true, false>(a, s);
+    return a.w1 ? launch_w<false, true>(a, s) : launch_w<false, false>(a, s);
 }
 
 }  // namespace moe
