@@ -10,8 +10,8 @@
 //   and as many CTAs as fit, each taking every (CTAs)-th row.  What bounds a row is latency (read, mean,
 //   mean, write), so every thread copies its own elements of the next rows into shared memory (cp.async,
 //   DEPTH rows ahead) while it computes; nothing but its own copies is waited for.
-// - norm_pair_kernel, the others: narrow rows take one warp each (no barrier), others 256 or 1024
-//   threads and a CTA a row.
+// - norm_pair_kernel, the others: narrow rows take one warp each (no barrier), others 128, 256
+//   or 1024 threads.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -30,16 +30,18 @@ __device__ __forceinline__ void store1(void* p, int type, int64_t i, float v) {
     else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
     else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
 }
-// Eight elements from a 16-byte boundary.
+// Eight elements from a 16-byte boundary.  ONCE: they are not read again.
+template <bool ONCE = false>
 __device__ __forceinline__ void load8(const void* p, int type, int64_t i, float (&v)[8]) {
     if (type == MOE_F32) {
         const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-        const float4 a = q[0], b = q[1];
+        const float4 a = ONCE ? __ldcs(q) : q[0], b = ONCE ? __ldcs(q + 1) : q[1];
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         return;
     }
-    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
+    const uint4 w = ONCE ? __ldcs(q) : *q;
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -82,17 +84,19 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
     __shared__ float part[2][kThreads / 32];
     const int tid = threadIdx.x, i0 = tid % TPR, lane = tid & 31;
     const int64_t t = (int64_t)blockIdx.x * (kThreads / TPR) + tid / TPR;
-    if (TPR == 32 && t >= a.T) return;                   // (a warp a row: no barrier below)
+    const bool live = t < a.T;                           // (threads of the last CTA without a row join its barriers)
+    if (TPR == 32 && !live) return;                      // (a warp a row: no barrier below)
+    const int H = live ? a.H : 0;                        // elements that this thread's row has to read and write
     auto first = [&](int c) { return VEC ? (c * TPR + i0) * 8 : c * 8 * TPR + i0; };
     constexpr int kStep = VEC ? 1 : TPR;
 
     auto row_in = [&](const void* p, int type, int64_t stride, int c, float (&v)[8]) {
         if constexpr (VEC) {
-            if (first(c) < a.H) load8(p, type, t * stride + first(c), v);
+            if (first(c) < H) load8<true>(p, type, t * stride + first(c), v);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (first(c) + j * kStep < a.H) v[j] = load1(p, type, t * stride + first(c) + j * kStep);
+                if (first(c) + j * kStep < H) v[j] = load1(p, type, t * stride + first(c) + j * kStep);
         }
     };
     auto vec_in = [&](const float* p, int c, float (&v)[8]) {     // a vector over the channels
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
             for (int j = 0; j < 8; ++j) ss = fmaf(r[c][j], r[c][j], ss);
         inv = inv_rms(ss, 0);
     }
-    const float gt = a.gate && a.gate_col == 0 ? __ldg(a.gate + t * a.gate_row) : 1.0f;
+    const float gt = live && a.gate && a.gate_col == 0 ? __ldg(a.gate + t * a.gate_row) : 1.0f;
     ss = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -156,11 +160,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = 0.f;
             if constexpr (VEC) {
-                if (first(c) < a.H) load8(a.gate, MOE_F32, t * a.gate_row + first(c), f);
+                if (first(c) < H) load8(a.gate, MOE_F32, t * a.gate_row + first(c), f);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (first(c) + j * kStep < a.H) f[j] = __ldg(a.gate + t * a.gate_row + (first(c) + j * kStep) * a.gate_col);
+                    if (first(c) + j * kStep < H) f[j] = __ldg(a.gate + t * a.gate_row + (first(c) + j * kStep) * a.gate_col);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[c][j] *= f[j];
@@ -178,11 +182,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             if constexpr (VEC) {
-                if (first(c) < a.H) store8(a.x_out, a.x_type, t * a.x_out_stride + first(c), r[c]);
+                if (first(c) < H) store8(a.x_out, a.x_type, t * a.x_out_stride + first(c), r[c]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (first(c) + j * kStep < a.H)
+                    if (first(c) + j * kStep < H)
                         store1(a.x_out, a.x_type, t * a.x_out_stride + first(c) + j * kStep, r[c][j]);
             }
         }
@@ -196,11 +200,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = r[c][j] * inv * f[j];
         if constexpr (VEC) {
-            if (first(c) < a.H) store8(a.u, a.u_type, t * a.u_stride + first(c), f);
+            if (first(c) < H) store8(a.u, a.u_type, t * a.u_stride + first(c), f);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (first(c) + j * kStep < a.H) store1(a.u, a.u_type, t * a.u_stride + first(c) + j * kStep, f[j]);
+                if (first(c) + j * kStep < H) store1(a.u, a.u_type, t * a.u_stride + first(c) + j * kStep, f[j]);
         }
     }
 }
@@ -376,6 +380,7 @@ cudaError_t launch_norm_pair(const NormPairArgs& a, cudaStream_t s) {
     if (vec && a.H > 8192 && a.H <= 16384) return launch_stream<1024, 2, 1, 1>(a, s);
     if (a.H <= 256) return launch<32, 1>(a, vec, s);
     if (a.H <= 512) return launch<32, 2>(a, vec, s);
+    if (a.H <= 1024) return launch<128, 1>(a, vec, s);
     if (a.H <= 2048) return launch<256, 1>(a, vec, s);
     if (a.H <= 4096) return launch<256, 2>(a, vec, s);
     if (a.H <= 8192) return launch<1024, 1>(a, vec, s);

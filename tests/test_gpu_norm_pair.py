@@ -59,6 +59,9 @@ _CASES = [
     (19, 256, HF, HF, HF, True, "full", 8),
     (70, 264, BF, BF, BF, True, "channel", 8),
     (9, 512, F32, F32, F32, True, "full", 0),
+    (7, 768, BF, F32, BF, True, "channel", 0),
+    (4, 1024, F32, BF, BF, True, None, 8),
+    (5, 1023, F32, F32, BF, True, "token", 0),
     (33, 1000, F32, BF, BF, True, "token", 3),
     (4, 2047, BF, BF, BF, True, "full", 1),
     (300, 2048, F32, F32, BF, True, None, 0),
