@@ -387,6 +387,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     }
     __syncwarp();
     cluster_arrive();                                    // (barriers and TMEM are ready; waited for below)
+    wait_for_previous();
+    allow_next();
     // ---- the order of the tiles, from the offsets (clamped into 0..P and into order)
     bool bad = false;
     for (int i = tid; i <= p.E; i += kThreads) {
@@ -711,8 +713,7 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     const int64_t most = ((int64_t)a.P / kMaxN + (a.E < a.P ? a.E : a.P)) * n_mb;
     const int pairs = (int)(most < sms / 2 ? most : sms / 2);
     void* args[] = {&p};
-    err = cudaLaunchKernel(fn, dim3(2 * (pairs > 0 ? pairs : 1)), dim3(kThreads), args, smem_bytes(a.E), s);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    return launch_early(fn, dim3(2 * (pairs > 0 ? pairs : 1)), kThreads, smem_bytes(a.E), s, args);
 }
 
 }  // namespace moe

@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
     constexpr int kThreads = TPR > 256 ? TPR : 256, kWarpsRow = TPR / 32;
     __shared__ float part[2][kThreads / 32];
     const int tid = threadIdx.x, i0 = tid % TPR, lane = tid & 31;
+    wait_for_previous();
+    allow_next();
     const int64_t t = (int64_t)blockIdx.x * (kThreads / TPR) + tid / TPR;
     const bool live = t < a.T;                           // (threads of the last CTA without a row join its barriers)
     if (TPR == 32 && !live) return;                      // (a warp a row: no barrier below)
@@ -275,6 +277,8 @@ __global__ void __launch_bounds__(TPR, CTAS) norm_stream_kernel(const __grid_con
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     };
+    wait_for_previous();
+    allow_next();
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) fetch(blockIdx.x + (int64_t)d * gridDim.x, d);
     int s = 0;
@@ -349,17 +353,17 @@ cudaError_t launch_stream(const NormPairArgs& a, cudaStream_t s) {
     cudaError_t err = prepare_kernel(fn, kMost, ready, &sms);
     if (err != cudaSuccess) return err;
     const int per_sm = std::max(1, std::min(CTAS, 220 * 1024 / (row * DEPTH + 1024)));
-    norm_stream_kernel<TPR, NC, CTAS, DEPTH><<<std::min(a.T, sms * per_sm), TPR, (size_t)row * DEPTH, s>>>(a);
-    return cudaGetLastError();
+    void* args[] = {const_cast<NormPairArgs*>(&a)};
+    return launch_early(fn, dim3(std::min(a.T, sms * per_sm)), TPR, (size_t)row * DEPTH, s, args);
 }
 
 template <int TPR, int NC>
 cudaError_t launch(const NormPairArgs& a, bool vec, cudaStream_t s) {
     constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = kThreads / TPR;
     const unsigned grid = (unsigned)((a.T + kRows - 1) / kRows);
-    if (vec) norm_pair_kernel<TPR, NC, true><<<grid, kThreads, 0, s>>>(a);
-    else norm_pair_kernel<TPR, NC, false><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    void* args[] = {const_cast<NormPairArgs*>(&a)};
+    return launch_early(vec ? (const void*)norm_pair_kernel<TPR, NC, true> : (const void*)norm_pair_kernel<TPR, NC, false>,
+                        dim3(grid), kThreads, 0, s, args);
 }
 
 bool rows16(const void* p, int type, int64_t stride) {

@@ -15,6 +15,7 @@
 // of each for [in][out] weights) of one expert; the warps split the sum over c and join in shared
 // memory at the end, in a fixed order.
 #include "internal.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -226,6 +227,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? W::kCtas : 1) rows_kernel(
     __shared__ float red[kWarps][kMats * kFrag][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2;
     int e, lo, cnt;
+    wait_for_previous();
+    allow_next();
     find_expert(a, blockIdx.y, e, lo, cnt);
     if (cnt == 0) return;
     const int r0 = blockIdx.x * W::kRows;
@@ -281,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? W::kCtas : 1) rows_kernel(
 template <class W, int NT>
 cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
     const dim3 grid((a.N + W::kRows - 1) / W::kRows, a.offsets ? min(a.E, a.P) : 1);
-    rows_kernel<W, NT><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    void* args[] = {const_cast<RowsArgs*>(&a)};
+    return launch_early((const void*)rows_kernel<W, NT>, grid, kThreads, 0, s, args);
 }
 template <bool BF16, bool UP>
 cudaError_t launch_w(const RowsArgs& a, cudaStream_t s) {

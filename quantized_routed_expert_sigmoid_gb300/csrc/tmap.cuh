@@ -1,5 +1,6 @@
-// tmap.cuh -- host side of the TMA kernels: the driver's tensor-map encoder, the SM count and
-// the shared-memory attribute of a kernel, each looked up once per process or device.
+// tmap.cuh -- host side of the kernels over dense and 4-bit weights and of the norm pair: the driver's
+// tensor-map encoder, the SM count and the shared-memory attribute of a kernel (each looked up once per
+// process or device), and a launch that may begin while the kernel before it in the stream ends.
 #pragma once
 
 #include <atomic>
@@ -38,6 +39,27 @@ inline bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const
     const cuuint32_t box[3] = {(cuuint32_t)box0, (cuuint32_t)box1, 1u}, one[3] = {1u, 1u, 1u};
     return fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Programmatic dependent launch: a kernel launched by launch_early may be set up while the one before
+// it ends; it calls wait_for_previous before its first access to memory, which returns when that kernel is done and
+// its writes are visible, and allow_next so that its own successor may do the same.  Between two calls in a
+// stream that saves 1 to 2 us.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+inline cudaError_t launch_early(const void* fn, dim3 grid, unsigned threads, size_t smem, cudaStream_t s, void** args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelExC(&cfg, fn, args);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 // SMs of the current device; a kernel's dynamic shared memory is raised to `smem` there, once per

@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    wait_for_previous();
+    allow_next();
     // ---- the experts that have rows
     bool bad = false;
     for (int i = tid; i <= a.E; i += kThreads) {
@@ -599,8 +601,7 @@ cudaError_t launch_as(const RowsArgs& a, cudaStream_t s) {
     const int64_t units = (int64_t)(a.offsets && a.E < a.P ? a.E : a.offsets ? a.P : 1) * ((a.N + kUnit - 1) / kUnit);
     void* args[] = {&p};
     const size_t smem = fixed + (size_t)p.cols * p.x_stride;
-    err = cudaLaunchKernel(fn, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads), args, smem, s);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    return launch_early(fn, dim3((unsigned)(units < sms ? units : sms)), kThreads, smem, s, args);
 }
 
 template <int G, bool UP, int NT>
