@@ -304,7 +304,7 @@ moe_status moe_rmsnorm_bf16(const float* x, const float* gamma, int T, int H, fl
  *   overlap x.  status (device int32, nullable, caller-owned, never cleared by the call) is
  *   raised from MOE_OK to MOE_ERR_DEVICE_CHECK when an offset leaves 0..T*k or decreases (it is
  *   clamped) or a pair leaves 0..T*k-1 (its row of y is undefined), and to MOE_ERR_TIMEOUT when a device-side wait ran out (y is
- *   undefined).  T*k <= 2^30; T * x_stride <= 2^35 with sorted_pairs; T = 0 is a no-op.  Launches one kernel, allocates nothing, needs no
+ *   undefined).  T*k <= 2^30, strides <= 2^32; T = 0 is a no-op.  Launches one kernel, allocates nothing, needs no
  *   workspace, keeps nothing between calls: two calls may overlap on the GPU, and a captured call
  *   replays with the bits of the eager one.
  * Kernels (moe_grouped_path tells which): MOE_GROUPED_ROWS streams the weights of the experts that
@@ -345,7 +345,8 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
  *   at most 32768.
  * A group's products of codes and x are exact and summed in fp32, the zero point is taken off that sum
  * and the scale applied to it in fp32: no weight is rounded.  x is held as fp16 scaled by a power of two
- * of its row's largest magnitude: exact down to 2^-27 of that (a row with an infinity gives infinities or NaN).
+ * of its row's largest magnitude: exact down to 2^-27 of that (a row with an infinity gives infinities or NaN, a row of
+ * nothing but subnormal numbers zeros).
  * For a few rows an expert (decode): an active expert's codes are read once per 8 or 16 of its rows.
  * Arguments, routing, y and status as moe_grouped_matmul; x of x_type MOE_BF16 or MOE_F16.
  * q, q_up 16-byte aligned; scales and zeros aligned to their element.  One launch, no workspace.
@@ -506,11 +507,12 @@ moe_status moe_permute_read_device_status(int T, int k, int E, void* workspace, 
  * moe_debug_set_waits -- test hook for the bounded device-side waits; off by
  * default.  Every wait of the library's kernels on a copy or an MMA gives up
  * after limit_ns nanoseconds (0 restores the default of 2 s), records
- * MOE_ERR_TIMEOUT in the workspace status word, waits (within the same limit)
+ * MOE_ERR_TIMEOUT in the workspace status word (the call's status argument for the grouped and
+ * 4-bit products), waits (within the same limit)
  * for the copies its CTA still has in flight, releases what it holds and
  * returns; the call's outputs are then undefined and moe_read_device_status
  * reports the code.  stall = 1 makes the first wait of the chained decode,
- * segmented GEMV and tensor-core kernels wait on a barrier that nothing
+ * segmented GEMV, tensor-core, grouped and 4-bit kernels wait on a barrier that nothing
  * completes, so that a test can run this path without a faulty input.
  * Applies to calls launched after it, from any host thread (a graph keeps the
  * setting it was captured with).  The failure reporting follows the pages'

@@ -307,8 +307,8 @@ moe_status check_product_call(const moe::RowsArgs& a, int T, int k, bool* todo) 
         return fail(MOE_ERR_INVALID_ARG, "x_stride %lld (need >= %d, a multiple of 8)", (long long)a.x_stride, a.K);
     if (a.y_stride < a.N) return fail(MOE_ERR_INVALID_ARG, "y_stride %lld < n_out %d", (long long)a.y_stride, a.N);
     const int64_t x_rows = a.sorted_pairs ? T : (int64_t)T * k, y_rows = (int64_t)T * k;
-    if (a.x_stride > ((int64_t)1 << 40) || a.y_stride > ((int64_t)1 << 40))
-        return fail(MOE_ERR_INVALID_ARG, "x_stride / y_stride too large");
+    if (a.x_stride > ((int64_t)1 << 32) || a.y_stride > ((int64_t)1 << 32))
+        return fail(MOE_ERR_INVALID_ARG, "x_stride / y_stride above 2^32");
     const uintptr_t x0 = (uintptr_t)a.x, y0 = (uintptr_t)a.y;
     const uintptr_t x1 = x0 + 2 * (uintptr_t)((x_rows - 1) * a.x_stride + a.K);
     const uintptr_t y1 = y0 + value_bytes(a.y_type) * (uintptr_t)((y_rows - 1) * a.y_stride + a.N);
@@ -622,8 +622,6 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
     moe_status st = check_product_call(a, T, k, &todo);
     if (st || !todo) return st;
     a.P = T * k;
-    if (sorted_pairs && (int64_t)T * x_stride > (int64_t)1 << 35)
-        return fail(MOE_ERR_INVALID_ARG, "T * x_stride above 2^35 elements with gathered rows");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err = grouped_tensor(a, T, k) ? launch_grouped_dense(a, s) : launch_rows(a, s);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product kernel");

@@ -679,8 +679,7 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     DenseParams p{};
     const cuuint64_t rows = a.in_out ? a.K : a.N, cols = a.in_out ? a.N : a.K;
     const cuuint64_t wd[3] = {cols, rows, (cuuint64_t)a.E};
-    const cuuint64_t ws[2] = {(cuuint64_t)a.row_stride * 2, a.E > 1 ? (cuuint64_t)a.expert_stride * 2
-                                                                    : (cuuint64_t)a.row_stride * rows * 2};
+    const cuuint64_t ws[2] = {(cuuint64_t)a.row_stride * 2, (cuuint64_t)(a.E > 1 ? a.expert_stride : a.row_stride) * 2};
     const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)(a.sorted_pairs ? a.P / a.k : a.P), 1};
     const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
     const CUtensorMapDataType type = a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;

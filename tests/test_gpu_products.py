@@ -240,6 +240,20 @@ def test_grouped_nan_and_inf_stay_in_their_row(T, order):
 
 
 @pytest.mark.parametrize("T", [2, 300])
+@pytest.mark.parametrize("order", ["out_in", "in_out"])
+def test_grouped_experts_apart_by_any_stride(T, order):
+    """Expert matrices that neither touch nor lie a whole number of rows apart."""
+    E, K, N_ = 3, 56, 40
+    a, b = (N_, K) if order == "out_in" else (K, N_)
+    flat = torch.full((E * (a * 72 + 8),), float("nan"), dtype=BF, device="cuda")
+    w = flat.as_strided((E, a, b), (a * 72 + 8, 72, 1))
+    w.copy_(torch.randn(E, a, b, generator=_gen(7), device="cuda") * 0.05)
+    x = torch.randn(T, K, generator=_gen(8), device="cuda").to(BF)
+    off = torch.tensor([0, 1, 1, T], dtype=torch.int32, device="cuda")
+    _run_dense(moe.GroupedExperts(w, order=order), T, 1, N_, False, False, off, None, x, w, None, order, F32)
+
+
+@pytest.mark.parametrize("T", [2, 300])
 def test_grouped_expert_stride_past_32_bits(T):
     """The second expert lies more than 2^32 bytes (and 2^31 elements) behind the first."""
     E, K, N_ = 2, 64, 40
@@ -364,6 +378,47 @@ def test_w4_every_code_and_zero_point_is_exact(dtype, group):
     y = op(torch.eye(K, dtype=dtype, device="cuda"))
     want = (code - zero.repeat_interleave(group, 1)).double() * scale.double().repeat_interleave(group, 1)
     assert torch.equal(y.double().cpu(), want.t())
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_w4_bad_routing_is_reported(T):
+    """Offsets and pairs outside their range are clamped and reported; nothing is read or written out of range."""
+    k, E, K, N_ = 2, 3, 256, 40
+    q = _quantize(torch.randn(E, N_, K, generator=_gen(6), device="cuda") * 0.05, 128, True)
+    op = moe.W4Experts(*q, group=128)
+    off, pairs = _routing([T, T, 0], T, k, _gen(1))
+    x = torch.randn(T, K, generator=_gen(2), device="cuda").to(BF)
+    good = op(x, off, pairs, k=k).clone()
+    for which in ("offset above", "offset below", "pair above", "pair below"):
+        o, p = off.clone(), pairs.clone()
+        if which == "offset above":
+            o[3] = 2 * T + 5
+        elif which == "offset below":
+            o[0] = -3
+        else:
+            p[1] = 2 * T if which == "pair above" else -1
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        y = op(x, o, p, k=k, status=status)
+        torch.cuda.synchronize()
+        assert status.item() == N.MOE_ERR_DEVICE_CHECK, which
+        keep = torch.ones(2 * T, dtype=torch.bool, device="cuda")
+        if which.startswith("pair"):
+            keep[1] = False
+        assert torch.equal(y[keep], good[keep]), which
+
+
+@pytest.mark.parametrize("offset", [1, 2, 8])
+def test_w4_scales_and_zero_points_at_any_place(offset):
+    """Scales and zero points that start on their element only (the fast copies need more)."""
+    E, N_, K, T = 2, 33, 512, 4
+    for group in (32, 64, 128):
+        q, s, z = _quantize(torch.randn(E, N_, K, generator=_gen(group), device="cuda") * 0.05, group, True)
+        x = torch.randn(T, K, generator=_gen(3), device="cuda").to(HF)
+        off = torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda")
+        ref = moe.W4Experts(q, s, z, group=group, x_dtype=HF)(x, off)
+        s2 = torch.empty(s.numel() + offset, dtype=HF, device="cuda")[offset:].view(s.shape).copy_(s)
+        z2 = torch.empty(z.numel() + offset, dtype=torch.uint8, device="cuda")[offset:].view(z.shape).copy_(z)
+        assert torch.equal(moe.W4Experts(q, s2, z2, group=group, x_dtype=HF)(x, off), ref)
 
 
 def test_w4_nan_and_inf_stay_in_their_row():
