@@ -34,7 +34,7 @@ namespace {
 constexpr int kStages = 6, kStepK = 64, kMaxN = 256;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;              // (a warp reads the TMEM lanes 32 (warp % 4)..)
-constexpr int kGatherWarps = 4;                          // warps 2, 3, 12, 13
+constexpr int kGatherWarps = 8, kGatherSets = 2;         // warps 2, 3, 12..17: four for every other step
 constexpr int kThreads = 32 * (2 + kEpiWarps + kGatherWarps);
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
@@ -357,9 +357,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     uint64_t* never = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [5] steps that warp 0 / each gathering warp has arrived for
-    int* scan = reinterpret_cast<int*>(tmem_slot + 10);  // [16]
-    int* totals = scan + 16;                             // [2] experts of several blocks, experts with rows
+    int* done = reinterpret_cast<int*>(tmem_slot + 2);   // [9] last step + 1 that warp 0 / each gathering warp has arrived for
+    int* scan = reinterpret_cast<int*>(tmem_slot + 12);  // [20]
+    int* totals = scan + 20;                             // [2] experts of several blocks, experts with rows
     int* off = totals + 2;                               // [E + 1]
     int* tb0 = off + p.E + 1;                            // [E + 1]
     uint16_t* expert = reinterpret_cast<uint16_t*>(tb0 + p.E + 1);   // [E]
@@ -367,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t cta = cta_rank();
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 2 + 2 * kGatherWarps : 2); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], p.sorted_pairs ? 2 + 2 * kGatherWarps / kGatherSets : 2); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kEpiWarps); }
         mbar_init(drain, 1);
         mbar_init(never, 1);
@@ -582,10 +582,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     } else if (warp < kEpiWarp0 || warp >= kEpiWarp0 + kEpiWarps) {
         // ======================= gathered rows of x =======================
         if (p.sorted_pairs) {
-            // warp w brings rows 32 w .. of a step, four to a copy
-            const int w = warp < kEpiWarp0 ? warp - 2 : warp - kEpiWarps - 2;
+            // warp w of a set brings rows 32 w .. of a step, four to a copy; the sets take turns (one set's
+            // waits and copies took as long as a step)
+            const int gw = warp < kEpiWarp0 ? warp - 2 : warp - kEpiWarps - 2, w = gw & 3, set = gw >> 2;
             const uint32_t full0 = in_leader(su32(full)), dst0 = su32(smem) + kABytes + w * 4096;
-            int g = 0;
+            int g = 0, last = 0;
             Ring ring;
             bool ok = true;
             Tile ti;
@@ -607,6 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 pair_of(t + n_pairs);
                 const int mine = uniform(min(max(ti.nh - 32 * w, 0), 32));   // rows: 0, 16 or 32
                 for (int c = 0; c < nk * kStepK; c += kStepK, ++g, ring.next()) {
+                    if ((g & 1) != set) continue;
                     if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
                     const uint32_t bar = full0 + 8 * ring.s, dst = dst0 + ring.s * kStageBytes;
                     if (elect_one()) {
@@ -621,9 +623,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                         }
                     }
                     __syncwarp();
+                    last = g + 1;
                 }
             }
-            if (lane == 0) done[1 + w] = g;
+            if (lane == 0) done[1 + gw] = last;
         }
     } else {
         // ======================= epilogue =======================
@@ -654,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             for (int s = max(0, last - kStages); s < last; ++s)
                 for (int c = 0; c < 2; ++c) {
                     if (of[c][0] <= s) mbar_arrive(&full[s % kStages]);
-                    for (int i = 1; p.sorted_pairs && i <= kGatherWarps; ++i)
+                    for (int i = 1 + 4 * (s & 1); p.sorted_pairs && i <= 4 + 4 * (s & 1); ++i)
                         if (of[c][i] <= s) mbar_arrive(&full[s % kStages]);
                 }
             for (int s = max(0, last - kStages); s < last; ++s) drain_wait(&full[s % kStages], (s / kStages) & 1, p.wait_ns);
@@ -669,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
 }
 
 size_t smem_bytes(int E) {
-    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 40 + 72 + 2 * (size_t)(E + 1) * 4 + 2 * (size_t)E;
+    return 1024 + (size_t)kStages * kStageBytes + kExchBytes + (2 * kStages + 6) * 8 + 48 + 88 + 2 * (size_t)(E + 1) * 4 + 2 * (size_t)E;
 }
 
 }  // namespace
