@@ -9,7 +9,7 @@
 #include <new>
 #include <vector>
 
-#include "internal.cuh"
+#include "products.cuh"
 
 using namespace moe;
 
