@@ -25,9 +25,9 @@
 // both took 1400 clocks a stage); a CTA per SM takes an even share of the (expert, 128 rows) units.
 //
 // Measured (device time): 16 tokens, 8 of 256 experts, 7168 -> 2048 gated, groups of 32 with zero points:
-// 372 us for 1.78 GB (266 us at the copy's rate).  What bounds it now is the matrix instruction: 512 of them a
-// stage and SM, one in 16 clocks on each of the four schedulers, against about 700 clocks that HBM needs for the stage; without
-// the products it takes 292 us.  One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 8.1 us for 13 MB, the
+// 372 to 381 us for 1.78 GB (266 us at the copy's rate).  What bounds it now is the matrix instruction: 512 of them a
+// stage and SM, one in 16 clocks on each of the four schedulers, against about 700 clocks that HBM needs for the stage; an
+// earlier form of 445 us took 292 us without its products.  One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 8.1 us for 13 MB, the
 // most of it the start: routing read, x staged, the first copies (4 us).
 #include <type_traits>
 
