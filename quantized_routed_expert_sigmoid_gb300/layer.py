@@ -136,13 +136,25 @@ class MoeLayer:
 _VT = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16, torch.float16: N.MOE_F16}
 
 
-def _cuda(t, name, dtypes=None, dim=None):
+def _cuda(t, name, dtypes=None, dim=None, device=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, not on device {device}")
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, not {t.dtype}")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
+
+
+def _on_current(device, **tensors):
+    """Refuse a call whose tensors are not all on `device`, or whose device is not the current one: the kernel
+    runs there, and an address of another device is nothing that it may read."""
+    if device != torch.cuda.current_device():
+        raise ValueError(f"device {device} of the call is not the current one ({torch.cuda.current_device()})")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} is on device {t.get_device()}, not on device {device}")
 
 
 def _row_stride(t, name):
@@ -165,7 +177,8 @@ class _Products:
 
         With sorted_pairs (int32 [T*k], moe_permute's) x holds the T tokens, row i being that of token
         sorted_pairs[i] // k; without, x holds the T*k rows in sorted order.  offsets (int32 [E+1], moe_permute's) may
-        be left out for one expert.  status: int32 [1], raised when a device-side check fails.
+        be left out for one expert.  status: int32 [1], raised when a device-side check fails.  All of them are on the
+        weights' device, which has to be the current one.
         """
         n, width = x.shape
         T = n if sorted_pairs is not None else n // k
@@ -186,6 +199,7 @@ class _Products:
             out = torch.empty((P, self.n_out), dtype=self.y_dtype, device=x.device)
         elif out.dtype is not self.y_dtype or out.shape != (P, self.n_out) or not out.is_cuda:
             raise ValueError(f"out must be a {self.y_dtype} CUDA tensor [{P}, {self.n_out}]")
+        _on_current(self.device, x=x, offsets=offsets, sorted_pairs=sorted_pairs, out=out, status=status)
         self._matmul(self.plan, x, _row_stride(x, "x"), T, k, sorted_pairs, offsets, out, _row_stride(out, "out"), status,
                      stream)
         return out
@@ -220,12 +234,12 @@ class GroupedExperts(_Products):
         if w.stride(2) != 1 and w.shape[2] != 1:
             raise ValueError("the last dimension of w must be dense")
         if w_up is not None:
-            _cuda(w_up, "w_up", (w.dtype,), 3)
+            _cuda(w_up, "w_up", (w.dtype,), 3, w.get_device())
             if w_up.shape != w.shape or w_up.stride() != w.stride():
                 raise ValueError("w_up must have w's shape and strides")
         self.n_experts = w.shape[0]
         self.n_out, self.n_in = (w.shape[1], w.shape[2]) if order == "out_in" else (w.shape[2], w.shape[1])
-        self.x_dtype, self.y_dtype = w.dtype, y_dtype
+        self.x_dtype, self.y_dtype, self.device = w.dtype, y_dtype, w.get_device()
         self._keep = (w, w_up)
         self.plan = N.moe_grouped_plan_create(N.moe_grouped_desc(
             _VT[w.dtype], _VT[y_dtype], N.MOE_W_OUT_IN if order == "out_in" else N.MOE_W_IN_OUT, self.n_experts,
@@ -272,11 +286,11 @@ class W4Experts(_Products):
                 if name in ("scales",) or (name == "scales_up" and up[0] is not None):
                     raise ValueError(f"{name} is missing")
                 continue
-            _cuda(t, name, dtypes, 3)
+            _cuda(t, name, dtypes, 3, q.get_device())
             if tuple(t.shape) != (E, n_out, width) or not t.is_contiguous():
                 raise ValueError(f"{name} must be dense [{E}, {n_out}, {width}]")
         self.n_experts, self.n_out, self.n_in = E, n_out, n_in
-        self.x_dtype, self.y_dtype = x_dtype, y_dtype
+        self.x_dtype, self.y_dtype, self.device = x_dtype, y_dtype, q.get_device()
         self._keep = (q, scales, zeros, up)
         p = [t.data_ptr() if t is not None else None for t in (q, scales, zeros) + up]
         self.plan = N.moe_w4_plan_create(N.moe_w4_desc(_VT[x_dtype], _VT[y_dtype], _VT[scales.dtype], group, E, n_out,
@@ -291,9 +305,11 @@ class NormResidual:
 
     def __init__(self, H: int, *, gamma_post: torch.Tensor | None = None, gamma_pre: torch.Tensor | None = None,
                  eps: float = 1e-6, res_scale: float = 1.0, scale: float = 1.0):
+        self.device = None               # the gains'; without any, each call's own
         for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
             if g is not None:
-                _cuda(g, name, (torch.float32,), 1)
+                _cuda(g, name, (torch.float32,), 1, self.device)
+                self.device = g.get_device()
                 if g.numel() != H or not g.is_contiguous():
                     raise ValueError(f"{name} must be dense [{H}]")
         self.H = H
@@ -306,7 +322,8 @@ class NormResidual:
         """(x_out, u): the residual stream behind the block (in x's type; x_out may be x) and its norm.
 
         x (None: 0), y: [T, H].  gate: fp32, broadcastable to [T, H] ([H], [1, H], [T, 1] or [T, H]).
-        Outputs that are not given are made: x_out like x (or y), u in bf16 when gamma_pre was given.
+        Outputs that are not given are made: x_out like x (or y), u in bf16 when gamma_pre was given.  All tensors are
+        on one device, which has to be the current one.
         """
         shape = y.shape
         T, H = shape
@@ -332,6 +349,10 @@ class NormResidual:
             if gate.dtype is not torch.float32 or not gate.is_cuda or len(gs) != 2 or gs[0] not in (1, T) or gs[1] not in (1, H):
                 raise ValueError(f"gate must be an fp32 CUDA tensor broadcastable to [{T}, {H}]")
             gate_row, gate_col = st[0] if gs[0] != 1 else 0, st[1] if gs[1] != 1 else 0
+        device = y.get_device()
+        if self.device is not None and device != self.device:
+            raise ValueError(f"y is on device {device}, gamma_post / gamma_pre on device {self.device}")
+        _on_current(device, x=x, gate=gate, x_out=x_out, u=u)
         types = (x_out.dtype, y.dtype, u.dtype if u is not None else torch.float32)
         desc = self._desc.get(types)
         if desc is None:
