@@ -180,6 +180,8 @@ class _Products:
         be left out for one expert.  status: int32 [1], raised when a device-side check fails.  All of them are on the
         weights' device, which has to be the current one.
         """
+        if k < 1:
+            raise ValueError(f"k = {k}: a token has at least one expert")
         n, width = x.shape
         T = n if sorted_pairs is not None else n // k
         P = T * k

@@ -67,6 +67,16 @@ def test_products_refuse_weights_of_a_device_that_is_not_current(ops, which, mon
     assert not ops[3]
 
 
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("k", [0, -1])
+def test_products_refuse_a_count_of_experts_below_one(ops, which, k):
+    with pytest.raises(ValueError, match="k = "):
+        ops[which](**dict(_args(), k=k))
+    with pytest.raises(ValueError, match="k = "):
+        ops[which](_args()["x"], k=k)
+    assert not ops[3]
+
+
 def test_plans_refuse_matrices_of_two_devices(ops):
     w = torch.zeros(2, 16, 32, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="w_up"):
