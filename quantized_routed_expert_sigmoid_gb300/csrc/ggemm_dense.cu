@@ -44,6 +44,12 @@ constexpr int kGatherWarps = 8, kGatherSets = 2;         // warps 2, 3, 12..17: 
 constexpr int kThreads = 32 * (2 + kEpiWarps + kGatherWarps);
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
+// The tensor cores cut the sum off after each instruction instead of rounding it: an error towards zero that grows
+// with the length of the sum (relative, in norm: 7e-7 over 768 elements, 8e-6 over 7168, twice that gated), far
+// below half a step of a 16-bit output but not of an fp32 one.  There a sum is made of runs of at most kRun steps,
+// which the epilogue adds with rounding in TMEM: columns kSumCol.., so that a tile has at most 128 columns.
+constexpr int kSumCol = 128;
+template <bool UP> constexpr int kRun = UP ? 6 : 12;     // steps of 64
 constexpr int kSpins = 64;                               // tests of a barrier before a wait looks at the clock
 
 struct DenseParams {
@@ -59,6 +65,8 @@ struct DenseParams {
     int64_t y_stride;
     int32_t* status;
     uint64_t wait_ns;
+    int run;                     // steps of 64 in a run (all of them: one run)
+    int max_n;                   // columns of a tile
     int stall;                   // test setting: the first wait of the MMA warp never completes
 };
 
@@ -243,12 +251,21 @@ struct Order {
     }
 };
 constexpr int kBuckets = 16;     // by columns of a block, 256 first: 8 for several blocks, 8 for one
-__device__ __forceinline__ int blocks_of(int cnt) { return (cnt + kMaxN - 1) / kMaxN; }
-__device__ __forceinline__ int bucket_of(int cnt) {
+__device__ __forceinline__ int blocks_of(int cnt, int max_n) { return (cnt + max_n - 1) / max_n; }
+__device__ __forceinline__ int bucket_of(int cnt, int max_n) {
     if (cnt <= 0) return kBuckets;                       // no rows, no tiles
-    const int nb = blocks_of(cnt), cols = ((cnt + nb - 1) / nb + 31) >> 5;
+    const int nb = blocks_of(cnt, max_n), cols = ((cnt + nb - 1) / nb + 31) >> 5;
     return (nb > 1 ? 0 : 8) + 8 - cols;
 }
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <typename T> __device__ __forceinline__ T to_out(float v);
 template <> __device__ __forceinline__ float to_out<float>(float v) { return v; }
@@ -266,15 +283,60 @@ __device__ __forceinline__ void epilogue(const DenseParams& p, const Order& orde
     const uint32_t accr0 = in_leader(su32(accr));
     const int pairbar = 1 + side * 2 + (q & 1);          // gated: warps q and q + 2 trade columns
     int j = 0, turn = 0;
-    Tile ti;
-    for (int t = first; order.at(t, ti); t += n_pairs, ++j) {
-        const int b = j & 1;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const int nk = (p.K + kStepK - 1) / kStepK;
+    auto complete = [&](int b) {
         bool ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
         // (the two warps of a trade leave together, or one would wait for the other for ever)
         if constexpr (UP) ok = all_of(pairbar, 64, ok);
-        if (!ok) break;
         tc_after();
-        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)b * kMaxN;
+        return ok;
+    };
+    auto release = [&](int b) {
+        tc_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(accr0 + 8 * b);
+    };
+    Tile ti;
+    for (int t = first; order.at(t, ti); t += n_pairs, ++j) {
+        int b = j & 1;
+        if (!complete(b)) break;
+        uint32_t acc = lanes + (uint32_t)b * kMaxN;
+        const bool runs = sizeof(T) == 4 && p.run < nk;
+        if constexpr (sizeof(T) == 4) {
+            if (runs) {
+                // this warp's columns of the runs, summed where it reads them from afterwards
+                constexpr int kCols = UP ? 16 : 32;
+                bool ok = true;
+                for (int k0 = 0;;) {
+                    for (int c0 = kCols * side; c0 < ti.ntok; c0 += 2 * kCols)
+#pragma unroll
+                        for (int h = 0; h < kCols; h += 16) {
+                            uint32_t r[16], s[16];
+                            tmem_ld16(acc + c0 + h, r);
+                            if (k0 > 0) {
+                                tmem_ld16(lanes + kSumCol + c0 + h, s);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    r[i] = __float_as_uint(__fadd_rn(__uint_as_float(s[i]), __uint_as_float(r[i])));
+                            } else {
+                                tmem_ld_wait();
+                            }
+                            tmem_st16(lanes + kSumCol + c0 + h, r);
+                        }
+                    tmem_st_wait();
+                    release(b);
+                    if ((k0 += p.run) >= nk) break;
+                    b = ++j & 1;
+                    ok = complete(b);
+                    if (!ok) break;
+                    acc = lanes + (uint32_t)b * kMaxN;
+                }
+                if (!ok) break;
+                acc = lanes + kSumCol;
+            }
+        }
         if constexpr (UP) {
             const int row = ti.mb * kRowsTile + cta * 64 + (q & 1) * 32 + lane;
             const bool is_up = q >= 2;
@@ -344,9 +406,7 @@ __device__ __forceinline__ void epilogue(const DenseParams& p, const Order& orde
                 }
             }
         }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(accr0 + 8 * b);
+        if (!runs) release(b);
     }
 }
 
@@ -404,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     }
     bool big = false;
     __syncthreads();
-    for (int i = tid; i < p.E; i += kThreads) big |= off[i + 1] - off[i] > kMaxN;
+    for (int i = tid; i < p.E; i += kThreads) big |= off[i + 1] - off[i] > p.max_n;
     big = __syncthreads_or(big);
     int* hist = reinterpret_cast<int*>(exch);            // (before its use by the epilogue)
     const int n_chunks = (p.E + 31) / 32;
@@ -436,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         // experts sorted by bucket, stably (every CTA finds the same order): counts per 32 experts and
         // bucket, their running sums over the buckets, ranks
         for (int c = warp; c < n_chunks; c += kThreads / 32) {
-            const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
+            const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e], p.max_n) : kBuckets;
             if (lane < kBuckets) hist[c * kBuckets + lane] = 0;
             __syncwarp();
             const unsigned same = __match_any_sync(0xffffffffu, k);
@@ -463,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         }
         __syncthreads();
         for (int c = warp; c < n_chunks; c += kThreads / 32) {
-            const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e]) : kBuckets;
+            const int e = 32 * c + lane, k = e < p.E ? bucket_of(off[e + 1] - off[e], p.max_n) : kBuckets;
             const unsigned same = __match_any_sync(0xffffffffu, k);
             if (k < kBuckets) expert[scan[k] + hist[c * kBuckets + k] + __popc(same & ((1u << lane) - 1u))] = (uint16_t)e;
         }
@@ -472,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         {
             // thread t: places t * per .. of a scan of the block counts over the whole CTA
             const int per = (n_big + kThreads - 1) / kThreads, i0 = tid * per;
-            auto blocks_at = [&](int i) { return blocks_of(off[expert[i] + 1] - off[expert[i]]); };
+            auto blocks_at = [&](int i) { return blocks_of(off[expert[i] + 1] - off[expert[i]], p.max_n); };
             int sum = 0;
             for (int i = i0; i < min(i0 + per, n_big); ++i) sum += blocks_at(i);
             int inc = sum;
@@ -553,13 +613,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             int j = 0;
             bool ok = true, any = false;
             Tile ti;
-            for (int t = first; ok && order.at(t, ti); t += n_pairs, ++j) {
+            for (int t = first; ok && order.at(t, ti); t += n_pairs) {
                 const uint32_t idesc = uniform(idesc_mma(256, 2 * ti.nh, p.bf16) | (IN_OUT ? 1u << 15 : 0u));
-                const int b = j & 1;
-                if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
-                tc_after();
-                const uint32_t acc = uniform(tmem + (uint32_t)b * kMaxN);
-                for (int kb = 0; kb < nk; ++kb, ring.next()) {
+                for (int kb = 0, start = 0, b = 0; kb < nk; ++kb, ring.next()) {
+                    if (kb == start) {                               // the first step of a run
+                        b = j & 1;
+                        if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                        tc_after();
+                    }
+                    const uint32_t acc = uniform(tmem + (uint32_t)b * kMaxN);
+                    const bool first_step = kb == start, last_step = kb == nk - 1 || kb - start == p.run - 1;
                     const bool stalled = p.stall && !any;            // (test setting)
                     if (!wait_warp(stalled ? never : &full[ring.s], stalled ? 0u : ring.ph, abort_flag, p.wait_ns)) { ok = false; break; }
                     tc_after();
@@ -568,11 +631,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kStepK / 16; ++kk)
-                            mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 ? 1u : (uint32_t)(kb > 0));
+                            mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 ? 1u : (uint32_t)!first_step);
                         commit_pair(&empty[ring.s]);
-                        if (kb == nk - 1) commit_pair(&accf[b]);
+                        if (last_step) commit_pair(&accf[b]);
                     }
                     __syncwarp();
+                    if (last_step) { start = kb + 1; ++j; }
                     any = true;
                 }
             }
@@ -707,6 +771,10 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     p.y = a.y; p.y_type = a.y_type; p.y_stride = a.y_stride; p.status = a.status;
     const WaitCfg wc = wait_cfg();
     p.wait_ns = wc.limit_ns; p.stall = wc.stall;
+    const int nk = (a.K + kStepK - 1) / kStepK, longest = a.w1 ? kRun<true> : kRun<false>;
+    const int n_runs = a.y_type == MOE_F32 ? (nk + longest - 1) / longest : 1;
+    p.run = (nk + n_runs - 1) / n_runs;
+    p.max_n = n_runs > 1 ? kSumCol : kMaxN;
     const int v = (a.w1 ? 2 : 0) + (a.in_out ? 1 : 0);
     const void* fn = v == 3   ? (const void*)grouped_dense_kernel<true, true>
                      : v == 2 ? (const void*)grouped_dense_kernel<true, false>
@@ -718,7 +786,7 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     // one pair per two SMs, and no more pairs than there can be tiles
     const int64_t n_mb = (a.N + (a.w1 ? 127 : 255)) / (a.w1 ? 128 : 256);
-    const int64_t most = ((int64_t)a.P / kMaxN + (a.E < a.P ? a.E : a.P)) * n_mb;
+    const int64_t most = ((int64_t)a.P / p.max_n + (a.E < a.P ? a.E : a.P)) * n_mb;
     const int pairs = (int)(most < sms / 2 ? most : sms / 2);
     void* args[] = {&p};
     return launch_early(fn, dim3(2 * (pairs > 0 ? pairs : 1)), kThreads, smem_bytes(a.E), s, args);

@@ -127,6 +127,19 @@ __device__ __forceinline__ int64_t x_row(const RowsArgs& a, int i) {
 // Each fills acc[mat][tile][nt] (m16n8 accumulators: c0, c1 = row g, columns 2t, 2t + 1; c2, c3 = row
 // g + 8) with this warp's share.  xr[j]: this lane's row of x in column tile j (NULL: none).
 
+// The matrix instruction cuts its sum off instead of rounding it, an error towards zero that grows with the number of
+// instructions in a row (8.6e-7, gated 1.7e-6, at 7168 elements); so what a warp loads at once is summed by
+// itself and added with rounding.
+template <int TI, int NT>
+__device__ __forceinline__ void add(float (&acc)[TI][NT][4], const float (&part)[TI][NT][4]) {
+#pragma unroll
+    for (int j = 0; j < TI; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][n][i] += part[j][n][i];
+}
+
 // [out][in] weights: warps take chunks of 32 c, lane (g, t) 8 of them of rows g and g + 8.
 template <bool BF16, bool UP, int NT>
 struct OutIn {
@@ -156,6 +169,7 @@ struct OutIn {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) w[u][j][h] = load8<true>(wr[j][h], i, a.K);
             }
+            float part[kMats][kTiles][NT][4] = {};      // (see add)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = (c0 + u * kWarps) * 32 + 8 * t;
@@ -165,12 +179,14 @@ struct OutIn {
                     const uint4 b = xr[n] ? load8<false>(xr[n], i, a.K) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float(&c)[4] = acc[UP ? j : 0][UP ? 0 : j][n];
+                        float(&c)[4] = part[UP ? j : 0][UP ? 0 : j][n];
                         mma16816<BF16>(c, w[u][j][0].x, w[u][j][1].x, w[u][j][0].y, w[u][j][1].y, b.x, b.y);
                         mma16816<BF16>(c, w[u][j][0].z, w[u][j][1].z, w[u][j][0].w, w[u][j][1].w, b.z, b.w);
                     }
                 }
             }
+#pragma unroll
+            for (int m = 0; m < kMats; ++m) add(acc[m], part[m]);
         }
     }
 };
@@ -201,24 +217,26 @@ struct InOut {
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = (c0 + u * kWarps) * 16 + 4 * t;
+            for (int m = 0; m < kMats; ++m) {
+                float part[kTiles][NT][4] = {};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n >= nt) break;
-                    const uint2 b = xr[n] ? load4(xr[n], i, a.K) : make_uint2(0u, 0u);
+                for (int u = 0; u < U; ++u) {
+                    const int i = (c0 + u * kWarps) * 16 + 4 * t;
+                    const uint32_t* q0 = &w[u][m][0].x;
+                    const uint32_t* q1 = &w[u][m][1].x;
+                    const uint32_t* q2 = &w[u][m][2].x;
+                    const uint32_t* q3 = &w[u][m][3].x;
 #pragma unroll
-                    for (int m = 0; m < kMats; ++m) {
-                        const uint32_t* q0 = &w[u][m][0].x;
-                        const uint32_t* q1 = &w[u][m][1].x;
-                        const uint32_t* q2 = &w[u][m][2].x;
-                        const uint32_t* q3 = &w[u][m][3].x;
+                    for (int n = 0; n < NT; ++n) {
+                        if (n >= nt) break;
+                        const uint2 b = xr[n] ? load4(xr[n], i, a.K) : make_uint2(0u, 0u);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma16816<BF16>(acc[m][j][n], __byte_perm(q0[j], q1[j], 0x5410), __byte_perm(q0[j], q1[j], 0x7632),
+                            mma16816<BF16>(part[j][n], __byte_perm(q0[j], q1[j], 0x5410), __byte_perm(q0[j], q1[j], 0x7632),
                                            __byte_perm(q2[j], q3[j], 0x5410), __byte_perm(q2[j], q3[j], 0x7632), b.x, b.y);
                     }
                 }
+                add(acc[m], part);
             }
         }
     }
