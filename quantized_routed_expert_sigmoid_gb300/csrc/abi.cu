@@ -323,10 +323,11 @@ moe_status check_product_call(const moe::RowsArgs& a, int T, int k, bool* todo) 
 // (16) and the start of the tensor-core kernel (about 5 us) shows.  Measured, rows / tensor, hidden 2048,
 // intermediate 768, 128 experts: gated T*k = 8: 11.8 / 15.8 us, 32: 33.4 / 37.2, 64: 56.5 / 57.0; down 64: 38.4 / 30.9; one
 // expert of 2048 x 2048, T = 16: 7.3 / 11.3, 64: 21.1 / 11.5.  [in][out] weights, which the streaming kernel
-// reads in narrower strips: gated T*k = 8: 20.2 / 15.6.
+// reads in narrower strips, one token: gated, k = 1: 21.2 / 12.0, 7: 22.1 / 15.1 (768 -> 2048, 7: 15.4 / 14.5); plain 768 -> 2048,
+// k = 1: 6.5 / 7.7, 2048 -> 2048: 10.6 / 11.8, 7168 -> 2048: 36.2 / 28.7.
 static bool grouped_tensor(const moe::RowsArgs& a, int T, int k) {
     const int64_t P = (int64_t)T * k;
-    return a.in_out ? P >= 8 : P > 32 || T > 16;
+    return a.in_out ? a.w1 || a.K > 2048 || P >= 8 : P > 32 || T > 16;
 }
 
 struct moe_grouped_plan {

@@ -48,6 +48,8 @@ constexpr uint32_t kTmemCols = 512;
 // with the length of the sum (relative, in norm: 7e-7 over 768 elements, 8e-6 over 7168, twice that gated), far
 // below half a step of a 16-bit output but not of an fp32 one.  There a sum is made of runs of at most kRun steps,
 // which the epilogue adds with rounding in TMEM: columns kSumCol.., so that a tile has at most 128 columns.
+// Measured with runs / without, fp32 outputs: 4096 tokens gated 265 / 181 us (error 6.9e-7 / 4.2e-6), 2048 tokens, 6 of 64
+// experts of 7168 -> 1024 221 / 181 us (7.2e-7 / 7.9e-6), 64 tokens of those 156 / 154 us.
 constexpr int kSumCol = 128;
 template <bool UP> constexpr int kRun = UP ? 6 : 12;     // steps of 64
 constexpr int kSpins = 64;                               // tests of a barrier before a wait looks at the clock

@@ -12,7 +12,7 @@
 // weights lie in memory: lane (g, t) of a warp holds 16 consecutive bytes of weight row g, and the
 // same elements of x row g, and no element is moved between lanes.
 // Layout: a CTA of 8 warps takes 32 weight rows (16 of W and the same 16 of W_up when gated; 64
-// of each for [in][out] weights) of one expert; the warps split the sum over c and join in shared
+// for [in][out] weights, which come here ungated) of one expert; the warps split the sum over c and join in shared
 // memory at the end, in a fixed order.
 // Measured: one token, 8 of 128 experts, 2048 -> 768 gated, bf16: 11.7 us for 50 MB (7.5 us at the copy's
 // rate); three CTAs an SM with two chunks in flight a warp, so that all 384 run at once (with one to two CTAs and four
@@ -191,53 +191,47 @@ struct OutIn {
     }
 };
 
-// [in][out] weights: warps take chunks of 16 c; lane (g, t) holds outputs 8g .. 8g + 7 of c = 4t ..
-// 4t + 3, and byte permutes pair the c of one output.  Output 8g + 2 tile + half is row g + 8 half.
-template <bool BF16, bool UP, int NT>
+// [in][out] weights (one matrix: the gated pair is the tensor-core kernel's): warps take chunks of 16 c; lane (g, t)
+// holds outputs 8g .. 8g + 7 of c = 4t .. 4t + 3, and byte permutes pair the c of one output.  Output 8g + 2 tile + half
+// is row g + 8 half.
+template <bool BF16, int NT>
 struct InOut {
-    static constexpr int kMats = UP ? 2 : 1, kTiles = 4, kRows = 64, kCtas = 2;
+    static constexpr int kMats = 1, kTiles = 4, kRows = 64, kCtas = 2;
     __device__ static __forceinline__ int row(int tile, int g, int half) { return 8 * g + 2 * tile + half; }
     __device__ static __forceinline__ void run(const RowsArgs& a, int e, int r0, const uint16_t* const (&xr)[NT],
                                                int nt, float (&acc)[kMats][kTiles][NT][4]) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-        constexpr int U = UP ? 2 : 4;
+        constexpr int U = 4;
         const int n_chunks = (a.K + 15) / 16, n0 = r0 + 8 * g;
+        const uint16_t* p = static_cast<const uint16_t*>(a.w0) + (int64_t)e * a.expert_stride;
         for (int c0 = warp; c0 < n_chunks; c0 += U * kWarps) {
-            uint4 w[U][kMats][4];
+            uint4 w[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = (c0 + u * kWarps) * 16 + 4 * t;
 #pragma unroll
-                for (int m = 0; m < kMats; ++m) {
-                    const uint16_t* p = static_cast<const uint16_t*>(m ? a.w1 : a.w0) + (int64_t)e * a.expert_stride;
+                for (int r = 0; r < 4; ++r)
+                    w[u][r] = i + r < a.K ? load8<true>(p + (int64_t)(i + r) * a.row_stride, n0, a.N) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            float part[kTiles][NT][4] = {};
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        w[u][m][r] = i + r < a.K ? load8<true>(p + (int64_t)(i + r) * a.row_stride, n0, a.N)
-                                                 : make_uint4(0u, 0u, 0u, 0u);
+            for (int u = 0; u < U; ++u) {
+                const int i = (c0 + u * kWarps) * 16 + 4 * t;
+                const uint32_t* q0 = &w[u][0].x;
+                const uint32_t* q1 = &w[u][1].x;
+                const uint32_t* q2 = &w[u][2].x;
+                const uint32_t* q3 = &w[u][3].x;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (n >= nt) break;
+                    const uint2 b = xr[n] ? load4(xr[n], i, a.K) : make_uint2(0u, 0u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma16816<BF16>(part[j][n], __byte_perm(q0[j], q1[j], 0x5410), __byte_perm(q0[j], q1[j], 0x7632),
+                                       __byte_perm(q2[j], q3[j], 0x5410), __byte_perm(q2[j], q3[j], 0x7632), b.x, b.y);
                 }
             }
-#pragma unroll
-            for (int m = 0; m < kMats; ++m) {
-                float part[kTiles][NT][4] = {};
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = (c0 + u * kWarps) * 16 + 4 * t;
-                    const uint32_t* q0 = &w[u][m][0].x;
-                    const uint32_t* q1 = &w[u][m][1].x;
-                    const uint32_t* q2 = &w[u][m][2].x;
-                    const uint32_t* q3 = &w[u][m][3].x;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (n >= nt) break;
-                        const uint2 b = xr[n] ? load4(xr[n], i, a.K) : make_uint2(0u, 0u);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma16816<BF16>(part[j][n], __byte_perm(q0[j], q1[j], 0x5410), __byte_perm(q0[j], q1[j], 0x7632),
-                                           __byte_perm(q2[j], q3[j], 0x5410), __byte_perm(q2[j], q3[j], 0x7632), b.x, b.y);
-                    }
-                }
-                add(acc[m], part);
-            }
+            add(acc[0], part);
         }
     }
 };
@@ -311,9 +305,10 @@ cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
 template <bool BF16, bool UP>
 cudaError_t launch_w(const RowsArgs& a, cudaStream_t s) {
     // columns held at once: what an expert can have at most (a token asks for an expert once, so T rows;
-    // more than the columns are taken in passes).  [in][out] weights come here with less than 8 rows in all.
+    // more than the columns are taken in passes).  [in][out] weights come here ungated, with less than 8 rows in all.
     const int most = a.offsets ? a.P / a.k : a.P;
-    if (a.in_out) return launch<InOut<BF16, UP, 1>, 1>(a, s);
+    if constexpr (!UP)
+        if (a.in_out) return launch<InOut<BF16, 1>, 1>(a, s);
     if (most <= 8) return launch<OutIn<BF16, UP, 1>, 1>(a, s);
     return launch<OutIn<BF16, UP, 2>, 2>(a, s);
 }
