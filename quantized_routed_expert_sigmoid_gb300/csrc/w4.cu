@@ -11,10 +11,13 @@
 // - The products run on the warps' m16n8k16 instruction, weights as the 16-row operand (8 rows of W
 //   and the same 8 of W_up when gated, so that both halves of an output meet in one thread), up to 8 rows of
 //   x as its columns.  Its sum over c may run in any order, so codes are used in the order in which they lie: a
-//   32-bit word gives four operand registers by one mask each (and one shift): nibble j and j + 4 become the
-//   16-bit halves.  A masked nibble q, read as fp16, is the subnormal q * 2^-24 (nibbles 0, 2) or q * 2^-20
-//   (1, 3: x is stored with 1/16 there), exactly; the instruction takes subnormals exactly.  Five
-//   instructions a word instead of the eleven of an exact integer-to-float conversion and subtraction.
+//   32-bit word gives four operand registers by one mask each and two shifts: nibble j and j + 4 become the 16-bit
+//   halves, at bits 2..5 (nibbles 0, 2) or 6..9 (1, 3).  A masked nibble q, read as fp16, is the subnormal q * 2^-22 or
+//   q * 2^-18 (x is stored with 1/16 there).  Where in the subnormal the code lies does not change its products, but
+//   the sums of the instruction lose low bits with it, as if products were lined up by the operands' exponent
+//   fields.  Measured for fp16 x, largest relative error of fp32 outputs over 20 inputs of 64 to 2080 elements, and
+//   time of the large case below: bits 0..3 and 4..7 2.1e-6, 381 us; this 2.5e-7, 385 us; all at 4..7 1.4e-7, 401 us;
+//   all at 6..9 1.6e-7, 410 us (the same in 32 bits without matrix instructions: 1.5e-7).
 // - The zero point is taken off the group's sum, with the group's sum of x: z is at most 15, so that costs at
 //   most one bit of the fp32 sum.  Sums are fp32; the scale is applied to them in fp32.
 // - x is staged once per expert: scaled by a power of two of its row's largest magnitude into fp16 (a
@@ -25,7 +28,7 @@
 // both took 1400 clocks a stage); a CTA per SM takes an even share of the (expert, 128 rows) units.
 //
 // Measured (device time): 16 tokens, 8 of 256 experts, 7168 -> 2048 gated, groups of 32 with zero points:
-// 372 to 381 us for 1.78 GB (266 us at the copy's rate).  What bounds it now is the matrix instruction: 512 of them a
+// 385 us for 1.78 GB (266 us at the copy's rate).  What bounds it now is the matrix instruction: 512 of them a
 // stage and SM, one in 16 clocks on each of the four schedulers, against about 700 clocks that HBM needs for the stage; an
 // earlier form of 445 us took 292 us without its products.  One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 8.1 us for 13 MB, the
 // most of it the start: routing read, x staged, the first copies (4 us).
@@ -43,6 +46,7 @@ constexpr int kTiles = 2, kScaleWarps = 3, kAllWarps = kWarps + 1 + kScaleWarps,
 constexpr int kStages = 6, kStageBytes = 128 * 128, kStageK = 256;
 constexpr int kSmemMax = 227 * 1024;
 
+constexpr uint32_t kCode = 0x03C003C0u;    // bits 6..9 of each half
 struct W4Params {
     CUtensorMap tw0, tw1;        // codes of W and W_up: [E * N][K / 2] bytes, boxes of 128 bytes x 128 (gated: 64) rows
     RowsArgs a;
@@ -461,21 +465,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                                 lds16_if(x, xc[n] + xk + 2 * (q * G + 8 * w), has[n]);
 #pragma unroll
                                 for (int j = 0; j < kTiles; ++j) {
-                                    const uint32_t va = v[j][0][w], vb = v[j][1][w], a8 = va >> 8, b8 = vb >> 8;
+                                    const uint32_t va = v[j][0][w], vb = v[j][1][w];
+                                    const uint32_t al = va << 2, ah = va >> 6, a0 = al & 0x003C003Cu, a1 = al & kCode, a2 = ah & 0x003C003Cu, a3 = ah & kCode;
+                                    const uint32_t bl = vb << 2, bh = vb >> 6, b0 = bl & 0x003C003Cu, b1 = bl & kCode, b2 = bh & 0x003C003Cu, b3 = bh & kCode;
                                     float(&lo)[4] = part[j][n];
                                     float(&hi)[4] = kWords > 1 ? high[j][n] : part[j][n];
-                                    if (w == 0)
-                                        mma_f16_16816_first(lo, va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u,
-                                                            x.x, x.y);
-                                    else
-                                        mma_f16_16816(lo, va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, x.x,
-                                                      x.y);
-                                    if (w == 0 && kWords > 1)
-                                        mma_f16_16816_first(hi, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
-                                                            x.z, x.w);
-                                    else
-                                        mma_f16_16816(hi, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, x.z,
-                                                      x.w);
+                                    if (w == 0) mma_f16_16816_first(lo, a0, b0, a1, b1, x.x, x.y);
+                                    else mma_f16_16816(lo, a0, b0, a1, b1, x.x, x.y);
+                                    if (w == 0 && kWords > 1) mma_f16_16816_first(hi, a2, b2, a3, b3, x.z, x.w);
+                                    else mma_f16_16816(hi, a2, b2, a3, b3, x.z, x.w);
                                 }
                             }
 #pragma unroll
@@ -497,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                                         const __half2 hw = *reinterpret_cast<const __half2*>(&sw);
                                         f = q & 1 ? __high2float(hw) : __low2float(hw);
                                     }
-                                    // -z * 2^-24, exactly: 2^23 + z as a float's bits, times -2^-24, plus 1/2
+                                    // -z * 2^-22, exactly: 2^23 + z as a float's bits, times -2^-22, plus 2
                                     const float z = fmaf(__uint_as_float(__byte_perm(fz[j][h][q >> 2], 0x4B000000u, 0x7650u | (q & 3))),
-                                                         -0x1p-24f, 0.5f);
+                                                         -0x1p-22f, 2.0f);
                                     float p0 = part[j][n][2 * h], p1 = part[j][n][2 * h + 1];
                                     if constexpr (kWords > 1) {
                                         p0 += high[j][n][2 * h];
@@ -545,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                         for (int i = 0; i < 2; ++i) {
                             const int c = 8 * n + 2 * t + i, ya = b * kUnit + ra[j];
                             if (c >= nc) continue;
-                            const float v0 = acc[j][n][i] * 0x1p24f * unscale[c], v1 = acc[j][n][2 + i] * 0x1p24f * unscale[c];
+                            const float v0 = acc[j][n][i] * 0x1p22f * unscale[c], v1 = acc[j][n][2 + i] * 0x1p22f * unscale[c];
                             const int64_t at = (int64_t)(lo + base + c) * a.y_stride + ya;
                             if constexpr (UP) {
                                 if (ya < a.N) store_y(a.y, a.y_type, at, v0 / (1.0f + expf(-v0)) * v1);
