@@ -309,11 +309,11 @@ moe_status moe_rmsnorm_bf16(const float* x, const float* gamma, int T, int H, fl
  *   replays with the bits of the eager one.
  * Kernels (moe_grouped_path tells which): MOE_GROUPED_ROWS streams the weights of the experts that
  *   have rows through the warps' matrix instructions; MOE_GROUPED_TENSOR tiles 256 weight rows
- *   by up to 256 of an expert's rows on tcgen05.  Both sum in fp32, in a fixed order; with y_type MOE_F32 long sums
- *   are made of runs of at most 768 elements (gated: 384) that are added with rounding, so that the error of the
- *   matrix instructions, which cut their sums off, does not grow with n_in (about 7e-7 relative, in norm); 16-bit outputs
- *   are summed in one run, whose error (8e-6 at 7168, gated 1.6e-5) is below a thirtieth of their half step for bf16 and
- *   a tenth for fp16.
+ *   by up to 256 of an expert's rows on tcgen05.  Both sum in fp32, in a fixed order; long sums
+ *   are made of runs that are added with rounding, so that the error of the matrix instructions, which cut their sums
+ *   off, does not grow with n_in: of at most 768 elements (gated: 384) with y_type MOE_F32 (about 7e-7 relative, in
+ *   norm), of at most 8192 with a 16-bit y_type, whose error (9e-6, gated 1.8e-5) is below a 27th of its half step for fp16
+ *   and a 200th for bf16.
  * Errors: MOE_ERR_INVALID_ARG (NULL, size, stride, alignment), MOE_ERR_UNSUPPORTED (a type),
  *   MOE_ERR_CUDA (a launch failed).
  */

@@ -45,13 +45,15 @@ constexpr int kThreads = 32 * (2 + kEpiWarps + kGatherWarps);
 constexpr int kExchBytes = 4 * 2 * 2 * 8 * 32 * 4;       // [warp pair][buffer][half][column][lane] floats
 constexpr uint32_t kTmemCols = 512;
 // The tensor cores cut the sum off after each instruction instead of rounding it: an error towards zero that grows
-// with the length of the sum (relative, in norm: 7e-7 over 768 elements, 8e-6 over 7168, twice that gated), far
-// below half a step of a 16-bit output but not of an fp32 one.  There a sum is made of runs of at most kRun steps,
-// which the epilogue adds with rounding in TMEM: columns kSumCol.., so that a tile has at most 128 columns.
+// with the length of the sum (relative, in norm: 7e-7 over 768 elements, 8e-6 over 7168, 2.7e-4 over 2^18, twice that gated).
+// So a sum is made of runs of at most kRun steps, which the epilogue adds with rounding in TMEM: columns kSumCol..,
+// so that a tile of more than one run has at most 128 columns.  fp32 outputs have short runs; 16-bit outputs have runs
+// of 8192 elements, whose error (9e-6, gated 1.8e-5) is below a 27th of half a step of fp16.
 // Measured with runs / without, fp32 outputs: 4096 tokens gated 265 / 181 us (error 6.9e-7 / 4.2e-6), 2048 tokens, 6 of 64
 // experts of 7168 -> 1024 221 / 181 us (7.2e-7 / 7.9e-6), 64 tokens of those 156 / 154 us.
 constexpr int kSumCol = 128;
-template <bool UP> constexpr int kRun = UP ? 6 : 12;     // steps of 64
+template <bool UP> constexpr int kRun = UP ? 6 : 12;     // steps of 64, fp32 outputs
+constexpr int kRun16 = 128;                              // 16-bit outputs
 constexpr int kSpins = 64;                               // tests of a barrier before a wait looks at the clock
 
 struct DenseParams {
@@ -304,40 +306,38 @@ __device__ __forceinline__ void epilogue(const DenseParams& p, const Order& orde
         int b = j & 1;
         if (!complete(b)) break;
         uint32_t acc = lanes + (uint32_t)b * kMaxN;
-        const bool runs = sizeof(T) == 4 && p.run < nk;
-        if constexpr (sizeof(T) == 4) {
-            if (runs) {
-                // this warp's columns of the runs, summed where it reads them from afterwards
-                constexpr int kCols = UP ? 16 : 32;
-                bool ok = true;
-                for (int k0 = 0;;) {
-                    for (int c0 = kCols * side; c0 < ti.ntok; c0 += 2 * kCols)
+        const bool runs = p.run < nk;
+        if (runs) {
+            // this warp's columns of the runs, summed where it reads them from afterwards
+            constexpr int kCols = UP ? 16 : 32;
+            bool ok = true;
+            for (int k0 = 0;;) {
+                for (int c0 = kCols * side; c0 < ti.ntok; c0 += 2 * kCols)
 #pragma unroll
-                        for (int h = 0; h < kCols; h += 16) {
-                            uint32_t r[16], s[16];
-                            tmem_ld16(acc + c0 + h, r);
-                            if (k0 > 0) {
-                                tmem_ld16(lanes + kSumCol + c0 + h, s);
-                                tmem_ld_wait();
+                    for (int h = 0; h < kCols; h += 16) {
+                        uint32_t r[16], s[16];
+                        tmem_ld16(acc + c0 + h, r);
+                        if (k0 > 0) {
+                            tmem_ld16(lanes + kSumCol + c0 + h, s);
+                            tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    r[i] = __float_as_uint(__fadd_rn(__uint_as_float(s[i]), __uint_as_float(r[i])));
-                            } else {
-                                tmem_ld_wait();
-                            }
-                            tmem_st16(lanes + kSumCol + c0 + h, r);
+                            for (int i = 0; i < 16; ++i)
+                                r[i] = __float_as_uint(__fadd_rn(__uint_as_float(s[i]), __uint_as_float(r[i])));
+                        } else {
+                            tmem_ld_wait();
                         }
-                    tmem_st_wait();
-                    release(b);
-                    if ((k0 += p.run) >= nk) break;
-                    b = ++j & 1;
-                    ok = complete(b);
-                    if (!ok) break;
-                    acc = lanes + (uint32_t)b * kMaxN;
-                }
+                        tmem_st16(lanes + kSumCol + c0 + h, r);
+                    }
+                tmem_st_wait();
+                release(b);
+                if ((k0 += p.run) >= nk) break;
+                b = ++j & 1;
+                ok = complete(b);
                 if (!ok) break;
-                acc = lanes + kSumCol;
+                acc = lanes + (uint32_t)b * kMaxN;
             }
+            if (!ok) break;
+            acc = lanes + kSumCol;
         }
         if constexpr (UP) {
             const int row = ti.mb * kRowsTile + cta * 64 + (q & 1) * 32 + lane;
@@ -773,8 +773,8 @@ cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s) {
     p.y = a.y; p.y_type = a.y_type; p.y_stride = a.y_stride; p.status = a.status;
     const WaitCfg wc = wait_cfg();
     p.wait_ns = wc.limit_ns; p.stall = wc.stall;
-    const int nk = (a.K + kStepK - 1) / kStepK, longest = a.w1 ? kRun<true> : kRun<false>;
-    const int n_runs = a.y_type == MOE_F32 ? (nk + longest - 1) / longest : 1;
+    const int nk = (a.K + kStepK - 1) / kStepK, longest = a.y_type != MOE_F32 ? kRun16 : a.w1 ? kRun<true> : kRun<false>;
+    const int n_runs = (nk + longest - 1) / longest;
     p.run = (nk + n_runs - 1) / n_runs;
     p.max_n = n_runs > 1 ? kSumCol : kMaxN;
     const int v = (a.w1 ? 2 : 0) + (a.in_out ? 1 : 0);
