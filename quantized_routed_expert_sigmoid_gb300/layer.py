@@ -37,6 +37,18 @@ def prepare_q8_0(t, rows: int, cols: int, n_experts: int = 1):
     return dst.view(*shape)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for what a call on `stream` writes, in the order of that stream: from the current stream's memory it could
+    be a block that kernels waiting there have yet to read, and would go back there while `stream` still writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = N._stream(stream)       # (0 and 1 are two names of the default stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class MoeLayer:
     """gate/up: uint8 [E, I, rb(H)], down: uint8 [E, H, rb(I)] on the GPU (qtype, or
     qtype_down for down); shared expert matrices in shared_qtype."""
@@ -90,18 +102,19 @@ class MoeLayer:
     def workspace_bytes(self, T: int) -> int:
         return N.moe_layer_workspace_size(self.plan, T)
 
-    def ensure_workspace(self, T: int, device=None):
+    def ensure_workspace(self, T: int, device=None, stream=None):
         if self.ws is None or T > self.ws_T:
             nbytes = self.workspace_bytes(T)
-            self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+            self.ws = _empty(nbytes, torch.uint8, device or "cuda", stream)
             self.ws_T = T
         return self.ws
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """An output that is not given is made in the order of `stream`, as under torch.cuda.stream(stream)."""
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.float32, device=x.device)
-        ws = self.ensure_workspace(T, x.device)
+            out = _empty((T, self.H), torch.float32, x.device, stream)
+        ws = self.ensure_workspace(T, x.device, stream)
         N.moe_layer(self.plan, x, T, out, ws, ws.numel(), stream)
         return out
 
@@ -178,7 +191,8 @@ class _Products:
         With sorted_pairs (int32 [T*k], moe_permute's) x holds the T tokens, row i being that of token
         sorted_pairs[i] // k; without, x holds the T*k rows in sorted order.  offsets (int32 [E+1], moe_permute's) may
         be left out for one expert.  status: int32 [1], raised when a device-side check fails.  All of them are on the
-        weights' device, which has to be the current one.
+        weights' device, which has to be the current one.  stream (None: the current one) has to come after what wrote
+        the inputs; without out, y is made in the order of that stream, as under torch.cuda.stream(stream).
         """
         if k < 1:
             raise ValueError(f"k = {k}: a token has at least one expert")
@@ -198,7 +212,7 @@ class _Products:
         if status is not None and (status.dtype is not torch.int32 or status.numel() < 1 or not status.is_cuda):
             raise ValueError("status must be an int32 CUDA tensor")
         if out is None:
-            out = torch.empty((P, self.n_out), dtype=self.y_dtype, device=x.device)
+            out = _empty((P, self.n_out), self.y_dtype, x.device, stream)
         elif out.dtype is not self.y_dtype or out.shape != (P, self.n_out) or not out.is_cuda:
             raise ValueError(f"out must be a {self.y_dtype} CUDA tensor [{P}, {self.n_out}]")
         _on_current(self.device, x=x, offsets=offsets, sorted_pairs=sorted_pairs, out=out, status=status)
@@ -325,16 +339,16 @@ class NormResidual:
 
         x (None: 0), y: [T, H].  gate: fp32, broadcastable to [T, H] ([H], [1, H], [T, 1] or [T, H]).
         Outputs that are not given are made: x_out like x (or y), u in bf16 when gamma_pre was given.  All tensors are
-        on one device, which has to be the current one.
+        on one device, which has to be the current one; stream as in the products' calls.
         """
         shape = y.shape
         T, H = shape
         if H != self.H:
             raise ValueError(f"y must be [T, {self.H}]")
         if x_out is None:
-            x_out = torch.empty((T, H), dtype=(x if x is not None else y).dtype, device=y.device)
+            x_out = _empty((T, H), (x if x is not None else y).dtype, y.device, stream)
         if u is None and self._keep[1] is not None:
-            u = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+            u = _empty((T, H), torch.bfloat16, y.device, stream)
         xs = us = gate_row = gate_col = 0
         ys = self._rows(y, "y", shape)
         os = self._rows(x_out, "x_out", shape)
