@@ -347,10 +347,9 @@ moe_status moe_grouped_matmul(const moe_grouped_plan* plan, const void* x, int64
  *   zeros (nullable): uint8 [n_experts][n_out][n_in / group], values 0..15 (the low four bits are used);
  *   NULL: every zero point is 8.  group: 32, 64 or 128;  n_in a multiple of group,
  *   at most 32768.
- * A group's products of codes and x are exact and summed in fp32, the zero point is taken off that sum
- * and the scale applied to it in fp32: no weight is rounded.  x is held as fp16 scaled by a power of two
- * of its row's largest magnitude: exact down to 2^-27 of that (a row with an infinity gives infinities or NaN, a row of
- * nothing but subnormal numbers zeros).
+ * Products of q - zero and x are exact and summed in fp32 over a group, the scale is applied to that sum in fp32: no
+ * weight is rounded, and one that equals its zero point adds nothing.  x is held as fp16: fp16 rows exactly, bf16 rows
+ * scaled by a power of two of their largest finite magnitude, exactly down to 2^-31 of that.
  * For a few rows an expert (decode): an active expert's codes are read once per 8 or 16 of its rows.
  * Arguments, routing, y and status as moe_grouped_matmul; x of x_type MOE_BF16 or MOE_F16.
  * q, q_up 16-byte aligned; scales and zeros aligned to their element.  One launch, no workspace.

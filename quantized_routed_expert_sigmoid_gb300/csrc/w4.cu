@@ -1,6 +1,6 @@
 // w4.cu -- products of a few rows per expert with 4-bit weights and group scales.
 //
-//   y[i, n] = sum_g s[n, g] * (sum_{c in g} q[n, c] v_i[c] - z[n, g] * sum_{c in g} v_i[c])
+//   y[i, n] = sum_g s[n, g] * sum_{c in g} (q[n, c] - z[n, g]) v_i[c]
 // (and silu(W v) * (W_up v) of two such products), v_i = x[sorted_pairs[i] / k] or x[i].
 //
 // Bound: the bytes of the codes and scales; next to that the instructions that turn a code into an
@@ -10,28 +10,29 @@
 //   warps' reads of 8 rows x 16 bytes free of bank conflicts.
 // - The products run on the warps' m16n8k16 instruction, weights as the 16-row operand (8 rows of W
 //   and the same 8 of W_up when gated, so that both halves of an output meet in one thread), up to 8 rows of
-//   x as its columns.  Its sum over c may run in any order, so codes are used in the order in which they lie: a
-//   32-bit word gives four operand registers by one mask each and two shifts: nibble j and j + 4 become the 16-bit
-//   halves, at bits 2..5 (nibbles 0, 2) or 6..9 (1, 3).  A masked nibble q, read as fp16, is the subnormal q * 2^-22 or
-//   q * 2^-18 (x is stored with 1/16 there).  Where in the subnormal the code lies does not change its products, but
-//   the sums of the instruction lose low bits with it, as if products were lined up by the operands' exponent
-//   fields.  Measured for fp16 x, largest relative error of fp32 outputs over 20 inputs of 64 to 2080 elements, and
-//   time of the large case below: bits 0..3 and 4..7 2.1e-6, 381 us; this 2.5e-7, 385 us; all at 4..7 1.4e-7, 401 us;
-//   all at 6..9 1.6e-7, 410 us (the same in 32 bits without matrix instructions: 1.5e-7).
-// - The zero point is taken off the group's sum, with the group's sum of x: z is at most 15, so that costs at
-//   most one bit of the fp32 sum.  Sums are fp32; the scale is applied to them in fp32.
-// - x is staged once per expert: scaled by a power of two of its row's largest magnitude into fp16 (a
-//   value keeps all its bits down to 2^-27 of the largest; what is lost below is less than the
-//   rounding of the fp32 sum), in the word order of the codes, with the sums of each group.
+//   x as its columns.  Its sum over c may run in any order, so codes are used in the order in which they lie: nibbles
+//   j and j + 4 of a 32-bit word become the 16-bit halves of an operand register.  Put into the low bits of 1024.0 in
+//   fp16 a nibble is 1024 + q (or, four bits higher, 1024 + 16 q); adding -1024 - z (or multiplying by 1/16 and
+//   adding -64 - z) leaves q - z, exactly: one mask, one packed addition and half a shift an operand.
+// - So a weight that equals its zero point is a 0 and adds nothing, whatever x is there.  (Taking z sum x off sum q x
+//   instead, with the codes as they are, saved the addition, but both sums are rounded to their own size: a
+//   channel of x far above the others whose codes equal the zero point left an error in proportion to it,
+//   8.6e-4 of the result at 20000 times the others.)
+// - A group's sum is at most two chains of four instructions, and the scale is applied to it in fp32.
+// - x is staged once per expert as fp16, in the word order of the codes: bf16 rows scaled by a power of two so that their
+//   largest finite magnitude is 2^14 to 2^15 (a value keeps all its bits down to 2^-31 of the largest), fp16 rows
+//   scaled up only, which loses nothing.
 // 8 computing warps (4 sets of 32 weight rows, every other stage each, joined at the end of a unit), one warp
 // that issues the codes' copies and three that copy scales and zero points, a stage each in turn (one warp for
 // both took 1400 clocks a stage); a CTA per SM takes an even share of the (expert, 128 rows) units.
 //
 // Measured (device time): 16 tokens, 8 of 256 experts, 7168 -> 2048 gated, groups of 32 with zero points:
-// 385 us for 1.78 GB (266 us at the copy's rate).  What bounds it now is the matrix instruction: 512 of them a
-// stage and SM, one in 16 clocks on each of the four schedulers, against about 700 clocks that HBM needs for the stage; an
-// earlier form of 445 us took 292 us without its products.  One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 8.1 us for 13 MB, the
-// most of it the start: routing read, x staged, the first copies (4 us).
+// 437 us for 1.78 GB (266 us at the copy's rate; 385 us with the zero points taken off the sums).  What bounds it now is the issue of
+// instructions: two computing warps a scheduler find one to issue in 61 % of the clocks (32 experts of that size, one row each: DRAM 48 %,
+// ALU pipe 58 %), and every instruction more shows (8 additions a group: 478 us); the 128 matrix instructions of
+// a stage, one in 16 clocks on each of the four schedulers, take 512 of the 700 clocks that HBM needs for it beside that.
+// One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 9.3 us for 13 MB; 96 units of 64 outputs leave 56 of
+// 152 SMs without work, and each CTA's eight stages follow a start of 4 us (routing read, x staged, the first copies).
 #include <type_traits>
 
 #include "products.cuh"
@@ -46,7 +47,18 @@ constexpr int kTiles = 2, kScaleWarps = 3, kAllWarps = kWarps + 1 + kScaleWarps,
 constexpr int kStages = 6, kStageBytes = 128 * 128, kStageK = 256;
 constexpr int kSmemMax = 227 * 1024;
 
-constexpr uint32_t kCode = 0x03C003C0u;    // bits 6..9 of each half
+// A word's nibbles 0 and 4 (1 and 5) as the halves of q - z: nz is -1024 - z (-64 - z) in both halves.
+__device__ __forceinline__ uint32_t low_codes(uint32_t v, uint32_t nz) {
+    const uint32_t m = (v & 0x000F000Fu) | 0x64006400u;      // 1024 + q
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&nz));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t v, uint32_t nz) {
+    const uint32_t m = (v & 0x00F000F0u) | 0x64006400u, sixteenth = 0x2C002C00u;   // 1024 + 16 q
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&sixteenth),
+                              *reinterpret_cast<const __half2*>(&nz));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 struct W4Params {
     CUtensorMap tw0, tw1;        // codes of W and W_up: [E * N][K / 2] bytes, boxes of 128 bytes x 128 (gated: 64) rows
     RowsArgs a;
@@ -140,8 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     const int n_groups = a.K / G, n_ks = (a.K + kStageK - 1) / kStageK;
     uint8_t* scales = ring_base + kStages * kStageBytes;   // [stages] scales, then zero points, of 128 rows
     uint8_t* xs = scales + kStages * stage_scales<G>();    // staged x: p.cols rows, p.x_stride bytes apart
-    float* sums = reinterpret_cast<float*>(xs + (size_t)p.cols * p.x_stride);   // [n_ks * kGroups][kCols]
-    float* unscale = sums + (size_t)n_ks * kGroups * kCols;                     // [kCols] the rows' powers of two
+    float* unscale = reinterpret_cast<float*>(xs + (size_t)p.cols * p.x_stride);   // [kCols] the rows' powers of two
     float* join = unscale + kCols;                         // [2][kTiles * 4 * NT][32 * kRowWarps] one of two warps' sums
     float* largest = join + 2 * kJoin;                     // [kWarps]
     uint64_t* full = reinterpret_cast<uint64_t*>(largest + kWarps);
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                         float v[8];
                         values(held[h], v);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
+                        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]) <= 3.402823466e38f ? fabsf(v[j]) : 0.f);
                     }
                 }
 #pragma unroll
@@ -339,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     computing_sync();
                     for (int w = 0; w < wc; ++w) most = fmaxf(most, largest[warp - sub + w]);
                 }
-                // the largest becomes 2^14 .. 2^15 (a row of zeros, and one that is not finite, stay)
+                // the largest finite magnitude becomes 2^14 .. 2^15 (that of a tiny row less: its values are exact all the
+                // same); infinities and NaN stay what they are
                 const int mexp = (int)(__float_as_uint(most) >> 23);
-                const int ex = mexp == 0 || mexp == 255 ? 0 : min(max(mexp - 127 - 14, -120), 113);
+                const int ex = min(max(mexp - 127 - 14, -120), a.bf16 ? 113 : 0);
                 const float scale = __int_as_float((127 - ex) << 23);
                 if (c < nc && sub == 0 && lane == 0) unscale[c] = __int_as_float((127 + ex) << 23);
                 const bool kept = kHold * step >= a.K;
@@ -357,23 +369,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     for (int h = 0; h < kHold; ++h) {
                         const int at = i + h * step;
                         if (at - 8 * lane >= n_ks * kStageK) break;          // (the same for the whole warp)
-                        float v[8], sum = 0.f;
+                        float v[8];
                         values(held[h], v);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            v[j] *= scale;
-                            sum += v[j];
-                        }
-                        const __half2 h0 = __floats2half2_rn(v[0], v[4]), h1 = __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f);
-                        const __half2 h2 = __floats2half2_rn(v[2], v[6]), h3 = __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f);
-#pragma unroll
-                        for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                        if (c < nc && at < n_ks * kStageK) {
+                        for (int j = 0; j < 8; ++j) v[j] *= scale;
+                        const __half2 h0 = __floats2half2_rn(v[0], v[4]), h1 = __floats2half2_rn(v[1], v[5]);
+                        const __half2 h2 = __floats2half2_rn(v[2], v[6]), h3 = __floats2half2_rn(v[3], v[7]);
+                        if (c < nc && at < n_ks * kStageK)
                             *reinterpret_cast<uint4*>(xs + (size_t)c * p.x_stride + 2 * at) =
                                 make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
                                            *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
-                            if (lane % (G / 8) == 0) sums[(at / G) * kCols + c] = sum;
-                        }
                     }
                 }
                 if (wc > 1 && c0 + kWarps / wc < nc) computing_sync();       // (largest is used again)
@@ -389,7 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                 has[n] = 8 * n + g < nc;
                 xc[n] = xs0 + (uint32_t)(min(8 * n + g, nc - 1) * p.x_stride);
             }
-            const uint32_t sums0 = su32(sums) + (uint32_t)(2 * t * 4);
             // Lane g's row of eight: the lanes whose reads go out together (8 lanes of 16 bytes, 16 of 8, 32 of 4) need
             // rows whose swizzles keep them in different banks: two rows that differ in bit 2, four in bits 1 and 2.
             const int gr = G == 128 ? (g & 1) << 2 | g >> 1 : G == 64 ? (g & 3) << 1 | g >> 2 : g;
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     const bool stalled = p.stall && u - b1 + b == u0 && ks == 0;      // (test setting)
                     wait(stalled ? never : &full[s], stalled ? 0u : ph);
                     const uint32_t codes = ring0 + s * kStageBytes;
-                    const uint32_t xk = (uint32_t)(ks * kStageK * 2), sk = sums0 + (uint32_t)(ks * kGroups * kCols * 4);
+                    const uint32_t xk = (uint32_t)(ks * kStageK * 2);
                     // the rows' scales and zero points: [tile][half]
                     constexpr int kS = scale_bytes<G>() / 4, kZ = zero_bytes<G>() / 4;
                     uint32_t fs[kTiles][2][kS], fz[kTiles][2][kZ];
@@ -456,6 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
                                 lds_words<G / 8>((codes ^ (uint32_t)(q * (G / 2))) + (j * kTileStep + h * kHalfStep) * 128, v[j][h]);
+                        // -1024 - z and -64 - z of the rows, in both halves
+                        uint32_t nz[kTiles][2], nz64[kTiles][2];
+#pragma unroll
+                        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                nz[j][h] = __byte_perm(fz[j][h][q >> 2], 0xE4E4E4E4u, 0x4040u + (q & 3) * 0x0101u);
+                                const uint32_t k960 = 0x63806380u;
+                                const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&nz[j][h]), *reinterpret_cast<const __half2*>(&k960));
+                                nz64[j][h] = *reinterpret_cast<const uint32_t*>(&r);
+                            }
                         // (two chains of products, of the low and of the high halves of the words)
                         float part[kTiles][NA][4], high[kTiles][NA][4];
 #pragma unroll
@@ -466,8 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 #pragma unroll
                                 for (int j = 0; j < kTiles; ++j) {
                                     const uint32_t va = v[j][0][w], vb = v[j][1][w];
-                                    const uint32_t al = va << 2, ah = va >> 6, a0 = al & 0x003C003Cu, a1 = al & kCode, a2 = ah & 0x003C003Cu, a3 = ah & kCode;
-                                    const uint32_t bl = vb << 2, bh = vb >> 6, b0 = bl & 0x003C003Cu, b1 = bl & kCode, b2 = bh & 0x003C003Cu, b3 = bh & kCode;
+                                    const uint32_t a0 = low_codes(va, nz[j][0]), a1 = high_codes(va, nz64[j][0]);
+                                    const uint32_t a2 = low_codes(va >> 8, nz[j][0]), a3 = high_codes(va >> 8, nz64[j][0]);
+                                    const uint32_t b0 = low_codes(vb, nz[j][1]), b1 = high_codes(vb, nz64[j][1]);
+                                    const uint32_t b2 = low_codes(vb >> 8, nz[j][1]), b3 = high_codes(vb >> 8, nz64[j][1]);
                                     float(&lo)[4] = part[j][n];
                                     float(&hi)[4] = kWords > 1 ? high[j][n] : part[j][n];
                                     if (w == 0) mma_f16_16816_first(lo, a0, b0, a1, b1, x.x, x.y);
@@ -477,12 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                                 }
                             }
 #pragma unroll
-                        for (int n = 0; n < NA; ++n) {
-                            const uint32_t xa = sk + (uint32_t)((q * kCols + 8 * n) * 4);
-                            uint2 xw;
-                            if constexpr (kKind == 0) xw.x = xw.y = lds4(xa);
-                            else xw = lds8(xa);
-                            const float x0 = __uint_as_float(xw.x), x1 = __uint_as_float(xw.y);
+                        for (int n = 0; n < NA; ++n)
 #pragma unroll
                             for (int j = 0; j < kTiles; ++j)
 #pragma unroll
@@ -495,18 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                                         const __half2 hw = *reinterpret_cast<const __half2*>(&sw);
                                         f = q & 1 ? __high2float(hw) : __low2float(hw);
                                     }
-                                    // -z * 2^-22, exactly: 2^23 + z as a float's bits, times -2^-22, plus 2
-                                    const float z = fmaf(__uint_as_float(__byte_perm(fz[j][h][q >> 2], 0x4B000000u, 0x7650u | (q & 3))),
-                                                         -0x1p-22f, 2.0f);
                                     float p0 = part[j][n][2 * h], p1 = part[j][n][2 * h + 1];
                                     if constexpr (kWords > 1) {
                                         p0 += high[j][n][2 * h];
                                         p1 += high[j][n][2 * h + 1];
                                     }
-                                    acc[j][n][2 * h] = fmaf(f, fmaf(z, x0, p0), acc[j][n][2 * h]);
-                                    if constexpr (kKind != 0) acc[j][n][2 * h + 1] = fmaf(f, fmaf(z, x1, p1), acc[j][n][2 * h + 1]);
+                                    acc[j][n][2 * h] = fmaf(f, p0, acc[j][n][2 * h]);
+                                    if constexpr (kKind != 0) acc[j][n][2 * h + 1] = fmaf(f, p1, acc[j][n][2 * h + 1]);
                                 }
-                        }
                     };
                     auto groups = [&](auto kind) {
                         const int left = n_groups - ks * kGroups;
@@ -543,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                         for (int i = 0; i < 2; ++i) {
                             const int c = 8 * n + 2 * t + i, ya = b * kUnit + ra[j];
                             if (c >= nc) continue;
-                            const float v0 = acc[j][n][i] * 0x1p22f * unscale[c], v1 = acc[j][n][2 + i] * 0x1p22f * unscale[c];
+                            const float v0 = acc[j][n][i] * unscale[c], v1 = acc[j][n][2 + i] * unscale[c];
                             const int64_t at = (int64_t)(lo + base + c) * a.y_stride + ya;
                             if constexpr (UP) {
                                 if (ya < a.N) store_y(a.y, a.y_type, at, v0 / (1.0f + expf(-v0)) * v1);
@@ -571,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
 }
 
 template <int G, bool UP, int NT>
-size_t fixed_bytes(const RowsArgs& a, int n_ks) {
-    return 1024 + (size_t)kStages * (kStageBytes + stage_scales<G>()) + (size_t)n_ks * (kStageK / G) * 8 * NT * 4 + 8 * NT * 4 + 2 * kTiles * 4 * NT * 32 * kRowWarps * 4 +
+size_t fixed_bytes(const RowsArgs& a) {
+    return 1024 + (size_t)kStages * (kStageBytes + stage_scales<G>()) + 8 * NT * 4 + 2 * kTiles * 4 * NT * 32 * kRowWarps * 4 +
            kWarps * 4 + (2 * kStages + 2) * 8 + 80 +
            (size_t)(a.E + 1) * 4 + (size_t)a.E * 2;
 }
@@ -583,7 +591,7 @@ cudaError_t launch_as(const RowsArgs& a, cudaStream_t s) {
     p.a = a;
     const int n_ks = (a.K + kStageK - 1) / kStageK;
     p.x_stride = n_ks * kStageK * 2 + 64;               // (8 rows' 16-byte reads fall into different banks)
-    const size_t fixed = fixed_bytes<G, UP, NT>(a, n_ks);
+    const size_t fixed = fixed_bytes<G, UP, NT>(a);
     const int most = a.offsets ? a.P / a.k : a.P;
     p.cols = (int)(((size_t)kSmemMax - fixed) / p.x_stride);
     if (p.cols > 8 * NT) p.cols = 8 * NT;
@@ -619,7 +627,7 @@ cudaError_t launch_g(const RowsArgs& a, cudaStream_t s) {
     // 16 rows at once where a token batch has more than 8 and they fit beside the ring
     const int n_ks = (a.K + kStageK - 1) / kStageK;
     const bool two = (a.offsets ? a.P / a.k : a.P) > 8 &&
-                     fixed_bytes<G, true, 2>(a, n_ks) + 16 * ((size_t)n_ks * kStageK * 2 + 64) <= (size_t)kSmemMax;
+                     fixed_bytes<G, true, 2>(a) + 16 * ((size_t)n_ks * kStageK * 2 + 64) <= (size_t)kSmemMax;
     if (a.w1) return two ? launch<G, true, 2>(a, s) : launch<G, true, 1>(a, s);
     return two ? launch<G, false, 2>(a, s) : launch<G, false, 1>(a, s);
 }
