@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     uint64_t* never = empty + kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
     int* cnt = reinterpret_cast<int*>(never + 2);          // [kAllWarps]
+    int* done = cnt + kAllWarps;                           // [kScaleWarps] last step + 1 that a scale warp has arrived for
     int* off = cnt + 20;                                   // [E + 1]
     uint16_t* expert = reinterpret_cast<uint16_t*>(off + a.E + 1);   // [E] those with rows
 
@@ -204,8 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
     const uint32_t share = units / gridDim.x, more = units - share * gridDim.x;
     const uint32_t u0 = share * blockIdx.x + min(blockIdx.x, more), u1 = u0 + share + (blockIdx.x < more ? 1 : 0);
 
-    // Bounded wait; after a wait has run out every wait returns at once and the loops run to their
-    // ends without waiting, loading or storing, so that the CTA's barriers stay matched.
+    // Bounded wait; after a wait has run out every wait returns at once and the loops run to their ends, so that the
+    // CTA's barriers stay matched: nothing more is copied into the ring, no warp arrives for a step that it has not
+    // filled, and nothing is stored.
     auto wait = [&](uint64_t* b, uint32_t parity) {
         for (int i = 0; i < 64; ++i) {
             if (mbar_test(b, parity)) return;
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
             if (gtime() - t0 > p.wait_ns) { *abort_flag = 1; return; }
         }
     };
-    int s = 0, n_issued = 0, step = 0;
+    int s = 0, n_issued = 0, step = 0, last = 0;
     uint32_t ph = 0;
     for (uint32_t u = u0; u < u1;) {
         // the units of one expert
@@ -256,10 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                     for (int i = 0; i < 4; ++i)
                         at[i] = ((int64_t)e * a.N + min(b * kUnit + (UP ? (32 * i + lane) & 63 : 32 * i + lane), a.N - 1)) * n_groups;
                     for (int ks = 0; ks < n_ks; ++ks) {
-                        const bool mine = step % kScaleWarps == warp - kWarps - 1;
+                        bool mine = step % kScaleWarps == warp - kWarps - 1;
                         ++step;
                         if (mine) {
                             wait(&empty[s], ph ^ 1);
+                            __syncwarp();
+                            mine = !__any_sync(0xffffffffu, *abort_flag);
+                        }
+                        if (mine) {
+                            last = step;
                             uint8_t* to = scales + s * stage_scales<G>();
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -564,15 +571,19 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
         }
     }
     if (bad && a.status) atomicCAS(a.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
+    if (warp > kWarps && lane == 0) done[warp - kWarps - 1] = last;
     __syncthreads();
     if (tid == kWarps * 32 && *abort_flag) {
-        // codes that no warp waited for may still be in flight: wait (within the limit) for their stages
-        // (the other warps have waited for their own copies and arrived)
-        for (int i = 0; i < min(n_issued, kStages); ++i) {
-            const int step = n_issued - 1 - i;
-            const uint64_t t0 = gtime();
-            while (!mbar_test(&full[step % kStages], (step / kStages) & 1) && gtime() - t0 < p.wait_ns) {}
-        }
+        // codes that no warp waited for may still be in flight: complete the phases of the steps that each stage was last
+        // filled for, on behalf of the scale warps that have not arrived for them, and wait, within the limit, for the
+        // bytes.  The scale warps have waited for their own copies.
+        const int first = max(0, n_issued - kStages);
+        for (int i = first; i < n_issued; ++i)
+            if (done[i % kScaleWarps] <= i)
+                for (int l = 0; l < 32; ++l) mbar_arrive(&full[i % kStages]);
+        const uint64_t t0 = gtime();
+        for (int i = first; i < n_issued; ++i)
+            while (!mbar_test(&full[i % kStages], (i / kStages) & 1) && gtime() - t0 < p.wait_ns) {}
         if (a.status) atomicCAS(a.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
     }
     __syncthreads();
