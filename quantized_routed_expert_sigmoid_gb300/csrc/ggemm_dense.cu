@@ -380,11 +380,7 @@ __device__ __forceinline__ void epilogue(const DenseParams& p, const Order& orde
 #pragma unroll
                 for (int i = 0; i < 8; ++i, at += p.y_stride) {
                     const float gv = is_up ? other[i] : keep[i], uv = is_up ? keep[i] : other[i];
-                    // (the approximate division is off by at most two units; its 0 for a divisor above 2^126
-                    // is what the exact one rounds to.  __expf is off by 2^-21 at most for the |g| whose
-                    // exponential matters beside 1, far below a 16-bit output's half step)
-                    const float ex = sizeof(T) == 2 ? __expf(-gv) : expf(-gv);
-                    if (i < n) *at = to_out<T>(__fdividef(gv, 1.0f + ex) * uv);
+                    if (i < n) *at = to_out<T>(silu_times<sizeof(T) == 2>(gv, uv));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) keep[i] = next[i];

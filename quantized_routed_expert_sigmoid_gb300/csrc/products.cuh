@@ -54,6 +54,17 @@ struct RowsArgs {
 };
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);            // streams the weights (rows.cu)
 cudaError_t launch_w4(const RowsArgs& a, cudaStream_t s);              // 4-bit weights (w4.cu)
+
+// silu(g) u = g / (1 + e^-g) u, from e^-|g|, which does not overflow: g / (1 + e^-g) with an e^-g past the largest number is 0
+// from g = -88.7 down, where silu is -2e-37 (and the quick division gives 0 from -87.3).  silu(g) is an fp32 number, below 2^-126
+// with the spacing of the subnormal ones.  FAST, for 16-bit outputs: the quick exponential is off by at most
+// 2 + 1.173 |g| units of 2^-23 (1.3e-5 at g = -88, a 39th of half a step of fp16), the quick division, by 1 to 2, by 2 units.
+template <bool FAST>
+__device__ __forceinline__ float silu_times(float g, float u) {
+    const float z = FAST ? __expf(-fabsf(g)) : expf(-fabsf(g));
+    const float top = g >= 0.f ? g : g * z;
+    return (FAST ? __fdividef(top, 1.0f + z) : top / (1.0f + z)) * u;
+}
 constexpr int kMaxW4In = 32768;      // n_in of 4-bit weights: one staged row of x has to fit beside the ring
 cudaError_t launch_grouped_dense(const RowsArgs& a, cudaStream_t s);   // tcgen05, dense weights (ggemm_dense.cu)
 

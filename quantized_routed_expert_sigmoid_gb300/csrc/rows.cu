@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? W::kCtas : 1) rows_kernel(
                 const int col = base + 8 * n + 2 * (lane & 3) + (f & 1), r = r0 + W::row(f >> 2, g, (f >> 1) & 1);
                 if (col < cnt && r < a.N) {
                     float out = v[0];
-                    if constexpr (kMats == 2) out = v[0] / (1.0f + expf(-v[0])) * v[1];
+                    if constexpr (kMats == 2) out = silu_times<false>(v[0], v[1]);
                     store_y(a.y, a.y_type, (int64_t)(lo + col) * a.y_stride + r, out);
                 }
             }

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                             const float v0 = acc[j][n][i] * unscale[c], v1 = acc[j][n][2 + i] * unscale[c];
                             const int64_t at = (int64_t)(lo + base + c) * a.y_stride + ya;
                             if constexpr (UP) {
-                                if (ya < a.N) store_y(a.y, a.y_type, at, v0 / (1.0f + expf(-v0)) * v1);
+                                if (ya < a.N) store_y(a.y, a.y_type, at, silu_times<false>(v0, v1));
                             } else {
                                 if (ya < a.N) store_y(a.y, a.y_type, at, v0);
                                 if (ya + 8 < a.N) store_y(a.y, a.y_type, at + 8, v1);
