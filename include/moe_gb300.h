@@ -301,7 +301,8 @@ moe_status moe_rmsnorm_bf16(const float* x, const float* gamma, int T, int H, fl
  *   with sorted_pairs, else T*k rows; offsets (device) int32 [n_experts + 1], non-decreasing within
  *   0..T*k (NULL: one expert over all T*k rows); y (device, aligned to its type) rows y_stride >= n_out elements
  *   apart.  Rows of y outside [offsets[0], offsets[n_experts]) are left as they were.  y must not
- *   overlap x.  status (device int32, nullable, caller-owned, never cleared by the call) is
+ *   overlap x: their rows may be columns of one buffer (one stride in bytes), else their spans must not meet.
+ *   status (device int32, nullable, caller-owned, never cleared by the call) is
  *   raised from MOE_OK to MOE_ERR_DEVICE_CHECK when an offset leaves 0..T*k or decreases (it is
  *   clamped) or a pair leaves 0..T*k-1 (its row of y is undefined), and to MOE_ERR_TIMEOUT when a device-side wait ran out (y is
  *   undefined).  T*k <= 2^30, strides <= 2^32; T = 0 is a no-op.  Launches one kernel, allocates nothing, needs no
@@ -392,7 +393,7 @@ moe_status moe_w4_matmul(const moe_w4_plan* plan, const void* x, int64_t x_strid
  *   gate per channel, (1, 0) one per token, (stride, 1) one per token and channel.
  * x (nullable: taken as 0), y, x_out (nullable; may be x itself, with the same stride), u (nullable;
  *   needs gamma_pre) (device): T rows, strides in elements, at least H.  x_out and u must not
- *   overlap y, each other or the gate; u must not overlap x.  Any H, stride and element-aligned pointer is accepted; rows that start on 16-byte
+ *   overlap y, each other or the gate, u must not overlap x (columns of one buffer, as for moe_grouped_matmul, do not).  Any H, stride and element-aligned pointer is accepted; rows that start on 16-byte
  *   boundaries with H a multiple of 8 are read 16 bytes at a time.
  * One launch, no workspace; T = 0 is a no-op.  Pages: none of the normalisation is printed; these
  * are the plain definitions.

@@ -283,6 +283,22 @@ bool is_value_type(int t) { return t == MOE_F32 || is_16bit(t); }
 size_t value_bytes(int t) { return t == MOE_F32 ? 4 : 2; }
 constexpr int kMaxDim = 1 << 20;
 
+// Rows of a call in memory: `width` bytes each, `stride` bytes apart.
+struct RowSpan {
+    uintptr_t at;
+    uint64_t width, stride;
+    int64_t rows;                // 0: none
+    uintptr_t end() const { return at + (uint64_t)(rows - 1) * stride + width; }
+};
+// Whether rows of a and b may have a byte in common.  Rows of one stride that lie beside one another (columns of one buffer) do
+// not; rows of different strides whose spans meet count as meeting.
+bool meet(const RowSpan& a, const RowSpan& b) {
+    if (a.rows == 0 || b.rows == 0 || a.at >= b.end() || b.at >= a.end()) return false;
+    if (a.stride != b.stride) return true;
+    const uint64_t s = a.stride, d = b.at >= a.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s;
+    return d < a.width || d + b.width > s;
+}
+
 moe_status check_product_shape(int E, int n_out, int n_in) {
     if (E < 1 || E > kMaxExperts) return fail(MOE_ERR_INVALID_ARG, "n_experts %d outside 1..%d", E, kMaxExperts);
     if (n_out < 1 || n_out > kMaxDim || n_in < 1 || n_in > kMaxDim)
@@ -309,10 +325,10 @@ moe_status check_product_call(const moe::RowsArgs& a, int T, int k, bool* todo) 
     const int64_t x_rows = a.sorted_pairs ? T : (int64_t)T * k, y_rows = (int64_t)T * k;
     if (a.x_stride > ((int64_t)1 << 32) || a.y_stride > ((int64_t)1 << 32))
         return fail(MOE_ERR_INVALID_ARG, "x_stride / y_stride above 2^32");
-    const uintptr_t x0 = (uintptr_t)a.x, y0 = (uintptr_t)a.y;
-    const uintptr_t x1 = x0 + 2 * (uintptr_t)((x_rows - 1) * a.x_stride + a.K);
-    const uintptr_t y1 = y0 + value_bytes(a.y_type) * (uintptr_t)((y_rows - 1) * a.y_stride + a.N);
-    if (x0 < y1 && y0 < x1) return fail(MOE_ERR_INVALID_ARG, "y overlaps x");
+    const uint64_t yb = value_bytes(a.y_type);
+    const RowSpan x{(uintptr_t)a.x, 2 * (uint64_t)a.K, 2 * (uint64_t)a.x_stride, x_rows};
+    const RowSpan y{(uintptr_t)a.y, yb * a.N, yb * a.y_stride, y_rows};
+    if (meet(x, y)) return fail(MOE_ERR_INVALID_ARG, "y overlaps x");
     *todo = true;
     return MOE_OK;
 }
@@ -709,16 +725,12 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
         !aligned(u, value_bytes(d.u_type)) || !aligned(gate, 4) || !aligned(d.gamma_post, 4) || !aligned(d.gamma_pre, 4))
         return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type");
     // what is written must not overlap what other threads still read (x_out == x with one stride may)
-    struct Span { uintptr_t lo, hi; };
     auto span = [&](const void* p, int type, int64_t st) {
-        const uintptr_t b = (uintptr_t)p;
-        return Span{b, p ? b + value_bytes(type) * (uintptr_t)((int64_t)(T - 1) * st + d.H) : b};
+        return RowSpan{(uintptr_t)p, value_bytes(type) * (uint64_t)d.H, value_bytes(type) * (uint64_t)st, p ? T : 0};
     };
-    auto meet = [](const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; };
-    const Span sx = span(x, d.x_type, x_stride), sy = span(y, d.y_type, y_stride),
-               so = span(x_out, d.x_type, x_out_stride), su = span(u, d.u_type, u_stride);
-    Span sg{(uintptr_t)gate, (uintptr_t)gate};
-    if (gate) sg.hi += 4 * (uintptr_t)((int64_t)(T - 1) * gate_row + (int64_t)(d.H - 1) * gate_col + 1);
+    const RowSpan sx = span(x, d.x_type, x_stride), sy = span(y, d.y_type, y_stride), so = span(x_out, d.x_type, x_out_stride),
+                  su = span(u, d.u_type, u_stride);
+    const RowSpan sg{(uintptr_t)gate, 4 * ((uint64_t)(d.H - 1) * gate_col + 1), 4 * (uint64_t)gate_row, gate ? T : 0};
     const bool in_place = x && x == x_out && x_stride == x_out_stride;
     if (meet(so, sy) || meet(su, sy) || meet(so, su) || meet(su, sx) || meet(so, sg) || meet(su, sg) ||
         (!in_place && meet(so, sx)))
