@@ -7,6 +7,8 @@ and calls moe_layer.  All arithmetic runs in the CUDA library.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import _native as N
@@ -179,10 +181,46 @@ def _row_stride(t, name):
     return row if n > 1 else (width + 7) // 8 * 8        # (one row: its stride is never used)
 
 
+_words: dict = {}                    # device: [words, how many are given away]
+_all_words: list = []
+_words_lock = threading.Lock()
+
+
+def _status_word(device):
+    """A status word (int32 [1], MOE_OK) that lives as long as the program: calls in flight and captured graphs may raise it after
+    the object that they were made with is gone.  None during a capture that would have to make the words."""
+    with _words_lock:
+        held = _words.get(device)
+        if held is None or held[1] == held[0].numel():
+            if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                return None
+            held = _words[device] = [torch.zeros(1024, dtype=torch.int32, device=device), 0]
+            _all_words.append(held[0])
+            if device.type == "cuda":                    # (zero before a call on any stream raises one)
+                torch.cuda.current_stream(device).synchronize()
+        held[1] += 1
+        return held[0][held[1] - 1: held[1]]
+
+
 class _Products:
     """What GroupedExperts and W4Experts share: the rows of a call, checked and passed on."""
 
     plan = None
+
+    def device_status(self, clear: bool = False) -> int:
+        """What the calls without a status of their own have raised so far, once all of them are done: MOE_OK,
+        MOE_ERR_DEVICE_CHECK or MOE_ERR_TIMEOUT.  clear: back to MOE_OK."""
+        word = self._status
+        if word is None:
+            raise RuntimeError("made during the first capture on its device, without a status word: pass status")
+        if word.is_cuda:
+            torch.cuda.synchronize(word.device)
+        code = int(word.item())
+        if clear:
+            word.zero_()
+            if word.is_cuda:
+                torch.cuda.synchronize(word.device)
+        return code
 
     def __call__(self, x: torch.Tensor, offsets: torch.Tensor | None = None, sorted_pairs: torch.Tensor | None = None,
                  k: int = 1, out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
@@ -190,9 +228,10 @@ class _Products:
 
         With sorted_pairs (int32 [T*k], moe_permute's) x holds the T tokens, row i being that of token
         sorted_pairs[i] // k; without, x holds the T*k rows in sorted order.  offsets (int32 [E+1], moe_permute's) may
-        be left out for one expert.  status: int32 [1], raised when a device-side check fails.  All of them are on the
-        weights' device, which has to be the current one.  stream (None: the current one) has to come after what wrote
-        the inputs; without out, y is made in the order of that stream, as under torch.cuda.stream(stream).
+        be left out for one expert.  status: int32 [1], raised when a device-side check fails (None: a word of
+        this object's own, which device_status() reads).  All of them are on the weights' device, which has to be the
+        current one.  stream (None: the current one) has to come after what wrote the inputs; without out, y is made
+        in the order of that stream, as under torch.cuda.stream(stream).
         """
         if k < 1:
             raise ValueError(f"k = {k}: a token has at least one expert")
@@ -216,8 +255,8 @@ class _Products:
         elif out.dtype is not self.y_dtype or out.shape != (P, self.n_out) or not out.is_cuda:
             raise ValueError(f"out must be a {self.y_dtype} CUDA tensor [{P}, {self.n_out}]")
         _on_current(self.device, x=x, offsets=offsets, sorted_pairs=sorted_pairs, out=out, status=status)
-        self._matmul(self.plan, x, _row_stride(x, "x"), T, k, sorted_pairs, offsets, out, _row_stride(out, "out"), status,
-                     stream)
+        self._matmul(self.plan, x, _row_stride(x, "x"), T, k, sorted_pairs, offsets, out, _row_stride(out, "out"),
+                     self._status if status is None else status, stream)
         return out
 
     def __del__(self):
@@ -257,6 +296,7 @@ class GroupedExperts(_Products):
         self.n_out, self.n_in = (w.shape[1], w.shape[2]) if order == "out_in" else (w.shape[2], w.shape[1])
         self.x_dtype, self.y_dtype, self.device = w.dtype, y_dtype, w.get_device()
         self._keep = (w, w_up)
+        self._status = _status_word(w.device)
         self.plan = N.moe_grouped_plan_create(N.moe_grouped_desc(
             _VT[w.dtype], _VT[y_dtype], N.MOE_W_OUT_IN if order == "out_in" else N.MOE_W_IN_OUT, self.n_experts,
             self.n_out, self.n_in, w.data_ptr(), w_up.data_ptr() if w_up is not None else None,
@@ -308,6 +348,7 @@ class W4Experts(_Products):
         self.n_experts, self.n_out, self.n_in = E, n_out, n_in
         self.x_dtype, self.y_dtype, self.device = x_dtype, y_dtype, q.get_device()
         self._keep = (q, scales, zeros, up)
+        self._status = _status_word(q.device)
         p = [t.data_ptr() if t is not None else None for t in (q, scales, zeros) + up]
         self.plan = N.moe_w4_plan_create(N.moe_w4_desc(_VT[x_dtype], _VT[y_dtype], _VT[scales.dtype], group, E, n_out,
                                                        n_in, *p))
