@@ -362,7 +362,7 @@ cudaError_t launch_stream(const NormPairArgs& a, cudaStream_t s) {
 template <int TPR, int NC>
 cudaError_t launch(const NormPairArgs& a, bool vec, cudaStream_t s) {
     constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = kThreads / TPR;
-    const unsigned grid = (unsigned)((a.T + kRows - 1) / kRows);
+    const unsigned grid = ((unsigned)a.T + kRows - 1) / kRows;           // (T up to 2^31 - 1)
     void* args[] = {const_cast<NormPairArgs*>(&a)};
     return launch_early(vec ? (const void*)norm_pair_kernel<TPR, NC, true> : (const void*)norm_pair_kernel<TPR, NC, false>,
                         dim3(grid), kThreads, 0, s, args);
