@@ -25,7 +25,9 @@ moe_status fail(moe_status st, const char* fmt, ...) {
     return st;
 }
 
+// Reports a call's error once: what the runtime keeps of it would be read by the next call's check of its launches.
 moe_status cuda_fail(cudaError_t err, const char* what) {
+    cudaGetLastError();
     return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
 }
 

@@ -58,8 +58,7 @@ inline cudaError_t launch_early(const void* fn, dim3 grid, unsigned threads, siz
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelExC(&cfg, fn, args);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 // SMs of the current device; a kernel's dynamic shared memory is raised to `smem` there, once per
