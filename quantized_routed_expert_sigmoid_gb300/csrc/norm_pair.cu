@@ -27,11 +27,6 @@ __device__ __forceinline__ float load1(const void* p, int type, int64_t i) {
     if (type == MOE_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
     return __half2float(reinterpret_cast<const __half*>(p)[i]);
 }
-__device__ __forceinline__ void store1(void* p, int type, int64_t i, float v) {
-    if (type == MOE_F32) reinterpret_cast<float*>(p)[i] = v;
-    else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 // Eight elements from a 16-byte boundary.  ONCE: they are not read again.
 template <bool ONCE = false>
 __device__ __forceinline__ void load8(const void* p, int type, int64_t i, float (&v)[8]) {
@@ -191,7 +186,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (first(c) + j * kStep < H)
-                        store1(a.x_out, a.x_type, t * a.x_out_stride + first(c) + j * kStep, r[c][j]);
+                        store_value(a.x_out, a.x_type, t * a.x_out_stride + first(c) + j * kStep, r[c][j]);
             }
         }
     }
@@ -208,7 +203,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_pair_kernel(const 
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (first(c) + j * kStep < H) store1(a.u, a.u_type, t * a.u_stride + first(c) + j * kStep, f[j]);
+                if (first(c) + j * kStep < H) store_value(a.u, a.u_type, t * a.u_stride + first(c) + j * kStep, f[j]);
         }
     }
 }
@@ -359,13 +354,16 @@ cudaError_t launch_stream(const NormPairArgs& a, cudaStream_t s) {
     return launch_early(fn, dim3(std::min(a.T, sms * per_sm)), TPR, (size_t)row * DEPTH, s, args);
 }
 
-template <int TPR, int NC>
+// VEC: the form with 16-byte accesses is there too (rows that launch_stream takes when they can be read so need it not).
+template <int TPR, int NC, bool VEC = true>
 cudaError_t launch(const NormPairArgs& a, bool vec, cudaStream_t s) {
     constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = kThreads / TPR;
     const unsigned grid = ((unsigned)a.T + kRows - 1) / kRows;           // (T up to 2^31 - 1)
     void* args[] = {const_cast<NormPairArgs*>(&a)};
-    return launch_early(vec ? (const void*)norm_pair_kernel<TPR, NC, true> : (const void*)norm_pair_kernel<TPR, NC, false>,
-                        dim3(grid), kThreads, 0, s, args);
+    const void* fn = (const void*)norm_pair_kernel<TPR, NC, false>;
+    if constexpr (VEC)
+        if (vec) fn = (const void*)norm_pair_kernel<TPR, NC, true>;
+    return launch_early(fn, dim3(grid), kThreads, 0, s, args);
 }
 
 bool rows16(const void* p, int type, int64_t stride) {
@@ -389,8 +387,8 @@ cudaError_t launch_norm_pair(const NormPairArgs& a, cudaStream_t s) {
     if (a.H <= 1024) return launch<128, 1>(a, vec, s);
     if (a.H <= 2048) return launch<256, 1>(a, vec, s);
     if (a.H <= 4096) return launch<256, 2>(a, vec, s);
-    if (a.H <= 8192) return launch<1024, 1>(a, vec, s);
-    if (a.H <= 16384) return launch<1024, 2>(a, vec, s);
+    if (a.H <= 8192) return launch<1024, 1, false>(a, false, s);
+    if (a.H <= 16384) return launch<1024, 2, false>(a, false, s);
     return launch<1024, 4>(a, vec, s);
 }
 

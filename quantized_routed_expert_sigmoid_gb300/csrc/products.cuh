@@ -55,6 +55,12 @@ struct RowsArgs {
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);            // streams the weights (rows.cu)
 cudaError_t launch_w4(const RowsArgs& a, cudaStream_t s);              // 4-bit weights (w4.cu)
 
+// Element i of a tensor of a value type.
+__device__ __forceinline__ void store_value(void* p, int type, int64_t i, float v) {
+    if (type == MOE_F32) reinterpret_cast<float*>(p)[i] = v;
+    else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+}
 // silu(g) u = g / (1 + e^-g) u, from e^-|g|, which does not overflow: g / (1 + e^-g) with an e^-g past the largest number is 0
 // from g = -88.7 down, where silu is -2e-37 (and the quick division gives 0 from -87.3).  silu(g) is an fp32 number, below 2^-126
 // with the spacing of the subnormal ones.  FAST, for 16-bit outputs: the quick exponential is off by at most

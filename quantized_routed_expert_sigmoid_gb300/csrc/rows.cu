@@ -71,12 +71,6 @@ __device__ __forceinline__ uint2 load4(const uint16_t* row, int i, int n) {
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ void store_y(void* y, int type, int64_t i, float v) {
-    if (type == MOE_F32) reinterpret_cast<float*>(y)[i] = v;
-    else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
-    else reinterpret_cast<__half*>(y)[i] = __float2half_rn(v);
-}
-
 __device__ __forceinline__ void raise(int32_t* status) {
     if (status) atomicCAS(status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
 }
@@ -289,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? W::kCtas : 1) rows_kernel(
                 if (col < cnt && r < a.N) {
                     float out = v[0];
                     if constexpr (kMats == 2) out = silu_times<false>(v[0], v[1]);
-                    store_y(a.y, a.y_type, (int64_t)(lo + col) * a.y_stride + r, out);
+                    store_value(a.y, a.y_type, (int64_t)(lo + col) * a.y_stride + r, out);
                 }
             }
         }

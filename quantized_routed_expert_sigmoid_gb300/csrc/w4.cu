@@ -104,11 +104,6 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-__device__ __forceinline__ void store_y(void* y, int type, int64_t i, float v) {
-    if (type == MOE_F32) reinterpret_cast<float*>(y)[i] = v;
-    else if (type == MOE_BF16) reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
-    else reinterpret_cast<__half*>(y)[i] = __float2half_rn(v);
-}
 __device__ __forceinline__ void computing_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // Bytes of a row's scales and zero points in a stage (a copy has at least 4 bytes: with groups of 128 the two
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
             // ======================= staging of x =======================
             const int nc = min(p.cols, rows - base);
             computing_sync();                            // the rows before have been used
-            // a set of wc warps a row: all 16 for one row, one each for 16
+            // a set of wc warps a row: all 8 for one row, one each for 5 and more (more than one: all rows at once)
             int wc = kWarps;
             while (wc > 1 && wc * nc > kWarps) wc >>= 1;
             for (int c0 = 0; c0 < nc; c0 += kWarps / wc) {
@@ -388,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                                            *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
                     }
                 }
-                if (wc > 1 && c0 + kWarps / wc < nc) computing_sync();       // (largest is used again)
             }
             computing_sync();
             // ======================= products =======================
@@ -561,10 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const __grid_constant__
                             const float v0 = acc[j][n][i] * unscale[c], v1 = acc[j][n][2 + i] * unscale[c];
                             const int64_t at = (int64_t)(lo + base + c) * a.y_stride + ya;
                             if constexpr (UP) {
-                                if (ya < a.N) store_y(a.y, a.y_type, at, silu_times<false>(v0, v1));
+                                if (ya < a.N) store_value(a.y, a.y_type, at, silu_times<false>(v0, v1));
                             } else {
-                                if (ya < a.N) store_y(a.y, a.y_type, at, v0);
-                                if (ya + 8 < a.N) store_y(a.y, a.y_type, at + 8, v1);
+                                if (ya < a.N) store_value(a.y, a.y_type, at, v0);
+                                if (ya + 8 < a.N) store_value(a.y, a.y_type, at + 8, v1);
                             }
                         }
             }
