@@ -25,11 +25,11 @@
 // reported (MOE_ERR_TIMEOUT), the copies in flight are waited for (bounded), TMEM is freed and the kernel returns.
 //
 // Measured (device time; bytes and flops that the products cannot do without against 6.69 TB/s and 1.95 PFLOP/s):
-// 4096 tokens, 8 of 128 experts, hidden 2048, intermediate 768: gated half 171 us (206 GFLOP, 822 MB: 72 % of its
-// 123 us; tensor pipe 55 %, DRAM 64 %), down with fp32 rows 115 us (90 % of 104 us, bytes); 32 tokens, down
-// 56.5 us (94 %, bytes); 512 tokens, 256 experts of 2048 x 7168 stored [in][out] 1.10 ms (7.6 GB, at the copy's
-// rate).  The gated half is what is left: without its gathers it takes 156 us, without its epilogue 154, without
-// both 141, and with no loads at all 125.
+// 4096 tokens, 8 of 128 experts, hidden 2048, intermediate 768: gated half 172 us (206 GFLOP, 822 MB: 72 % of its
+// 123 us; tensor pipe 55 %, DRAM 64 %), down with fp32 rows 116 us (90 % of 104 us, bytes); 32 tokens, down
+// 57.2 us (93 %, bytes); 512 tokens, 256 experts of 2048 x 7168 stored [in][out] 1.10 ms (7.6 GB, at the copy's
+// rate).  The gated half is what is left: of 171 us it took 156 without its gathers, 154 without its epilogue, 141 without
+// both, and 125 with no loads at all.
 #include "products.cuh"
 #include "tc_ptx.cuh"
 #include "tmap.cuh"

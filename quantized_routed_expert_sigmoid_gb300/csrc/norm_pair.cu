@@ -12,8 +12,8 @@
 //   DEPTH rows ahead) while it computes; nothing but its own copies is waited for.
 // - norm_pair_kernel, the others: narrow rows take one warp each (no barrier), others 128, 256
 //   or 1024 threads.
-// Measured: 4096 rows of 2048, fp32 stream, bf16 u: 22.4 us for 117 MB (17.6 us at the copy's rate); 512 rows
-// of 7168, bf16, gated: 10.0 us (4.4 us); one row of 2048: 2.8 us, a launch and two means.
+// Measured: 4096 rows of 2048, fp32 stream, bf16 u: 22.3 us for 117 MB (17.6 us at the copy's rate); 512 rows
+// of 7168, bf16, gated: 9.9 us (4.4 us); one row of 2048: 2.6 us, a launch and two means.
 #include <algorithm>
 
 #include "products.cuh"

@@ -27,11 +27,11 @@
 // both took 1400 clocks a stage); a CTA per SM takes an even share of the (expert, 128 rows) units.
 //
 // Measured (device time): 16 tokens, 8 of 256 experts, 7168 -> 2048 gated, groups of 32 with zero points:
-// 437 us for 1.78 GB (266 us at the copy's rate; 385 us with the zero points taken off the sums).  What bounds it now is the issue of
+// 438 us for 1.78 GB (266 us at the copy's rate; 385 us with the zero points taken off the sums).  What bounds it now is the issue of
 // instructions: two computing warps a scheduler find one to issue in 61 % of the clocks (32 experts of that size, one row each: DRAM 48 %,
 // ALU pipe 58 %), and every instruction more shows (8 additions a group: 478 us); the 128 matrix instructions of
 // a stage, one in 16 clocks on each of the four schedulers, take 512 of the 700 clocks that HBM needs for it beside that.
-// One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 9.3 us for 13 MB; 96 units of 64 outputs leave 56 of
+// One token, 8 of 128 experts, 2048 -> 768 gated, groups of 128: 9.2 us for 13 MB; 96 units of 64 outputs leave 56 of
 // 152 SMs without work, and each CTA's eight stages follow a start of 4 us (routing read, x staged, the first copies).
 #include <type_traits>
 
