@@ -290,7 +290,10 @@ struct RowSpan {
     uintptr_t at;
     uint64_t width, stride;
     int64_t rows;                // 0: none
-    uintptr_t end() const { return at + (uint64_t)(rows - 1) * stride + width; }
+    uintptr_t end() const {      // (past every address: the largest one)
+        const uint64_t room = ~(uint64_t)0 - at - width, n = (uint64_t)(rows - 1);
+        return stride && n > room / stride ? ~(uintptr_t)0 : at + n * stride + width;
+    }
 };
 // Whether rows of a and b may have a byte in common.  Rows of one stride that lie beside one another (columns of one buffer) do
 // not; rows of different strides whose spans meet count as meeting.

@@ -39,15 +39,20 @@ def prepare_q8_0(t, rows: int, cols: int, n_experts: int = 1):
     return dst.view(*shape)
 
 
+def _stream_object(stream, device):
+    """The torch stream of a stream's handle (0 and 1 are two names of the default stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = N._stream(stream)
+    return torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+
+
 def _empty(shape, dtype, device, stream):
     """Memory for what a call on `stream` writes, in the order of that stream: from the current stream's memory it could
     be a block that kernels waiting there have yet to read, and would go back there while `stream` still writes it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = N._stream(stream)       # (0 and 1 are two names of the default stream)
-        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_object(stream, device)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -95,7 +100,7 @@ class MoeLayer:
         self.desc = d
         self.plan = N.moe_layer_plan_create(d)
         self.ws = None
-        self.ws_T = -1
+        self.ws_T, self.ws_stream = -1, 0
 
     def path(self, T: int) -> str:
         """Which kernels a call with T tokens runs: "gemv", "decode_chain" or "tensor"."""
@@ -108,7 +113,7 @@ class MoeLayer:
         if self.ws is None or T > self.ws_T:
             nbytes = self.workspace_bytes(T)
             self.ws = _empty(nbytes, torch.uint8, device or "cuda", stream)
-            self.ws_T = T
+            self.ws_T, self.ws_stream = T, N._stream(stream)
         return self.ws
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -117,7 +122,10 @@ class MoeLayer:
         if out is None:
             out = _empty((T, self.H), torch.float32, x.device, stream)
         ws = self.ensure_workspace(T, x.device, stream)
-        N.moe_layer(self.plan, x, T, out, ws, ws.numel(), stream)
+        handle = N._stream(stream)
+        if handle != self.ws_stream:     # (a workspace of another stream's memory, which a larger one may replace meanwhile)
+            ws.record_stream(_stream_object(handle, x.device))
+        N.moe_layer(self.plan, x, T, out, ws, ws.numel(), handle)
         return out
 
     def debug_views(self, T: int):

@@ -66,3 +66,22 @@ def test_made_outputs_do_not_meet_the_current_stream_s_blocks(ops, name, handle)
     new = [torch.full(shape, 5.0, dtype=dtype, device="cuda") for shape, dtype in shapes]
     torch.cuda.synchronize()
     assert all(bool((t == 5.0).all()) for t in new)
+
+
+def test_a_dropped_layer_s_workspace_is_not_given_away_while_a_stream_writes_it():
+    tl = make_layer(synth.DECODE, 3, T)
+    x = tl.x.cuda()
+    layer = tl.moe_layer()
+    nbytes = layer.ensure_workspace(T).numel()       # (memory of the current stream)
+    side = torch.cuda.Stream()
+    out = layer(x, stream=side)
+    torch.cuda.synchronize()
+    want = out.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    out = layer(x, stream=side)
+    layer.ws, layer.ws_T = None, -1                  # (as a larger workspace or the end of the layer does)
+    new = torch.full((nbytes,), 5, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert bool((new == 5).all()) and torch.equal(out, want)

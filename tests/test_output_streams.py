@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import quantized_routed_expert_sigmoid_gb300 as moe
-from test_products_devices import _on
+from test_products_devices import _On, _on
 
 
 class _Stream:
@@ -42,6 +42,8 @@ def made(monkeypatch):
     layer.workspace_bytes = lambda T: 64
     monkeypatch.setattr(moe.layer.N, "moe_norm_residual", lambda *a: None)
     monkeypatch.setattr(moe.layer.N, "moe_layer", lambda *a: None)
+    monkeypatch.setattr(moe.layer.N, "_stream", lambda s: 5 if s is None else getattr(s, "cuda_stream", s))
+    monkeypatch.setattr(_On, "record_stream", lambda self, s: log.append(("used by", s)), raising=False)
     empty = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, **kw: (log.append(under[-1]), _on(empty(*a, **kw)))[1])
     return dict(grouped=g, w4=w, norm=moe.NormResidual(32, gamma_pre=_on(torch.ones(32))), layer=layer), log
@@ -66,3 +68,13 @@ def test_outputs_are_made_under_the_call_s_stream(made, name, n):
         ops["layer"].ws = None
         _call(name, ops[name], stream)
         assert log == [want] * n, (stream, log)
+
+
+def test_a_workspace_of_another_stream_is_kept_from_its_memory_until_the_call_is_done(made):
+    ops, log = made
+    layer, x = ops["layer"], _on(torch.zeros(4, 32, dtype=torch.bfloat16))
+    layer(x)
+    log.clear()
+    layer(x, stream=77)
+    layer(x)
+    assert log == [("external", 77), ("used by", ("external", 77)), "current"]
