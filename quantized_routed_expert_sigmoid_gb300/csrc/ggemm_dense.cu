@@ -48,7 +48,8 @@ constexpr uint32_t kTmemCols = 512;
 // with the length of the sum (relative, in norm: 7e-7 over 768 elements, 8e-6 over 7168, 2.7e-4 over 2^18, twice that gated).
 // So a sum is made of runs of at most kRun steps, which the epilogue adds with rounding in TMEM: columns kSumCol..,
 // so that a tile of more than one run has at most 128 columns.  fp32 outputs have short runs; 16-bit outputs have runs
-// of 8192 elements, whose error (9e-6, gated 1.8e-5) is below a 27th of half a step of fp16.
+// of 8192 elements, whose error (9e-6, gated 1.8e-5) is below a 27th of half a step of fp16 (runs of 1024: 225 against 170 us for the gated
+// case of 4096 tokens above).
 // Measured with runs / without, fp32 outputs: 4096 tokens gated 265 / 181 us (error 6.9e-7 / 4.2e-6), 2048 tokens, 6 of 64
 // experts of 7168 -> 1024 221 / 181 us (7.2e-7 / 7.9e-6), 64 tokens of those 156 / 154 us.
 constexpr int kSumCol = 128;
