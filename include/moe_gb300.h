@@ -412,6 +412,128 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
                              int64_t y_stride, const float* gate, int64_t gate_row, int64_t gate_col, int T,
                              void* x_out, int64_t x_out_stride, void* u, int64_t u_stride, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- dense product with its epilogue */
+
+/*
+ * moe_linear -- a dense projection and what follows it, in one kernel:
+ *     y[t, n] = res_scale * r[t, n] + scale * act(sum_c W[n, c] * x[t, c] + bias[n])
+ *   act: MOE_ACT_NONE; RELU max(z, 0) (NaN stays); GELU z * Phi(z), Phi the normal distribution function;
+ *   GELU_TANH z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))); SILU z / (1 + exp(-z)).
+ *   Products exact, sums in fp32 in a fixed order, one rounding to y_type at the end.  Long sums are made of runs of at
+ *   most 768 elements with y_type MOE_F32 and 8192 with a 16-bit one, added with rounding, as those of moe_grouped_matmul.
+ * The projections in front of and behind the routed experts, and dense blocks: an up half with its activation, a down
+ * half that adds to the residual stream (r the stream; y may be r itself).
+ * desc (host, read by plan_create):
+ *   type: MOE_BF16 or MOE_F16, of W and x;  y_type, bias_type: MOE_F32, MOE_BF16 or MOE_F16;  order, n_out, n_in, w and
+ *   row_stride as moe_grouped_desc for one expert;  bias (device, nullable, aligned to its type): [n_out], dense;
+ *   scale, res_scale: finite.
+ * The plan keeps the pointers; weights and bias must outlive it and may change between calls.
+ * Call: x (device, 16-byte aligned) T rows x_stride elements apart (a multiple of 8, >= n_in); r (device, nullable) T rows of
+ *   r_type, r_stride >= n_out elements apart; y (device) T rows, y_stride >= n_out; r and y aligned to their types.
+ *   y may be r with r's type and stride; otherwise y must not overlap r, and never x (columns of one
+ *   buffer, as for moe_grouped_matmul, do not).  status (device int32, nullable, never cleared by the call): raised from MOE_OK to
+ *   MOE_ERR_TIMEOUT when a device-side wait ran out (y is undefined).  T <= 2^30, strides <= 2^32; T = 0 is a no-op.
+ *   One launch, no workspace, nothing kept between calls; a captured call replays with the bits of the eager one.
+ * Kernels (moe_linear_path): MOE_LINEAR_SPLIT, tiles of 128 outputs by up to 128 rows, the sum of a tile split over a
+ *   cluster of up to 8 SMs where there are few tiles; MOE_LINEAR_PAIRS, tiles of 256 outputs by up to 256 rows on pairs of SMs.
+ * Errors: as moe_grouped_matmul.  Pages: the parts around the experts are not printed; these are the plain definitions.
+ */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 } moe_act;
+typedef struct {
+    moe_dtype type;              /* MOE_BF16 or MOE_F16: W and x */
+    moe_dtype y_type;            /* MOE_F32, MOE_BF16 or MOE_F16 */
+    moe_w_order order;
+    int n_out, n_in;
+    const void* w;               /* (device) */
+    int64_t row_stride;          /* elements */
+    const void* bias;            /* (device, nullable) */
+    moe_dtype bias_type;
+    moe_act act;
+    float scale, res_scale;
+} moe_linear_desc;
+typedef struct moe_linear_plan moe_linear_plan;
+#define MOE_LINEAR_SPLIT 0
+#define MOE_LINEAR_PAIRS 1
+moe_status moe_linear_plan_create(const moe_linear_desc* desc, moe_linear_plan** plan);
+moe_status moe_linear_plan_destroy(moe_linear_plan* plan);
+moe_status moe_linear_path(const moe_linear_plan* plan, int T, int* path);
+moe_status moe_linear(const moe_linear_plan* plan, const void* x, int64_t x_stride, int T, const void* r, moe_dtype r_type,
+                      int64_t r_stride, void* y, int64_t y_stride, int32_t* status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- layer norm */
+
+/*
+ * moe_layer_norm -- per row of x, with m = mean_h x, v = mean_h (x - m)^2, q = 1 / sqrt(v + eps):
+ *     y = (x - m) * q * gamma + beta;  mean[t] = m, rstd[t] = q
+ * moe_layer_norm_backward -- its gradient; with xh = (x - m) * q, g = dy * gamma, from the forward call's mean and rstd:
+ *     dx = add + q * (g - mean_h g - xh * mean_h(g * xh));  dgamma = sum_t dy * xh;  dbeta = sum_t dy
+ *   add: the gradient that the residual stream brings along (x went into it as well), NULL: 0.
+ * All arithmetic fp32, one rounding to each output's type; a row far from 0 loses nothing by its mean.
+ * desc (host, read during the call): H 1..32768; x_type (x, add, dx), y_type (y, dy): MOE_F32, MOE_BF16 or
+ *   MOE_F16; gamma (NULL: 1), beta (NULL: 0; not read by the backward call): device fp32 [H]; eps >= 0.
+ * x, y, dy, add, dx (device): T rows, strides in elements, at least H; mean, rstd: device fp32 [T] (the forward call's may be
+ *   NULL, as may y; not all three).  Any H, stride and element-aligned pointer is accepted; aligned rows (H and strides
+ *   multiples of 8, or of 4 with fp32 among the types, pointers of 16 bytes) are read 16 bytes at a time.
+ *   y must not overlap x unless it is x, with its type and stride; dx may be add, x or dy itself (same type and
+ *   stride; none of the others overlaps it).  dx, dgamma, dbeta: nullable, not all.
+ * dgamma, dbeta (device fp32 [H]): overwritten, or added to with accumulate = 1; the sums over the rows have one order (the
+ *   bits are those of every run).  They need a workspace (device, 256-byte aligned) of moe_layer_norm_backward_workspace_size
+ *   bytes, which is free again when the call is done; calls that may overlap need one each.  dx alone needs none.
+ * T <= 2^30; T = 0: nothing but dgamma = dbeta = 0 (unless accumulate).  The backward call launches two kernels.
+ */
+typedef struct {
+    int H;
+    moe_dtype x_type, y_type;
+    const float* gamma;          /* (device, nullable) */
+    const float* beta;           /* (device, nullable) */
+    float eps;
+} moe_layer_norm_desc;
+moe_status moe_layer_norm(const moe_layer_norm_desc* desc, const void* x, int64_t x_stride, int T, void* y, int64_t y_stride,
+                          float* mean, float* rstd, moe_stream_t stream);
+moe_status moe_layer_norm_backward_workspace_size(int H, int T, size_t* bytes);
+moe_status moe_layer_norm_backward(const moe_layer_norm_desc* desc, const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const float* mean, const float* rstd, const void* add, int64_t add_stride,
+                                   int T, void* dx, int64_t dx_stride, float* dgamma, float* dbeta, int accumulate,
+                                   void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- the router's balance */
+
+/*
+ * moe_balance_loss -- the auxiliary loss that keeps a router's load even, its counts and its gradient.
+ *   p_te = softmax(logits_t)_e (MOE_ROUTE_SOFTMAX) or sigmoid(logits_te) / sum_j sigmoid(logits_tj) (SIGMOID_GROUP; a
+ *   selection bias only shows in the ids).  For sequence b with n_b counted tokens:
+ *     counts[b][e] = pairs of its counted tokens that name e;  f_be = E * counts[b][e] / (k * n_b);  P_be = sum_t p_te / n_b
+ *     loss = coef / B' * sum_b sum_e f_be * P_be        (B': sequences with a counted token; 0 without any)
+ *     dlogits_te = upstream * d loss / d logits_te      (counts held constant)
+ *               = upstream * coef / (B' n_b) * p_te * (f_be - sum_j f_bj p_tj)  [sigmoid: * (1 - sigmoid(logits_te))]
+ *   coef for a perfectly even load.  A logit of -inf has p = 0 and no gradient; a token of nothing else has p = 0 throughout.
+ * desc (host, read during the call): mode; n_experts 1..1024, top_k 1..min(E, 32); coef finite; accumulate.
+ * logits (device, fp32): T rows, stride elements apart (>= E), as moe_route's logits_out;  ids (device, int32 [T][k]):
+ *   its topk_ids;  seq_offsets (device int32 [n_seqs + 1], nullable with n_seqs = 1: one sequence of all T tokens):
+ *   first tokens of the sequences, non-decreasing within 0..T; empty sequences have counts of 0;  mask (device, uint8 [T],
+ *   nullable): tokens with 0 do not count (their logits and ids are not read, or not used);  upstream (device fp32 [1],
+ *   nullable: 1): the gradient of what the loss goes into.
+ * Outputs (device, nullable, not all): loss fp32 [1];  counts int32 [n_seqs][E];  dlogits fp32, T rows dstride apart
+ *   (may be logits itself, with its stride, unless accumulating): overwritten, with 0 for tokens that do not count or that
+ *   no sequence has; with accumulate added to, those tokens' rows left as they were.
+ * workspace (device, 256-byte aligned): moe_balance_workspace_size bytes; it is free again when the call is done, calls that
+ *   may overlap need one each.  status (device int32, nullable, never cleared by the call): raised to MOE_ERR_DEVICE_CHECK when
+ *   an id of a counted token leaves 0..E-1 (it is not counted) or an offset leaves 0..T or decreases (the outputs are undefined).
+ * T*k <= 2^30, n_seqs 1..65535; T = 0: loss = 0, counts = 0.  All sums have one order: the same bits each time.
+ * Up to three launches.
+ */
+typedef struct {
+    moe_route_mode mode;
+    int n_experts, top_k;
+    float coef;
+    int accumulate;              /* 1: dlogits += */
+} moe_balance_desc;
+moe_status moe_balance_workspace_size(int n_experts, int T, int n_seqs, size_t* bytes);
+moe_status moe_balance_loss(const moe_balance_desc* desc, const float* logits, int64_t stride, const int32_t* ids, int T,
+                            const int32_t* seq_offsets, int n_seqs, const uint8_t* mask, const float* upstream, float* loss,
+                            int32_t* counts, float* dlogits, int64_t dstride, int32_t* status, void* workspace, size_t ws_bytes,
+                            moe_stream_t stream);
+
 /* ---------------------------------------------------------------- fused layer */
 
 typedef struct {

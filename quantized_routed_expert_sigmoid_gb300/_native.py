@@ -21,6 +21,8 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_gb300.h")
 MOE_F32, MOE_BF16, MOE_Q8_0, MOE_Q4_K, MOE_Q8_0_R, MOE_Q5_K, MOE_Q6_K, MOE_Q3_K, MOE_MXFP4, MOE_F16 = range(10)
 MOE_W_OUT_IN, MOE_W_IN_OUT = range(2)
 MOE_GROUPED_ROWS, MOE_GROUPED_TENSOR = range(2)
+MOE_LINEAR_SPLIT, MOE_LINEAR_PAIRS = range(2)
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU = range(5)
 MOE_ROUTE_SOFTMAX, MOE_ROUTE_SIGMOID_GROUP = range(2)
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -71,6 +73,22 @@ class moe_norm_desc(ctypes.Structure):
     _fields_ = [("H", ctypes.c_int), ("x_type", ctypes.c_int), ("y_type", ctypes.c_int), ("u_type", ctypes.c_int),
                 ("gamma_post", ctypes.c_void_p), ("gamma_pre", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("res_scale", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("y_type", ctypes.c_int), ("order", ctypes.c_int), ("n_out", ctypes.c_int),
+                ("n_in", ctypes.c_int), ("w", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("bias_type", ctypes.c_int), ("act", ctypes.c_int), ("scale", ctypes.c_float), ("res_scale", ctypes.c_float)]
+
+
+class moe_layer_norm_desc(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("x_type", ctypes.c_int), ("y_type", ctypes.c_int), ("gamma", ctypes.c_void_p),
+                ("beta", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class moe_balance_desc(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int), ("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("coef", ctypes.c_float),
+                ("accumulate", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -132,6 +150,16 @@ def _declare(lib):
         "moe_w4_plan_destroy": [P],
         "moe_w4_matmul": [P, P, I64, I, I, P, P, P, I64, P, P],
         "moe_norm_residual": [ctypes.POINTER(moe_norm_desc), P, I64, P, I64, P, I64, I64, I, P, I64, P, I64, P],
+        "moe_linear_plan_create": [ctypes.POINTER(moe_linear_desc), ctypes.POINTER(P)],
+        "moe_linear_plan_destroy": [P],
+        "moe_linear_path": [P, I, ctypes.POINTER(ctypes.c_int)],
+        "moe_linear": [P, P, I64, I, P, I, I64, P, I64, P, P],
+        "moe_layer_norm": [ctypes.POINTER(moe_layer_norm_desc), P, I64, I, P, I64, P, P, P],
+        "moe_layer_norm_backward_workspace_size": [I, I, PS],
+        "moe_layer_norm_backward": [ctypes.POINTER(moe_layer_norm_desc), P, I64, P, I64, P, P, P, I64, I, P, I64, P, P, I, P, S,
+                                    P],
+        "moe_balance_workspace_size": [I, I, I, PS],
+        "moe_balance_loss": [ctypes.POINTER(moe_balance_desc), P, I64, P, I, P, I, P, P, P, P, P, I64, P, P, S, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -286,6 +314,57 @@ def moe_norm_residual(desc: moe_norm_desc, x, x_stride, y, y_stride, gate, gate_
                       u, u_stride, stream=None):
     _check(load().moe_norm_residual(ctypes.byref(desc), _p(x), x_stride, _p(y), y_stride, _p(gate), gate_row, gate_col,
                                     T, _p(x_out), x_out_stride, _p(u), u_stride, _stream(stream)))
+
+
+def moe_linear_plan_create(desc: moe_linear_desc) -> int:
+    h = ctypes.c_void_p(0)
+    _check(load().moe_linear_plan_create(ctypes.byref(desc), ctypes.byref(h)))
+    return h.value
+
+
+def moe_linear_plan_destroy(plan: int):
+    _check(load().moe_linear_plan_destroy(plan))
+
+
+def moe_linear_path(plan, T) -> int:
+    """Which kernel moe_linear runs for T rows: a MOE_LINEAR_* value."""
+    v = ctypes.c_int(-1)
+    _check(load().moe_linear_path(plan, T, ctypes.byref(v)))
+    return v.value
+
+
+def moe_linear(plan, x, x_stride, T, r, r_type, r_stride, y, y_stride, status=None, stream=None):
+    _check(load().moe_linear(plan, _p(x), x_stride, T, _p(r), r_type, r_stride, _p(y), y_stride, _p(status), _stream(stream)))
+
+
+def moe_layer_norm(desc: moe_layer_norm_desc, x, x_stride, T, y, y_stride, mean, rstd, stream=None):
+    _check(load().moe_layer_norm(ctypes.byref(desc), _p(x), x_stride, T, _p(y), y_stride, _p(mean), _p(rstd), _stream(stream)))
+
+
+def moe_layer_norm_backward_workspace_size(H, T) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_layer_norm_backward_workspace_size(H, T, ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_norm_backward(desc: moe_layer_norm_desc, dy, dy_stride, x, x_stride, mean, rstd, add, add_stride, T, dx, dx_stride,
+                            dgamma, dbeta, accumulate, workspace, ws_bytes, stream=None):
+    _check(load().moe_layer_norm_backward(ctypes.byref(desc), _p(dy), dy_stride, _p(x), x_stride, _p(mean), _p(rstd), _p(add),
+                                          add_stride, T, _p(dx), dx_stride, _p(dgamma), _p(dbeta), int(accumulate),
+                                          _p(workspace), ws_bytes, _stream(stream)))
+
+
+def moe_balance_workspace_size(E, T, n_seqs=1) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_balance_workspace_size(E, T, n_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def moe_balance_loss(desc: moe_balance_desc, logits, stride, ids, T, seq_offsets, n_seqs, mask, upstream, loss, counts, dlogits,
+                     dstride, status, workspace, ws_bytes, stream=None):
+    _check(load().moe_balance_loss(ctypes.byref(desc), _p(logits), stride, _p(ids), T, _p(seq_offsets), n_seqs, _p(mask),
+                                   _p(upstream), _p(loss), _p(counts), _p(dlogits), dstride, _p(status), _p(workspace),
+                                   ws_bytes, _stream(stream)))
 
 
 def moe_layer_plan_create(desc: moe_layer_desc) -> int:

@@ -1,6 +1,7 @@
 // abi.cu -- the C ABI (include/moe_gb300.h): host-side validation, workspace
 // layout, and the order of launches for each call.  No device memory is
 // allocated here and no call synchronizes (the two status reads aside).
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -9,6 +10,7 @@
 #include <new>
 #include <vector>
 
+#include "block_ops.cuh"
 #include "products.cuh"
 
 using namespace moe;
@@ -356,6 +358,9 @@ struct moe_grouped_plan {
 };
 struct moe_w4_plan {
     moe::RowsArgs a;
+};
+struct moe_linear_plan {
+    moe::LinearArgs a;
 };
 
 extern "C" {
@@ -751,6 +756,272 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
     a.u = u; a.u_type = d.u_type; a.u_stride = u_stride;
     cudaError_t err = launch_norm_pair(a, reinterpret_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return cuda_fail(err, "norm kernel");
+    return MOE_OK;
+}
+
+moe_status moe_linear_plan_create(const moe_linear_desc* desc, moe_linear_plan** plan) {
+    if (!desc || !plan) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    *plan = nullptr;
+    const moe_linear_desc& d = *desc;
+    if (!is_16bit(d.type)) return fail(MOE_ERR_UNSUPPORTED, "type %d (supported: BF16, F16)", (int)d.type);
+    if (!is_value_type(d.y_type)) return fail(MOE_ERR_UNSUPPORTED, "y_type %d (supported: F32, BF16, F16)", (int)d.y_type);
+    if (d.order != MOE_W_OUT_IN && d.order != MOE_W_IN_OUT) return fail(MOE_ERR_INVALID_ARG, "unknown order %d", (int)d.order);
+    moe_status st = check_product_shape(1, d.n_out, d.n_in);
+    if (st) return st;
+    if (!d.w) return fail(MOE_ERR_INVALID_ARG, "w is NULL");
+    if (!aligned(d.w, 16)) return fail(MOE_ERR_INVALID_ARG, "w not 16-byte aligned");
+    const int64_t cols = d.order == MOE_W_OUT_IN ? d.n_in : d.n_out;
+    if (d.row_stride < cols || d.row_stride % 8 || d.row_stride > ((int64_t)1 << 32))
+        return fail(MOE_ERR_INVALID_ARG, "row_stride %lld (need >= %lld, a multiple of 8)", (long long)d.row_stride,
+                    (long long)cols);
+    if (d.bias && !is_value_type(d.bias_type))
+        return fail(MOE_ERR_UNSUPPORTED, "bias_type %d (supported: F32, BF16, F16)", (int)d.bias_type);
+    if (d.bias && !aligned(d.bias, value_bytes(d.bias_type))) return fail(MOE_ERR_INVALID_ARG, "bias not aligned to its type");
+    if ((int)d.act < MOE_ACT_NONE || (int)d.act > MOE_ACT_SILU) return fail(MOE_ERR_UNSUPPORTED, "unknown act %d", (int)d.act);
+    if (!isfinite(d.scale) || !isfinite(d.res_scale)) return fail(MOE_ERR_INVALID_ARG, "scale / res_scale not finite");
+    moe_linear_plan* p = new (std::nothrow) moe_linear_plan();
+    if (!p) return fail(MOE_ERR_INVALID_ARG, "out of host memory");
+    LinearArgs& a = p->a;
+    a.N = d.n_out; a.K = d.n_in;
+    a.bf16 = d.type == MOE_BF16;
+    a.w = d.w; a.w_stride = d.row_stride;
+    a.in_out = d.order == MOE_W_IN_OUT;
+    a.bias = d.bias; a.bias_type = d.bias_type;
+    a.act = d.act;
+    a.scale = d.scale; a.res_scale = d.res_scale;
+    a.y_type = d.y_type;
+    *plan = p;
+    return MOE_OK;
+}
+
+moe_status moe_linear_plan_destroy(moe_linear_plan* plan) {
+    delete plan;
+    return MOE_OK;
+}
+
+moe_status moe_linear_path(const moe_linear_plan* plan, int T, int* path) {
+    if (!plan || !path) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    if (T < 1) return fail(MOE_ERR_INVALID_ARG, "T = %d", T);
+    LinearArgs a = plan->a;
+    a.T = T;
+    *path = linear_pairs(a) ? MOE_LINEAR_PAIRS : MOE_LINEAR_SPLIT;
+    return MOE_OK;
+}
+
+moe_status moe_linear(const moe_linear_plan* plan, const void* x, int64_t x_stride, int T, const void* r, moe_dtype r_type,
+                      int64_t r_stride, void* y, int64_t y_stride, int32_t* status, moe_stream_t stream) {
+    if (!plan) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
+    LinearArgs a = plan->a;
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", T);
+    if (T > 1 << 30) return fail(MOE_ERR_INVALID_ARG, "T = %d too large", T);
+    if (r && !is_value_type(r_type)) return fail(MOE_ERR_UNSUPPORTED, "r_type %d (supported: F32, BF16, F16)", (int)r_type);
+    if (T == 0) return MOE_OK;
+    if (!x || !y) return fail(MOE_ERR_INVALID_ARG, "x / y are NULL");
+    if (!aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x not 16-byte aligned");
+    if (!aligned(y, value_bytes(a.y_type))) return fail(MOE_ERR_INVALID_ARG, "y not aligned to its type");
+    if (r && !aligned(r, value_bytes(r_type))) return fail(MOE_ERR_INVALID_ARG, "r not aligned to its type");
+    if (!aligned(status, 4)) return fail(MOE_ERR_INVALID_ARG, "status not 4-byte aligned");
+    const int64_t most = (int64_t)1 << 32;
+    if (x_stride < a.K || x_stride % 8 || x_stride > most)
+        return fail(MOE_ERR_INVALID_ARG, "x_stride %lld (need >= %d, a multiple of 8)", (long long)x_stride, a.K);
+    if (y_stride < a.N || y_stride > most) return fail(MOE_ERR_INVALID_ARG, "y_stride %lld < n_out %d", (long long)y_stride, a.N);
+    if (r && (r_stride < a.N || r_stride > most))
+        return fail(MOE_ERR_INVALID_ARG, "r_stride %lld < n_out %d", (long long)r_stride, a.N);
+    const RowSpan sx{(uintptr_t)x, 2 * (uint64_t)a.K, 2 * (uint64_t)x_stride, T};
+    const RowSpan sy{(uintptr_t)y, value_bytes(a.y_type) * (uint64_t)a.N, value_bytes(a.y_type) * (uint64_t)y_stride, T};
+    const uint64_t rb = r ? value_bytes(r_type) : 0;
+    const RowSpan sr{(uintptr_t)r, rb * a.N, rb * r_stride, r ? T : 0};
+    const bool in_place = r == y && (int)r_type == a.y_type && (r_stride == y_stride || T == 1);
+    if (meet(sx, sy)) return fail(MOE_ERR_INVALID_ARG, "y overlaps x");
+    if (!in_place && meet(sr, sy)) return fail(MOE_ERR_INVALID_ARG, "y overlaps r without being it");
+    a.T = T;
+    a.x = x; a.x_stride = x_stride;
+    a.r = r; a.r_type = r_type; a.r_stride = r_stride;
+    a.y = y; a.y_stride = y_stride; a.status = status;
+    cudaError_t err = launch_linear(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "dense product kernel");
+    return MOE_OK;
+}
+
+static moe_status check_layer_norm(const moe_layer_norm_desc* desc, int T) {
+    if (!desc) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+    const moe_layer_norm_desc& d = *desc;
+    if (!is_value_type(d.x_type) || !is_value_type(d.y_type))
+        return fail(MOE_ERR_UNSUPPORTED, "types %d / %d (supported: F32, BF16, F16)", (int)d.x_type, (int)d.y_type);
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", T);
+    if (T > 1 << 30) return fail(MOE_ERR_INVALID_ARG, "T = %d too large", T);
+    if (d.H < 1 || d.H > 32768) return fail(MOE_ERR_INVALID_ARG, "H = %d outside 1..32768", d.H);
+    if (!(d.eps >= 0.0f) || !isfinite(d.eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    if (!aligned(d.gamma, 4) || !aligned(d.beta, 4)) return fail(MOE_ERR_INVALID_ARG, "gamma / beta not aligned to their type");
+    return MOE_OK;
+}
+static RowSpan span_of(const void* p, int type, int64_t H, int64_t stride, int T) {
+    return RowSpan{(uintptr_t)p, value_bytes(type) * (uint64_t)H, value_bytes(type) * (uint64_t)stride, p ? T : 0};
+}
+static RowSpan vector_span(const void* p, int64_t n) { return RowSpan{(uintptr_t)p, 4 * (uint64_t)n, 4 * (uint64_t)n, p && n ? 1 : 0}; }
+static bool bad_row_stride(const void* p, int64_t stride, int H) { return p && (stride < H || stride > (int64_t)1 << 32); }
+
+moe_status moe_layer_norm(const moe_layer_norm_desc* desc, const void* x, int64_t x_stride, int T, void* y, int64_t y_stride,
+                          float* mean, float* rstd, moe_stream_t stream) {
+    moe_status st = check_layer_norm(desc, T);
+    if (st) return st;
+    const moe_layer_norm_desc& d = *desc;
+    if (T == 0) return MOE_OK;
+    if (!y && !mean && !rstd) return fail(MOE_ERR_INVALID_ARG, "none of y, mean and rstd is asked for");
+    if (!x) return fail(MOE_ERR_INVALID_ARG, "x is NULL");
+    if (bad_row_stride(x, x_stride, d.H) || bad_row_stride(y, y_stride, d.H))
+        return fail(MOE_ERR_INVALID_ARG, "a row stride is smaller than H = %d (or too large)", d.H);
+    if (!aligned(x, value_bytes(d.x_type)) || !aligned(y, value_bytes(d.y_type)) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+    const RowSpan sx = span_of(x, d.x_type, d.H, x_stride, T), sy = span_of(y, d.y_type, d.H, y_stride, T),
+                  sg = vector_span(d.gamma, d.H), sb = vector_span(d.beta, d.H), sm = vector_span(mean, T), sr = vector_span(rstd, T);
+    const bool in_place = x == y && d.x_type == d.y_type && (x_stride == y_stride || T == 1);
+    if ((!in_place && meet(sx, sy)) || meet(sm, sx) || meet(sr, sx) || meet(sm, sy) || meet(sr, sy) || meet(sm, sr) || meet(sy, sg) ||
+        meet(sy, sb) || meet(sm, sg) || meet(sm, sb) || meet(sr, sg) || meet(sr, sb))
+        return fail(MOE_ERR_INVALID_ARG, "y / mean / rstd overlap an input or each other");
+    LayerNormArgs a{};
+    a.T = T; a.H = d.H;
+    a.x = x; a.x_type = d.x_type; a.x_stride = x_stride;
+    a.y = y; a.y_type = d.y_type; a.y_stride = y_stride;
+    a.gamma = d.gamma; a.beta = d.beta; a.eps = d.eps;
+    a.mean = mean; a.rstd = rstd;
+    cudaError_t err = launch_layer_norm(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "layer norm kernel");
+    return MOE_OK;
+}
+
+moe_status moe_layer_norm_backward_workspace_size(int H, int T, size_t* bytes) {
+    if (!bytes) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    if (H < 1 || H > 32768) return fail(MOE_ERR_INVALID_ARG, "H = %d outside 1..32768", H);
+    if (T < 0 || T > 1 << 30) return fail(MOE_ERR_INVALID_ARG, "T = %d outside 0..2^30", T);
+    *bytes = (size_t)norm_partial_rows(T) * 2 * H * sizeof(float);
+    return MOE_OK;
+}
+
+moe_status moe_layer_norm_backward(const moe_layer_norm_desc* desc, const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const float* mean, const float* rstd, const void* add, int64_t add_stride,
+                                   int T, void* dx, int64_t dx_stride, float* dgamma, float* dbeta, int accumulate,
+                                   void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    moe_status st = check_layer_norm(desc, T);
+    if (st) return st;
+    const moe_layer_norm_desc& d = *desc;
+    if (T > 0 && !dx && !dgamma && !dbeta) return fail(MOE_ERR_INVALID_ARG, "none of dx, dgamma and dbeta is asked for");
+    if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return fail(MOE_ERR_INVALID_ARG, "dgamma / dbeta not 4-byte aligned");
+    const bool sums = dgamma || dbeta;
+    size_t need = 0;
+    if (sums) moe_layer_norm_backward_workspace_size(d.H, T, &need);
+    const RowSpan sdg = vector_span(dgamma, d.H), sdb = vector_span(dbeta, d.H);
+    if (T > 0) {
+        if (!dy || !x || !mean || !rstd) return fail(MOE_ERR_INVALID_ARG, "dy / x / mean / rstd are NULL");
+        if (bad_row_stride(dy, dy_stride, d.H) || bad_row_stride(x, x_stride, d.H) || bad_row_stride(add, add_stride, d.H) ||
+            bad_row_stride(dx, dx_stride, d.H))
+            return fail(MOE_ERR_INVALID_ARG, "a row stride is smaller than H = %d (or too large)", d.H);
+        const size_t xb = value_bytes(d.x_type);
+        if (!aligned(dy, value_bytes(d.y_type)) || !aligned(x, xb) || !aligned(add, xb) || !aligned(dx, xb) || !aligned(mean, 4) ||
+            !aligned(rstd, 4))
+            return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+        if (need && (!workspace || ws_bytes < need))
+            return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+        if (need && !aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+        const RowSpan sx = span_of(x, d.x_type, d.H, x_stride, T), sdy = span_of(dy, d.y_type, d.H, dy_stride, T),
+                      sa = span_of(add, d.x_type, d.H, add_stride, T), sdx = span_of(dx, d.x_type, d.H, dx_stride, T);
+        const RowSpan sw{(uintptr_t)workspace, need, need, need ? 1 : 0};
+        const RowSpan vecs[] = {vector_span(d.gamma, d.H), vector_span(mean, T), vector_span(rstd, T)};
+        auto same = [&](const void* p, int type, int64_t stride) {
+            return p == dx && type == d.x_type && (stride == dx_stride || T == 1);
+        };
+        bool clash = (!same(x, d.x_type, x_stride) && meet(sdx, sx)) || (!same(dy, d.y_type, dy_stride) && meet(sdx, sdy)) ||
+                     (!same(add, d.x_type, add_stride) && meet(sdx, sa));
+        for (const RowSpan& o : {sdg, sdb, sw}) clash |= meet(o, sx) || meet(o, sdy) || meet(o, sa) || meet(o, sdx);
+        for (const RowSpan& v : vecs)
+            for (const RowSpan& o : {sdg, sdb, sw, sdx}) clash |= meet(o, v);
+        clash |= meet(sw, sdg) || meet(sw, sdb);
+        if (clash) return fail(MOE_ERR_INVALID_ARG, "dx / dgamma / dbeta / workspace overlap an input or each other");
+    }
+    if (meet(sdg, sdb)) return fail(MOE_ERR_INVALID_ARG, "dgamma and dbeta overlap each other");
+    if (T == 0 && (!sums || accumulate)) return MOE_OK;
+    LayerNormArgs a{};
+    a.T = T; a.H = d.H;
+    a.x = x; a.x_type = d.x_type; a.x_stride = x_stride;
+    a.y = const_cast<void*>(dy); a.y_type = d.y_type; a.y_stride = dy_stride;
+    a.gamma = d.gamma; a.eps = d.eps;
+    a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+    a.add = add; a.add_stride = add_stride;
+    a.dx = dx; a.dx_stride = dx_stride;
+    a.dgamma = dgamma; a.dbeta = dbeta;
+    a.accumulate = accumulate != 0;
+    a.partial = sums && T > 0 ? static_cast<float*>(workspace) : nullptr;
+    cudaError_t err = launch_layer_norm_backward(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "layer norm backward kernels");
+    return MOE_OK;
+}
+
+static moe_status check_balance_shape(int E, int T, int n_seqs) {
+    if (E < 1 || E > kMaxExperts) return fail(MOE_ERR_INVALID_ARG, "n_experts %d outside 1..%d", E, kMaxExperts);
+    if (T < 0 || T > 1 << 30) return fail(MOE_ERR_INVALID_ARG, "T = %d outside 0..2^30", T);
+    if (n_seqs < 1 || n_seqs > 65535) return fail(MOE_ERR_INVALID_ARG, "n_seqs %d outside 1..65535", n_seqs);
+    return MOE_OK;
+}
+
+moe_status moe_balance_workspace_size(int n_experts, int T, int n_seqs, size_t* bytes) {
+    if (!bytes) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    moe_status st = check_balance_shape(n_experts, T, n_seqs);
+    if (st) return st;
+    *bytes = balance_ws_bytes(n_experts, T, n_seqs);
+    return MOE_OK;
+}
+
+moe_status moe_balance_loss(const moe_balance_desc* desc, const float* logits, int64_t stride, const int32_t* ids, int T,
+                            const int32_t* seq_offsets, int n_seqs, const uint8_t* mask, const float* upstream, float* loss,
+                            int32_t* counts, float* dlogits, int64_t dstride, int32_t* status, void* workspace, size_t ws_bytes,
+                            moe_stream_t stream) {
+    if (!desc) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+    const moe_balance_desc& d = *desc;
+    if (d.mode != MOE_ROUTE_SOFTMAX && d.mode != MOE_ROUTE_SIGMOID_GROUP)
+        return fail(MOE_ERR_INVALID_ARG, "unknown routing mode %d", (int)d.mode);
+    const int E = d.n_experts, k = d.top_k;
+    moe_status st = check_balance_shape(E, T, n_seqs);
+    if (st) return st;
+    if (k < 1 || k > E || k > kMaxTopK) return fail(MOE_ERR_INVALID_ARG, "top_k %d outside 1..min(E, %d)", k, kMaxTopK);
+    if ((int64_t)T * k > (int64_t)1 << 30) return fail(MOE_ERR_INVALID_ARG, "T*k too large");
+    if (!isfinite(d.coef)) return fail(MOE_ERR_INVALID_ARG, "coef not finite");
+    if (T > 0 && !loss && !counts && !dlogits) return fail(MOE_ERR_INVALID_ARG, "none of loss, counts and dlogits is asked for");
+    if (!seq_offsets && n_seqs != 1) return fail(MOE_ERR_INVALID_ARG, "seq_offsets may be NULL for one sequence only");
+    if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(seq_offsets, 4) || !aligned(upstream, 4) || !aligned(loss, 4) ||
+        !aligned(counts, 4) || !aligned(dlogits, 4) || !aligned(status, 4))
+        return fail(MOE_ERR_INVALID_ARG, "a pointer is not 4-byte aligned");
+    const size_t need = balance_ws_bytes(E, T, n_seqs);
+    if (!workspace || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+    if (!aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    if (T > 0) {
+        if (!ids || ((loss || dlogits) && !logits)) return fail(MOE_ERR_INVALID_ARG, "logits / ids are NULL");
+        const bool in_place = logits == dlogits && (stride == dstride || T == 1);
+        if (bad_row_stride(loss || dlogits ? logits : nullptr, stride, E) || bad_row_stride(dlogits, dstride, E))
+            return fail(MOE_ERR_INVALID_ARG, "a row stride is smaller than E = %d (or too large)", E);
+        if (in_place && dlogits && d.accumulate) return fail(MOE_ERR_INVALID_ARG, "dlogits is logits: nothing to add to");
+        const RowSpan sl = span_of(logits, MOE_F32, E, stride, T), sd = span_of(dlogits, MOE_F32, E, dstride, T);
+        const RowSpan in[] = {vector_span(ids, (int64_t)T * k), vector_span(seq_offsets, n_seqs + 1),
+                              RowSpan{(uintptr_t)mask, (uint64_t)T, (uint64_t)T, mask ? 1 : 0}, vector_span(upstream, 1)};
+        const RowSpan out[] = {vector_span(loss, 1), vector_span(counts, (int64_t)n_seqs * E), vector_span(status, 1),
+                               RowSpan{(uintptr_t)workspace, need, need, 1}, sd};
+        bool clash = !in_place && meet(sl, sd);
+        for (int i = 0; i < 5; ++i) {
+            for (const RowSpan& v : in) clash |= meet(out[i], v);
+            if (i < 4) clash |= meet(out[i], sl);
+            for (int j = 0; j < i; ++j) clash |= meet(out[i], out[j]);
+        }
+        if (clash) return fail(MOE_ERR_INVALID_ARG, "an output or the workspace overlaps an input or another output");
+    }
+    BalanceArgs a{};
+    a.E = E; a.k = k; a.T = T; a.n_seqs = n_seqs;
+    a.sigmoid = d.mode == MOE_ROUTE_SIGMOID_GROUP;
+    a.accumulate = d.accumulate != 0;
+    a.coef = d.coef;
+    a.logits = logits; a.stride = stride; a.ids = ids; a.seq_offsets = seq_offsets; a.mask = mask; a.upstream = upstream;
+    a.loss = loss; a.counts = counts; a.dlogits = dlogits; a.dstride = dstride; a.status = status;
+    a.ws = workspace;
+    cudaError_t err = launch_balance(a, reinterpret_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "balance loss kernels");
     return MOE_OK;
 }
 

@@ -30,9 +30,8 @@
 // 57.2 us (93 %, bytes); 512 tokens, 256 experts of 2048 x 7168 stored [in][out] 1.10 ms (7.6 GB, at the copy's
 // rate).  The gated half is what is left: of 171 us it took 156 without its gathers, 154 without its epilogue, 141 without
 // both, and 125 with no loads at all.
+#include "cluster_ptx.cuh"
 #include "products.cuh"
-#include "tc_ptx.cuh"
-#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -55,7 +54,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kSumCol = 128;
 template <bool UP> constexpr int kRun = UP ? 6 : 12;     // steps of 64, fp32 outputs
 constexpr int kRun16 = 128;                              // 16-bit outputs
-constexpr int kSpins = 64;                               // tests of a barrier before a wait looks at the clock
 
 struct DenseParams {
     CUtensorMap tw0, tw1;        // W, W_up: [E][rows][cols], boxes of 64 x 64
@@ -75,141 +73,7 @@ struct DenseParams {
     int stall;                   // test setting: the first wait of the MMA warp never completes
 };
 
-__device__ __forceinline__ uint32_t cta_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-    cluster_arrive();
-    cluster_wait();
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
-// The pair's barriers order copies and MMAs, which carry their own ordering; no plain loads or stores
-// pass from CTA to CTA through them.  So their operations take the default scope: with release and
-// acquire at cluster scope every step of the pipeline waited about 0.5 us for its arrival.
-// Shared address of the pair's first CTA (the one that issues the MMAs) for an address of this one.
-__device__ __forceinline__ uint32_t in_leader(uint32_t a) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t in_peer(uint32_t a) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(r) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-// Bounded wait on a barrier that either CTA of the pair arrives on: false after limit_ns (raising
-// abort_flag) or when another warp of this CTA has raised it.
-__device__ __forceinline__ bool wait_one(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-    for (int i = 0; i < kSpins; ++i)
-        if (mbar_test(b, parity)) return true;
-    const uint64_t t0 = gtime();                         // (reading the clock takes long: not before the spins)
-    while (!mbar_test(b, parity)) {
-        if (*abort_flag) return false;
-        if (gtime() - t0 > limit_ns) { *abort_flag = 1; return false; }
-    }
-    return true;
-}
-// The same for a whole warp: the answer is that of all its lanes.
-__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-    return __all_sync(0xffffffffu, wait_one(b, parity, abort_flag, limit_ns));
-}
-// The same value on every lane, for the compiler to know it.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-// True on one lane of the (converged) warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
-    return r != 0;
-}
-// A position in the ring of stages and the parity of its round.
-struct Ring {
-    int s = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void next() {
-        if (++s == kStages) { s = 0; ph ^= 1; }
-    }
-};
-__device__ __forceinline__ void drain_wait(uint64_t* b, uint32_t parity, uint64_t limit_ns) {
-    const uint64_t t0 = gtime();
-    while (!mbar_test(b, parity))
-        if (gtime() - t0 > limit_ns) return;
-}
-
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(dst),
-        "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(m), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, int x, int r0, int r1, int r2, int r3, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(m), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// All MMAs issued so far arrive on this barrier of both CTAs when they are done.
-__device__ __forceinline__ void commit_pair(uint64_t* b) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(b)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-// MN-major operand, 128-byte swizzle: 64-element blocks along M 8192 bytes apart, groups of 8 c 1024.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(8192 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-        "%31}, [%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-}
-// True on every thread of the named barrier when it is true on all of them.
-__device__ __forceinline__ bool all_of(int barrier, int threads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"(barrier), "r"(threads), "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void named_sync(int barrier, int threads) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
-}
+using Ring = RingOf<kStages>;
 
 struct Tile {
     int e, mb, tok0, ntok, nh;   // expert, block of M rows, first sorted position, rows, columns per CTA
@@ -262,20 +126,6 @@ __device__ __forceinline__ int bucket_of(int cnt, int max_n) {
     const int nb = blocks_of(cnt, max_n), cols = ((cnt + nb - 1) / nb + 31) >> 5;
     return (nb > 1 ? 0 : 8) + 8 - cols;
 }
-
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-template <typename T> __device__ __forceinline__ T to_out(float v);
-template <> __device__ __forceinline__ float to_out<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half to_out<__half>(float v) { return __float2half_rn(v); }
 
 // An epilogue warp: warp w reads TMEM lanes 32 (w % 4).. (weight rows) and every other group of columns
 // (rows of x) of each tile, and stores 32 neighbouring outputs of one row at a time.

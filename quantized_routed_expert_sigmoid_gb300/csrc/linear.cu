@@ -1,0 +1,668 @@
+// linear.cu -- a dense product with its epilogue on the 5th-generation tensor cores:
+//   y[t, n] = res_scale * r[t, n] + scale * act(sum_c W[n, c] x[t, c] + bias[n])
+// The weights are the M operand (a lane of TMEM holds one output channel, a column one row of x): a few rows of x
+// then cost a few columns, and the bias is one register.  Everything behind the sum happens between TMEM and
+// the one store of y, in fp32.  Two kernels:
+// - split_kernel: tiles of 128 channels by up to 128 rows of x, one CTA each; where that leaves SMs idle, a cluster
+//   of up to 8 CTAs splits the sum of a tile.  Each CTA sends the columns of its part to the CTA of the cluster that finishes
+//   them (shared memory of the cluster, no workspace), which adds the parts in their order.
+// - pair_kernel: tiles of 256 channels by up to 256 rows, a pair of CTAs (cta_group::2) each, persistent, two accumulators: one
+//   is read out while the next tile runs.  A weight is read from L2 once per 256 rows.
+// The tensor cores cut a sum off after each instruction instead of rounding it, an error that grows with the
+// sum's length; so long sums are made of runs (768 elements for fp32 outputs, 8192 for 16-bit ones), which the epilogue
+// adds with rounding in its registers.
+// Every wait is bounded; one that runs out is reported (MOE_ERR_TIMEOUT), the copies and MMAs in flight are waited for
+// (bounded), TMEM is freed and the kernel returns.
+#include <algorithm>
+
+#include "block_ops.cuh"
+#include "cluster_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kStepK = 64;
+constexpr int kRun32 = 12, kRun16 = 128;                 // steps of a run: fp32 outputs, 16-bit outputs
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;              // (a warp reads the TMEM lanes 32 (warp % 4)..)
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+
+struct Epilogue {
+    const void* bias;
+    const void* r;
+    void* y;
+    int bias_type, r_type, y_type, act;
+    int64_t r_stride, y_stride;
+    float scale, res_scale;
+    int T, N;
+};
+
+struct LinearParams {
+    CUtensorMap tw;              // W: boxes of 64 x 128, or 64 x 64 of [K][N]
+    CUtensorMap tx[4];           // x: boxes of 64 x 16, 32, 64, 128
+    Epilogue e;
+    int K, nk, run;              // nk: steps of the sum, run: of one run
+    bool bf16;
+    int cols;                    // columns of a tile (split: 16, 32, 64 or 128; pairs: a multiple of 32)
+    int box;                     // which of tx
+    int stages;
+    int n_mb, n_tb;              // tiles along the channels and along the rows of x
+    int32_t* status;
+    uint64_t wait_ns;
+    int stall;                   // test setting: the first wait of the MMA warp never completes
+};
+
+// ---------------------------------------------------------------- what follows the sum
+// Phi(-z) e^(z^2/2), z >= 0, the normal distribution's tail without its exponential: a polynomial in
+// t = 1 / (1 + 0.31 z) without constant term, fitted to it (least squares of the relative error, reweighted towards its
+// largest values) on 0..14, where e^(-z^2/2) leaves fp32; relative error below 5e-6.
+__device__ __forceinline__ float tail_factor(float z) {
+    const float t = __fdividef(1.0f, fmaf(0.31f, z, 1.0f));
+    float p = fmaf(t, -0.07392511516809464f, 0.18043823540210724f);
+    p = fmaf(t, p, 0.01575886830687523f);
+    p = fmaf(t, p, 0.13342174887657166f);
+    p = fmaf(t, p, 0.12044348567724228f);
+    p = fmaf(t, p, 0.12386047095060349f);
+    return t * p;
+}
+// FAST, for 16-bit outputs: relative error below 2e-5 (a 20th of half a step of fp16), by quick exponentials (off by
+// 2 + 1.17 |argument| units of 2^-23) and quick divisions.
+template <int ACT, bool FAST>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == MOE_ACT_RELU) {
+        return z < 0.f ? 0.f : z;                         // (a NaN stays)
+    } else if constexpr (ACT == MOE_ACT_SILU) {
+        return silu_times<FAST>(z, 1.0f);
+    } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
+        // z / (1 + e^(-2u)), from e^(-|2u|), which does not overflow
+        const float w = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+        const float q = FAST ? __expf(-fabsf(w)) : expf(-fabsf(w));
+        const float top = w >= 0.f ? z : z * q;
+        return FAST ? __fdividef(top, 1.0f + q) : top / (1.0f + q);
+    } else if constexpr (FAST) {
+        const float q = tail_factor(fabsf(z)) * __expf(-0.5f * z * z);
+        return z * (z >= 0.f ? 1.0f - q : q);
+    } else {
+        return z * normcdff(z);
+    }
+}
+template <int ACT, int C>
+__device__ __forceinline__ void activate_all(float (&v)[C], bool fast) {
+    if (fast) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = activate<ACT, true>(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = activate<ACT, false>(v[i]);
+    }
+}
+
+// C values of channel `row`, of the rows of x t0, t0 + step, ..: those below e.T and `end` are finished and stored.
+template <int C>
+__device__ __forceinline__ void finish(const Epilogue& e, float bias, float (&v)[C], int row, int t0, int step, int end) {
+    if (row >= e.N) return;
+    const int n = min(end, e.T) - t0;                    // (i * step < n: in range)
+    float r[C];
+    if (e.r) {
+        const int64_t at = (int64_t)t0 * e.r_stride + row, by = (int64_t)step * e.r_stride;
+        if (e.r_type == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) r[i] = i * step < n ? static_cast<const float*>(e.r)[at + i * by] : 0.f;
+        } else if (e.r_type == MOE_BF16) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                r[i] = i * step < n ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.r)[at + i * by]) : 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i) r[i] = i * step < n ? __half2float(static_cast<const __half*>(e.r)[at + i * by]) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] += bias;
+    const bool fast = e.y_type != MOE_F32;
+    switch (e.act) {
+        case MOE_ACT_RELU: activate_all<MOE_ACT_RELU>(v, fast); break;
+        case MOE_ACT_GELU: activate_all<MOE_ACT_GELU>(v, fast); break;
+        case MOE_ACT_GELU_TANH: activate_all<MOE_ACT_GELU_TANH>(v, fast); break;
+        case MOE_ACT_SILU: activate_all<MOE_ACT_SILU>(v, fast); break;
+        default: break;
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        v[i] *= e.scale;
+        if (e.r) v[i] = fmaf(e.res_scale, r[i], v[i]);
+    }
+    const int64_t at = (int64_t)t0 * e.y_stride + row, by = (int64_t)step * e.y_stride;
+    if (e.y_type == MOE_F32) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i * step < n) static_cast<float*>(e.y)[at + i * by] = v[i];
+    } else if (e.y_type == MOE_BF16) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i * step < n) static_cast<__nv_bfloat16*>(e.y)[at + i * by] = __float2bfloat16_rn(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i * step < n) static_cast<__half*>(e.y)[at + i * by] = __float2half_rn(v[i]);
+    }
+}
+__device__ __forceinline__ float bias_at(const Epilogue& e, int row) {
+    return e.bias && row < e.N ? load1(e.bias, e.bias_type, row) : 0.f;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+
+// ---------------------------------------------------------------- one CTA a tile, the sum split over a cluster
+constexpr int kMaxStages = 12, kMaxCols = 128;
+constexpr int kABytes = 128 * 128;                       // a step's weights
+
+template <bool IN_OUT>
+__global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constant__ LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accf[2], accr[2], drain, never;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, issued;
+    volatile int* abort_flag = &abort_word;
+    const int stage_bytes = kABytes + p.cols * 128;
+    float* parts = reinterpret_cast<float*>(smem + p.stages * stage_bytes);   // [CTA][its columns here][128]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cta_rank();
+    uint32_t splits;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+    const int mb = blockIdx.x / splits, tok0 = blockIdx.y * p.cols;
+    const int k0 = (int)((int64_t)p.nk * rank / splits), k1 = (int)((int64_t)p.nk * (rank + 1) / splits);
+    const int n_runs = (k1 - k0 + p.run - 1) / p.run;
+    const uint32_t tmem_cols = max(32, 2 * p.cols);
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], kEpiWarps); }
+        mbar_init(&drain, 1);
+        mbar_init(&never, 1);
+        abort_word = 0;
+        issued = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tw);
+        prefetch_map(&p.tx[p.box]);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)), "r"(tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    cluster_arrive();                                    // (the cluster's CTAs run: waited for before the first part is sent)
+    tc_after();
+    const uint32_t tmem = tmem_slot;
+    wait_for_previous();
+    allow_next();
+
+    if (warp == 0) {
+        // ======================= loads =======================
+        int g = 0, s = 0;
+        uint32_t ph = 1;
+        const uint32_t bytes = (uint32_t)stage_bytes;
+        for (int kb = k0; kb < k1; ++kb, ++g) {
+            if (!wait_warp(&empty[s], ph, abort_flag, p.wait_ns)) break;
+            if (elect_one()) {
+                uint8_t* a = smem + s * stage_bytes;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[s])), "r"(bytes) : "memory");
+                if constexpr (IN_OUT) {
+                    tma_load_2d(a, &p.tw, mb * 128, kb * kStepK, &full[s]);
+                    tma_load_2d(a + 8192, &p.tw, mb * 128 + 64, kb * kStepK, &full[s]);
+                } else {
+                    tma_load_2d(a, &p.tw, kb * kStepK, mb * 128, &full[s]);
+                }
+                tma_load_2d(a + kABytes, &p.tx[p.box], kb * kStepK, tok0, &full[s]);
+            }
+            __syncwarp();
+            if (++s == p.stages) { s = 0; ph ^= 1; }
+        }
+        if (lane == 0) issued = g;
+    } else if (warp == 1) {
+        // ======================= MMA issue =======================
+        const uint32_t idesc = idesc_mma(128, p.cols, p.bf16) | (IN_OUT ? 1u << 15 : 0u);
+        constexpr uint32_t kAdvA = (IN_OUT ? 2048 : 32) >> 4, kAdvB = 32 >> 4;
+        int s = 0, j = 0;
+        uint32_t ph = 0;
+        bool ok = true, any = false;
+        for (int r0 = k0; ok && r0 < k1; r0 += p.run, ++j) {
+            const int b = j & 1, r1 = min(r0 + p.run, k1);
+            if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
+            tc_after();
+            const uint32_t acc = tmem + (uint32_t)b * p.cols;
+            for (int kb = r0; kb < r1; ++kb) {
+                const bool stalled = p.stall && !any;    // (test setting)
+                if (!wait_warp(stalled ? &never : &full[s], stalled ? 0u : ph, abort_flag, p.wait_ns)) { ok = false; break; }
+                tc_after();
+                if (elect_one()) {
+                    const uint32_t a = su32(smem + s * stage_bytes);
+                    const uint64_t da = IN_OUT ? sdesc_mn(a) : sdesc(a), db = sdesc(a + kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < kStepK / 16; ++kk) mma_f16(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 || kb > r0);
+                    mma_commit(&empty[s]);
+                    if (kb == r1 - 1) mma_commit(&accf[b]);
+                }
+                __syncwarp();
+                any = true;
+                if (++s == p.stages) { s = 0; ph ^= 1; }
+            }
+        }
+        if (any) {                                       // every MMA issued has completed before TMEM is freed
+            if (elect_one()) mma_commit(&drain);
+            __syncwarp();
+            drain_wait(&drain, 0, p.wait_ns);
+        }
+    }
+    __syncwarp();
+    cluster_wait();
+    const int q = warp & 3, side = (warp - kEpiWarp0) >> 2, half = p.cols / 2;
+    const int row = mb * 128 + q * 32 + lane;
+    const bool epi = warp >= kEpiWarp0;
+    const int own = p.cols / (int)splits;                // columns that a CTA of the cluster finishes
+    if (epi) {
+        // ======================= the sums, run by run =======================
+        const float bias = bias_at(p.e, row);
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + side * half;
+        float sum[kMaxCols / 2];
+        bool ok = true;
+        for (int j = 0; j < n_runs; ++j) {
+            const int b = j & 1;
+            ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int c = 0; c < kMaxCols / 2; c += 8)
+                if (c < half) {
+                    uint32_t v[8];
+                    tmem_ld8(lanes + b * p.cols + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sum[c + i] = j ? __fadd_rn(sum[c + i], __uint_as_float(v[i])) : __uint_as_float(v[i]);
+                }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accr[b]);
+        }
+        if (ok && splits == 1) {
+#pragma unroll
+            for (int c = 0; c < kMaxCols / 2; c += 8)
+                if (c < half) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = sum[c + i];
+                    finish<8>(p.e, bias, v, row, tok0 + side * half + c, 1, p.e.T);
+                }
+        } else if (ok) {
+            const uint32_t here = su32(parts) + (uint32_t)(q * 32 + lane) * 4;
+#pragma unroll
+            for (int c = 0; c < kMaxCols / 2; ++c)
+                if (c < half) {
+                    const int col = side * half + c, to = col / own;
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cta(here + (uint32_t)(rank * own + col - to * own) * 512, to)),
+                                 "f"(sum[c])
+                                 : "memory");
+                }
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (tid == 0 && *abort_flag) {
+        // copies in flight: wait, within the limit, for their bytes
+        for (int g = max(0, issued - p.stages); g < issued; ++g) drain_wait(&full[g % p.stages], (g / p.stages) & 1, p.wait_ns);
+        if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
+    }
+    __syncwarp();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
+    if (splits == 1) return;
+    cluster_sync();                                      // the parts are here
+    if (!epi || *abort_flag) return;
+    const float bias = bias_at(p.e, row);
+    const float* at = parts + q * 32 + lane;
+    for (int c = side; c < own; c += 8) {                // columns c, c + 2, c + 4, c + 6
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = 0.f;
+            if (c + 2 * i < own)
+                for (int s = 0; s < (int)splits; ++s) v[i] += at[(s * own + c + 2 * i) * 128];
+        }
+        finish<4>(p.e, bias, v, row, tok0 + rank * own + c, 2, tok0 + (rank + 1) * own);
+    }
+}
+
+// ---------------------------------------------------------------- a pair of CTAs a tile
+constexpr int kPairStages = 6, kPairCols = 256;
+constexpr int kPairStageBytes = kABytes + 128 * 128;
+constexpr uint32_t kPairTmem = 512;
+
+template <bool IN_OUT, bool RUNS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ LinearParams p) {
+    using Ring = RingOf<kPairStages>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[kPairStages], empty[kPairStages], accf[2], accr[2], drain, never;   // full, accr: the first CTA's
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, issued;
+    volatile int* abort_flag = &abort_word;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t cta = cta_rank();
+    if (tid == 0) {
+        for (int i = 0; i < kPairStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kEpiWarps); }
+        mbar_init(&drain, 1);
+        mbar_init(&never, 1);
+        abort_word = 0;
+        issued = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tw);
+        prefetch_map(&p.tx[p.box]);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)), "n"(kPairTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    cluster_sync();
+    tc_after();
+    const uint32_t tmem = tmem_slot;
+    wait_for_previous();
+    allow_next();
+    const int n_pairs = gridDim.x >> 1, first = blockIdx.x >> 1, n_tiles = p.n_mb * p.n_tb;
+    const int nh = p.cols >> 1;                          // this CTA's columns
+
+    if (warp == 0) {
+        // ======================= loads =======================
+        const uint32_t full0 = in_leader(su32(full)), stage0 = su32(smem);
+        const uint32_t bytes = kABytes + (2048u << p.box);
+        int g = 0;
+        Ring ring;
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += n_pairs) {
+            const int tb = t / p.n_mb, mb = t - tb * p.n_mb;
+            const int c0 = uniform(tb * p.cols + (int)cta * nh), r0 = uniform(mb * 256 + (int)cta * 128);
+            for (int kb = 0; kb < p.nk; ++kb, ++g, ring.next()) {
+                if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                const uint32_t bar = full0 + 8 * ring.s, a = stage0 + ring.s * kPairStageBytes;
+                if (elect_one()) {
+                    arrive_tx_cluster(bar, bytes);
+                    if constexpr (IN_OUT) {
+                        tma_2d(a, &p.tw, r0, kb * kStepK, bar);
+                        tma_2d(a + 8192, &p.tw, r0 + 64, kb * kStepK, bar);
+                    } else {
+                        tma_2d(a, &p.tw, kb * kStepK, r0, bar);
+                    }
+                    tma_2d(a + kABytes, &p.tx[p.box], kb * kStepK, c0, bar);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) issued = g;
+        // the last steps' arrivals on this CTA's barriers have landed before it may leave
+        if (g < kPairStages) { ring.s = 0; ring.ph = 1; }
+        for (int i = 0; ok && i < min(g, kPairStages); ++i, ring.next())
+            ok = wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns);
+    } else if (warp == 1) {
+        // ======================= MMA issue (in the first CTA) =======================
+        if (cta == 0) {
+            const uint32_t a0 = su32(smem);
+            const uint64_t da0 = IN_OUT ? sdesc_mn(a0) : sdesc(a0), db0 = sdesc(a0 + kABytes);
+            constexpr uint32_t kAdvA = (IN_OUT ? 2048 : 32) >> 4, kAdvB = 32 >> 4;
+            const uint32_t idesc = uniform(idesc_mma(256, p.cols, p.bf16) | (IN_OUT ? 1u << 15 : 0u));
+            Ring ring;
+            int j = 0;
+            bool ok = true, any = false;
+            for (int t = first; ok && t < n_tiles; t += n_pairs) {
+                for (int kb = 0, start = 0, b = 0; kb < p.nk; ++kb, ring.next()) {
+                    if (kb == start) {                   // the first step of a run
+                        b = j & 1;
+                        if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
+                        tc_after();
+                    }
+                    const uint32_t acc = uniform(tmem + (uint32_t)b * kPairCols);
+                    const bool last_step = kb == p.nk - 1 || kb - start == p.run - 1;
+                    const bool stalled = p.stall && !any;            // (test setting)
+                    if (!wait_warp(stalled ? &never : &full[ring.s], stalled ? 0u : ring.ph, abort_flag, p.wait_ns)) { ok = false; break; }
+                    tc_after();
+                    const uint32_t adv = (uint32_t)ring.s * (kPairStageBytes >> 4);
+                    const uint64_t da = da0 + adv, db = db0 + adv;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < kStepK / 16; ++kk)
+                            mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 || kb > start);
+                        commit_pair(&empty[ring.s]);
+                        if (last_step) commit_pair(&accf[b]);
+                    }
+                    __syncwarp();
+                    if (last_step) { start = kb + 1; ++j; }
+                    any = true;
+                }
+            }
+            if (any) {                                   // every MMA issued has completed before TMEM is freed
+                if (elect_one())
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(&drain))
+                                 : "memory");
+                __syncwarp();
+                drain_wait(&drain, 0, p.wait_ns);
+            }
+        }
+    } else if (warp >= kEpiWarp0) {
+        // ======================= epilogue: lanes 32 q.. of TMEM, every other group of columns =======================
+        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16), accr0 = in_leader(su32(accr));
+        auto release = [&](int b) {
+            tc_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(accr0 + 8 * b);
+        };
+        int j = 0;
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += n_pairs) {
+            const int tb = t / p.n_mb, mb = t - tb * p.n_mb;
+            const int row = mb * 256 + (int)cta * 128 + q * 32 + lane, tok0 = tb * p.cols;
+            const int end = min(tok0 + p.cols, p.e.T);
+            const float bias = bias_at(p.e, row);
+            if constexpr (RUNS) {
+                // columns 32 side + 64 i .. of the runs, summed in registers
+                float sum[kPairCols / 2];
+                for (int k0 = 0; k0 < p.nk; k0 += p.run, ++j) {
+                    const int b = j & 1;
+                    ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
+                    if (!ok) break;
+                    tc_after();
+#pragma unroll
+                    for (int i = 0; i < kPairCols / 2; i += 16) {
+                        const int c = (i & ~31) * 2 + 32 * side + (i & 31);
+                        if (tok0 + c < end) {
+                            uint32_t v[16];
+                            tmem_ld16(lanes + b * kPairCols + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                sum[i + e] = k0 ? __fadd_rn(sum[i + e], __uint_as_float(v[e])) : __uint_as_float(v[e]);
+                        }
+                    }
+                    release(b);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kPairCols / 2; i += 16) {
+                    const int c = (i & ~31) * 2 + 32 * side + (i & 31);
+                    if (tok0 + c < end) {
+                        float v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = sum[i + e];
+                        finish<16>(p.e, bias, v, row, tok0 + c, 1, end);
+                    }
+                }
+            } else {
+                const int b = j & 1;
+                ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
+                if (!ok) break;
+                tc_after();
+                for (int c = 32 * side; tok0 + c < end; c += 64) {
+                    uint32_t u[32];
+                    tmem_ld32(lanes + b * kPairCols + c, u);
+                    tmem_ld_wait();
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[e]);
+                    finish<32>(p.e, bias, v, row, tok0 + c, 1, end);
+                }
+                release(b);
+                ++j;
+            }
+        }
+    }
+    tc_before();
+    __syncwarp();
+    cluster_sync();                                      // both CTAs' roles have left their loops
+    if (cta == 0 && tid == 0) {
+        // after a timeout copies may still be in flight: complete the phases of the steps that one of the CTAs has not
+        // arrived for and wait, within the limit, for the bytes
+        int other_abort, other_issued;
+        asm volatile("ld.volatile.shared::cluster.u32 %0, [%1];" : "=r"(other_abort) : "r"(in_peer(su32(&abort_word))) : "memory");
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other_issued) : "r"(in_peer(su32(&issued))) : "memory");
+        if (*abort_flag || other_abort) {
+            const int last = max(issued, other_issued);
+            for (int s = max(0, last - kPairStages); s < last; ++s) {
+                if (issued <= s) mbar_arrive(&full[s % kPairStages]);
+                if (other_issued <= s) mbar_arrive(&full[s % kPairStages]);
+            }
+            for (int s = max(0, last - kPairStages); s < last; ++s) drain_wait(&full[s % kPairStages], (s / kPairStages) & 1, p.wait_ns);
+            if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    tc_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kPairTmem) : "memory");
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+cudaError_t launch_clusters(const void* fn, dim3 grid, int cluster, size_t smem, cudaStream_t s, void** args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+bool fill(LinearParams& p, const LinearArgs& a) {
+    const cuuint64_t wd[3] = {(cuuint64_t)(a.in_out ? a.N : a.K), (cuuint64_t)(a.in_out ? a.K : a.N), 1};
+    const cuuint64_t ws[2] = {(cuuint64_t)a.w_stride * 2, 0};
+    const cuuint64_t xd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.T, 1};
+    const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
+    const CUtensorMapDataType type = a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (!encode_map(&p.tw, type, 2, a.w, wd, ws, 64, a.in_out ? 64 : 128)) return false;
+    if (!encode_map(&p.tx[p.box], type, 2, a.x, xd, xs, 64, 16 << p.box)) return false;
+    p.e = Epilogue{a.bias, a.r, a.y, a.bias_type, a.r_type, a.y_type, a.act, a.r_stride, a.y_stride, a.scale, a.res_scale, a.T, a.N};
+    p.K = a.K;
+    p.nk = ceil_div(a.K, kStepK);
+    p.bf16 = a.bf16;
+    p.status = a.status;
+    const WaitCfg wc = wait_cfg();
+    p.wait_ns = wc.limit_ns;
+    p.stall = wc.stall;
+    return true;
+}
+// Runs of even length, none longer than the output's type allows.
+int run_of(int steps, int y_type) {
+    const int longest = y_type == MOE_F32 ? kRun32 : kRun16;
+    return ceil_div(steps, ceil_div(steps, longest));
+}
+
+cudaError_t launch_split(const LinearArgs& a, cudaStream_t s) {
+    LinearParams p{};
+    p.box = a.T <= 16 ? 0 : a.T <= 32 ? 1 : a.T <= 64 ? 2 : 3;
+    p.cols = 16 << p.box;
+    if (!fill(p, a)) return cudaErrorInvalidValue;
+    p.n_mb = ceil_div(a.N, 128);
+    p.n_tb = ceil_div(a.T, p.cols);
+    const void* fn = a.in_out ? (const void*)split_kernel<true> : (const void*)split_kernel<false>;
+    static std::atomic<uint64_t> ready[2];
+    int sms = 0;
+    const int stage = kABytes + p.cols * 128, parts = p.cols * 512, most = 227 * 1024 - 1024;
+    cudaError_t err = prepare_kernel(fn, most, ready[a.in_out], &sms);
+    if (err != cudaSuccess) return err;
+    int splits = 1;
+    while (splits < 8 && (int64_t)p.n_mb * p.n_tb * splits * 2 <= sms && p.nk >= splits * 4) splits *= 2;
+    const int steps = ceil_div(p.nk, splits);
+    p.run = run_of(steps, a.y_type);
+    p.stages = std::min(std::min(steps, kMaxStages), (most - 1024 - parts) / stage);
+    void* args[] = {&p};
+    return launch_clusters(fn, dim3(p.n_mb * splits, p.n_tb), splits, 1024 + (size_t)p.stages * stage + (splits > 1 ? parts : 0), s, args);
+}
+
+cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
+    LinearParams p{};
+    static std::atomic<uint64_t> ready[4];
+    int sms = 0;
+    const bool runs = ceil_div(a.K, kStepK) > (a.y_type == MOE_F32 ? kRun32 : kRun16);
+    const int v = (a.in_out ? 2 : 0) + (runs ? 1 : 0);
+    const void* fn = v == 3   ? (const void*)pair_kernel<true, true>
+                     : v == 2 ? (const void*)pair_kernel<true, false>
+                     : v == 1 ? (const void*)pair_kernel<false, true>
+                              : (const void*)pair_kernel<false, false>;
+    constexpr size_t kSmem = 1024 + (size_t)kPairStages * kPairStageBytes;
+    cudaError_t err = prepare_kernel(fn, (int)kSmem, ready[v], &sms);
+    if (err != cudaSuccess) return err;
+    const int pairs = sms / 2;
+    p.n_mb = ceil_div(a.N, 256);
+    // columns of a tile: those with the least time of all waves
+    int64_t best = -1;
+    for (int nb = ceil_div(a.T, kPairCols), most = std::min(ceil_div(a.T, 32), nb + 64); nb <= most; ++nb) {
+        const int cols = (ceil_div(a.T, nb) + 31) & ~31;
+        const int64_t cost = (int64_t)ceil_div((int64_t)p.n_mb * ceil_div(a.T, cols), pairs) * (cols + 64);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.cols = cols;
+        }
+    }
+    p.n_tb = ceil_div(a.T, p.cols);
+    p.box = p.cols > 128 ? 3 : p.cols > 64 ? 2 : p.cols > 32 ? 1 : 0;
+    if (!fill(p, a)) return cudaErrorInvalidValue;
+    p.run = run_of(p.nk, a.y_type);
+    const int64_t tiles = (int64_t)p.n_mb * p.n_tb;
+    void* args[] = {&p};
+    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, pairs)), kThreads, kSmem, s, args);
+}
+
+}  // namespace
+
+bool linear_pairs(const LinearArgs& a) { return (int64_t)ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 48; }
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+    if (a.T <= 0) return cudaSuccess;
+    return linear_pairs(a) ? launch_pairs(a, s) : launch_split(a, s);
+}
+
+}  // namespace moe

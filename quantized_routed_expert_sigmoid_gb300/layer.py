@@ -210,8 +210,8 @@ def _status_word(device):
         return held[0][held[1] - 1: held[1]]
 
 
-class _Products:
-    """What GroupedExperts and W4Experts share: the rows of a call, checked and passed on."""
+class _Checked:
+    """A status word of the object's own for calls that are given none, and the end of its plan, if it has one."""
 
     plan = None
 
@@ -229,6 +229,18 @@ class _Products:
             if word.is_cuda:
                 torch.cuda.synchronize(word.device)
         return code
+
+    def __del__(self):
+        try:
+            if self.plan:
+                self._destroy(self.plan)
+                self.plan = None
+        except Exception:
+            pass
+
+
+class _Products(_Checked):
+    """What GroupedExperts and W4Experts share: the rows of a call, checked and passed on."""
 
     def __call__(self, x: torch.Tensor, offsets: torch.Tensor | None = None, sorted_pairs: torch.Tensor | None = None,
                  k: int = 1, out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
@@ -266,14 +278,6 @@ class _Products:
         self._matmul(self.plan, x, _row_stride(x, "x"), T, k, sorted_pairs, offsets, out, _row_stride(out, "out"),
                      self._status if status is None else status, stream)
         return out
-
-    def __del__(self):
-        try:
-            if self.plan:
-                self._destroy(self.plan)
-                self.plan = None
-        except Exception:
-            pass
 
 
 class GroupedExperts(_Products):
@@ -434,3 +438,230 @@ class NormResidual:
         if col != 1 and shape[1] != 1:
             raise ValueError(f"the last dimension of {name} must be dense")
         return row if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+
+
+_ACTS = {"none": N.MOE_ACT_NONE, "relu": N.MOE_ACT_RELU, "gelu": N.MOE_ACT_GELU, "gelu_tanh": N.MOE_ACT_GELU_TANH,
+         "silu": N.MOE_ACT_SILU}
+
+
+def _value_rows(t, name, T, width):
+    """Elements between the rows of t, fp32, bf16 or fp16 [T, width] on the GPU."""
+    if t.shape != (T, width) or t.dtype not in _VT or not t.is_cuda:
+        raise ValueError(f"{name} must be an fp32, bf16 or fp16 CUDA tensor [{T}, {width}]")
+    return _row_stride(t, name)
+
+
+def _given(t, name, dtypes, numel):
+    """t (or None), after checks: dense, of one of these types, numel entries, on the GPU."""
+    if t is not None and (t.dtype not in dtypes or t.numel() != numel or not t.is_contiguous() or not t.is_cuda):
+        raise ValueError(f"{name} must be a dense CUDA tensor of {numel} entries, one of {[str(d) for d in dtypes]}")
+    return t
+
+
+class Linear(_Checked):
+    """A dense product with its epilogue: y = res_scale * r + scale * act(x W^T + bias) (moe_linear).
+
+    w: bf16 or fp16 [n_out, n_in] (order "out_in") or [n_in, n_out] ("in_out") on the GPU, last dimension dense, the
+    row stride a multiple of 8 elements; bias: [n_out], fp32, bf16 or fp16, or None; act: "none", "relu", "gelu" (of
+    the normal distribution function), "gelu_tanh" or "silu"; y_dtype: fp32, bf16 or fp16 (None: w's type).
+    """
+
+    _destroy = staticmethod(N.moe_linear_plan_destroy)
+
+    def __init__(self, w: torch.Tensor, bias: torch.Tensor | None = None, *, order: str = "out_in", act: str = "none",
+                 y_dtype: torch.dtype | None = None, scale: float = 1.0, res_scale: float = 1.0):
+        if order not in ("out_in", "in_out"):
+            raise ValueError(f"order must be 'out_in' or 'in_out', not {order!r}")
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {list(_ACTS)}, not {act!r}")
+        y_dtype = w.dtype if y_dtype is None else y_dtype
+        if y_dtype not in _VT:
+            raise ValueError(f"y_dtype must be one of {[str(d) for d in _VT]}")
+        _cuda(w, "w", (torch.bfloat16, torch.float16), 2)
+        self.n_out, self.n_in = w.shape if order == "out_in" else (w.shape[1], w.shape[0])
+        if bias is not None:
+            _cuda(bias, "bias", tuple(_VT), 1, w.get_device())
+            _given(bias, "bias", tuple(_VT), self.n_out)
+        self.x_dtype, self.y_dtype, self.device = w.dtype, y_dtype, w.get_device()
+        self._keep = (w, bias)
+        self._status = _status_word(w.device)
+        self.plan = N.moe_linear_plan_create(N.moe_linear_desc(
+            _VT[w.dtype], _VT[y_dtype], N.MOE_W_OUT_IN if order == "out_in" else N.MOE_W_IN_OUT, self.n_out, self.n_in,
+            w.data_ptr(), _row_stride(w, "w"), bias.data_ptr() if bias is not None else None,
+            _VT[bias.dtype] if bias is not None else N.MOE_F32, _ACTS[act], scale, res_scale))
+
+    def path(self, T: int) -> str:
+        """Which kernel a call with T rows runs: "split" or "pairs"."""
+        return ("split", "pairs")[N.moe_linear_path(self.plan, T)]
+
+    def __call__(self, x: torch.Tensor, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """y [T, n_out] of x [T, n_in] and the residual r ([T, n_out], any value type; out may be the residual).
+
+        status and stream as in the products' calls; an output that is not given is made in the order of `stream`.
+        """
+        T, width = x.shape
+        if x.dtype is not self.x_dtype or width != self.n_in or not x.is_cuda:
+            raise ValueError(f"x must be a {self.x_dtype} CUDA tensor [T, {self.n_in}]")
+        rs, rt = 0, N.MOE_F32
+        if residual is not None:
+            rs, rt = _value_rows(residual, "residual", T, self.n_out), _VT[residual.dtype]
+        if status is not None and (status.dtype is not torch.int32 or status.numel() < 1 or not status.is_cuda):
+            raise ValueError("status must be an int32 CUDA tensor")
+        if out is None:
+            out = _empty((T, self.n_out), self.y_dtype, x.device, stream)
+        elif out.dtype is not self.y_dtype or out.shape != (T, self.n_out) or not out.is_cuda:
+            raise ValueError(f"out must be a {self.y_dtype} CUDA tensor [{T}, {self.n_out}]")
+        _on_current(self.device, x=x, residual=residual, out=out, status=status)
+        N.moe_linear(self.plan, x, _row_stride(x, "x"), T, residual, rt, rs, out, _row_stride(out, "out"),
+                     self._status if status is None else status, stream)
+        return out
+
+
+class LayerNorm:
+    """Layer norm over rows of H and its gradient (moe_layer_norm, moe_layer_norm_backward).
+
+    gamma, beta: fp32 [H] on the GPU (None: 1 and 0).  y_dtype: the type of outputs that a call makes.
+    """
+
+    def __init__(self, H: int, *, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None, eps: float = 1e-5,
+                 y_dtype: torch.dtype = torch.bfloat16):
+        if y_dtype not in _VT:
+            raise ValueError(f"y_dtype must be one of {[str(d) for d in _VT]}")
+        self.device = None               # gamma's and beta's; without them, each call's own
+        for name, g in (("gamma", gamma), ("beta", beta)):
+            if g is not None:
+                _cuda(g, name, (torch.float32,), 1, self.device)
+                self.device = g.get_device()
+                _given(g, name, (torch.float32,), H)
+        self.H, self.eps, self.y_dtype = H, eps, y_dtype
+        self._keep = (gamma, beta)
+        self._desc = {}                  # the call's description, by the types of its tensors
+
+    def _described(self, x, y_dtype, **tensors):
+        device = x.get_device()
+        if self.device is not None and device != self.device:
+            raise ValueError(f"x is on device {device}, gamma / beta on device {self.device}")
+        _on_current(device, **tensors)
+        desc = self._desc.get((x.dtype, y_dtype))
+        if desc is None:
+            g = [t.data_ptr() if t is not None else None for t in self._keep]
+            desc = self._desc[x.dtype, y_dtype] = N.moe_layer_norm_desc(self.H, _VT[x.dtype], _VT[y_dtype], *g, self.eps)
+        return desc
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                 rstd: torch.Tensor | None = None, *, stats: bool = True, stream=None):
+        """(y, mean, rstd) of x [T, H]; mean and rstd (fp32 [T]) are what backward() needs (stats=False: None unless given).
+
+        Outputs that are not given are made in the order of `stream`; out may be x.  All tensors are on one
+        device, which has to be the current one.
+        """
+        T = x.shape[0]
+        xs = _value_rows(x, "x", T, self.H)
+        if out is None:
+            out = _empty((T, self.H), self.y_dtype, x.device, stream)
+        ys = _value_rows(out, "out", T, self.H)
+        if stats and (mean is None or rstd is None):
+            made = _empty((2, T), torch.float32, x.device, stream)
+            mean, rstd = made[0] if mean is None else mean, made[1] if rstd is None else rstd
+        _given(mean, "mean", (torch.float32,), T)
+        _given(rstd, "rstd", (torch.float32,), T)
+        desc = self._described(x, out.dtype, out=out, mean=mean, rstd=rstd)
+        N.moe_layer_norm(desc, x, xs, T, out, ys, mean, rstd, stream)
+        return out, mean, rstd
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, *,
+                 add: torch.Tensor | None = None, dx: torch.Tensor | None = None, dgamma: torch.Tensor | None = None,
+                 dbeta: torch.Tensor | None = None, accumulate: bool = False, stream=None):
+        """(dx, dgamma, dbeta) of the output's gradient dy [T, H] and the forward call's x, mean and rstd.
+
+        add (x's type): the gradient of the residual stream, which dx takes along; dx (x's type) may be add, x or dy.
+        dgamma and dbeta (fp32 [H]) are made when gamma and beta are there (None otherwise, unless given); accumulate:
+        they are given and added to.
+        """
+        T = x.shape[0]
+        xs, gs = _value_rows(x, "x", T, self.H), _value_rows(dy, "dy", T, self.H)
+        if dx is None:
+            dx = _empty((T, self.H), x.dtype, x.device, stream)
+        ds, as_ = _value_rows(dx, "dx", T, self.H), 0
+        if dx.dtype is not x.dtype or (add is not None and add.dtype is not x.dtype):
+            raise ValueError("dx and add must have x's type")
+        if add is not None:
+            as_ = _value_rows(add, "add", T, self.H)
+        sums = []
+        for name, t, weight in (("dgamma", dgamma, self._keep[0]), ("dbeta", dbeta, self._keep[1])):
+            if t is None and weight is not None:
+                if accumulate:
+                    raise ValueError(f"{name} must be given to be added to")
+                t = _empty((self.H,), torch.float32, x.device, stream)
+            sums.append(_given(t, name, (torch.float32,), self.H))
+        if _given(mean, "mean", (torch.float32,), T) is None or _given(rstd, "rstd", (torch.float32,), T) is None:
+            raise ValueError("mean and rstd are those of the forward call")
+        desc = self._described(x, dy.dtype, dy=dy, mean=mean, rstd=rstd, add=add, dx=dx, dgamma=sums[0], dbeta=sums[1])
+        nbytes = N.moe_layer_norm_backward_workspace_size(self.H, T) if sums[0] is not None or sums[1] is not None else 0
+        ws = _empty((nbytes,), torch.uint8, x.device, stream) if nbytes else None    # (of the stream's memory: free again behind it)
+        N.moe_layer_norm_backward(desc, dy, gs, x, xs, mean, rstd, add, as_, T, dx, ds, *sums, accumulate, ws, nbytes, stream)
+        return dx, sums[0], sums[1]
+
+
+class BalanceLoss(_Checked):
+    """The auxiliary loss that keeps a router's load even, with its counts and its gradient (moe_balance_loss).
+
+    E experts, k a token; mode: "softmax" or "sigmoid" (what makes a token's scores of its logits); coef: the loss's weight.
+    device: of the calls (None: the current one).
+    """
+
+    def __init__(self, E: int, k: int, *, mode: str = "softmax", coef: float = 1.0, device=None):
+        if mode not in ("softmax", "sigmoid"):
+            raise ValueError(f"mode must be 'softmax' or 'sigmoid', not {mode!r}")
+        self.E, self.k = E, k
+        self._desc = [N.moe_balance_desc(N.MOE_ROUTE_SIGMOID_GROUP if mode == "sigmoid" else N.MOE_ROUTE_SOFTMAX, E, k, coef, a)
+                      for a in (0, 1)]
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self._status = _status_word(device)
+
+    def __call__(self, logits: torch.Tensor, ids: torch.Tensor, *, offsets: torch.Tensor | None = None,
+                 mask: torch.Tensor | None = None, upstream: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                 counts: torch.Tensor | None = None, dlogits: torch.Tensor | bool | None = None, accumulate: bool = False,
+                 status: torch.Tensor | None = None, stream=None):
+        """(loss [1], counts [n_seqs, E], dlogits) of the router's logits (fp32 [T, E]) and chosen experts (int32 [T, k]).
+
+        offsets: int32 [n_seqs + 1], first tokens of the sequences (None: one of all tokens); mask: bool or uint8 [T],
+        tokens that count; upstream: fp32 [1], the gradient of the loss (None: 1).  dlogits (fp32 [T, E]): None: no
+        gradient, True: made; given, it is overwritten (it may be logits) or, with accumulate, added to.  Bad ids and offsets are
+        reported by device_status() or in status.  Outputs that are not given are made in the order of `stream`.
+        """
+        T = logits.shape[0]
+        if logits.dtype is not torch.float32 or logits.shape != (T, self.E) or not logits.is_cuda:
+            raise ValueError(f"logits must be an fp32 CUDA tensor [T, {self.E}]")
+        n_seqs = 1 if offsets is None else offsets.numel() - 1
+        if n_seqs < 1:
+            raise ValueError("offsets must have an entry for every sequence and one more")
+        _given(offsets, "offsets", (torch.int32,), n_seqs + 1)
+        if _given(ids, "ids", (torch.int32,), T * self.k) is None:
+            raise ValueError("ids are missing")
+        _given(mask, "mask", (torch.bool, torch.uint8), T)
+        _given(upstream, "upstream", (torch.float32,), 1)
+        if status is not None and (status.dtype is not torch.int32 or status.numel() < 1 or not status.is_cuda):
+            raise ValueError("status must be an int32 CUDA tensor")
+        if dlogits is True or dlogits is False:
+            if accumulate and dlogits:
+                raise ValueError("dlogits must be given to be added to")
+            dlogits = _empty((T, self.E), torch.float32, logits.device, stream) if dlogits else None
+        elif dlogits is not None and (dlogits.dtype is not torch.float32 or dlogits.shape != (T, self.E) or not dlogits.is_cuda):
+            raise ValueError(f"dlogits must be an fp32 CUDA tensor [{T}, {self.E}]")
+        loss = _empty((1,), torch.float32, logits.device, stream) if loss is None else _given(loss, "loss", (torch.float32,), 1)
+        counts = (_empty((n_seqs, self.E), torch.int32, logits.device, stream) if counts is None
+                  else _given(counts, "counts", (torch.int32,), n_seqs * self.E))
+        _on_current(logits.get_device(), ids=ids, offsets=offsets, mask=mask, upstream=upstream, loss=loss, counts=counts,
+                    dlogits=dlogits, status=status)
+        if status is None:
+            status = self._status
+            if status is not None and status.get_device() != logits.get_device():
+                raise ValueError(f"logits are on device {logits.get_device()}, this object's calls on device {status.get_device()}")
+        nbytes = N.moe_balance_workspace_size(self.E, T, n_seqs)
+        ws = _empty((nbytes,), torch.uint8, logits.device, stream)
+        N.moe_balance_loss(self._desc[bool(accumulate)], logits, _row_stride(logits, "logits"), ids, T, offsets, n_seqs, mask,
+                           upstream, loss, counts, dlogits, _row_stride(dlogits, "dlogits") if dlogits is not None else 0, status,
+                           ws, nbytes, stream)
+        return loss, counts, dlogits
