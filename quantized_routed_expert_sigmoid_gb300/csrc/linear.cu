@@ -86,45 +86,62 @@ __device__ __forceinline__ float activate(float z) {
     }
 }
 template <int ACT, int C>
-__device__ __forceinline__ void activate_all(float (&v)[C], bool fast) {
-    if (fast) {
+__device__ __forceinline__ void activate_all(float (&v)[C]) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = activate<ACT, true>(v[i]);
-    } else {
+    for (int i = 0; i < C; ++i) v[i] = activate<ACT, true>(v[i]);
+}
+// The accurate forms, for fp32 outputs: one copy of their code (some hundred instructions), the values pass by.
+template <int C>
+__device__ __forceinline__ void activate_exactly(float (&v)[C], int act) {
+#pragma unroll 1
+    for (int i = 0; i < C; ++i) {
+        float z = v[0];
+        if (act == MOE_ACT_RELU) z = activate<MOE_ACT_RELU, false>(z);
+        else if (act == MOE_ACT_SILU) z = activate<MOE_ACT_SILU, false>(z);
+        else if (act == MOE_ACT_GELU_TANH) z = activate<MOE_ACT_GELU_TANH, false>(z);
+        else z = activate<MOE_ACT_GELU, false>(z);
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = activate<ACT, false>(v[i]);
+        for (int j = 0; j + 1 < C; ++j) v[j] = v[j + 1];
+        v[C - 1] = z;
     }
 }
-
-// C values of channel `row`, of the rows of x t0, t0 + step, ..: those below e.T and `end` are finished and stored.
+// What the epilogue needs of the residual for C values of channel `row`, of the rows of x t0, t0 + step, .. (those below
+// e.T and `end`).  Asked for before the sums are there, so that the two latencies overlap.
 template <int C>
-__device__ __forceinline__ void finish(const Epilogue& e, float bias, float (&v)[C], int row, int t0, int step, int end) {
-    if (row >= e.N) return;
+__device__ __forceinline__ void load_residual(const Epilogue& e, float (&r)[C], int row, int t0, int step, int end) {
+    if (!e.r || row >= e.N) return;
     const int n = min(end, e.T) - t0;                    // (i * step < n: in range)
-    float r[C];
-    if (e.r) {
-        const int64_t at = (int64_t)t0 * e.r_stride + row, by = (int64_t)step * e.r_stride;
-        if (e.r_type == MOE_F32) {
+    const int64_t at = (int64_t)t0 * e.r_stride + row, by = (int64_t)step * e.r_stride;
+    if (e.r_type == MOE_F32) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) r[i] = i * step < n ? static_cast<const float*>(e.r)[at + i * by] : 0.f;
-        } else if (e.r_type == MOE_BF16) {
+        for (int i = 0; i < C; ++i) r[i] = i * step < n ? static_cast<const float*>(e.r)[at + i * by] : 0.f;
+    } else if (e.r_type == MOE_BF16) {
 #pragma unroll
-            for (int i = 0; i < C; ++i)
-                r[i] = i * step < n ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.r)[at + i * by]) : 0.f;
-        } else {
+        for (int i = 0; i < C; ++i)
+            r[i] = i * step < n ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.r)[at + i * by]) : 0.f;
+    } else {
 #pragma unroll
-            for (int i = 0; i < C; ++i) r[i] = i * step < n ? __half2float(static_cast<const __half*>(e.r)[at + i * by]) : 0.f;
-        }
+        for (int i = 0; i < C; ++i) r[i] = i * step < n ? __half2float(static_cast<const __half*>(e.r)[at + i * by]) : 0.f;
     }
+}
+// The same values, finished and stored.
+template <int C>
+__device__ __forceinline__ void finish(const Epilogue& e, float bias, float (&v)[C], const float (&r)[C], int row, int t0, int step,
+                                       int end) {
+    if (row >= e.N) return;
+    const int n = min(end, e.T) - t0;
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] += bias;
-    const bool fast = e.y_type != MOE_F32;
-    switch (e.act) {
-        case MOE_ACT_RELU: activate_all<MOE_ACT_RELU>(v, fast); break;
-        case MOE_ACT_GELU: activate_all<MOE_ACT_GELU>(v, fast); break;
-        case MOE_ACT_GELU_TANH: activate_all<MOE_ACT_GELU_TANH>(v, fast); break;
-        case MOE_ACT_SILU: activate_all<MOE_ACT_SILU>(v, fast); break;
-        default: break;
+    if (e.act == MOE_ACT_NONE) {
+    } else if (e.y_type == MOE_F32) {
+        activate_exactly(v, e.act);
+    } else {
+        switch (e.act) {
+            case MOE_ACT_RELU: activate_all<MOE_ACT_RELU>(v); break;
+            case MOE_ACT_GELU: activate_all<MOE_ACT_GELU>(v); break;
+            case MOE_ACT_GELU_TANH: activate_all<MOE_ACT_GELU_TANH>(v); break;
+            default: activate_all<MOE_ACT_SILU>(v); break;
+        }
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -155,6 +172,9 @@ __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(a));
 }
+__device__ __forceinline__ void prefetch_l2(const void* p, int type, int64_t i) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i * (type == MOE_F32 ? 4 : 2)));
+}
 __device__ __forceinline__ uint32_t in_cta(uint32_t a, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
@@ -162,44 +182,51 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t a, uint32_t rank) {
 }
 
 // ---------------------------------------------------------------- one CTA a tile, the sum split over a cluster
-constexpr int kMaxStages = 12, kMaxCols = 128;
+constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128;                       // a step's weights
 
-template <bool IN_OUT>
-__global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constant__ LinearParams p) {
+template <bool IN_OUT, int COLS>
+__global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(const __grid_constant__ LinearParams p) {
+    constexpr int kStage = kABytes + COLS * 128, kHalf = COLS / 2;
+    constexpr uint32_t kTmem = 2 * COLS < 32 ? 32 : 2 * COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accf[2], accr[2], drain, never;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accf[2], accr[2], drain, never, parts_here;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, issued;
     volatile int* abort_flag = &abort_word;
-    const int stage_bytes = kABytes + p.cols * 128;
-    float* parts = reinterpret_cast<float*>(smem + p.stages * stage_bytes);   // [CTA][its columns here][128]
+    // parts: [CTA of the cluster][columns that this one finishes][128 channels], as the others send them.  What this CTA sends,
+    // [column][128 channels], takes the place of the stages, which are used up by then (alone, it finishes that itself).
+    float* parts = reinterpret_cast<float*>(smem + max(p.stages * kStage, COLS * 512));
+    float* sent = reinterpret_cast<float*>(smem);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cta_rank();
     uint32_t splits;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
-    const int mb = blockIdx.x / splits, tok0 = blockIdx.y * p.cols;
+    const int mb = blockIdx.x / splits, tok0 = blockIdx.y * COLS;
     const int k0 = (int)((int64_t)p.nk * rank / splits), k1 = (int)((int64_t)p.nk * (rank + 1) / splits);
     const int n_runs = (k1 - k0 + p.run - 1) / p.run;
-    const uint32_t tmem_cols = max(32, 2 * p.cols);
+    const int own = COLS / (int)splits;                  // columns that a CTA of the cluster finishes
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], kEpiWarps); }
         mbar_init(&drain, 1);
         mbar_init(&never, 1);
+        mbar_init(&parts_here, 1);
         abort_word = 0;
         issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_map(&p.tw);
-        prefetch_map(&p.tx[p.box]);
+        if (splits > 1)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&parts_here)), "r"(COLS * 512) : "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)), "r"(tmem_cols)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)), "n"(kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (tid == 64) prefetch_map(&p.tw);
+    if (tid == 96) prefetch_map(&p.tx[p.box]);
     __syncwarp();
     tc_before();
     __syncthreads();
@@ -213,12 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constan
         // ======================= loads =======================
         int g = 0, s = 0;
         uint32_t ph = 1;
-        const uint32_t bytes = (uint32_t)stage_bytes;
         for (int kb = k0; kb < k1; ++kb, ++g) {
             if (!wait_warp(&empty[s], ph, abort_flag, p.wait_ns)) break;
             if (elect_one()) {
-                uint8_t* a = smem + s * stage_bytes;
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[s])), "r"(bytes) : "memory");
+                uint8_t* a = smem + s * kStage;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[s])), "r"(kStage) : "memory");
                 if constexpr (IN_OUT) {
                     tma_load_2d(a, &p.tw, mb * 128, kb * kStepK, &full[s]);
                     tma_load_2d(a + 8192, &p.tw, mb * 128 + 64, kb * kStepK, &full[s]);
@@ -233,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constan
         if (lane == 0) issued = g;
     } else if (warp == 1) {
         // ======================= MMA issue =======================
-        const uint32_t idesc = idesc_mma(128, p.cols, p.bf16) | (IN_OUT ? 1u << 15 : 0u);
+        const uint32_t idesc = idesc_mma(128, COLS, p.bf16) | (IN_OUT ? 1u << 15 : 0u);
         constexpr uint32_t kAdvA = (IN_OUT ? 2048 : 32) >> 4, kAdvB = 32 >> 4;
         int s = 0, j = 0;
         uint32_t ph = 0;
@@ -242,13 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constan
             const int b = j & 1, r1 = min(r0 + p.run, k1);
             if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
             tc_after();
-            const uint32_t acc = tmem + (uint32_t)b * p.cols;
+            const uint32_t acc = tmem + (uint32_t)b * COLS;
             for (int kb = r0; kb < r1; ++kb) {
                 const bool stalled = p.stall && !any;    // (test setting)
                 if (!wait_warp(stalled ? &never : &full[s], stalled ? 0u : ph, abort_flag, p.wait_ns)) { ok = false; break; }
                 tc_after();
                 if (elect_one()) {
-                    const uint32_t a = su32(smem + s * stage_bytes);
+                    const uint32_t a = su32(smem + s * kStage);
                     const uint64_t da = IN_OUT ? sdesc_mn(a) : sdesc(a), db = sdesc(a + kABytes);
 #pragma unroll
                     for (int kk = 0; kk < kStepK / 16; ++kk) mma_f16(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 || kb > r0);
@@ -268,55 +294,85 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constan
     }
     __syncwarp();
     cluster_wait();
-    const int q = warp & 3, side = (warp - kEpiWarp0) >> 2, half = p.cols / 2;
-    const int row = mb * 128 + q * 32 + lane;
-    const bool epi = warp >= kEpiWarp0;
-    const int own = p.cols / (int)splits;                // columns that a CTA of the cluster finishes
-    if (epi) {
-        // ======================= the sums, run by run =======================
+    if (warp >= kEpiWarp0) {
+        // ======================= epilogue =======================
+        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
+        const int row = mb * 128 + q * 32 + lane, t0 = tok0 + rank * own;
         const float bias = bias_at(p.e, row);
-        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + side * half;
-        float sum[kMaxCols / 2];
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + side * kHalf;
+        const float* at = (splits > 1 ? parts : sent) + q * 32 + lane;
+        float res[8] = {};
         bool ok = true;
-        for (int j = 0; j < n_runs; ++j) {
-            const int b = j & 1;
-            ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
-            if (!ok) break;
-            tc_after();
+        // Turn 0 runs the code that ends the kernel on no rows at all, while the first weights are on their way: read
+        // from memory at its first use, it takes longer than what it does (2.5 us for one row of x, of 12).
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            const int end = turn ? t0 + own : t0;
+            if (turn) {
+                load_residual<8>(p.e, res, row, t0 + side, 2, end);
+                // the sums, run by run
+                float sum[kHalf];
+                for (int j = 0; j < n_runs; ++j) {
+                    const int b = j & 1;
+                    ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
+                    if (!ok) break;
+                    tc_after();
 #pragma unroll
-            for (int c = 0; c < kMaxCols / 2; c += 8)
-                if (c < half) {
-                    uint32_t v[8];
-                    tmem_ld8(lanes + b * p.cols + c, v);
-                    tmem_ld_wait();
+                    for (int c = 0; c < kHalf; c += 8) {
+                        uint32_t v[8];
+                        tmem_ld8(lanes + b * COLS + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sum[c + i] = j ? __fadd_rn(sum[c + i], __uint_as_float(v[i])) : __uint_as_float(v[i]);
+                    }
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&accr[b]);
+                }
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) sent[(side * kHalf + c) * 128 + q * 32 + lane] = sum[c];
+                }
+                if (splits > 1) fence_async_smem();
+                ok = all_of(1, 32 * kEpiWarps, ok);
+                if (splits > 1) {
+                    if (ok && warp == kEpiWarp0 && lane < (int)splits) {
+                        // columns lane * own .. to CTA `lane`, where this CTA's place is `rank`
+                        const uint32_t bytes = (uint32_t)own * 512;
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                in_cta(su32(parts) + rank * bytes, lane)),
+                            "r"(su32(sent) + lane * bytes), "r"(bytes), "r"(in_cta(su32(&parts_here), lane))
+                            : "memory");
+                    }
+                    __syncwarp();
+                    ok = ok && wait_warp(&parts_here, 0, abort_flag, p.wait_ns);
+                    if (!ok && lane == 0) drain_wait(&parts_here, 0, p.wait_ns);
+                    __syncwarp();
+                    cluster_arrive();                    // (what the others sent here has arrived, or this CTA has given up)
+                }
+                if (!ok) break;
+            }
+#pragma unroll 1
+            for (int c0 = side; c0 < own; c0 += 16) {    // columns c0, c0 + 2 ..
+                float v[8], r[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    r[i] = res[i];
+                    v[i] = 0.f;
+                }
+                if (c0 + 16 < own) load_residual<8>(p.e, res, row, t0 + c0 + 16, 2, end);
+                for (int s = 0; s < (int)splits; ++s)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        sum[c + i] = j ? __fadd_rn(sum[c + i], __uint_as_float(v[i])) : __uint_as_float(v[i]);
-                }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&accr[b]);
+                        if (c0 + 2 * i < own) v[i] += at[(s * own + c0 + 2 * i) * 128];
+                finish<8>(p.e, bias, v, r, row, t0 + c0, 2, end);
+                if (!turn) break;
+            }
         }
-        if (ok && splits == 1) {
-#pragma unroll
-            for (int c = 0; c < kMaxCols / 2; c += 8)
-                if (c < half) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = sum[c + i];
-                    finish<8>(p.e, bias, v, row, tok0 + side * half + c, 1, p.e.T);
-                }
-        } else if (ok) {
-            const uint32_t here = su32(parts) + (uint32_t)(q * 32 + lane) * 4;
-#pragma unroll
-            for (int c = 0; c < kMaxCols / 2; ++c)
-                if (c < half) {
-                    const int col = side * half + c, to = col / own;
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cta(here + (uint32_t)(rank * own + col - to * own) * 512, to)),
-                                 "f"(sum[c])
-                                 : "memory");
-                }
-        }
+    } else if (splits > 1) {
+        cluster_arrive();
     }
     tc_before();
     __syncthreads();
@@ -327,31 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const __grid_constan
         if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
     }
     __syncwarp();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
-    if (splits == 1) return;
-    cluster_sync();                                      // the parts are here
-    if (!epi || *abort_flag) return;
-    const float bias = bias_at(p.e, row);
-    const float* at = parts + q * 32 + lane;
-    for (int c = side; c < own; c += 8) {                // columns c, c + 2, c + 4, c + 6
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = 0.f;
-            if (c + 2 * i < own)
-                for (int s = 0; s < (int)splits; ++s) v[i] += at[(s * own + c + 2 * i) * 128];
-        }
-        finish<4>(p.e, bias, v, row, tok0 + rank * own + c, 2, tok0 + (rank + 1) * own);
-    }
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmem) : "memory");
+    __syncwarp();
+    if (splits > 1) cluster_wait();                      // (what this CTA sent is no longer read)
 }
 
 // ---------------------------------------------------------------- a pair of CTAs a tile
 constexpr int kPairStages = 6, kPairCols = 256;
 constexpr int kPairStageBytes = kABytes + 128 * 128;
 constexpr uint32_t kPairTmem = 512;
+constexpr int kPairEpiWarps = 16, kPairThreads = 32 * (kEpiWarp0 + kPairEpiWarps);
 
 template <bool IN_OUT, bool RUNS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ LinearParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ LinearParams p) {
     using Ring = RingOf<kPairStages>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -363,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
     const uint32_t cta = cta_rank();
     if (tid == 0) {
         for (int i = 0; i < kPairStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kEpiWarps); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kPairEpiWarps); }
         mbar_init(&drain, 1);
         mbar_init(&never, 1);
         abort_word = 0;
@@ -464,9 +508,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
             }
         }
     } else if (warp >= kEpiWarp0) {
-        // ======================= epilogue: lanes 32 q.. of TMEM, every other group of columns =======================
+        // ======================= epilogue: lanes 32 q.. of TMEM, columns 16 side .. of every 64 =======================
         const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
-        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16), accr0 = in_leader(su32(accr));
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + 16 * side, accr0 = in_leader(su32(accr));
         auto release = [&](int b) {
             tc_before();
             __syncwarp();
@@ -476,55 +520,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
         bool ok = true;
         for (int t = first; ok && t < n_tiles; t += n_pairs) {
             const int tb = t / p.n_mb, mb = t - tb * p.n_mb;
-            const int row = mb * 256 + (int)cta * 128 + q * 32 + lane, tok0 = tb * p.cols;
-            const int end = min(tok0 + p.cols, p.e.T);
+            const int row = mb * 256 + (int)cta * 128 + q * 32 + lane, tok0 = tb * p.cols + 16 * side;
+            const int end = min(tb * p.cols + p.cols, p.e.T);
             const float bias = bias_at(p.e, row);
+            if (p.e.r) {
+                // the tile's residual into L2 (a line of a row of x a lane; the first channel of the warp's 32)
+                const int64_t at = row - lane;
+                for (int c = (lane & 15) + 64 * (lane >> 4); c < p.cols; c += 128)
+                    if (tok0 + c < end && at < p.e.N) prefetch_l2(p.e.r, p.e.r_type, (tok0 + c) * p.e.r_stride + at);
+            }
             if constexpr (RUNS) {
-                // columns 32 side + 64 i .. of the runs, summed in registers
-                float sum[kPairCols / 2];
+                float sum[kPairCols / 4];
                 for (int k0 = 0; k0 < p.nk; k0 += p.run, ++j) {
                     const int b = j & 1;
                     ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_after();
 #pragma unroll
-                    for (int i = 0; i < kPairCols / 2; i += 16) {
-                        const int c = (i & ~31) * 2 + 32 * side + (i & 31);
+                    for (int c = 0; c < kPairCols; c += 64)
                         if (tok0 + c < end) {
                             uint32_t v[16];
                             tmem_ld16(lanes + b * kPairCols + c, v);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                sum[i + e] = k0 ? __fadd_rn(sum[i + e], __uint_as_float(v[e])) : __uint_as_float(v[e]);
+                            for (int i = 0; i < 16; ++i)
+                                sum[c / 4 + i] = k0 ? __fadd_rn(sum[c / 4 + i], __uint_as_float(v[i])) : __uint_as_float(v[i]);
                         }
-                    }
                     release(b);
                 }
                 if (!ok) break;
+#pragma unroll 1
+                for (int i = 0; i < kPairCols / 4; i += 8) {         // (one copy of the code: the sums pass by)
+                    const int c = (i >> 4) * 64 + (i & 8);
+                    if (tok0 + c >= end) break;
+                    float v[8], r[8];
+                    load_residual<8>(p.e, r, row, tok0 + c, 1, end);
 #pragma unroll
-                for (int i = 0; i < kPairCols / 2; i += 16) {
-                    const int c = (i & ~31) * 2 + 32 * side + (i & 31);
-                    if (tok0 + c < end) {
-                        float v[16];
+                    for (int e = 0; e < 8; ++e) v[e] = sum[e];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = sum[i + e];
-                        finish<16>(p.e, bias, v, row, tok0 + c, 1, end);
-                    }
+                    for (int e = 0; e + 8 < kPairCols / 4; ++e) sum[e] = sum[e + 8];
+                    finish<8>(p.e, bias, v, r, row, tok0 + c, 1, end);
                 }
             } else {
                 const int b = j & 1;
+                float res[16];
+                load_residual<16>(p.e, res, row, tok0, 1, end);
                 ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
                 if (!ok) break;
                 tc_after();
-                for (int c = 32 * side; tok0 + c < end; c += 64) {
-                    uint32_t u[32];
-                    tmem_ld32(lanes + b * kPairCols + c, u);
-                    tmem_ld_wait();
-                    float v[32];
+                for (int c = 0; tok0 + c < end; c += 64) {
+                    uint32_t u[16];
+                    tmem_ld16(lanes + b * kPairCols + c, u);
+                    float v[16], r[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[e]);
-                    finish<32>(p.e, bias, v, row, tok0 + c, 1, end);
+                    for (int i = 0; i < 16; ++i) r[i] = res[i];
+                    if (tok0 + c + 64 < end) load_residual<16>(p.e, res, row, tok0 + c + 64, 1, end);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+                    finish<16>(p.e, bias, v, r, row, tok0 + c, 1, end);
                 }
                 release(b);
                 ++j;
@@ -607,11 +661,16 @@ cudaError_t launch_split(const LinearArgs& a, cudaStream_t s) {
     if (!fill(p, a)) return cudaErrorInvalidValue;
     p.n_mb = ceil_div(a.N, 128);
     p.n_tb = ceil_div(a.T, p.cols);
-    const void* fn = a.in_out ? (const void*)split_kernel<true> : (const void*)split_kernel<false>;
-    static std::atomic<uint64_t> ready[2];
+    const int v = (a.in_out ? 4 : 0) + p.box;
+    const void* const fns[8] = {(const void*)split_kernel<false, 16>, (const void*)split_kernel<false, 32>,
+                                (const void*)split_kernel<false, 64>, (const void*)split_kernel<false, 128>,
+                                (const void*)split_kernel<true, 16>, (const void*)split_kernel<true, 32>,
+                                (const void*)split_kernel<true, 64>, (const void*)split_kernel<true, 128>};
+    const void* fn = fns[v];
+    static std::atomic<uint64_t> ready[8];
     int sms = 0;
     const int stage = kABytes + p.cols * 128, parts = p.cols * 512, most = 227 * 1024 - 1024;
-    cudaError_t err = prepare_kernel(fn, most, ready[a.in_out], &sms);
+    cudaError_t err = prepare_kernel(fn, most, ready[v], &sms);
     if (err != cudaSuccess) return err;
     int splits = 1;
     while (splits < 8 && (int64_t)p.n_mb * p.n_tb * splits * 2 <= sms && p.nk >= splits * 4) splits *= 2;
@@ -619,7 +678,7 @@ cudaError_t launch_split(const LinearArgs& a, cudaStream_t s) {
     p.run = run_of(steps, a.y_type);
     p.stages = std::min(std::min(steps, kMaxStages), (most - 1024 - parts) / stage);
     void* args[] = {&p};
-    return launch_clusters(fn, dim3(p.n_mb * splits, p.n_tb), splits, 1024 + (size_t)p.stages * stage + (splits > 1 ? parts : 0), s, args);
+    return launch_clusters(fn, dim3(p.n_mb * splits, p.n_tb), splits, 1024 + (size_t)std::max(p.stages * stage, parts) + (splits > 1 ? parts : 0), s, args);
 }
 
 cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
@@ -653,7 +712,7 @@ cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
     p.run = run_of(p.nk, a.y_type);
     const int64_t tiles = (int64_t)p.n_mb * p.n_tb;
     void* args[] = {&p};
-    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, pairs)), kThreads, kSmem, s, args);
+    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, pairs)), kPairThreads, kSmem, s, args);
 }
 
 }  // namespace
