@@ -45,6 +45,7 @@ struct LinearParams {
     int cols;                    // columns of a tile (split: 16, 32, 64 or 128; pairs: a multiple of 32)
     int box;                     // which of tx
     int stages;
+    bool vec;                    // four neighbouring channels of r and y can be read and written at once (split)
     int n_mb, n_tb;              // tiles along the channels and along the rows of x
     int32_t* status;
     uint64_t wait_ns;
@@ -105,6 +106,21 @@ __device__ __forceinline__ void activate_exactly(float (&v)[C], int act) {
         v[C - 1] = z;
     }
 }
+template <int C>
+__device__ __forceinline__ void activate_some(const Epilogue& e, float (&v)[C]) {
+    if (e.act == MOE_ACT_NONE) {
+    } else if (e.y_type == MOE_F32) {
+        activate_exactly(v, e.act);
+    } else {
+        switch (e.act) {
+            case MOE_ACT_RELU: activate_all<MOE_ACT_RELU>(v); break;
+            case MOE_ACT_GELU: activate_all<MOE_ACT_GELU>(v); break;
+            case MOE_ACT_GELU_TANH: activate_all<MOE_ACT_GELU_TANH>(v); break;
+            default: activate_all<MOE_ACT_SILU>(v); break;
+        }
+    }
+}
+
 // What the epilogue needs of the residual for C values of channel `row`, of the rows of x t0, t0 + step, .. (those below
 // e.T and `end`).  Asked for before the sums are there, so that the two latencies overlap.
 template <int C>
@@ -132,17 +148,7 @@ __device__ __forceinline__ void finish(const Epilogue& e, float bias, float (&v)
     const int n = min(end, e.T) - t0;
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] += bias;
-    if (e.act == MOE_ACT_NONE) {
-    } else if (e.y_type == MOE_F32) {
-        activate_exactly(v, e.act);
-    } else {
-        switch (e.act) {
-            case MOE_ACT_RELU: activate_all<MOE_ACT_RELU>(v); break;
-            case MOE_ACT_GELU: activate_all<MOE_ACT_GELU>(v); break;
-            case MOE_ACT_GELU_TANH: activate_all<MOE_ACT_GELU_TANH>(v); break;
-            default: activate_all<MOE_ACT_SILU>(v); break;
-        }
-    }
+    activate_some(e, v);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         v[i] *= e.scale;
@@ -182,6 +188,40 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t a, uint32_t rank) {
 }
 
 // ---------------------------------------------------------------- one CTA a tile, the sum split over a cluster
+// A lane's four channels of the 128 of a tile: neighbours where r and y can be read and written 4 at a time, else each 32nd.
+__device__ __forceinline__ int channel(int lane, int i, bool vec) { return vec ? 4 * lane + i : lane + 32 * i; }
+__device__ __forceinline__ void load_residual4(const LinearParams& p, float (&r)[4], int n0, int lane, int64_t t) {
+    const Epilogue& e = p.e;
+    const int64_t at = t * e.r_stride + n0;
+    if (p.vec) {
+        if (n0 + 4 * lane < e.N) load_once<4>(e.r, e.r_type, at + 4 * lane, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + lane + 32 * i < e.N) r[i] = load1(e.r, e.r_type, at + lane + 32 * i);
+    }
+}
+__device__ __forceinline__ void finish4(const LinearParams& p, const float (&bias)[4], float (&v)[4], const float (&r)[4], int n0,
+                                        int lane, int64_t t, bool store) {
+    const Epilogue& e = p.e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += bias[i];
+    activate_some(e, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] *= e.scale;
+        if (e.r) v[i] = fmaf(e.res_scale, r[i], v[i]);
+    }
+    const int64_t at = t * e.y_stride + n0;
+    if (p.vec) {
+        if (store && n0 + 4 * lane < e.N) store_row<4>(e.y, e.y_type, at + 4 * lane, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (store && n0 + lane + 32 * i < e.N) store_value(e.y, e.y_type, at + lane + 32 * i, v[i]);
+    }
+}
+
 constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128;                       // a step's weights
 
@@ -207,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
     const int mb = blockIdx.x / splits, tok0 = blockIdx.y * COLS;
     const int k0 = (int)((int64_t)p.nk * rank / splits), k1 = (int)((int64_t)p.nk * (rank + 1) / splits);
     const int n_runs = (k1 - k0 + p.run - 1) / p.run;
-    const int own = COLS / (int)splits;                  // columns that a CTA of the cluster finishes
+    const int most = (COLS + (int)splits - 1) / (int)splits;           // columns that a CTA of the cluster finishes, at most
+    const int own = max(0, min(most, COLS - rank * most));
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], kEpiWarps); }
@@ -218,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
         issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (splits > 1)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&parts_here)), "r"(COLS * 512) : "memory");
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&parts_here)), "r"(own * (int)splits * 512)
+                         : "memory");
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)), "n"(kTmem)
@@ -296,20 +338,27 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
     cluster_wait();
     if (warp >= kEpiWarp0) {
         // ======================= epilogue =======================
-        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
-        const int row = mb * 128 + q * 32 + lane, t0 = tok0 + rank * own;
-        const float bias = bias_at(p.e, row);
+        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2, w = warp - kEpiWarp0, n0 = mb * 128, t0 = tok0 + rank * most;
+        float bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias[i] = bias_at(p.e, n0 + channel(lane, i, p.vec));
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + side * kHalf;
-        const float* at = (splits > 1 ? parts : sent) + q * 32 + lane;
-        float res[8] = {};
+        const float* at = splits > 1 ? parts : sent;
+        float res[2][4] = {};                            // of columns c and c + 8
+        if (p.e.r)                                       // the residual into L2, a line of 32 channels a lane
+            for (int c = w + (lane >> 2) * kEpiWarps; c < own; c += 8 * kEpiWarps)
+                if (t0 + c < p.e.T && n0 + 32 * (lane & 3) < p.e.N)
+                    prefetch_l2(p.e.r, p.e.r_type, (t0 + c) * p.e.r_stride + n0 + 32 * (lane & 3));
         bool ok = true;
         // Turn 0 runs the code that ends the kernel on no rows at all, while the first weights are on their way: read
         // from memory at its first use, it takes longer than what it does (2.5 us for one row of x, of 12).
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
-            const int end = turn ? t0 + own : t0;
+            const int end = turn ? min(t0 + own, p.e.T) : t0;
             if (turn) {
-                load_residual<8>(p.e, res, row, t0 + side, 2, end);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (p.e.r && t0 + w + h * kEpiWarps < end) load_residual4(p, res[h], n0, lane, t0 + w + h * kEpiWarps);
                 // the sums, run by run
                 float sum[kHalf];
                 for (int j = 0; j < n_runs; ++j) {
@@ -338,13 +387,14 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
                 ok = all_of(1, 32 * kEpiWarps, ok);
                 if (splits > 1) {
                     if (ok && warp == kEpiWarp0 && lane < (int)splits) {
-                        // columns lane * own .. to CTA `lane`, where this CTA's place is `rank`
-                        const uint32_t bytes = (uint32_t)own * 512;
-                        asm volatile(
-                            "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                in_cta(su32(parts) + rank * bytes, lane)),
-                            "r"(su32(sent) + lane * bytes), "r"(bytes), "r"(in_cta(su32(&parts_here), lane))
-                            : "memory");
+                        // columns lane * most .. to CTA `lane`, where this CTA's place is `rank`
+                        const uint32_t bytes = (uint32_t)max(0, min(most, COLS - lane * most)) * 512;
+                        if (bytes)
+                            asm volatile(
+                                "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                    in_cta(su32(parts) + rank * bytes, lane)),
+                                "r"(su32(sent) + lane * most * 512), "r"(bytes), "r"(in_cta(su32(&parts_here), lane))
+                                : "memory");
                     }
                     __syncwarp();
                     ok = ok && wait_warp(&parts_here, 0, abort_flag, p.wait_ns);
@@ -355,19 +405,33 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
                 if (!ok) break;
             }
 #pragma unroll 1
-            for (int c0 = side; c0 < own; c0 += 16) {    // columns c0, c0 + 2 ..
-                float v[8], r[8];
+            for (int c = w; !turn || t0 + c < end; c += 2 * kEpiWarps) {
+                float v[2][4] = {}, r[2][4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    r[i] = res[i];
-                    v[i] = 0.f;
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[h][i] = res[h][i];
+                    const int next = t0 + c + (2 + h) * kEpiWarps;
+                    if (p.e.r && next < end) load_residual4(p, res[h], n0, lane, next);
                 }
-                if (c0 + 16 < own) load_residual<8>(p.e, res, row, t0 + c0 + 16, 2, end);
-                for (int s = 0; s < (int)splits; ++s)
+                const float* from = at + c * 128;
+                if (turn)
+                    for (int s = 0; s < (int)splits; ++s, from += own * 128)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c0 + 2 * i < own) v[i] += at[(s * own + c0 + 2 * i) * 128];
-                finish<8>(p.e, bias, v, r, row, t0 + c0, 2, end);
+                        for (int h = 0; h < 2; ++h) {
+                            if (h && t0 + c + kEpiWarps >= end) break;
+                            const float* f = from + h * kEpiWarps * 128;
+                            if (p.vec) {
+                                const float4 u = *reinterpret_cast<const float4*>(f + 4 * lane);
+                                v[h][0] += u.x; v[h][1] += u.y; v[h][2] += u.z; v[h][3] += u.w;
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[h][i] += f[lane + 32 * i];
+                            }
+                        }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    finish4(p, bias, v[h], r[h], n0, lane, t0 + c + h * kEpiWarps, turn && t0 + c + h * kEpiWarps < end);
                 if (!turn) break;
             }
         }
@@ -654,6 +718,31 @@ int run_of(int steps, int y_type) {
     return ceil_div(steps, ceil_div(steps, longest));
 }
 
+// Clusters of c CTAs with this much shared memory that run at one time on the current device.  A cluster lies within one of the
+// GPU's groups of SMs, which are not multiples of it: of 8 CTAs, one an SM, 15 fit 152 SMs, of 4 36, of 6 23.
+int clusters_at_once(const void* fn, int c, int smem) {
+    static std::atomic<int> known[64][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if ((n = known[dev][c].load(std::memory_order_relaxed)) > 0) return n - 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c * 64);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    known[dev][c].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t launch_split(const LinearArgs& a, cudaStream_t s) {
     LinearParams p{};
     p.box = a.T <= 16 ? 0 : a.T <= 32 ? 1 : a.T <= 64 ? 2 : 3;
@@ -669,16 +758,24 @@ cudaError_t launch_split(const LinearArgs& a, cudaStream_t s) {
     const void* fn = fns[v];
     static std::atomic<uint64_t> ready[8];
     int sms = 0;
-    const int stage = kABytes + p.cols * 128, parts = p.cols * 512, most = 227 * 1024 - 1024;
+    const int stage = kABytes + p.cols * 128, sent = p.cols * 512, most = 227 * 1024 - 1024;
     cudaError_t err = prepare_kernel(fn, most, ready[v], &sms);
     if (err != cudaSuccess) return err;
     int splits = 1;
-    while (splits < 8 && (int64_t)p.n_mb * p.n_tb * splits * 2 <= sms && p.nk >= splits * 4) splits *= 2;
-    const int steps = ceil_div(p.nk, splits);
+    for (int c = 8; c > 1; --c)
+        if (p.nk >= 2 * c && (int64_t)p.n_mb * p.n_tb <= clusters_at_once(fn, c, most)) {
+            splits = c;
+            break;
+        }
+    const int steps = ceil_div(p.nk, splits), parts = splits > 1 ? ceil_div(p.cols, splits) * splits * 512 : 0;
     p.run = run_of(steps, a.y_type);
+    auto fours = [](const void* q, int type, int64_t stride) {
+        return !q || ((uintptr_t)q % (type == MOE_F32 ? 16 : 8) == 0 && stride % 4 == 0);
+    };
+    p.vec = a.N % 4 == 0 && fours(a.y, a.y_type, a.y_stride) && fours(a.r, a.r_type, a.r_stride);
     p.stages = std::min(std::min(steps, kMaxStages), (most - 1024 - parts) / stage);
     void* args[] = {&p};
-    return launch_clusters(fn, dim3(p.n_mb * splits, p.n_tb), splits, 1024 + (size_t)std::max(p.stages * stage, parts) + (splits > 1 ? parts : 0), s, args);
+    return launch_clusters(fn, dim3(p.n_mb * splits, p.n_tb), splits, 1024 + (size_t)std::max(p.stages * stage, sent) + parts, s, args);
 }
 
 cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
