@@ -53,34 +53,44 @@ struct LinearParams {
 };
 
 // ---------------------------------------------------------------- what follows the sum
-// Phi(-z) e^(z^2/2), z >= 0, the normal distribution's tail without its exponential: a polynomial in
-// t = 1 / (1 + 0.31 z) without constant term, fitted to it (least squares of the relative error, reweighted towards its
-// largest values) on 0..14, where e^(-z^2/2) leaves fp32; relative error below 5e-6.
-__device__ __forceinline__ float tail_factor(float z) {
-    const float t = __fdividef(1.0f, fmaf(0.31f, z, 1.0f));
-    float p = fmaf(t, -0.07392511516809464f, 0.18043823540210724f);
-    p = fmaf(t, p, 0.01575886830687523f);
-    p = fmaf(t, p, 0.13342174887657166f);
-    p = fmaf(t, p, 0.12044348567724228f);
-    p = fmaf(t, p, 0.12386047095060349f);
-    return t * p;
+// Powers of two and reciprocals by the one instruction (relative error of 2^-22 and 2^-23; subnormal results are 0).
+__device__ __forceinline__ float exp2_quick(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-// FAST, for 16-bit outputs: relative error below 2e-5 (a 20th of half a step of fp16), by quick exponentials (off by
-// 2 + 1.17 |argument| units of 2^-23) and quick divisions.
+__device__ __forceinline__ float rcp_quick(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// FAST, for 16-bit outputs: relative error below 2e-5 (a 20th of half a step of fp16), most of it from the exponential's
+// argument, rounded twice (2^-23 of up to 126 binary places) and from the polynomial below (5e-6).  Exponentials are taken
+// 2^32 times too large, so that those of results that are subnormal are not, and are brought back by a product.
+// GELU: Phi(-z) e^(z^2/2), z >= 0, the normal distribution's tail without its exponential, is a polynomial in
+// t = 1 / (1 + 0.31 z) without constant term, fitted to it (least squares of the relative error, reweighted towards its
+// largest values) on 0..14, where e^(-z^2/2) leaves fp32.
 template <int ACT, bool FAST>
 __device__ __forceinline__ float activate(float z) {
+    constexpr float kBack = 2.3283064365386963e-10f;      // 2^-32
     if constexpr (ACT == MOE_ACT_RELU) {
         return z < 0.f ? 0.f : z;                         // (a NaN stays)
-    } else if constexpr (ACT == MOE_ACT_SILU) {
-        return silu_times<FAST>(z, 1.0f);
-    } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
-        // z / (1 + e^(-2u)), from e^(-|2u|), which does not overflow
-        const float w = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
-        const float q = FAST ? __expf(-fabsf(w)) : expf(-fabsf(w));
+    } else if constexpr (ACT == MOE_ACT_SILU && !FAST) {
+        return silu_times<false>(z, 1.0f);
+    } else if constexpr (ACT == MOE_ACT_SILU || ACT == MOE_ACT_GELU_TANH) {
+        // z / (1 + e^-w), w = z or twice tanh's argument, from e^-|w|, which does not overflow
+        const float w = ACT == MOE_ACT_SILU ? z : 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+        const float q = FAST ? kBack * exp2_quick(fmaf(-1.4426950408889634f, fabsf(w), 32.0f)) : expf(-fabsf(w));
         const float top = w >= 0.f ? z : z * q;
-        return FAST ? __fdividef(top, 1.0f + q) : top / (1.0f + q);
+        return FAST ? top * rcp_quick(1.0f + q) : top / (1.0f + q);
     } else if constexpr (FAST) {
-        const float q = tail_factor(fabsf(z)) * __expf(-0.5f * z * z);
+        const float t = rcp_quick(fmaf(0.31f, fabsf(z), 1.0f));
+        float p = fmaf(t, kBack * -0.07392511516809464f, kBack * 0.18043823540210724f);
+        p = fmaf(t, p, kBack * 0.01575886830687523f);
+        p = fmaf(t, p, kBack * 0.13342174887657166f);
+        p = fmaf(t, p, kBack * 0.12044348567724228f);
+        p = fmaf(t, p, kBack * 0.12386047095060349f);
+        const float q = t * p * exp2_quick(fmaf(z * z, -0.72134752044448170f, 32.0f));
         return z * (z >= 0.f ? 1.0f - q : q);
     } else {
         return z * normcdff(z);
@@ -121,53 +131,57 @@ __device__ __forceinline__ void activate_some(const Epilogue& e, float (&v)[C]) 
     }
 }
 
-// What the epilogue needs of the residual for C values of channel `row`, of the rows of x t0, t0 + step, .. (those below
-// e.T and `end`).  Asked for before the sums are there, so that the two latencies overlap.
+// The residual of channel n0 + lane for C rows of x from t0 on, of which n are there.  n0, t0 and n are the warp's, so that all but
+// the lane's own offset is computed once for its lanes.  Asked for before the sums are there: the two latencies overlap.
+template <int C, typename T>
+__device__ __forceinline__ void load_channel(const Epilogue& e, float (&r)[C], int n0, int lane, int t0, int n) {
+    const T* q = static_cast<const T*>(e.r) + ((int64_t)t0 * e.r_stride + n0);
+    if (n0 + lane >= e.N) return;
+#pragma unroll
+    for (int i = 0; i < C; ++i, q += e.r_stride)
+        if (i < n) r[i] = (float)q[lane];
+}
 template <int C>
-__device__ __forceinline__ void load_residual(const Epilogue& e, float (&r)[C], int row, int t0, int step, int end) {
-    if (!e.r || row >= e.N) return;
-    const int n = min(end, e.T) - t0;                    // (i * step < n: in range)
-    const int64_t at = (int64_t)t0 * e.r_stride + row, by = (int64_t)step * e.r_stride;
-    if (e.r_type == MOE_F32) {
+__device__ __forceinline__ void load_residual(const Epilogue& e, float (&r)[C], int n0, int lane, int t0, int n) {
+    if (!e.r) return;
+    if (e.r_type == MOE_F32) load_channel<C, float>(e, r, n0, lane, t0, n);
+    else if (e.r_type == MOE_BF16) load_channel<C, __nv_bfloat16>(e, r, n0, lane, t0, n);
+    else load_channel<C, __half>(e, r, n0, lane, t0, n);
+}
+template <int C, typename T>
+__device__ __forceinline__ void store_channel(const Epilogue& e, const float (&v)[C], int n0, int lane, int t0, int n) {
+    T* q = static_cast<T*>(e.y) + ((int64_t)t0 * e.y_stride + n0);
+    if (n0 + lane >= e.N) return;
+    if (n >= C) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) r[i] = i * step < n ? static_cast<const float*>(e.r)[at + i * by] : 0.f;
-    } else if (e.r_type == MOE_BF16) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            r[i] = i * step < n ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.r)[at + i * by]) : 0.f;
+        for (int i = 0; i < C; ++i, q += e.y_stride) q[lane] = to_out<T>(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i) r[i] = i * step < n ? __half2float(static_cast<const __half*>(e.r)[at + i * by]) : 0.f;
+        for (int i = 0; i < C; ++i, q += e.y_stride)
+            if (i < n) q[lane] = to_out<T>(v[i]);
     }
 }
 // The same values, finished and stored.
 template <int C>
-__device__ __forceinline__ void finish(const Epilogue& e, float bias, float (&v)[C], const float (&r)[C], int row, int t0, int step,
-                                       int end) {
-    if (row >= e.N) return;
-    const int n = min(end, e.T) - t0;
+__device__ __forceinline__ void finish(const Epilogue& e, float bias, float (&v)[C], const float (&r)[C], int n0, int lane, int t0, int n) {
+    if (e.act == MOE_ACT_NONE) {
+        const float b = bias * e.scale;
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] += bias;
-    activate_some(e, v);
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        v[i] *= e.scale;
-        if (e.r) v[i] = fmaf(e.res_scale, r[i], v[i]);
-    }
-    const int64_t at = (int64_t)t0 * e.y_stride + row, by = (int64_t)step * e.y_stride;
-    if (e.y_type == MOE_F32) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i * step < n) static_cast<float*>(e.y)[at + i * by] = v[i];
-    } else if (e.y_type == MOE_BF16) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i * step < n) static_cast<__nv_bfloat16*>(e.y)[at + i * by] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < C; ++i) v[i] = fmaf(v[i], e.scale, b);
     } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i * step < n) static_cast<__half*>(e.y)[at + i * by] = __float2half_rn(v[i]);
+        for (int i = 0; i < C; ++i) v[i] += bias;
+        activate_some(e, v);
+        if (e.scale != 1.0f)
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[i] *= e.scale;
     }
+    if (e.r)
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = fmaf(e.res_scale, r[i], v[i]);
+    if (e.y_type == MOE_F32) store_channel<C, float>(e, v, n0, lane, t0, n);
+    else if (e.y_type == MOE_BF16) store_channel<C, __nv_bfloat16>(e, v, n0, lane, t0, n);
+    else store_channel<C, __half>(e, v, n0, lane, t0, n);
 }
 __device__ __forceinline__ float bias_at(const Epilogue& e, int row) {
     return e.bias && row < e.N ? load1(e.bias, e.bias_type, row) : 0.f;
@@ -204,14 +218,19 @@ __device__ __forceinline__ void load_residual4(const LinearParams& p, float (&r)
 __device__ __forceinline__ void finish4(const LinearParams& p, const float (&bias)[4], float (&v)[4], const float (&r)[4], int n0,
                                         int lane, int64_t t, bool store) {
     const Epilogue& e = p.e;
+    if (e.act == MOE_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += bias[i];
-    activate_some(e, v);
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(v[i], e.scale, bias[i] * e.scale);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] *= e.scale;
-        if (e.r) v[i] = fmaf(e.res_scale, r[i], v[i]);
+        for (int i = 0; i < 4; ++i) v[i] += bias[i];
+        activate_some(e, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= e.scale;
     }
+    if (e.r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(e.res_scale, r[i], v[i]);
     const int64_t at = t * e.y_stride + n0;
     if (p.vec) {
         if (store && n0 + 4 * lane < e.N) store_row<4>(e.y, e.y_type, at + 4 * lane, v);
@@ -456,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
 constexpr int kPairStages = 6, kPairCols = 256;
 constexpr int kPairStageBytes = kABytes + 128 * 128;
 constexpr uint32_t kPairTmem = 512;
-constexpr int kPairEpiWarps = 16, kPairThreads = 32 * (kEpiWarp0 + kPairEpiWarps);
+constexpr int kPairEpi0 = 2, kPairEpiWarps = 16, kPairThreads = 32 * (kPairEpi0 + kPairEpiWarps);
 
 template <bool IN_OUT, bool RUNS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ LinearParams p) {
@@ -467,8 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, issued;
     volatile int* abort_flag = &abort_word;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t cta = cta_rank();
+    const int tid = threadIdx.x, warp = uniform((int)threadIdx.x >> 5), lane = tid & 31;
+    const uint32_t cta = uniform(cta_rank());
     if (tid == 0) {
         for (int i = 0; i < kPairStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kPairEpiWarps); }
@@ -571,9 +590,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
                 drain_wait(&drain, 0, p.wait_ns);
             }
         }
-    } else if (warp >= kEpiWarp0) {
+    } else {
         // ======================= epilogue: lanes 32 q.. of TMEM, columns 16 side .. of every 64 =======================
-        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
+        const int q = uniform(warp & 3), side = uniform((warp - kPairEpi0) >> 2);
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + 16 * side, accr0 = in_leader(su32(accr));
         auto release = [&](int b) {
             tc_before();
@@ -584,14 +603,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
         bool ok = true;
         for (int t = first; ok && t < n_tiles; t += n_pairs) {
             const int tb = t / p.n_mb, mb = t - tb * p.n_mb;
-            const int row = mb * 256 + (int)cta * 128 + q * 32 + lane, tok0 = tb * p.cols + 16 * side;
-            const int end = min(tb * p.cols + p.cols, p.e.T);
-            const float bias = bias_at(p.e, row);
+            const int n0 = uniform(mb * 256 + (int)cta * 128 + q * 32), tok0 = uniform(tb * p.cols + 16 * side);
+            const int n = uniform(min(tb * p.cols + p.cols, p.e.T)) - tok0;      // (columns c < n are there)
+            const float bias = bias_at(p.e, n0 + lane);
             if (p.e.r) {
                 // the tile's residual into L2 (a line of a row of x a lane; the first channel of the warp's 32)
-                const int64_t at = row - lane;
-                for (int c = (lane & 15) + 64 * (lane >> 4); c < p.cols; c += 128)
-                    if (tok0 + c < end && at < p.e.N) prefetch_l2(p.e.r, p.e.r_type, (tok0 + c) * p.e.r_stride + at);
+                for (int c = (lane & 15) + 64 * (lane >> 4); c < n; c += 128)
+                    if (n0 < p.e.N) prefetch_l2(p.e.r, p.e.r_type, (tok0 + c) * p.e.r_stride + n0);
             }
             if constexpr (RUNS) {
                 float sum[kPairCols / 4];
@@ -601,50 +619,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
                     if (!ok) break;
                     tc_after();
 #pragma unroll
-                    for (int c = 0; c < kPairCols; c += 64)
-                        if (tok0 + c < end) {
-                            uint32_t v[16];
-                            tmem_ld16(lanes + b * kPairCols + c, v);
+                    for (int c = 0; c < kPairCols; c += 128)
+                        if (c < n) {
+                            uint32_t v[2][16];
+                            tmem_ld16(lanes + b * kPairCols + c, v[0]);
+                            if (c + 64 < n) tmem_ld16(lanes + b * kPairCols + c + 64, v[1]);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                sum[c / 4 + i] = k0 ? __fadd_rn(sum[c / 4 + i], __uint_as_float(v[i])) : __uint_as_float(v[i]);
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float& to = sum[c / 4 + 16 * h + i];
+                                    to = k0 ? __fadd_rn(to, __uint_as_float(v[h][i])) : __uint_as_float(v[h][i]);
+                                }
                         }
                     release(b);
                 }
                 if (!ok) break;
 #pragma unroll 1
-                for (int i = 0; i < kPairCols / 4; i += 8) {         // (one copy of the code: the sums pass by)
-                    const int c = (i >> 4) * 64 + (i & 8);
-                    if (tok0 + c >= end) break;
-                    float v[8], r[8];
-                    load_residual<8>(p.e, r, row, tok0 + c, 1, end);
+                for (int i = 0; i < kPairCols / 4; i += 16) {        // (one copy of the code: the sums pass by)
+                    const int c = 4 * i;
+                    if (c >= n) break;
+                    float v[16], r[16];
+                    load_residual<16>(p.e, r, n0, lane, tok0 + c, n - c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = sum[e];
+                    for (int e = 0; e < 16; ++e) v[e] = sum[e];
 #pragma unroll
-                    for (int e = 0; e + 8 < kPairCols / 4; ++e) sum[e] = sum[e + 8];
-                    finish<8>(p.e, bias, v, r, row, tok0 + c, 1, end);
+                    for (int e = 0; e + 16 < kPairCols / 4; ++e) sum[e] = sum[e + 16];
+                    finish<16>(p.e, bias, v, r, n0, lane, tok0 + c, n - c);
                 }
             } else {
                 const int b = j & 1;
                 float res[16];
-                load_residual<16>(p.e, res, row, tok0, 1, end);
+                load_residual<16>(p.e, res, n0, lane, tok0, n);
                 ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
                 if (!ok) break;
                 tc_after();
-                for (int c = 0; tok0 + c < end; c += 64) {
-                    uint32_t u[16];
-                    tmem_ld16(lanes + b * kPairCols + c, u);
+                uint32_t u[16];
+                if (n > 0) tmem_ld16(lanes + b * kPairCols, u);
+                for (int c = 0; c < n; c += 64) {
                     float v[16], r[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) r[i] = res[i];
-                    if (tok0 + c + 64 < end) load_residual<16>(p.e, res, row, tok0 + c + 64, 1, end);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
-                    finish<16>(p.e, bias, v, r, row, tok0 + c, 1, end);
+                    if (c + 64 < n) {
+                        tmem_ld16(lanes + b * kPairCols + c + 64, u);
+                        load_residual<16>(p.e, res, n0, lane, tok0 + c + 64, n - c - 64);
+                    } else {
+                        release(b);                      // (everything is read)
+                    }
+                    finish<16>(p.e, bias, v, r, n0, lane, tok0 + c, n - c);
                 }
-                release(b);
+                if (n <= 0) release(b);
                 ++j;
             }
         }
