@@ -475,10 +475,13 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
 constexpr int kPairStages = 6, kPairCols = 256;
 constexpr int kPairStageBytes = kABytes + 128 * 128;
 constexpr uint32_t kPairTmem = 512;
-constexpr int kPairEpi0 = 2, kPairEpiWarps = 16, kPairThreads = 32 * (kPairEpi0 + kPairEpiWarps);
+constexpr int kPairEpi0 = 2;
+// Epilogue warps: 16, or 8 that have the registers for the sums of 128 columns each.
+template <bool RUNS> constexpr int kPairEpiWarps = RUNS ? 8 : 16;
+template <bool RUNS> constexpr int kPairThreads = 32 * (kPairEpi0 + kPairEpiWarps<RUNS>);
 
 template <bool IN_OUT, bool RUNS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ LinearParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 1) pair_kernel(const __grid_constant__ LinearParams p) {
     using Ring = RingOf<kPairStages>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -490,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
     const uint32_t cta = uniform(cta_rank());
     if (tid == 0) {
         for (int i = 0; i < kPairStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kPairEpiWarps); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kPairEpiWarps<RUNS>); }
         mbar_init(&drain, 1);
         mbar_init(&never, 1);
         abort_word = 0;
@@ -591,7 +594,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
             }
         }
     } else {
-        // ======================= epilogue: lanes 32 q.. of TMEM, columns 16 side .. of every 64 =======================
+        // ======================= epilogue: lanes 32 q.. of TMEM, columns 16 side .. of every kEvery =======================
+        constexpr int kSides = kPairEpiWarps<RUNS> / 4, kEvery = 16 * kSides;
         const int q = uniform(warp & 3), side = uniform((warp - kPairEpi0) >> 2);
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + 16 * side, accr0 = in_leader(su32(accr));
         auto release = [&](int b) {
@@ -606,46 +610,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
             const int n0 = uniform(mb * 256 + (int)cta * 128 + q * 32), tok0 = uniform(tb * p.cols + 16 * side);
             const int n = uniform(min(tb * p.cols + p.cols, p.e.T)) - tok0;      // (columns c < n are there)
             const float bias = bias_at(p.e, n0 + lane);
-            if (p.e.r) {
-                // the tile's residual into L2 (a line of a row of x a lane; the first channel of the warp's 32)
-                for (int c = (lane & 15) + 64 * (lane >> 4); c < n; c += 128)
-                    if (n0 < p.e.N) prefetch_l2(p.e.r, p.e.r_type, (tok0 + c) * p.e.r_stride + n0);
-            }
             if constexpr (RUNS) {
-                float sum[kPairCols / 4];
+                float sum[kPairCols / kSides];
                 for (int k0 = 0; k0 < p.nk; k0 += p.run, ++j) {
                     const int b = j & 1;
                     ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_after();
 #pragma unroll
-                    for (int c = 0; c < kPairCols; c += 128)
-                        if (c < n) {
-                            uint32_t v[2][16];
-                            tmem_ld16(lanes + b * kPairCols + c, v[0]);
-                            if (c + 64 < n) tmem_ld16(lanes + b * kPairCols + c + 64, v[1]);
+                    for (int i = 0; i < kPairCols / kSides; i += 16)
+                        if (i * kSides < n) {
+                            uint32_t v[16];
+                            tmem_ld16(lanes + b * kPairCols + i * kSides, v);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    float& to = sum[c / 4 + 16 * h + i];
-                                    to = k0 ? __fadd_rn(to, __uint_as_float(v[h][i])) : __uint_as_float(v[h][i]);
-                                }
+                            for (int e = 0; e < 16; ++e)
+                                sum[i + e] = k0 ? __fadd_rn(sum[i + e], __uint_as_float(v[e])) : __uint_as_float(v[e]);
                         }
                     release(b);
                 }
                 if (!ok) break;
 #pragma unroll 1
-                for (int i = 0; i < kPairCols / 4; i += 16) {        // (one copy of the code: the sums pass by)
-                    const int c = 4 * i;
-                    if (c >= n) break;
+                for (int c = 0; c < n; c += kEvery) {                // (one copy of the code: the sums pass by)
                     float v[16], r[16];
                     load_residual<16>(p.e, r, n0, lane, tok0 + c, n - c);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = sum[e];
 #pragma unroll
-                    for (int e = 0; e + 16 < kPairCols / 4; ++e) sum[e] = sum[e + 16];
+                    for (int e = 0; e + 16 < kPairCols / kSides; ++e) sum[e] = sum[e + 16];
                     finish<16>(p.e, bias, v, r, n0, lane, tok0 + c, n - c);
                 }
             } else {
@@ -657,16 +649,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) pai
                 tc_after();
                 uint32_t u[16];
                 if (n > 0) tmem_ld16(lanes + b * kPairCols, u);
-                for (int c = 0; c < n; c += 64) {
+                for (int c = 0; c < n; c += kEvery) {
                     float v[16], r[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) r[i] = res[i];
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
-                    if (c + 64 < n) {
-                        tmem_ld16(lanes + b * kPairCols + c + 64, u);
-                        load_residual<16>(p.e, res, n0, lane, tok0 + c + 64, n - c - 64);
+                    if (c + kEvery < n) {
+                        tmem_ld16(lanes + b * kPairCols + c + kEvery, u);
+                        load_residual<16>(p.e, res, n0, lane, tok0 + c + kEvery, n - c - kEvery);
                     } else {
                         release(b);                      // (everything is read)
                     }
@@ -837,7 +829,7 @@ cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
     p.run = run_of(p.nk, a.y_type);
     const int64_t tiles = (int64_t)p.n_mb * p.n_tb;
     void* args[] = {&p};
-    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, pairs)), kPairThreads, kSmem, s, args);
+    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, pairs)), runs ? kPairThreads<true> : kPairThreads<false>, kSmem, s, args);
 }
 
 }  // namespace
