@@ -195,6 +195,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
 __device__ __forceinline__ void prefetch_l2(const void* p, int type, int64_t i) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i * (type == MOE_F32 ? 4 : 2)));
 }
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ uint32_t in_cta(uint32_t a, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
@@ -259,10 +265,11 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
     float* parts = reinterpret_cast<float*>(smem + max(p.stages * kStage, COLS * 512));
     float* sent = reinterpret_cast<float*>(smem);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)cta_rank();
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    const int rank = uniform((int)cta_rank());
     uint32_t splits;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+    splits = uniform(splits);
     const int mb = blockIdx.x / splits, tok0 = blockIdx.y * COLS;
     const int k0 = (int)((int64_t)p.nk * rank / splits), k1 = (int)((int64_t)p.nk * (rank + 1) / splits);
     const int n_runs = (k1 - k0 + p.run - 1) / p.run;
@@ -299,20 +306,23 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
 
     if (warp == 0) {
         // ======================= loads =======================
+        // (the whole warp keeps step, so that what one lane issues lies in uniform registers)
+        const uint32_t stage0 = su32(smem), full0 = su32(full);
+        const CUtensorMap* xmap = &p.tx[p.box];
         int g = 0, s = 0;
         uint32_t ph = 1;
         for (int kb = k0; kb < k1; ++kb, ++g) {
             if (!wait_warp(&empty[s], ph, abort_flag, p.wait_ns)) break;
+            const uint32_t bar = full0 + 8 * s, a = stage0 + s * kStage;
             if (elect_one()) {
-                uint8_t* a = smem + s * kStage;
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[s])), "r"(kStage) : "memory");
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kStage) : "memory");
                 if constexpr (IN_OUT) {
-                    tma_load_2d(a, &p.tw, mb * 128, kb * kStepK, &full[s]);
-                    tma_load_2d(a + 8192, &p.tw, mb * 128 + 64, kb * kStepK, &full[s]);
+                    tma_load(a, &p.tw, mb * 128, kb * kStepK, bar);
+                    tma_load(a + 8192, &p.tw, mb * 128 + 64, kb * kStepK, bar);
                 } else {
-                    tma_load_2d(a, &p.tw, kb * kStepK, mb * 128, &full[s]);
+                    tma_load(a, &p.tw, kb * kStepK, mb * 128, bar);
                 }
-                tma_load_2d(a + kABytes, &p.tx[p.box], kb * kStepK, tok0, &full[s]);
+                tma_load(a + kABytes, xmap, kb * kStepK, tok0, bar);
             }
             __syncwarp();
             if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -320,7 +330,9 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
         if (lane == 0) issued = g;
     } else if (warp == 1) {
         // ======================= MMA issue =======================
-        const uint32_t idesc = idesc_mma(128, COLS, p.bf16) | (IN_OUT ? 1u << 15 : 0u);
+        const uint32_t idesc = uniform(idesc_mma(128, COLS, p.bf16) | (IN_OUT ? 1u << 15 : 0u));
+        const uint32_t a0 = su32(smem);
+        const uint64_t da0 = IN_OUT ? sdesc_mn(a0) : sdesc(a0), db0 = sdesc(a0 + kABytes);
         constexpr uint32_t kAdvA = (IN_OUT ? 2048 : 32) >> 4, kAdvB = 32 >> 4;
         int s = 0, j = 0;
         uint32_t ph = 0;
@@ -329,14 +341,14 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
             const int b = j & 1, r1 = min(r0 + p.run, k1);
             if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
             tc_after();
-            const uint32_t acc = tmem + (uint32_t)b * COLS;
+            const uint32_t acc = uniform(tmem + (uint32_t)b * COLS);
             for (int kb = r0; kb < r1; ++kb) {
                 const bool stalled = p.stall && !any;    // (test setting)
                 if (!wait_warp(stalled ? &never : &full[s], stalled ? 0u : ph, abort_flag, p.wait_ns)) { ok = false; break; }
                 tc_after();
+                const uint32_t adv = (uint32_t)s * (kStage >> 4);
+                const uint64_t da = da0 + adv, db = db0 + adv;
                 if (elect_one()) {
-                    const uint32_t a = su32(smem + s * kStage);
-                    const uint64_t da = IN_OUT ? sdesc_mn(a) : sdesc(a), db = sdesc(a + kABytes);
 #pragma unroll
                     for (int kk = 0; kk < kStepK / 16; ++kk) mma_f16(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 || kb > r0);
                     mma_commit(&empty[s]);
@@ -738,13 +750,25 @@ int run_of(int steps, int y_type) {
     return ceil_div(steps, ceil_div(steps, longest));
 }
 
-// Clusters of c CTAs with this much shared memory that run at one time on the current device.  A cluster lies within one of the
-// GPU's groups of SMs, which are not multiples of it: of 8 CTAs, one an SM, 15 fit 152 SMs, of 4 36, of 6 23.
-int clusters_at_once(const void* fn, int c, int smem) {
-    static std::atomic<int> known[64][9];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if ((n = known[dev][c].load(std::memory_order_relaxed)) > 0) return n - 1;
+constexpr int kSplitSmem = 227 * 1024 - 1024;            // dynamic shared memory of split_kernel, at most
+
+int sm_count() {
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed), dev = 0;
+    if (n) return n;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;                                      // (no device: moe_linear_path answers for a GB300)
+    }
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
+// Clusters of c CTAs of the split kernel, one an SM, that run at one time.  A cluster lies within one of the GPU's groups
+// of SMs, which are not multiples of it: of 8 CTAs 15 fit 152 SMs, of 6 23, of 4 36.  (One more than fit takes twice the time.)
+int clusters_at_once(const void* fn, int c) {
+    static std::atomic<int> known[9];                    // (the same for every form of the kernel: its shared memory decides)
+    int n = known[c].load(std::memory_order_relaxed);
+    if (n > 0) return n - 1;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = c;
@@ -752,53 +776,88 @@ int clusters_at_once(const void* fn, int c, int smem) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c * 64);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSplitSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
         cudaGetLastError();
-        n = 0;
+        static const int gb300[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+        return gb300[c];
     }
-    known[dev][c].store(n + 1, std::memory_order_relaxed);
+    known[c].store(n + 1, std::memory_order_relaxed);
     return n;
 }
 
-cudaError_t launch_split(const LinearArgs& a, cudaStream_t s) {
+// How a product is cut: columns of a tile, and CTAs that share its sum (split) or 0 for the kernel of pairs.
+struct Shape {
+    int cols, splits;
+};
+// The least time by a model of both kernels, in us, fitted to graphs of calls on weights that come from HBM (512..7168 wide,
+// T = 16..1024; it is within 15 % there):
+//   split, of `cols` columns:  start[cols] + steps of the sum a CTA * step[cols] + 0.4 where CTAs share a sum
+//   pairs, of `cols` columns:  3.5 + 0.009 cols + waves * steps * pair_step(cols)
+// A step is bound by what an SM can load (18 to 32 KB); the start holds launch, first load and epilogue.  Measured, split /
+// pairs at their best: 64 rows, 2048 -> 2048: 7.2 / 9.8; 256 rows, 2048 -> 2048: 10.2 / 10.2, 768 -> 2048: 7.7 / 6.4, 7168 -> 2048:
+// 17.1 / 25.6, 2048 -> 7168: 16.8 / 12.5; 512 rows, 2048 -> 2048: 14.0 / 10.8.
+Shape shape_of(const LinearArgs& a, const void* const (&fns)[4]) {
+    static const float start[4] = {3.4f, 3.9f, 5.2f, 7.4f}, step[4] = {0.229f, 0.241f, 0.236f, 0.252f};
+    const int nk = ceil_div(a.K, kStepK), sms = sm_count();
+    Shape best{0, 0};
+    float least = 1e30f;
+    auto take = [&](float t, int cols, int splits) {
+        if (t < least) {
+            least = t;
+            best = Shape{cols, splits};
+        }
+    };
+    for (int i = 0; i < 4 && (16 << i) < 2 * a.T + 16; ++i) {
+        const int64_t tiles = (int64_t)ceil_div(a.N, 128) * ceil_div(a.T, 16 << i);
+        if (tiles > 4 * sms) continue;
+        take(start[i] + ceil_div(tiles, sms) * nk * step[i], 16 << i, 1);
+        for (int c = 2; c <= 8 && c <= nk && tiles * c <= sms; ++c)
+            if (tiles <= clusters_at_once(fns[i], c)) take(start[i] + 0.4f + ceil_div(nk, c) * step[i], 16 << i, c);
+    }
+    // (beyond some waves, all of them full: the largest tiles)
+    for (int nb = ceil_div(a.T, kPairCols), most = std::min(ceil_div(a.T, 32), nb + 64); nb <= most; ++nb) {
+        const int cols = (ceil_div(a.T, nb) + 31) & ~31;
+        const float per = cols <= 128 ? 0.193f : 0.193f + (cols - 128) * 0.00053f;
+        const int64_t waves = ceil_div((int64_t)ceil_div(a.N, 256) * ceil_div(a.T, cols), sms / 2);
+        take(3.5f + 0.009f * cols + waves * nk * per, cols, 0);
+    }
+    return best;
+}
+const void* const kSplit[2][4] = {{(const void*)split_kernel<false, 16>, (const void*)split_kernel<false, 32>,
+                                   (const void*)split_kernel<false, 64>, (const void*)split_kernel<false, 128>},
+                                  {(const void*)split_kernel<true, 16>, (const void*)split_kernel<true, 32>,
+                                   (const void*)split_kernel<true, 64>, (const void*)split_kernel<true, 128>}};
+
+cudaError_t launch_split(const LinearArgs& a, Shape shape, cudaStream_t s) {
     LinearParams p{};
-    p.box = a.T <= 16 ? 0 : a.T <= 32 ? 1 : a.T <= 64 ? 2 : 3;
-    p.cols = 16 << p.box;
+    p.cols = shape.cols;
+    p.box = p.cols > 64 ? 3 : p.cols > 32 ? 2 : p.cols > 16 ? 1 : 0;
     if (!fill(p, a)) return cudaErrorInvalidValue;
     p.n_mb = ceil_div(a.N, 128);
     p.n_tb = ceil_div(a.T, p.cols);
-    const int v = (a.in_out ? 4 : 0) + p.box;
-    const void* const fns[8] = {(const void*)split_kernel<false, 16>, (const void*)split_kernel<false, 32>,
-                                (const void*)split_kernel<false, 64>, (const void*)split_kernel<false, 128>,
-                                (const void*)split_kernel<true, 16>, (const void*)split_kernel<true, 32>,
-                                (const void*)split_kernel<true, 64>, (const void*)split_kernel<true, 128>};
-    const void* fn = fns[v];
+    const void* fn = kSplit[a.in_out][p.box];
     static std::atomic<uint64_t> ready[8];
     int sms = 0;
-    const int stage = kABytes + p.cols * 128, sent = p.cols * 512, most = 227 * 1024 - 1024;
-    cudaError_t err = prepare_kernel(fn, most, ready[v], &sms);
+    cudaError_t err = prepare_kernel(fn, kSplitSmem, ready[4 * a.in_out + p.box], &sms);
     if (err != cudaSuccess) return err;
-    int splits = 1;
-    for (int c = 8; c > 1; --c)
-        if (p.nk >= 2 * c && (int64_t)p.n_mb * p.n_tb <= clusters_at_once(fn, c, most)) {
-            splits = c;
-            break;
-        }
-    const int steps = ceil_div(p.nk, splits), parts = splits > 1 ? ceil_div(p.cols, splits) * splits * 512 : 0;
+    const int steps = ceil_div(p.nk, shape.splits), stage = kABytes + p.cols * 128, sent = p.cols * 512;
+    const int parts = shape.splits > 1 ? ceil_div(p.cols, shape.splits) * shape.splits * 512 : 0;
     p.run = run_of(steps, a.y_type);
     auto fours = [](const void* q, int type, int64_t stride) {
         return !q || ((uintptr_t)q % (type == MOE_F32 ? 16 : 8) == 0 && stride % 4 == 0);
     };
     p.vec = a.N % 4 == 0 && fours(a.y, a.y_type, a.y_stride) && fours(a.r, a.r_type, a.r_stride);
-    p.stages = std::min(std::min(steps, kMaxStages), (most - 1024 - parts) / stage);
+    p.stages = std::min(std::min(steps, kMaxStages), (kSplitSmem - 1024 - parts) / stage);
     void* args[] = {&p};
-    return launch_clusters(fn, dim3(p.n_mb * splits, p.n_tb), splits, 1024 + (size_t)std::max(p.stages * stage, sent) + parts, s, args);
+    return launch_clusters(fn, dim3(p.n_mb * shape.splits, p.n_tb), shape.splits, 1024 + (size_t)std::max(p.stages * stage, sent) + parts,
+                           s, args);
 }
 
-cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
+cudaError_t launch_pairs(const LinearArgs& a, Shape shape, cudaStream_t s) {
     LinearParams p{};
     static std::atomic<uint64_t> ready[4];
     int sms = 0;
@@ -811,34 +870,26 @@ cudaError_t launch_pairs(const LinearArgs& a, cudaStream_t s) {
     constexpr size_t kSmem = 1024 + (size_t)kPairStages * kPairStageBytes;
     cudaError_t err = prepare_kernel(fn, (int)kSmem, ready[v], &sms);
     if (err != cudaSuccess) return err;
-    const int pairs = sms / 2;
-    p.n_mb = ceil_div(a.N, 256);
-    // columns of a tile: those with the least time of all waves
-    int64_t best = -1;
-    for (int nb = ceil_div(a.T, kPairCols), most = std::min(ceil_div(a.T, 32), nb + 64); nb <= most; ++nb) {
-        const int cols = (ceil_div(a.T, nb) + 31) & ~31;
-        const int64_t cost = (int64_t)ceil_div((int64_t)p.n_mb * ceil_div(a.T, cols), pairs) * (cols + 64);
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.cols = cols;
-        }
-    }
-    p.n_tb = ceil_div(a.T, p.cols);
+    p.cols = shape.cols;
     p.box = p.cols > 128 ? 3 : p.cols > 64 ? 2 : p.cols > 32 ? 1 : 0;
     if (!fill(p, a)) return cudaErrorInvalidValue;
+    p.n_mb = ceil_div(a.N, 256);
+    p.n_tb = ceil_div(a.T, p.cols);
     p.run = run_of(p.nk, a.y_type);
     const int64_t tiles = (int64_t)p.n_mb * p.n_tb;
     void* args[] = {&p};
-    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, pairs)), runs ? kPairThreads<true> : kPairThreads<false>, kSmem, s, args);
+    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, sms / 2)), runs ? kPairThreads<true> : kPairThreads<false>, kSmem,
+                        s, args);
 }
 
 }  // namespace
 
-bool linear_pairs(const LinearArgs& a) { return (int64_t)ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 48; }
+bool linear_pairs(const LinearArgs& a) { return shape_of(a, kSplit[a.in_out]).splits == 0; }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     if (a.T <= 0) return cudaSuccess;
-    return linear_pairs(a) ? launch_pairs(a, s) : launch_split(a, s);
+    const Shape shape = shape_of(a, kSplit[a.in_out]);
+    return shape.splits ? launch_split(a, shape, s) : launch_pairs(a, shape, s);
 }
 
 }  // namespace moe
