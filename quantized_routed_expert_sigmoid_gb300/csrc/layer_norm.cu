@@ -168,7 +168,7 @@ __device__ __forceinline__ void wait_ahead(int depth) {
     if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
-template <typename T, int V>
+template <typename T>
 __device__ __forceinline__ void load_pairs(const T* row, const Place& at, int H, F2 (&v)[kPairs], float none) {
     // (element by element: V = 1)
 #pragma unroll
@@ -184,7 +184,7 @@ __device__ __forceinline__ void load_channels(const float* p, const Place& at, i
     for (int i = 0; i < kPairs; ++i) v[i] = pair(none, none);
     if (!p) return;
     if constexpr (V == 1) {
-        load_pairs<float, 1>(p, at, H, v, 0.f);
+        load_pairs<float>(p, at, H, v, 0.f);
     } else {
 #pragma unroll
         for (int c = 0; c < kChannels / V; ++c)
@@ -198,7 +198,8 @@ __device__ __forceinline__ void load_channels(const float* p, const Place& at, i
 }
 
 // ---------------------------------------------------------------- forward
-template <typename X, typename Y, int V>
+// FULL: the row's threads have all their channels (H = 512 warps): nothing is compared with the row's end.
+template <typename X, typename Y, int V, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_constant__ NormParams p) {
     constexpr int NC = kChannels / V, kBytes = V * sizeof(X), kSlot = kThreads * NC * kBytes;
     const LayerNormArgs& a = p.a;
@@ -208,47 +209,53 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     const Place at(p.warps, V);
     const int tid = threadIdx.x, groups = kWarps / p.warps, g0 = at.group * p.warps;
     const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + tid * kBytes;
-    const int64_t every = (int64_t)gridDim.x * groups;
+    const int every = gridDim.x * groups, T = a.T;
+    auto here = [&](int c) { return FULL || at.first + c * at.step < a.H; };
     wait_for_previous();
     allow_next();
     if (at.idle) return;
-    const X* x_in = static_cast<const X*>(a.x);
-    Y* y_out = static_cast<Y*>(a.y);
-    auto fetch = [&](int64_t t, int s) {                  // row t into slot s (always one group of copies)
+    int t = blockIdx.x + gridDim.x * at.group, ahead = t;
+    const X* x_next = static_cast<const X*>(a.x) + (int64_t)t * a.x_stride + (V > 1 ? at.first : 0);
+    Y* y_out = static_cast<Y*>(a.y) + (int64_t)t * a.y_stride + (V > 1 ? at.first : 0);
+    const int64_t x_step = every * a.x_stride, y_step = every * a.y_stride;
+    auto fetch = [&](int s) {                             // the next row into slot s (always one group of copies)
         if constexpr (V > 1) {
-            if (t < a.T) {
-                const X* src = x_in + t * a.x_stride + at.first;
+            if (ahead < T) {
+                const X* src = x_next;
 #pragma unroll
                 for (int c = 0; c < NC; ++c, src += at.step)
-                    if (at.first + c * at.step < a.H) copy_ahead<kBytes>(mine + s * kSlot + c * kThreads * kBytes, src);
+                    if (here(c)) copy_ahead<kBytes>(mine + s * kSlot + c * kThreads * kBytes, src);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            ahead += every;                               // (T + 5 * every < 2^31)
+            x_next += x_step;
         }
     };
-    int64_t t = blockIdx.x + (int64_t)gridDim.x * at.group;
-    for (int d = 0; V > 1 && d < p.depth; ++d) fetch(t + d * every, d);
+    for (int d = 0; V > 1 && d < p.depth; ++d) fetch(d);
     F2 gamma[kPairs], beta[kPairs];
     load_channels<V>(a.gamma, at, a.H, 1.f, gamma);
     load_channels<V>(a.beta, at, a.H, 0.f, beta);
     const float inv = 1.0f / (float)a.H;
     int turn = 0, s = 0;
-    for (; t < a.T; t += every, turn ^= 1) {
+    for (; t < T; t += every, turn ^= 1, y_out += y_step) {
         F2 x[kPairs];
         if constexpr (V > 1) {
             wait_ahead(p.depth);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 F2 v[V / 2];
+                if (!FULL)
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) v[j] = 0;
-                if (at.first + c * at.step < a.H) from_shared<X, V>(mine + s * kSlot + c * kThreads * kBytes, v);
+                    for (int j = 0; j < V / 2; ++j) v[j] = 0;
+                if (here(c)) from_shared<X, V>(mine + s * kSlot + c * kThreads * kBytes, v);
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) x[c * (V / 2) + j] = v[j];
             }
-            fetch(t + p.depth * every, s);                // (this thread has read its share of the slot)
+            fetch(s);                                     // (this thread has read its share of the slot)
             if (++s == p.depth) s = 0;
         } else {
-            load_pairs<X, 1>(x_in + t * a.x_stride, at, a.H, x, 0.f);
+            load_pairs<X>(x_next, at, a.H, x, 0.f);
+            x_next += x_step;
         }
         F2 sum = x[0];
 #pragma unroll
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             x[i] = add2(x[i], minus);
             // (what lies behind the row's end is 0, which must not count)
             if constexpr (V > 1) {
-                if (at.first + (i / (V / 2)) * at.step >= a.H) x[i] = 0;
+                if (!here(i / (V / 2))) x[i] = 0;
             } else {
                 const int e0 = at.first + 2 * i * at.step;
                 if (e0 + at.step >= a.H) x[i] = e0 < a.H ? pair(split(x[i]).x, 0.f) : 0;
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
         const float d = q.x * inv;
         float var = q.y * inv - d * d;
         if (var < 0.f) var = 0.f;                         // (a NaN stays)
-        const float r = 1.0f / sqrtf(var + a.eps);
+        const float r = rsqrtf(var + a.eps);
         if (at.w == 0 && (tid & 31) == 0) {
             if (a.mean) a.mean[t] = m + d;
             if (a.rstd) a.rstd[t] = r;
@@ -281,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
         if (!a.y) continue;
         const F2 scale = pair(r, r), shift = pair(-d, -d);
         if constexpr (V > 1) {
-            Y* out = y_out + t * a.y_stride + at.first;
+            Y* out = y_out;
 #pragma unroll
             for (int c = 0; c < NC; ++c, out += at.step) {
-                if (at.first + c * at.step >= a.H) continue;
+                if (!here(c)) continue;
                 F2 v[V / 2];
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) {
@@ -294,13 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 to_row<Y, V>(out, v);
             }
         } else {
-            Y* out = y_out + t * a.y_stride;
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {
                 const float2 v = split(fma2(mul2(add2(x[i], shift), scale), gamma[i], beta[i]));
                 const int e0 = at.first + 2 * i * at.step;
-                if (e0 < a.H) out[e0] = rounded<Y>(v.x);
-                if (e0 + at.step < a.H) out[e0 + at.step] = rounded<Y>(v.y);
+                if (e0 < a.H) y_out[e0] = rounded<Y>(v.x);
+                if (e0 + at.step < a.H) y_out[e0 + at.step] = rounded<Y>(v.y);
             }
         }
     }
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
 // ---------------------------------------------------------------- backward
 // A thread keeps the sums for gamma and beta of its channels in registers; the CTA's groups join theirs in shared memory and
 // write one row of partial sums, which sums_kernel adds in a fixed order.
-template <typename X, typename Y, int V>
+template <typename X, typename Y, int V, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int NC = kChannels / V, kX = V * sizeof(X), kY = V * sizeof(Y);
     constexpr int kOffY = kThreads * NC * kX, kOffAdd = kOffY + kThreads * NC * kY;
@@ -320,41 +326,48 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     const Place at(p.warps, V);
     const int tid = threadIdx.x, groups = kWarps / p.warps, g0 = at.group * p.warps;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(shared), slot = kOffAdd + (a.add ? kOffY : 0);
-    const int64_t every = (int64_t)gridDim.x * groups;
-    const X* x_in = static_cast<const X*>(a.x);
-    const Y* dy_in = static_cast<const Y*>(a.y);
-    const X* add_in = static_cast<const X*>(a.add);
-    X* dx_out = static_cast<X*>(a.dx);
+    const int every = gridDim.x * groups, T = a.T;
+    auto here = [&](int c) { return FULL || at.first + c * at.step < a.H; };
     wait_for_previous();
     allow_next();
-    int64_t t = at.idle ? a.T : blockIdx.x + (int64_t)gridDim.x * at.group;
-    auto fetch = [&](int64_t t, int s) {                  // row t into slot s (always one group of copies)
+    int t = at.idle ? T : blockIdx.x + gridDim.x * at.group, ahead = t;
+    const int off = V > 1 ? at.first : 0;
+    // (rows by their number each time: pointers and strides kept for four of them would not fit the registers)
+    auto x_row = [&](int t) { return static_cast<const X*>(a.x) + (t * a.x_stride + off); };
+    auto dy_row = [&](int t) { return static_cast<const Y*>(a.y) + (t * a.y_stride + off); };
+    auto add_row = [&](int t) { return static_cast<const X*>(a.add) + (t * a.add_stride + off); };
+    auto fetch = [&](int s) {                             // the next row into slot s (always one group of copies)
         if constexpr (V > 1) {
-            if (t < a.T) {
+            if (ahead < T) {
                 const uint32_t dst = ring + s * slot;
-                const X* px = x_in + t * a.x_stride + at.first;
-                const Y* py = dy_in + t * a.y_stride + at.first;
-                const X* pa = add_in + t * a.add_stride + at.first;
+                const X* px = x_row(ahead);
+                const Y* py = dy_row(ahead);
 #pragma unroll
-                for (int c = 0; c < NC; ++c, px += at.step, py += at.step, pa += at.step) {
-                    if (at.first + c * at.step >= a.H) continue;
+                for (int c = 0; c < NC; ++c, px += at.step, py += at.step) {
+                    if (!here(c)) continue;
                     copy_ahead<kX>(dst + (c * kThreads + tid) * kX, px);
                     copy_ahead<kY>(dst + kOffY + (c * kThreads + tid) * kY, py);
-                    if (a.add) copy_ahead<kX>(dst + kOffAdd + (c * kThreads + tid) * kX, pa);
+                }
+                if (a.add) {
+                    const X* pa = add_row(ahead);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c, pa += at.step)
+                        if (here(c)) copy_ahead<kX>(dst + kOffAdd + (c * kThreads + tid) * kX, pa);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            ahead += every;                               // (T + 5 * every < 2^31)
         }
     };
-    for (int d = 0; V > 1 && d < p.depth; ++d) fetch(t + d * every, d);
-    float m = t < a.T ? __ldg(a.mean + t) : 0.f, r = t < a.T ? __ldg(a.rstd + t) : 0.f;
+    for (int d = 0; V > 1 && d < p.depth; ++d) fetch(d);
+    float m = t < T ? __ldg(a.mean + t) : 0.f, r = t < T ? __ldg(a.rstd + t) : 0.f;
     F2 gamma[kPairs], sg[kPairs], sb[kPairs];
     load_channels<V>(a.gamma, at, a.H, 1.f, gamma);
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) sg[i] = sb[i] = 0;
     const float inv = 1.0f / (float)a.H;
     int turn = 0, s = 0;
-    for (; t < a.T; t += every, turn ^= 1) {
+    for (; t < T; t += every, turn ^= 1) {
         F2 x[kPairs], dy[kPairs];
         if constexpr (V > 1) {
             wait_ahead(p.depth);
@@ -362,9 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 F2 u[V / 2], v[V / 2];
+                if (!FULL)
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) { u[j] = pair(m, m); v[j] = 0; }
-                if (at.first + c * at.step < a.H) {
+                    for (int j = 0; j < V / 2; ++j) { u[j] = pair(m, m); v[j] = 0; }
+                if (here(c)) {
                     from_shared<X, V>(src + (c * kThreads + tid) * kX, u);
                     from_shared<Y, V>(src + kOffY + (c * kThreads + tid) * kY, v);
                 }
@@ -372,11 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                 for (int j = 0; j < V / 2; ++j) { x[c * (V / 2) + j] = u[j]; dy[c * (V / 2) + j] = v[j]; }
             }
         } else {
-            load_pairs<X, 1>(x_in + t * a.x_stride, at, a.H, x, m);
-            load_pairs<Y, 1>(dy_in + t * a.y_stride, at, a.H, dy, 0.f);
+            load_pairs<X>(x_row(t), at, a.H, x, m);
+            load_pairs<Y>(dy_row(t), at, a.H, dy, 0.f);
         }
         // (the next row's, early: their latency passes behind this one's sums)
-        const bool more = t + every < a.T;
+        const bool more = t + every < T;
         const float next_m = more ? __ldg(a.mean + t + every) : 0.f, next_r = more ? __ldg(a.rstd + t + every) : 0.f;
         const F2 minus = pair(-m, -m);
         F2 q0 = 0, q1 = 0, q2 = 0;
@@ -392,68 +406,87 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         // h = x r - d r, dx = g r - m1 r - h m2 r (+ add)
         const float d = q.z * inv, c1 = -q.x * inv * r, c2 = -(q.y - d * q.x) * r * inv * r;
         const F2 rr = pair(r, r), dd = pair(-d, -d), m1 = pair(c1, c1), m2 = pair(c2, c2);
-        F2 o[kPairs];
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < kPairs; ++i) {                // (from here on x holds dx)
             const F2 h = mul2(add2(x[i], dd), rr);
             sg[i] = fma2(dy[i], h, sg[i]);
             sb[i] = add2(sb[i], dy[i]);
-            o[i] = fma2(mul2(dy[i], gamma[i]), rr, fma2(h, m2, m1));
+            x[i] = fma2(mul2(dy[i], gamma[i]), rr, fma2(h, m2, m1));
         }
-        if (dx_out) {
+        if (a.dx) {
+            X* out = static_cast<X*>(a.dx) + (t * a.dx_stride + off);
             if constexpr (V > 1) {
-                X* out = dx_out + t * a.dx_stride + at.first;
+                if (a.add) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (here(c)) {
+                            F2 v[V / 2];
+                            from_shared<X, V>(ring + s * slot + kOffAdd + (c * kThreads + tid) * kX, v);
+#pragma unroll
+                            for (int j = 0; j < V / 2; ++j) x[c * (V / 2) + j] = add2(v[j], x[c * (V / 2) + j]);
+                        }
+                }
 #pragma unroll
                 for (int c = 0; c < NC; ++c, out += at.step) {
-                    if (at.first + c * at.step >= a.H) continue;
+                    if (!here(c)) continue;
                     F2 v[V / 2];
 #pragma unroll
-                    for (int j = 0; j < V / 2; ++j) v[j] = 0;
-                    if (a.add) from_shared<X, V>(ring + s * slot + kOffAdd + (c * kThreads + tid) * kX, v);
-#pragma unroll
-                    for (int j = 0; j < V / 2; ++j) v[j] = a.add ? add2(v[j], o[c * (V / 2) + j]) : o[c * (V / 2) + j];
+                    for (int j = 0; j < V / 2; ++j) v[j] = x[c * (V / 2) + j];
                     to_row<X, V>(out, v);
                 }
             } else {
-                X* out = dx_out + t * a.dx_stride;
                 if (a.add) {
                     F2 v[kPairs];
-                    load_pairs<X, 1>(add_in + t * a.add_stride, at, a.H, v, 0.f);
+                    load_pairs<X>(add_row(t), at, a.H, v, 0.f);
 #pragma unroll
-                    for (int i = 0; i < kPairs; ++i) o[i] = add2(o[i], v[i]);
+                    for (int i = 0; i < kPairs; ++i) x[i] = add2(x[i], v[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) {
-                    const float2 v = split(o[i]);
+                    const float2 v = split(x[i]);
                     const int e0 = at.first + 2 * i * at.step;
                     if (e0 < a.H) out[e0] = rounded<X>(v.x);
                     if (e0 + at.step < a.H) out[e0 + at.step] = rounded<X>(v.y);
                 }
             }
         }
-        fetch(t + p.depth * every, s);                    // (this thread has read its shares of the slot)
+        fetch(s);                                         // (this thread has read its shares of the slot)
         if (++s == p.depth) s = 0;
         m = next_m;
         r = next_r;
     }
     if constexpr (V > 1) asm volatile("cp.async.wait_all;" ::: "memory");
     if (!a.partial) return;
+    float* out = a.partial + (int64_t)blockIdx.x * 2 * a.H;
+    // this thread's sums to the vectors of gamma's and beta's
+    auto put = [&](float* g, float* b, int end) {
+        if constexpr (V > 1) {
+#pragma unroll
+            for (int i = 0; i < kPairs; i += 2) {
+                const int e = at.first + (2 * i / V) * at.step + 2 * i % V;
+                if (e >= end) continue;
+                *reinterpret_cast<ulonglong2*>(g + e) = make_ulonglong2(sg[i], sg[i + 1]);
+                *reinterpret_cast<ulonglong2*>(b + e) = make_ulonglong2(sb[i], sb[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const float2 u = split(sg[i]), v = split(sb[i]);
+                const int e0 = at.first + 2 * i * at.step, e1 = e0 + at.step;
+                if (e0 < end) { g[e0] = u.x; b[e0] = v.x; }
+                if (e1 < end) { g[e1] = u.y; b[e1] = v.y; }
+            }
+        }
+    };
+    if (groups == 1) {
+        if (!at.idle) put(out, out + a.H, a.H);
+        return;
+    }
     __syncthreads();                                      // (everyone has read its last rows)
     const int width = kChannels * 32 * p.warps;           // [gamma, beta][group][width]
-    if (!at.idle)
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            const float2 g = split(sg[i]), b = split(sb[i]);
-            const int e0 = V > 1 ? at.first + (2 * i / V) * at.step + 2 * i % V : at.first + 2 * i * at.step, e1 = V > 1 ? e0 + 1 : e0 + at.step;
-            float* to = shared + at.group * width;
-            to[e0] = g.x;
-            to[e1] = g.y;
-            to += groups * width;
-            to[e0] = b.x;
-            to[e1] = b.y;
-        }
+    if (!at.idle) put(shared + at.group * width, shared + (groups + at.group) * width, width);
     __syncthreads();
-    float* out = a.partial + (int64_t)blockIdx.x * 2 * a.H;
+#pragma unroll 4
     for (int i = tid; i < 2 * a.H; i += kThreads) {
         const int which = i >= a.H;
         const float* from = shared + which * groups * width + (i - which * a.H);
@@ -520,7 +553,7 @@ __global__ void __launch_bounds__(TPR) row_kernel(const __grid_constant__ LayerN
     const float d = q[0] / (float)a.H;
     float var = q[1] / (float)a.H - d * d;
     if (var < 0.f) var = 0.f;                            // (a NaN stays)
-    const float r = 1.0f / sqrtf(var + a.eps);
+    const float r = rsqrtf(var + a.eps);
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[t] = m + d;
         if (a.rstd) a.rstd[t] = r;
@@ -595,23 +628,25 @@ __global__ void __launch_bounds__(1024) wide_backward_kernel(const __grid_consta
 }
 
 // dgamma, dbeta: the sums of the partial rows, 32 channels a CTA (blockIdx.y: gamma or beta).
-__global__ void __launch_bounds__(512) sums_kernel(const float* partial, int rows, int H, float* dgamma, float* dbeta, bool accumulate) {
-    __shared__ float part[16][33];
+__global__ void __launch_bounds__(1024) sums_kernel(const float* partial, int rows, int H, float* dgamma, float* dbeta, bool accumulate) {
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, h = blockIdx.x * 32 + lane;
     float* out = blockIdx.y ? dbeta : dgamma;
     wait_for_previous();
     allow_next();
     if (!out) return;
     float v = 0.f;
-    if (h < H)
-#pragma unroll 4
-        for (int i = w; i < rows; i += 16) v += partial[((int64_t)2 * i + blockIdx.y) * H + h];
+    if (h < H) {
+        const float* from = partial + (int64_t)blockIdx.y * H + h;
+#pragma unroll 5
+        for (int i = w; i < rows; i += 32) v += from[(int64_t)2 * i * H];
+    }
     part[w][lane] = v;
     __syncthreads();
     if (w == 0 && h < H) {
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v += part[i][lane];
+        for (int i = 0; i < 32; ++i) v += part[i][lane];
         out[h] = accumulate ? out[h] + v : v;
     }
 }
@@ -632,10 +667,12 @@ bool all_aligned(const LayerNormArgs& a, int v) {
 
 template <typename X, typename Y, int V>
 cudaError_t launch_typed(const LayerNormArgs& a, bool backward, int grid, cudaStream_t s) {
-    static std::atomic<uint64_t> ready[2];
+    static std::atomic<uint64_t> ready[4];
+    const bool full = V > 1 && a.H % (32 * kChannels) == 0;
     int sms = 0;
-    const void* fn = backward ? (const void*)backward_kernel<X, Y, V> : (const void*)forward_kernel<X, Y, V>;
-    cudaError_t err = prepare_kernel(fn, kMostShared, ready[backward], &sms);
+    const void* fn = backward ? (full ? (const void*)backward_kernel<X, Y, V, V != 1> : (const void*)backward_kernel<X, Y, V, false>)
+                              : (full ? (const void*)forward_kernel<X, Y, V, V != 1> : (const void*)forward_kernel<X, Y, V, false>);
+    cudaError_t err = prepare_kernel(fn, kMostShared, ready[2 * full + backward], &sms);
     if (err != cudaSuccess) return err;
     NormParams p{a, (a.H + 32 * kChannels - 1) / (32 * kChannels), 2};
     const int slot = kThreads * kChannels * (int)(backward ? sizeof(X) + sizeof(Y) + (a.add ? sizeof(X) : 0) : sizeof(X));
@@ -708,7 +745,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, cudaStream_t s) {
     float *dgamma = a.dgamma, *dbeta = a.dbeta;
     bool accumulate = a.accumulate;
     void* args[] = {&partial, &grid, &H, &dgamma, &dbeta, &accumulate};
-    return launch_early((const void*)sums_kernel, dim3((H + 31) / 32, 2), 512, 0, s, args);
+    return launch_early((const void*)sums_kernel, dim3((H + 31) / 32, 2), 1024, 0, s, args);
 }
 
 }  // namespace moe
