@@ -5,12 +5,13 @@
 //   d loss / d l_te = coef / (B' n_b) p_te (f_be - sum_j f_bj p_tj)   [sigmoid: times 1 - sigmoid(l_te)]
 // Bound: bytes, the logits once and their gradient once.  The gradient needs f, which comes from the ids alone, and not P:
 // so the ids are counted first (count_kernel), one pass over the logits then gives the gradient and the partial
-// sums of p (pass_kernel), and those are added up (finish_kernel).
+// sums of p (pass_kernel), and those are added up (finish_kernel).  A few tokens take one CTA that does all three (small_kernel).
 // The tokens are cut into even chunks, one for a CTA, whatever the sequences' lengths.  Chunk c of the tokens and sequence b
 // that have tokens in common own row c + b of the partial sums: both only grow along the tokens, so no
-// two such pairs share a row, and C chunks and B sequences need C + B rows.  Every sum has one order: no atomics, the same
-// bits each time.
+// two such pairs share a row, and C chunks and B sequences need C + B rows.  Every sum has one order: the same bits each time
+// (the only atomics are on whole numbers).
 // f - 1 = (E c - k n) / (k n) takes the place of f in the gradient (the p sum to 1): nothing cancels where the load is balanced.
+// No 64-bit floating point: its rate is a 64th of fp32's, and a handful of divisions took longer than the rest of a small call.
 #include <algorithm>
 
 #include "block_ops.cuh"
@@ -20,8 +21,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMostChunks = 1024;
+constexpr int kMostChunks = 1024, kMostCounts = 128;
 constexpr float kInf = __builtin_huge_valf();
+constexpr unsigned kAll = 0xffffffffu;
 
 struct BalanceParams {
     BalanceArgs a;
@@ -30,7 +32,7 @@ struct BalanceParams {
     int row;                     // entries of a row of counts: E, the counted tokens, padding
     int32_t* counts;             // [chunks1 + n_seqs][row]
     float* sums;                 // [chunks2 + n_seqs][E]
-    double* losses;              // [n_seqs][blocks of 32 experts]
+    float* losses;               // [n_seqs][blocks of 32 experts]
     uint32_t* ticket;
 };
 
@@ -48,39 +50,37 @@ __device__ __forceinline__ int sequence_at(const BalanceArgs& a, int t) {
     }
     return lo;
 }
-// Calls f(chunk's row of the partial sums) for every chunk of `len` tokens that has tokens of sequence b.
-template <typename F>
-__device__ __forceinline__ void rows_of(const BalanceArgs& a, int b, int len, F f) {
-    const int t0 = start_of(a, b), t1 = start_of(a, b + 1);
-    if (t1 <= t0) return;
-    for (int c = t0 / len; c <= (t1 - 1) / len; ++c) f(c + b);
-}
-// Counted tokens of sequence b.
+// Counted tokens of sequence b (a whole warp asks).
 __device__ __forceinline__ int tokens_of(const BalanceParams& p, int b) {
-    if (!p.a.mask) return max(start_of(p.a, b + 1) - start_of(p.a, b), 0);
+    const int t0 = start_of(p.a, b), t1 = start_of(p.a, b + 1);
+    if (!p.a.mask || t1 <= t0) return max(t1 - t0, 0);
     int n = 0;
-    rows_of(p.a, b, p.len1, [&](int r) { n += p.counts[(int64_t)r * p.row + p.a.E]; });
-    return n;
+    for (int c = t0 / p.len1 + (threadIdx.x & 31); c <= (t1 - 1) / p.len1; c += 32) n += p.counts[(int64_t)(c + b) * p.row + p.a.E];
+    return __reduce_add_sync(kAll, n);
 }
-// Sequences with a counted token (every thread of the CTA calls it).
-__device__ __forceinline__ int used_sequences(const BalanceParams& p) {
-    int n = 0;
-    for (int b0 = 0; b0 < p.a.n_seqs; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        n += __syncthreads_count(b < p.a.n_seqs && tokens_of(p, b) > 0);
+// Sequences with a counted token (the whole CTA asks).  word: shared.
+__device__ __forceinline__ int used_sequences(const BalanceParams& p, int* word) {
+    if (p.a.n_seqs == 1) return tokens_of(p, 0) > 0;
+    if (threadIdx.x == 0) *word = 0;
+    __syncthreads();
+    if (!p.a.mask) {
+        for (int b = threadIdx.x; b < p.a.n_seqs; b += kThreads)
+            if (start_of(p.a, b + 1) > start_of(p.a, b)) atomicAdd(word, 1);
+    } else {
+        for (int b = threadIdx.x >> 5; b < p.a.n_seqs; b += kWarps)
+            if (tokens_of(p, b) > 0 && (threadIdx.x & 31) == 0) atomicAdd(word, 1);
     }
-    return n;
+    __syncthreads();
+    return *word;
 }
 
 // ---------------------------------------------------------------- counts
-__global__ void __launch_bounds__(kThreads) count_kernel(const __grid_constant__ BalanceParams p) {
-    extern __shared__ int hist[];                        // [E + 1]
+// The pairs of chunk c by sequence and expert.  hist: shared, [E + 1].
+__device__ __forceinline__ void count_chunk(const BalanceParams& p, int c, int* hist) {
     const BalanceArgs& a = p.a;
-    const int tid = threadIdx.x;
-    wait_for_previous();
-    allow_next();
+    const int tid = threadIdx.x, t0 = c * p.len1, t1 = min(t0 + p.len1, a.T);
     bool bad = false;
-    if (blockIdx.x == 0) {
+    if (c == 0) {
         if (tid == 0) *p.ticket = 0;
         if (a.seq_offsets)
             for (int b = tid; b <= a.n_seqs; b += kThreads) {
@@ -88,7 +88,6 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const __grid_constant__
                 bad |= o < 0 || o > a.T || (b > 0 && __ldg(a.seq_offsets + b - 1) > o);
             }
     }
-    const int c = blockIdx.x, t0 = c * p.len1, t1 = min(t0 + p.len1, a.T);
     for (int b = sequence_at(a, t0); b < a.n_seqs; ++b) {
         const int s0 = max(start_of(a, b), t0), s1 = min(start_of(a, b + 1), t1);
         if (start_of(a, b) >= t1) break;
@@ -98,8 +97,9 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const __grid_constant__
         if (a.mask)
             for (int t = s0 + tid; t < s1; t += kThreads)
                 if (a.mask[t]) atomicAdd(&hist[a.E], 1);
-        for (int64_t i = (int64_t)s0 * a.k + tid; i < (int64_t)s1 * a.k; i += kThreads) {
-            if (a.mask && !a.mask[i / a.k]) continue;
+#pragma unroll 4
+        for (int i = s0 * a.k + tid; i < s1 * a.k; i += kThreads) {      // (T k <= 2^30)
+            if (a.mask && !a.mask[(unsigned)i / (unsigned)a.k]) continue;
             const int e = __ldg(a.ids + i);
             if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
             else bad = true;
@@ -111,48 +111,59 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const __grid_constant__
     }
     if (bad && a.status) atomicCAS(a.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
 }
+__global__ void __launch_bounds__(kThreads) count_kernel(const __grid_constant__ BalanceParams p) {
+    extern __shared__ int hist[];
+    wait_for_previous();
+    allow_next();
+    count_chunk(p, blockIdx.x, hist);
+}
 
 // ---------------------------------------------------------------- the pass over the logits
-// A warp takes TOK tokens at a time; lane l holds experts (32 i + l) V + j of each, EPL in all.
-template <int EPL, int V, int TOK>
-__global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ BalanceParams p) {
-    extern __shared__ float fsm[];                       // [E] f - 1, then [warps][E] sums
+__device__ __forceinline__ float exp2_quick(float x) {    // relative error 2^-22; results below 2^-126 are 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Chunk c of the tokens.  A warp takes TOK tokens at a time; lane l holds experts (32 i + l) V + j of each, EPL in all.
+// fsm: shared, [E] f - 1, then [warps][E] sums; word: shared.
+template <int EPL, int V, int TOK, bool SIGMOID>
+__device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float* fsm, int* word) {
     constexpr int NC = EPL / V;
+    constexpr float kLog2e = 1.4426950408889634f;
     const BalanceArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto expert = [&](int i) { return (i * 32 + lane) * V; };
-    wait_for_previous();
-    allow_next();
-    const int used = a.dlogits ? used_sequences(p) : 0;
-    const float up = a.upstream ? __ldg(a.upstream) : 1.0f;
-    const int c = blockIdx.x, t0 = c * p.len2, t1 = min(t0 + p.len2, a.T);
+    const int used = a.dlogits ? used_sequences(p, word) : 0;
+    const float up = a.coef * (a.upstream ? __ldg(a.upstream) : 1.0f);
+    const int t0 = c * p.len2, t1 = min(t0 + p.len2, a.T);
     // gradient of the tokens that no sequence has
     auto clear = [&](int g0, int g1) {
         if (!a.dlogits || a.accumulate) return;
-        for (int64_t i = tid; i < (int64_t)(g1 - g0) * a.E; i += kThreads)
-            a.dlogits[(g0 + i / a.E) * a.dstride + i % a.E] = 0.f;
+        for (int t = g0 + warp; t < g1; t += kWarps)
+            for (int e = lane; e < a.E; e += 32) a.dlogits[t * a.dstride + e] = 0.f;
     };
     clear(t0, min(start_of(a, 0), t1));
     clear(max(start_of(a, a.n_seqs), t0), t1);
     for (int b = sequence_at(a, t0); b < a.n_seqs; ++b) {
-        const int s0 = max(start_of(a, b), t0), s1 = min(start_of(a, b + 1), t1);
-        if (start_of(a, b) >= t1) break;
+        const int b0 = start_of(a, b), b1 = start_of(a, b + 1), s0 = max(b0, t0), s1 = min(b1, t1);
+        if (b0 >= t1) break;
         if (s1 <= s0) continue;
         const int n = tokens_of(p, b);
-        const int64_t kn = (int64_t)a.k * n;
         if (a.dlogits) {
             int* cnt = reinterpret_cast<int*>(fsm);
             for (int e = tid; e < a.E; e += kThreads) cnt[e] = 0;
             __syncthreads();
-            const int first = start_of(a, b) / p.len1, rows = (start_of(a, b + 1) - 1) / p.len1 - first + 1;
+            const int first = b0 / p.len1, rows = (b1 - 1) / p.len1 - first + 1;
+#pragma unroll 2
             for (int i = warp; i < rows; i += kWarps)
                 for (int e = lane; e < a.E; e += 32) atomicAdd(&cnt[e], p.counts[(int64_t)(first + i + b) * p.row + e]);
             __syncthreads();
-            for (int e = tid; e < a.E; e += kThreads)
-                fsm[e] = n > 0 ? (float)((double)((int64_t)a.E * cnt[e] - kn) / (double)kn) : 0.f;
+            const int64_t kn = (int64_t)a.k * n;
+            const float inv = n > 0 ? 1.0f / (float)kn : 0.f;
+            for (int e = tid; e < a.E; e += kThreads) fsm[e] = (float)((int64_t)a.E * cnt[e] - kn) * inv;
             __syncthreads();
         }
-        const float scale = n > 0 && used > 0 ? (float)((double)a.coef * up / ((double)used * n)) : 0.f;
+        const float scale = n > 0 && used > 0 ? up / ((float)used * (float)n) : 0.f;
         float acc[NC][V], f[NC][V];
 #pragma unroll
         for (int i = 0; i < NC; ++i)
@@ -162,22 +173,19 @@ __global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ 
                 f[i][j] = a.dlogits && expert(i) + j < a.E ? fsm[expert(i) + j] : 0.f;
             }
         for (int tw = s0 + warp * TOK; tw < s1; tw += kWarps * TOK) {
-            float l[TOK][NC][V], q[TOK][NC][V];
+            float l[TOK][NC][V], q[TOK][NC][V], m[TOK], sum[TOK], dot[TOK];
             bool live[TOK];
 #pragma unroll
             for (int o = 0; o < TOK; ++o) {
                 const int t = tw + o;
                 live[o] = t < s1 && (!a.mask || a.mask[t]);
+                const float* row = a.logits + t * a.stride;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) l[o][i][j] = -kInf;
-                    if (live[o] && expert(i) < a.E) load_once<V>(a.logits, MOE_F32, t * a.stride + expert(i), l[o][i]);
+                    if (live[o] && expert(i) < a.E) load_once<V>(row, MOE_F32, expert(i), l[o][i]);
                 }
-            }
-            float m[TOK], sum[TOK], dot[TOK];
-#pragma unroll
-            for (int o = 0; o < TOK; ++o) {
                 m[o] = -kInf;
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
@@ -187,58 +195,61 @@ __global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ 
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
-                for (int o = 0; o < TOK; ++o) m[o] = fmaxf(m[o], __shfl_xor_sync(0xffffffffu, m[o], s));
-            // q: p before its division, relative to the largest of them so that nothing underflows as a whole; a logit
-            // of -inf has p = 0, a token of nothing else no p at all
+                for (int o = 0; o < TOK; ++o) m[o] = fmaxf(m[o], __shfl_xor_sync(kAll, m[o], s));
+            // q: p before its division, relative to the largest of them so that nothing underflows as a whole, and 2^32 times too
+            // large so that none is lost that is not lost in p.  A logit of -inf has p = 0, a token of nothing else no p at all.
 #pragma unroll
             for (int o = 0; o < TOK; ++o) {
                 sum[o] = dot[o] = 0.f;
+                const float top = SIGMOID ? fminf(m[o], 0.f) : m[o], away = top == -kInf ? 0.f : top;
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float v = l[o][i][j];
-                        if (a.sigmoid) {
-                            const float z = expf(-fabsf(v)), one = 1.0f / (1.0f + z);
-                            q[o][i][j] = v == -kInf ? 0.f : v > 0.f ? one : (m[o] < 0.f ? expf(v - m[o]) : z) * one;
-                            l[o][i][j] = v > 0.f ? z * one : one;        // 1 - sigmoid
-                        } else {
-                            q[o][i][j] = v == -kInf ? 0.f : expf(v - m[o]);
+                        float e = exp2_quick(fmaf(kLog2e, (SIGMOID ? fminf(v, 0.f) : v) - away, 32.0f));
+                        if constexpr (SIGMOID) {
+                            // sigmoid = e^min(v, 0) / (1 + e^-|v|), 1 - sigmoid = e^-max(v, 0) / (1 + e^-|v|)
+                            const float z = __expf(-fabsf(v)), one = __fdividef(1.0f, 1.0f + z);
+                            e *= one;
+                            l[o][i][j] = v > 0.f ? z * one : one;
                         }
-                        sum[o] += q[o][i][j];
-                        dot[o] = fmaf(q[o][i][j], f[i][j], dot[o]);
+                        q[o][i][j] = e;
+                        sum[o] += e;
+                        dot[o] = fmaf(e, f[i][j], dot[o]);
                     }
             }
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
                 for (int o = 0; o < TOK; ++o) {
-                    sum[o] += __shfl_xor_sync(0xffffffffu, sum[o], s);
-                    dot[o] += __shfl_xor_sync(0xffffffffu, dot[o], s);
+                    sum[o] += __shfl_xor_sync(kAll, sum[o], s);
+                    dot[o] += __shfl_xor_sync(kAll, dot[o], s);
                 }
 #pragma unroll
             for (int o = 0; o < TOK; ++o) {
                 const int t = tw + o;
                 const float inv = sum[o] == 0.f ? 0.f : 1.0f / sum[o];
                 dot[o] *= inv;
+                float* row = a.dlogits + t * a.dstride;
+                const bool write = a.dlogits && t < s1 && (live[o] || !a.accumulate);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        q[o][i][j] *= inv;
-                        acc[i][j] += q[o][i][j];         // (0 unless live)
-                        q[o][i][j] *= scale * (f[i][j] - dot[o]);
-                        if (a.sigmoid) q[o][i][j] *= l[o][i][j];
+                        const float prob = q[o][i][j] * inv;
+                        acc[i][j] += prob;               // (0 unless live)
+                        q[o][i][j] = prob * (scale * (f[i][j] - dot[o]));
+                        if (SIGMOID) q[o][i][j] *= l[o][i][j];
                     }
-                    if (!a.dlogits || t >= s1 || expert(i) >= a.E) continue;
+                    if (!write || expert(i) >= a.E) continue;
                     if (a.accumulate) {
-                        if (!live[o]) continue;
                         float old[V];
-                        load_once<V>(a.dlogits, MOE_F32, t * a.dstride + expert(i), old);
+                        load_once<V>(row, MOE_F32, expert(i), old);
 #pragma unroll
                         for (int j = 0; j < V; ++j) q[o][i][j] += old[j];
                     }
-                    store_row<V>(a.dlogits, MOE_F32, t * a.dstride + expert(i), q[o][i]);
+                    store_row<V>(row, MOE_F32, expert(i), q[o][i]);
                 }
             }
         }
@@ -261,43 +272,60 @@ __global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ 
         __syncthreads();                                 // (fsm and the sums of the next sequence)
     }
 }
+template <int EPL, int V, int TOK, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ BalanceParams p) {
+    extern __shared__ float fsm[];
+    __shared__ int word;
+    wait_for_previous();
+    allow_next();
+    pass_chunk<EPL, V, TOK, SIGMOID>(p, blockIdx.x, fsm, &word);
+}
 
 // ---------------------------------------------------------------- counts and loss of each sequence
-// The sum of a double over the CTA's threads, in one order (thread 0 has it).
-__device__ __forceinline__ double cta_sum(double v, double* part) {
+// The sum over the CTA's threads, in one order (thread 0 has it).
+__device__ __forceinline__ float cta_sum(float v, float* part) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
+    v = 0.f;
     if (threadIdx.x == 0)
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) v += part[w];
     return v;
+}
+// What expert e's count and sum of p add to a sequence's loss (f P), n counted tokens.
+__device__ __forceinline__ float share_of(const BalanceArgs& a, int count, float sum, int n) {
+    const float inv = 1.0f / (float)n;
+    return ((float)count * (float)a.E / (float)a.k * inv) * (sum * inv);
 }
 // A CTA adds 32 experts' (blockIdx.x) partial rows of a sequence (blockIdx.y), the rows dealt to its warps.
 __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int cnt[kWarps][32];
     __shared__ float sum[kWarps][32];
-    __shared__ double part[kWarps];
+    __shared__ float part[kWarps];
+    __shared__ int word;
     __shared__ bool last;
     const BalanceArgs& a = p.a;
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x * 32 + lane;
     wait_for_previous();
     allow_next();
-    const int n = tokens_of(p, b), t0 = start_of(a, b), t1 = start_of(a, b + 1);
+    const int t0 = start_of(a, b), t1 = start_of(a, b + 1);
     int c = 0;
     float s = 0.f;
     if (e < a.E && t1 > t0) {
-        for (int i = t0 / p.len1 + warp; i <= (t1 - 1) / p.len1; i += kWarps) c += p.counts[(int64_t)(i + b) * p.row + e];
         if (a.loss) {
-#pragma unroll 4
+#pragma unroll 8
             for (int i = t0 / p.len2 + warp; i <= (t1 - 1) / p.len2; i += kWarps) s += p.sums[(int64_t)(i + b) * a.E + e];
         }
+#pragma unroll 4
+        for (int i = t0 / p.len1 + warp; i <= (t1 - 1) / p.len1; i += kWarps) c += p.counts[(int64_t)(i + b) * p.row + e];
     }
+    const int n = tokens_of(p, b);
     cnt[warp][lane] = c;
     sum[warp][lane] = s;
     __syncthreads();
-    double v = 0.0;
+    float v = 0.f;
     if (warp == 0 && e < a.E) {
         c = 0;
         s = 0.f;
@@ -307,30 +335,63 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
             s += sum[w][lane];
         }
         if (a.counts) a.counts[(int64_t)b * a.E + e] = c;
-        if (n > 0) v = (double)c * (double)s * a.E / ((double)a.k * n * n);
+        if (n > 0) v = share_of(a, c, s, n);
     }
     if (!a.loss) return;
-    v = cta_sum(v, part);
-    if (tid == 0) {
-        p.losses[(int64_t)b * gridDim.x + blockIdx.x] = v;
-        __threadfence();
-        last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    if (warp == 0) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+        if (lane == 0) {
+            p.losses[(int64_t)b * gridDim.x + blockIdx.x] = v;
+            __threadfence();
+            last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
+        }
     }
     __syncthreads();
     if (!last) return;
     __threadfence();
-    const int used = used_sequences(p);
-    v = 0.0;
+    const int used = used_sequences(p, &word);
+    v = 0.f;
     for (int64_t i = tid; i < (int64_t)gridDim.x * gridDim.y; i += kThreads) v += __ldcg(p.losses + i);
     v = cta_sum(v, part);
-    if (tid == 0) *a.loss = used > 0 ? (float)(v * (double)a.coef / used) : 0.f;
+    if (tid == 0) *a.loss = used > 0 ? v * a.coef / (float)used : 0.f;
+}
+
+// ---------------------------------------------------------------- a few tokens: one CTA, one launch
+// (one chunk, so that a sequence has one row of counts and of sums)
+template <int EPL, int V, int TOK, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ BalanceParams p) {
+    extern __shared__ float fsm[];
+    __shared__ float part[kWarps];
+    __shared__ int word;
+    const BalanceArgs& a = p.a;
+    wait_for_previous();
+    allow_next();
+    count_chunk(p, 0, reinterpret_cast<int*>(fsm));
+    __syncthreads();
+    if (a.loss || a.dlogits) pass_chunk<EPL, V, TOK, SIGMOID>(p, 0, fsm, &word);
+    __syncthreads();
+    float v = 0.f;
+    for (int b = threadIdx.x >> 5; b < a.n_seqs; b += kWarps) {
+        const bool some = start_of(a, b + 1) > start_of(a, b);
+        const int n = tokens_of(p, b);
+        for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+            const int c = some ? p.counts[(int64_t)b * p.row + e] : 0;
+            if (a.counts) a.counts[(int64_t)b * a.E + e] = c;
+            if (a.loss && n > 0) v += share_of(a, c, p.sums[(int64_t)b * a.E + e], n);
+        }
+    }
+    if (!a.loss) return;
+    const int used = used_sequences(p, &word);
+    v = cta_sum(v, part);
+    if (threadIdx.x == 0) *a.loss = used > 0 ? v * a.coef / (float)used : 0.f;
 }
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-// Chunks of the counts: enough that a CTA has a few thousand pairs, few enough that their rows are quickly added.
+// Chunks of the counts: about a thousand pairs each, and few enough that their rows are quickly added.
 int count_chunks(int k, int T, int n_seqs) {
-    const int64_t want = std::max<int64_t>((int64_t)T * k / 4096, n_seqs / 4);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, T), 128));
+    const int64_t want = std::max<int64_t>((int64_t)T * k / 1024, n_seqs / 4);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, T), kMostCounts));
 }
 struct Layout {
     size_t counts, sums, losses, total;
@@ -342,25 +403,40 @@ Layout layout(int E, int n_seqs, int chunks1, int chunks2) {
     l.counts = 256;
     l.sums = align_up(l.counts + (size_t)(chunks1 + n_seqs) * l.row * 4, 256);
     l.losses = align_up(l.sums + (size_t)(chunks2 + n_seqs) * E * 4, 256);
-    l.total = align_up(l.losses + (size_t)n_seqs * ((E + 31) / 32) * 8, 256);
+    l.total = align_up(l.losses + (size_t)n_seqs * ((E + 31) / 32) * 4, 256);
     return l;
 }
 
-template <int EPL, int V, int TOK>
-cudaError_t launch_pass(const BalanceParams& p, cudaStream_t s) {
-    static std::atomic<uint64_t> ready;
+template <int EPL, int V, int TOK, bool SIGMOID>
+cudaError_t launch_pass(const BalanceParams& p, bool small, cudaStream_t s) {
+    static std::atomic<uint64_t> ready[2];
     int sms = 0;
-    const void* fn = (const void*)pass_kernel<EPL, V, TOK>;
-    const int most = 32 * EPL * (1 + kWarps) * 4;
-    cudaError_t err = prepare_kernel(fn, most, ready, &sms);
+    const void* fn = small ? (const void*)small_kernel<EPL, V, TOK, SIGMOID> : (const void*)pass_kernel<EPL, V, TOK, SIGMOID>;
+    cudaError_t err = prepare_kernel(fn, 32 * EPL * (1 + kWarps) * 4 + 16, ready[small], &sms);
     if (err != cudaSuccess) return err;
     void* args[] = {const_cast<BalanceParams*>(&p)};
-    return launch_early(fn, dim3(p.chunks2), kThreads, (size_t)p.a.E * (1 + kWarps) * 4, s, args);
+    return launch_early(fn, dim3(p.chunks2), kThreads, (size_t)p.a.E * (1 + kWarps) * 4 + 16, s, args);
+}
+template <bool SIGMOID>
+cudaError_t launch_pass_of(const BalanceParams& p, bool small, cudaStream_t s) {
+    const BalanceArgs& a = p.a;
+    const bool vec = a.E % 4 == 0 && (uintptr_t)a.logits % 16 == 0 && a.stride % 4 == 0 &&
+                     (!a.dlogits || ((uintptr_t)a.dlogits % 16 == 0 && a.dstride % 4 == 0));
+    if (vec)
+        return a.E <= 128   ? launch_pass<4, 4, 2, SIGMOID>(p, small, s)
+               : a.E <= 256 ? launch_pass<8, 4, 2, SIGMOID>(p, small, s)
+               : a.E <= 512 ? launch_pass<16, 4, 1, SIGMOID>(p, small, s)
+                            : launch_pass<32, 4, 1, SIGMOID>(p, small, s);
+    return a.E <= 32    ? launch_pass<1, 1, 4, SIGMOID>(p, small, s)
+           : a.E <= 128 ? launch_pass<4, 1, 2, SIGMOID>(p, small, s)
+           : a.E <= 256 ? launch_pass<8, 1, 2, SIGMOID>(p, small, s)
+           : a.E <= 512 ? launch_pass<16, 1, 1, SIGMOID>(p, small, s)
+                        : launch_pass<32, 1, 1, SIGMOID>(p, small, s);
 }
 
 }  // namespace
 
-size_t balance_ws_bytes(int E, int T, int n_seqs) { return layout(E, n_seqs, 128, std::min(T, kMostChunks)).total; }
+size_t balance_ws_bytes(int E, int T, int n_seqs) { return layout(E, n_seqs, kMostCounts, std::min(T, kMostChunks)).total; }
 
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
     static std::atomic<uint64_t> ready;
@@ -369,34 +445,24 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     BalanceParams p{};
     p.a = a;
-    p.len1 = std::max(1, ceil_div(a.T, count_chunks(a.k, a.T, a.n_seqs)));
+    const bool small = a.T <= 64;                        // (a chunk of 16 warps, 4 tokens each at most)
+    p.len1 = small ? std::max(a.T, 1) : ceil_div(a.T, count_chunks(a.k, a.T, a.n_seqs));
     p.chunks1 = std::max(1, ceil_div(a.T, p.len1));
-    p.len2 = std::max(kWarps, ceil_div(a.T, std::min(2 * sms, kMostChunks)));
-    p.chunks2 = ceil_div(a.T, p.len2);
+    p.len2 = small ? std::max(a.T, 1) : std::max(kWarps, ceil_div(a.T, std::min(2 * sms, kMostChunks)));
+    p.chunks2 = std::max(1, ceil_div(a.T, p.len2));
     const Layout l = layout(a.E, a.n_seqs, p.chunks1, p.chunks2);
     char* ws = static_cast<char*>(a.ws);
     p.row = l.row;
     p.ticket = reinterpret_cast<uint32_t*>(ws);
     p.counts = reinterpret_cast<int32_t*>(ws + l.counts);
     p.sums = reinterpret_cast<float*>(ws + l.sums);
-    p.losses = reinterpret_cast<double*>(ws + l.losses);
+    p.losses = reinterpret_cast<float*>(ws + l.losses);
+    if (small) return a.sigmoid ? launch_pass_of<true>(p, true, s) : launch_pass_of<false>(p, true, s);
     void* args[] = {&p};
     err = launch_early((const void*)count_kernel, dim3(p.chunks1), kThreads, (size_t)(a.E + 1) * 4, s, args);
     if (err != cudaSuccess) return err;
-    if (a.T > 0 && (a.loss || a.dlogits)) {
-        const bool vec = a.E % 4 == 0 && (uintptr_t)a.logits % 16 == 0 && a.stride % 4 == 0 &&
-                         (!a.dlogits || ((uintptr_t)a.dlogits % 16 == 0 && a.dstride % 4 == 0));
-        if (vec)
-            err = a.E <= 128   ? launch_pass<4, 4, 4>(p, s)
-                  : a.E <= 256 ? launch_pass<8, 4, 2>(p, s)
-                  : a.E <= 512 ? launch_pass<16, 4, 1>(p, s)
-                               : launch_pass<32, 4, 1>(p, s);
-        else
-            err = a.E <= 32    ? launch_pass<1, 1, 4>(p, s)
-                  : a.E <= 128 ? launch_pass<4, 1, 4>(p, s)
-                  : a.E <= 256 ? launch_pass<8, 1, 2>(p, s)
-                  : a.E <= 512 ? launch_pass<16, 1, 1>(p, s)
-                               : launch_pass<32, 1, 1>(p, s);
+    if (a.loss || a.dlogits) {
+        err = a.sigmoid ? launch_pass_of<true>(p, false, s) : launch_pass_of<false>(p, false, s);
         if (err != cudaSuccess) return err;
     }
     if (!a.loss && !a.counts) return cudaSuccess;
