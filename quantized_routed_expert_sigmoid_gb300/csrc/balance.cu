@@ -3,11 +3,12 @@
 //   f_be = E c_be / (k n_b)  (c_be: its tokens' pairs that name expert e),  P_be = sum_t p_te / n_b
 //   loss = coef / B' sum_b sum_e f_be P_be   (B': sequences with a counted token)
 //   d loss / d l_te = coef / (B' n_b) p_te (f_be - sum_j f_bj p_tj)   [sigmoid: times 1 - sigmoid(l_te)]
-// Bound: bytes, the logits once and their gradient once.  The gradient needs f, which comes from the ids alone, and not P:
-// so the ids are counted first (count_kernel), one pass over the logits then gives the gradient and the partial
-// sums of p (pass_kernel), and those are added up (finish_kernel).  A few tokens take one CTA that does all three (small_kernel).
+// Bound: bytes, the logits once and their gradient once.  The gradient needs f, which comes from the ids alone, and so does
+// a token's share of the loss, coef / (B' n_b) sum_e f_be p_te, which the gradient needs as well: no sums of p by expert.
+// So the ids are counted first (count_kernel), and one pass over the logits gives gradient and loss (pass_kernel; the CTA
+// that ends last adds the others' shares of the loss).  A few tokens take one CTA that does both (small_kernel).
 // The tokens are cut into even chunks, one for a CTA, whatever the sequences' lengths.  Chunk c of the tokens and sequence b
-// that have tokens in common own row c + b of the partial sums: both only grow along the tokens, so no
+// that have tokens in common own row c + b of the partial counts: both only grow along the tokens, so no
 // two such pairs share a row, and C chunks and B sequences need C + B rows.  Every sum has one order: the same bits each time
 // (the only atomics are on whole numbers).
 // f - 1 = (E c - k n) / (k n) takes the place of f in the gradient (the p sum to 1): nothing cancels where the load is balanced.
@@ -31,8 +32,7 @@ struct BalanceParams {
     int chunks2, len2;           // pass_kernel
     int row;                     // entries of a row of counts: E, the counted tokens, padding
     int32_t* counts;             // [chunks1 + n_seqs][row]
-    float* sums;                 // [chunks2 + n_seqs][E]
-    float* losses;               // [n_seqs][blocks of 32 experts]
+    float* losses;               // [chunks2] shares of the loss
     uint32_t* ticket;
 };
 
@@ -124,19 +124,33 @@ __device__ __forceinline__ float exp2_quick(float x) {    // relative error 2^-2
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Chunk c of the tokens.  A warp takes TOK tokens at a time; lane l holds experts (32 i + l) V + j of each, EPL in all.
-// fsm: shared, [E] f - 1, then [warps][E] sums; word: shared.
+// The sum over the CTA's threads, in one order (thread 0 has it).
+__device__ __forceinline__ float cta_sum(float v, float* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    if (threadIdx.x == 0)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += part[w];
+    return v;
+}
+// Chunk c of the tokens; the chunk's share of the loss (thread 0 has it).  A warp takes TOK tokens at a time; lane l holds
+// experts (32 i + l) V + j of each, EPL in all.  fsm: shared, [E]; part: shared; word: shared.
 template <int EPL, int V, int TOK, bool SIGMOID>
-__device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float* fsm, int* word) {
+__device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float* fsm, float* part, int* word) {
     constexpr int NC = EPL / V;
-    constexpr float kLog2e = 1.4426950408889634f;
+    constexpr float kLog2e = 1.4426950408889634f, kBack = 2.3283064365386963e-10f;      // 2^-32
     const BalanceArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto expert = [&](int i) { return (i * 32 + lane) * V; };
-    const int used = a.dlogits ? used_sequences(p, word) : 0;
-    const float up = a.coef * (a.upstream ? __ldg(a.upstream) : 1.0f);
+    const bool logits = a.loss || a.dlogits;
+    const int used = logits ? used_sequences(p, word) : 0;
+    const float up = a.upstream ? __ldg(a.upstream) : 1.0f;
     const int t0 = c * p.len2, t1 = min(t0 + p.len2, a.T);
-    // gradient of the tokens that no sequence has
+    float loss = 0.f;
+    // gradient of the tokens that no sequence has, counts of the sequences without a token
     auto clear = [&](int g0, int g1) {
         if (!a.dlogits || a.accumulate) return;
         for (int t = g0 + warp; t < g1; t += kWarps)
@@ -144,35 +158,38 @@ __device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float*
     };
     clear(t0, min(start_of(a, 0), t1));
     clear(max(start_of(a, a.n_seqs), t0), t1);
+    if (a.counts)
+        for (int b = c; b < a.n_seqs; b += p.chunks2)
+            if (start_of(a, b + 1) <= start_of(a, b))
+                for (int e = tid; e < a.E; e += kThreads) a.counts[(int64_t)b * a.E + e] = 0;
     for (int b = sequence_at(a, t0); b < a.n_seqs; ++b) {
         const int b0 = start_of(a, b), b1 = start_of(a, b + 1), s0 = max(b0, t0), s1 = min(b1, t1);
         if (b0 >= t1) break;
         if (s1 <= s0) continue;
-        const int n = tokens_of(p, b);
-        if (a.dlogits) {
-            int* cnt = reinterpret_cast<int*>(fsm);
-            for (int e = tid; e < a.E; e += kThreads) cnt[e] = 0;
-            __syncthreads();
-            const int first = b0 / p.len1, rows = (b1 - 1) / p.len1 - first + 1;
+        int* cnt = reinterpret_cast<int*>(fsm);
+        for (int e = tid; e < a.E; e += kThreads) cnt[e] = 0;
+        __syncthreads();
+        const int first = b0 / p.len1, rows = (b1 - 1) / p.len1 - first + 1;
 #pragma unroll 2
-            for (int i = warp; i < rows; i += kWarps)
-                for (int e = lane; e < a.E; e += 32) atomicAdd(&cnt[e], p.counts[(int64_t)(first + i + b) * p.row + e]);
-            __syncthreads();
-            const int64_t kn = (int64_t)a.k * n;
-            const float inv = n > 0 ? 1.0f / (float)kn : 0.f;
-            for (int e = tid; e < a.E; e += kThreads) fsm[e] = (float)((int64_t)a.E * cnt[e] - kn) * inv;
-            __syncthreads();
+        for (int i = warp; i < rows; i += kWarps)
+            for (int e = lane; e < a.E; e += 32) atomicAdd(&cnt[e], p.counts[(int64_t)(first + i + b) * p.row + e]);
+        const int n = tokens_of(p, b);
+        const int64_t kn = (int64_t)a.k * n;
+        const float inv_kn = n > 0 ? 1.0f / (float)kn : 0.f;
+        __syncthreads();
+        for (int e = tid; e < a.E; e += kThreads) {
+            const int count = cnt[e];
+            if (a.counts && b0 >= t0) a.counts[(int64_t)b * a.E + e] = count;     // (the chunk of its first token)
+            fsm[e] = (float)((int64_t)a.E * count - kn) * inv_kn;
         }
-        const float scale = n > 0 && used > 0 ? up / ((float)used * (float)n) : 0.f;
-        float acc[NC][V], f[NC][V];
+        __syncthreads();
+        const float weight = n > 0 && used > 0 ? a.coef / ((float)used * (float)n) : 0.f, scale = up * weight;
+        float f[NC][V], shares = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                acc[i][j] = 0.f;
-                f[i][j] = a.dlogits && expert(i) + j < a.E ? fsm[expert(i) + j] : 0.f;
-            }
-        for (int tw = s0 + warp * TOK; tw < s1; tw += kWarps * TOK) {
+            for (int j = 0; j < V; ++j) f[i][j] = expert(i) + j < a.E ? fsm[expert(i) + j] : 0.f;
+        for (int tw = logits ? s0 + warp * TOK : s1; tw < s1; tw += kWarps * TOK) {
             float l[TOK][NC][V], q[TOK][NC][V], m[TOK], sum[TOK], dot[TOK];
             bool live[TOK];
 #pragma unroll
@@ -186,6 +203,9 @@ __device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float*
                     for (int j = 0; j < V; ++j) l[o][i][j] = -kInf;
                     if (live[o] && expert(i) < a.E) load_once<V>(row, MOE_F32, expert(i), l[o][i]);
                 }
+            }
+#pragma unroll
+            for (int o = 0; o < TOK; ++o) {
                 m[o] = -kInf;
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
@@ -200,23 +220,31 @@ __device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float*
             // large so that none is lost that is not lost in p.  A logit of -inf has p = 0, a token of nothing else no p at all.
 #pragma unroll
             for (int o = 0; o < TOK; ++o) {
-                sum[o] = dot[o] = 0.f;
-                const float top = SIGMOID ? fminf(m[o], 0.f) : m[o], away = top == -kInf ? 0.f : top;
+                const float top = m[o] == -kInf ? 0.f : m[o];
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float v = l[o][i][j];
-                        float e = exp2_quick(fmaf(kLog2e, (SIGMOID ? fminf(v, 0.f) : v) - away, 32.0f));
                         if constexpr (SIGMOID) {
-                            // sigmoid = e^min(v, 0) / (1 + e^-|v|), 1 - sigmoid = e^-max(v, 0) / (1 + e^-|v|)
-                            const float z = __expf(-fabsf(v)), one = __fdividef(1.0f, 1.0f + z);
-                            e *= one;
-                            l[o][i][j] = v > 0.f ? z * one : one;
+                            // sigmoid = (v > 0 ? 1 : z) / (1 + z), 1 - sigmoid = (v > 0 ? z : 1) / (1 + z), z = e^-|v|; a token of negative
+                            // logits alone (its whole warp) takes e^(v - max) for z above
+                            const float z = kBack * exp2_quick(fmaf(-kLog2e, fabsf(v), 32.0f)), one = __fdividef(1.0f, 1.0f + z);
+                            float num = v > 0.f ? 1.0f : z;
+                            if (top < 0.f) num = exp2_quick(fmaf(kLog2e, v - top, 32.0f));
+                            q[o][i][j] = num * one;
+                            l[o][i][j] = (v > 0.f ? z : 1.0f) * one;
+                        } else {
+                            q[o][i][j] = exp2_quick(fmaf(kLog2e, v - top, 32.0f));
                         }
-                        q[o][i][j] = e;
-                        sum[o] += e;
-                        dot[o] = fmaf(e, f[i][j], dot[o]);
+                    }
+                sum[o] = dot[o] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        sum[o] += q[o][i][j];
+                        dot[o] = fmaf(q[o][i][j], f[i][j], dot[o]);
                     }
             }
 #pragma unroll
@@ -229,20 +257,21 @@ __device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float*
 #pragma unroll
             for (int o = 0; o < TOK; ++o) {
                 const int t = tw + o;
-                const float inv = sum[o] == 0.f ? 0.f : 1.0f / sum[o];
+                const bool none = sum[o] == 0.f;
+                const float inv = none ? 0.f : __fdividef(1.0f, sum[o]);
                 dot[o] *= inv;
+                if (!none) shares += 1.0f + dot[o];
+                if (!a.dlogits || t >= s1 || (!live[o] && a.accumulate)) continue;
                 float* row = a.dlogits + t * a.dstride;
-                const bool write = a.dlogits && t < s1 && (live[o] || !a.accumulate);
+                const float by = inv * scale;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        const float prob = q[o][i][j] * inv;
-                        acc[i][j] += prob;               // (0 unless live)
-                        q[o][i][j] = prob * (scale * (f[i][j] - dot[o]));
+                        q[o][i][j] = (q[o][i][j] * by) * (f[i][j] - dot[o]);
                         if (SIGMOID) q[o][i][j] *= l[o][i][j];
                     }
-                    if (!write || expert(i) >= a.E) continue;
+                    if (expert(i) >= a.E) continue;
                     if (a.accumulate) {
                         float old[V];
                         load_once<V>(row, MOE_F32, expert(i), old);
@@ -253,138 +282,49 @@ __device__ __forceinline__ void pass_chunk(const BalanceParams& p, int c, float*
                 }
             }
         }
-        if (a.loss) {
-            float* part = fsm + a.E;
-            __syncthreads();                             // (the last sequence's sums have been read)
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (expert(i) + j < a.E) part[warp * a.E + expert(i) + j] = acc[i][j];
-            __syncthreads();
-            for (int e = tid; e < a.E; e += kThreads) {
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += part[w * a.E + e];
-                p.sums[(int64_t)(c + b) * a.E + e] = v;
-            }
-        }
-        __syncthreads();                                 // (fsm and the sums of the next sequence)
+        loss += shares * weight;
+        __syncthreads();                                 // (fsm of the next sequence)
     }
+    return a.loss ? cta_sum(lane == 0 ? loss : 0.f, part) : 0.f;
 }
 template <int EPL, int V, int TOK, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ BalanceParams p) {
     extern __shared__ float fsm[];
-    __shared__ int word;
-    wait_for_previous();
-    allow_next();
-    pass_chunk<EPL, V, TOK, SIGMOID>(p, blockIdx.x, fsm, &word);
-}
-
-// ---------------------------------------------------------------- counts and loss of each sequence
-// The sum over the CTA's threads, in one order (thread 0 has it).
-__device__ __forceinline__ float cta_sum(float v, float* part) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    if (threadIdx.x == 0)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += part[w];
-    return v;
-}
-// What expert e's count and sum of p add to a sequence's loss (f P), n counted tokens.
-__device__ __forceinline__ float share_of(const BalanceArgs& a, int count, float sum, int n) {
-    const float inv = 1.0f / (float)n;
-    return ((float)count * (float)a.E / (float)a.k * inv) * (sum * inv);
-}
-// A CTA adds 32 experts' (blockIdx.x) partial rows of a sequence (blockIdx.y), the rows dealt to its warps.
-__global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant__ BalanceParams p) {
-    __shared__ int cnt[kWarps][32];
-    __shared__ float sum[kWarps][32];
     __shared__ float part[kWarps];
     __shared__ int word;
     __shared__ bool last;
     const BalanceArgs& a = p.a;
-    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x * 32 + lane;
+    const int tid = threadIdx.x;
     wait_for_previous();
     allow_next();
-    const int t0 = start_of(a, b), t1 = start_of(a, b + 1);
-    int c = 0;
-    float s = 0.f;
-    if (e < a.E && t1 > t0) {
-        if (a.loss) {
-#pragma unroll 8
-            for (int i = t0 / p.len2 + warp; i <= (t1 - 1) / p.len2; i += kWarps) s += p.sums[(int64_t)(i + b) * a.E + e];
-        }
-#pragma unroll 4
-        for (int i = t0 / p.len1 + warp; i <= (t1 - 1) / p.len1; i += kWarps) c += p.counts[(int64_t)(i + b) * p.row + e];
-    }
-    const int n = tokens_of(p, b);
-    cnt[warp][lane] = c;
-    sum[warp][lane] = s;
-    __syncthreads();
-    float v = 0.f;
-    if (warp == 0 && e < a.E) {
-        c = 0;
-        s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            c += cnt[w][lane];
-            s += sum[w][lane];
-        }
-        if (a.counts) a.counts[(int64_t)b * a.E + e] = c;
-        if (n > 0) v = share_of(a, c, s, n);
-    }
+    float v = pass_chunk<EPL, V, TOK, SIGMOID>(p, blockIdx.x, fsm, part, &word);
     if (!a.loss) return;
-    if (warp == 0) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-        if (lane == 0) {
-            p.losses[(int64_t)b * gridDim.x + blockIdx.x] = v;
-            __threadfence();
-            last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
-        }
+    if (tid == 0) {
+        p.losses[blockIdx.x] = v;
+        __threadfence();
+        last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
     __threadfence();
-    const int used = used_sequences(p, &word);
     v = 0.f;
-    for (int64_t i = tid; i < (int64_t)gridDim.x * gridDim.y; i += kThreads) v += __ldcg(p.losses + i);
+    for (int i = tid; i < (int)gridDim.x; i += kThreads) v += __ldcg(p.losses + i);
     v = cta_sum(v, part);
-    if (tid == 0) *a.loss = used > 0 ? v * a.coef / (float)used : 0.f;
+    if (tid == 0) *a.loss = v;
 }
 
 // ---------------------------------------------------------------- a few tokens: one CTA, one launch
-// (one chunk, so that a sequence has one row of counts and of sums)
 template <int EPL, int V, int TOK, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ BalanceParams p) {
     extern __shared__ float fsm[];
     __shared__ float part[kWarps];
     __shared__ int word;
-    const BalanceArgs& a = p.a;
     wait_for_previous();
     allow_next();
     count_chunk(p, 0, reinterpret_cast<int*>(fsm));
     __syncthreads();
-    if (a.loss || a.dlogits) pass_chunk<EPL, V, TOK, SIGMOID>(p, 0, fsm, &word);
-    __syncthreads();
-    float v = 0.f;
-    for (int b = threadIdx.x >> 5; b < a.n_seqs; b += kWarps) {
-        const bool some = start_of(a, b + 1) > start_of(a, b);
-        const int n = tokens_of(p, b);
-        for (int e = threadIdx.x & 31; e < a.E; e += 32) {
-            const int c = some ? p.counts[(int64_t)b * p.row + e] : 0;
-            if (a.counts) a.counts[(int64_t)b * a.E + e] = c;
-            if (a.loss && n > 0) v += share_of(a, c, p.sums[(int64_t)b * a.E + e], n);
-        }
-    }
-    if (!a.loss) return;
-    const int used = used_sequences(p, &word);
-    v = cta_sum(v, part);
-    if (threadIdx.x == 0) *a.loss = used > 0 ? v * a.coef / (float)used : 0.f;
+    const float v = pass_chunk<EPL, V, TOK, SIGMOID>(p, 0, fsm, part, &word);
+    if (p.a.loss && threadIdx.x == 0) *p.a.loss = v;
 }
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -394,16 +334,15 @@ int count_chunks(int k, int T, int n_seqs) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, T), kMostCounts));
 }
 struct Layout {
-    size_t counts, sums, losses, total;
+    size_t counts, losses, total;
     int row;
 };
 Layout layout(int E, int n_seqs, int chunks1, int chunks2) {
     Layout l;
     l.row = (E + 4) & ~3;
     l.counts = 256;
-    l.sums = align_up(l.counts + (size_t)(chunks1 + n_seqs) * l.row * 4, 256);
-    l.losses = align_up(l.sums + (size_t)(chunks2 + n_seqs) * E * 4, 256);
-    l.total = align_up(l.losses + (size_t)n_seqs * ((E + 31) / 32) * 4, 256);
+    l.losses = align_up(l.counts + (size_t)(chunks1 + n_seqs) * l.row * 4, 256);
+    l.total = align_up(l.losses + (size_t)chunks2 * 4, 256);
     return l;
 }
 
@@ -412,10 +351,10 @@ cudaError_t launch_pass(const BalanceParams& p, bool small, cudaStream_t s) {
     static std::atomic<uint64_t> ready[2];
     int sms = 0;
     const void* fn = small ? (const void*)small_kernel<EPL, V, TOK, SIGMOID> : (const void*)pass_kernel<EPL, V, TOK, SIGMOID>;
-    cudaError_t err = prepare_kernel(fn, 32 * EPL * (1 + kWarps) * 4 + 16, ready[small], &sms);
+    cudaError_t err = prepare_kernel(fn, 32 * EPL * 4 + 16, ready[small], &sms);
     if (err != cudaSuccess) return err;
     void* args[] = {const_cast<BalanceParams*>(&p)};
-    return launch_early(fn, dim3(p.chunks2), kThreads, (size_t)p.a.E * (1 + kWarps) * 4 + 16, s, args);
+    return launch_early(fn, dim3(p.chunks2), kThreads, (size_t)p.a.E * 4 + 16, s, args);
 }
 template <bool SIGMOID>
 cudaError_t launch_pass_of(const BalanceParams& p, bool small, cudaStream_t s) {
@@ -423,12 +362,12 @@ cudaError_t launch_pass_of(const BalanceParams& p, bool small, cudaStream_t s) {
     const bool vec = a.E % 4 == 0 && (uintptr_t)a.logits % 16 == 0 && a.stride % 4 == 0 &&
                      (!a.dlogits || ((uintptr_t)a.dlogits % 16 == 0 && a.dstride % 4 == 0));
     if (vec)
-        return a.E <= 128   ? launch_pass<4, 4, 2, SIGMOID>(p, small, s)
+        return a.E <= 128   ? launch_pass<4, 4, 4, SIGMOID>(p, small, s)
                : a.E <= 256 ? launch_pass<8, 4, 2, SIGMOID>(p, small, s)
                : a.E <= 512 ? launch_pass<16, 4, 1, SIGMOID>(p, small, s)
                             : launch_pass<32, 4, 1, SIGMOID>(p, small, s);
     return a.E <= 32    ? launch_pass<1, 1, 4, SIGMOID>(p, small, s)
-           : a.E <= 128 ? launch_pass<4, 1, 2, SIGMOID>(p, small, s)
+           : a.E <= 128 ? launch_pass<4, 1, 4, SIGMOID>(p, small, s)
            : a.E <= 256 ? launch_pass<8, 1, 2, SIGMOID>(p, small, s)
            : a.E <= 512 ? launch_pass<16, 1, 1, SIGMOID>(p, small, s)
                         : launch_pass<32, 1, 1, SIGMOID>(p, small, s);
@@ -436,7 +375,7 @@ cudaError_t launch_pass_of(const BalanceParams& p, bool small, cudaStream_t s) {
 
 }  // namespace
 
-size_t balance_ws_bytes(int E, int T, int n_seqs) { return layout(E, n_seqs, kMostCounts, std::min(T, kMostChunks)).total; }
+size_t balance_ws_bytes(int E, int T, int n_seqs) { return layout(E, n_seqs, kMostCounts, std::max(1, std::min(T, kMostChunks))).total; }
 
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
     static std::atomic<uint64_t> ready;
@@ -455,18 +394,12 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
     p.row = l.row;
     p.ticket = reinterpret_cast<uint32_t*>(ws);
     p.counts = reinterpret_cast<int32_t*>(ws + l.counts);
-    p.sums = reinterpret_cast<float*>(ws + l.sums);
     p.losses = reinterpret_cast<float*>(ws + l.losses);
     if (small) return a.sigmoid ? launch_pass_of<true>(p, true, s) : launch_pass_of<false>(p, true, s);
     void* args[] = {&p};
     err = launch_early((const void*)count_kernel, dim3(p.chunks1), kThreads, (size_t)(a.E + 1) * 4, s, args);
     if (err != cudaSuccess) return err;
-    if (a.loss || a.dlogits) {
-        err = a.sigmoid ? launch_pass_of<true>(p, false, s) : launch_pass_of<false>(p, false, s);
-        if (err != cudaSuccess) return err;
-    }
-    if (!a.loss && !a.counts) return cudaSuccess;
-    return launch_early((const void*)finish_kernel, dim3((a.E + 31) / 32, a.n_seqs), kThreads, 0, s, args);
+    return a.sigmoid ? launch_pass_of<true>(p, false, s) : launch_pass_of<false>(p, false, s);
 }
 
 }  // namespace moe
