@@ -136,6 +136,7 @@ __device__ __forceinline__ float cta_sum(float v, float* part) {
         for (int w = 0; w < kWarps; ++w) v += part[w];
     return v;
 }
+template <int EPL> constexpr int kResident = EPL <= 8 ? 2 : 1;     // CTAs an SM
 // Chunk c of the tokens; the chunk's share of the loss (thread 0 has it).  A warp takes TOK tokens at a time; lane l holds
 // experts (32 i + l) V + j of each, EPL in all.  fsm: shared, [E]; part: shared; word: shared.
 template <int EPL, int V, int TOK, bool SIGMOID>
@@ -170,9 +171,28 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
         for (int e = tid; e < a.E; e += kThreads) cnt[e] = 0;
         __syncthreads();
         const int first = b0 / p.len1, rows = (b1 - 1) / p.len1 - first + 1;
-#pragma unroll 2
-        for (int i = warp; i < rows; i += kWarps)
-            for (int e = lane; e < a.E; e += 32) atomicAdd(&cnt[e], p.counts[(int64_t)(first + i + b) * p.row + e]);
+        {
+            // (four experts a lane, the rows dealt to the warps)
+            constexpr int kFours = EPL <= 4 ? 1 : EPL / 4;
+            int4 mine[kFours] = {};
+#pragma unroll 4
+            for (int i = warp; i < rows; i += kWarps)
+#pragma unroll
+                for (int j = 0; j < kFours; ++j)
+                    if (4 * (lane + 32 * j) < a.E) {
+                        const int4 v = *reinterpret_cast<const int4*>(p.counts + (int64_t)(first + i + b) * p.row + 4 * (lane + 32 * j));
+                        mine[j].x += v.x; mine[j].y += v.y; mine[j].z += v.z; mine[j].w += v.w;
+                    }
+#pragma unroll
+            for (int j = 0; j < kFours; ++j) {
+                const int e = 4 * (lane + 32 * j);
+                if (warp >= rows) continue;
+                if (e < a.E) atomicAdd(&cnt[e], mine[j].x);
+                if (e + 1 < a.E) atomicAdd(&cnt[e + 1], mine[j].y);
+                if (e + 2 < a.E) atomicAdd(&cnt[e + 2], mine[j].z);
+                if (e + 3 < a.E) atomicAdd(&cnt[e + 3], mine[j].w);
+            }
+        }
         const int n = tokens_of(p, b);
         const int64_t kn = (int64_t)a.k * n;
         const float inv_kn = n > 0 ? 1.0f / (float)kn : 0.f;
@@ -288,7 +308,7 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
     return a.loss ? cta_sum(lane == 0 ? loss : 0.f, part) : 0.f;
 }
 template <int EPL, int V, int TOK, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) pass_kernel(const __grid_constant__ BalanceParams p) {
+__global__ void __launch_bounds__(kThreads, kResident<EPL>) pass_kernel(const __grid_constant__ BalanceParams p) {
     extern __shared__ float fsm[];
     __shared__ float part[kWarps];
     __shared__ int word;
@@ -347,28 +367,32 @@ Layout layout(int E, int n_seqs, int chunks1, int chunks2) {
 }
 
 template <int EPL, int V, int TOK, bool SIGMOID>
-cudaError_t launch_pass(const BalanceParams& p, bool small, cudaStream_t s) {
+cudaError_t launch_pass(BalanceParams& p, bool small, cudaStream_t s) {
     static std::atomic<uint64_t> ready[2];
     int sms = 0;
     const void* fn = small ? (const void*)small_kernel<EPL, V, TOK, SIGMOID> : (const void*)pass_kernel<EPL, V, TOK, SIGMOID>;
     cudaError_t err = prepare_kernel(fn, 32 * EPL * 4 + 16, ready[small], &sms);
     if (err != cudaSuccess) return err;
-    void* args[] = {const_cast<BalanceParams*>(&p)};
+    // even chunks, one for each CTA that runs at a time, of a token a warp at least
+    p.len2 = small ? std::max(p.a.T, 1) : std::max(kWarps, ceil_div(p.a.T, std::min(kResident<EPL> * sms, kMostChunks)));
+    p.chunks2 = std::max(1, ceil_div(p.a.T, p.len2));
+    void* args[] = {&p};
     return launch_early(fn, dim3(p.chunks2), kThreads, (size_t)p.a.E * 4 + 16, s, args);
 }
 template <bool SIGMOID>
-cudaError_t launch_pass_of(const BalanceParams& p, bool small, cudaStream_t s) {
+cudaError_t launch_pass_of(BalanceParams& p, bool small, cudaStream_t s) {
+    constexpr int kLess = SIGMOID ? 2 : 1;               // (its 1 - sigmoid takes registers)
     const BalanceArgs& a = p.a;
     const bool vec = a.E % 4 == 0 && (uintptr_t)a.logits % 16 == 0 && a.stride % 4 == 0 &&
                      (!a.dlogits || ((uintptr_t)a.dlogits % 16 == 0 && a.dstride % 4 == 0));
     if (vec)
-        return a.E <= 128   ? launch_pass<4, 4, 4, SIGMOID>(p, small, s)
-               : a.E <= 256 ? launch_pass<8, 4, 2, SIGMOID>(p, small, s)
+        return a.E <= 128   ? launch_pass<4, 4, 4 / kLess, SIGMOID>(p, small, s)
+               : a.E <= 256 ? launch_pass<8, 4, 2 / kLess, SIGMOID>(p, small, s)
                : a.E <= 512 ? launch_pass<16, 4, 1, SIGMOID>(p, small, s)
                             : launch_pass<32, 4, 1, SIGMOID>(p, small, s);
     return a.E <= 32    ? launch_pass<1, 1, 4, SIGMOID>(p, small, s)
-           : a.E <= 128 ? launch_pass<4, 1, 4, SIGMOID>(p, small, s)
-           : a.E <= 256 ? launch_pass<8, 1, 2, SIGMOID>(p, small, s)
+           : a.E <= 128 ? launch_pass<4, 1, 4 / kLess, SIGMOID>(p, small, s)
+           : a.E <= 256 ? launch_pass<8, 1, 2 / kLess, SIGMOID>(p, small, s)
            : a.E <= 512 ? launch_pass<16, 1, 1, SIGMOID>(p, small, s)
                         : launch_pass<32, 1, 1, SIGMOID>(p, small, s);
 }
@@ -387,9 +411,7 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
     const bool small = a.T <= 64;                        // (a chunk of 16 warps, 4 tokens each at most)
     p.len1 = small ? std::max(a.T, 1) : ceil_div(a.T, count_chunks(a.k, a.T, a.n_seqs));
     p.chunks1 = std::max(1, ceil_div(a.T, p.len1));
-    p.len2 = small ? std::max(a.T, 1) : std::max(kWarps, ceil_div(a.T, std::min(2 * sms, kMostChunks)));
-    p.chunks2 = std::max(1, ceil_div(a.T, p.len2));
-    const Layout l = layout(a.E, a.n_seqs, p.chunks1, p.chunks2);
+    const Layout l = layout(a.E, a.n_seqs, p.chunks1, 0);
     char* ws = static_cast<char*>(a.ws);
     p.row = l.row;
     p.ticket = reinterpret_cast<uint32_t*>(ws);

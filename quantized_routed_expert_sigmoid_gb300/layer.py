@@ -536,7 +536,7 @@ class LayerNorm:
                 _given(g, name, (torch.float32,), H)
         self.H, self.eps, self.y_dtype = H, eps, y_dtype
         self._keep = (gamma, beta)
-        self._desc = {}                  # the call's description, by the types of its tensors
+        self._desc, self._bytes = {}, {}  # the call's description, by the types of its tensors; its workspace, by T
 
     def _described(self, x, y_dtype, **tensors):
         device = x.get_device()
@@ -561,11 +561,14 @@ class LayerNorm:
         if out is None:
             out = _empty((T, self.H), self.y_dtype, x.device, stream)
         ys = _value_rows(out, "out", T, self.H)
-        if stats and (mean is None or rstd is None):
-            made = _empty((2, T), torch.float32, x.device, stream)
-            mean, rstd = made[0] if mean is None else mean, made[1] if rstd is None else rstd
-        _given(mean, "mean", (torch.float32,), T)
-        _given(rstd, "rstd", (torch.float32,), T)
+        if mean is not None:
+            _given(mean, "mean", (torch.float32,), T)
+        elif stats:
+            mean = _empty((T,), torch.float32, x.device, stream)
+        if rstd is not None:
+            _given(rstd, "rstd", (torch.float32,), T)
+        elif stats:
+            rstd = _empty((T,), torch.float32, x.device, stream)
         desc = self._described(x, out.dtype, out=out, mean=mean, rstd=rstd)
         N.moe_layer_norm(desc, x, xs, T, out, ys, mean, rstd, stream)
         return out, mean, rstd
@@ -579,29 +582,48 @@ class LayerNorm:
         dgamma and dbeta (fp32 [H]) are made when gamma and beta are there (None otherwise, unless given); accumulate:
         they are given and added to.
         """
-        T = x.shape[0]
-        xs, gs = _value_rows(x, "x", T, self.H), _value_rows(dy, "dy", T, self.H)
+        T, H = x.shape[0], self.H
+        xs, gs = _value_rows(x, "x", T, H), _value_rows(dy, "dy", T, H)
         if dx is None:
-            dx = _empty((T, self.H), x.dtype, x.device, stream)
-        ds, as_ = _value_rows(dx, "dx", T, self.H), 0
-        if dx.dtype is not x.dtype or (add is not None and add.dtype is not x.dtype):
-            raise ValueError("dx and add must have x's type")
+            dx = _empty((T, H), x.dtype, x.device, stream)
+        elif dx.dtype is not x.dtype:
+            raise ValueError("dx must have x's type")
+        ds, as_ = _value_rows(dx, "dx", T, H), 0
         if add is not None:
-            as_ = _value_rows(add, "add", T, self.H)
-        sums = []
-        for name, t, weight in (("dgamma", dgamma, self._keep[0]), ("dbeta", dbeta, self._keep[1])):
-            if t is None and weight is not None:
-                if accumulate:
-                    raise ValueError(f"{name} must be given to be added to")
-                t = _empty((self.H,), torch.float32, x.device, stream)
-            sums.append(_given(t, name, (torch.float32,), self.H))
-        if _given(mean, "mean", (torch.float32,), T) is None or _given(rstd, "rstd", (torch.float32,), T) is None:
+            if add.dtype is not x.dtype:
+                raise ValueError("add must have x's type")
+            as_ = _value_rows(add, "add", T, H)
+        if mean is None or rstd is None:
             raise ValueError("mean and rstd are those of the forward call")
-        desc = self._described(x, dy.dtype, dy=dy, mean=mean, rstd=rstd, add=add, dx=dx, dgamma=sums[0], dbeta=sums[1])
-        nbytes = N.moe_layer_norm_backward_workspace_size(self.H, T) if sums[0] is not None or sums[1] is not None else 0
-        ws = _empty((nbytes,), torch.uint8, x.device, stream) if nbytes else None    # (of the stream's memory: free again behind it)
-        N.moe_layer_norm_backward(desc, dy, gs, x, xs, mean, rstd, add, as_, T, dx, ds, *sums, accumulate, ws, nbytes, stream)
-        return dx, sums[0], sums[1]
+        _given(mean, "mean", (torch.float32,), T)
+        _given(rstd, "rstd", (torch.float32,), T)
+        if dgamma is not None:
+            _given(dgamma, "dgamma", (torch.float32,), H)
+        if dbeta is not None:
+            _given(dbeta, "dbeta", (torch.float32,), H)
+        make = [t is None and w is not None for t, w in zip((dgamma, dbeta), self._keep)]
+        if accumulate and any(make):
+            raise ValueError("dgamma and dbeta must be given to be added to")
+        ws, nbytes = None, 0
+        if dgamma is not None or dbeta is not None or any(make):
+            # (of the stream's memory: free again behind the call)
+            nbytes = self._workspace(T)
+            ws = _empty((nbytes,), torch.uint8, x.device, stream) if nbytes else None
+            if make[0]:
+                dgamma = _empty((H,), torch.float32, x.device, stream)
+            if make[1]:
+                dbeta = _empty((H,), torch.float32, x.device, stream)
+        desc = self._described(x, dy.dtype, dy=dy, mean=mean, rstd=rstd, add=add, dx=dx, dgamma=dgamma, dbeta=dbeta)
+        N.moe_layer_norm_backward(desc, dy, gs, x, xs, mean, rstd, add, as_, T, dx, ds, dgamma, dbeta, accumulate, ws, nbytes,
+                                  stream)
+        return dx, dgamma, dbeta
+
+    def _workspace(self, T):
+        """Bytes of the backward call's workspace for T rows (by T: the query takes 1 us)."""
+        nbytes = self._bytes.get(T)
+        if nbytes is None:
+            nbytes = self._bytes[T] = N.moe_layer_norm_backward_workspace_size(self.H, T)
+        return nbytes
 
 
 class BalanceLoss(_Checked):
@@ -615,6 +637,7 @@ class BalanceLoss(_Checked):
         if mode not in ("softmax", "sigmoid"):
             raise ValueError(f"mode must be 'softmax' or 'sigmoid', not {mode!r}")
         self.E, self.k = E, k
+        self._bytes = {}                 # of the workspace, by T and sequences
         self._desc = [N.moe_balance_desc(N.MOE_ROUTE_SIGMOID_GROUP if mode == "sigmoid" else N.MOE_ROUTE_SOFTMAX, E, k, coef, a)
                       for a in (0, 1)]
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -659,8 +682,10 @@ class BalanceLoss(_Checked):
             status = self._status
             if status is not None and status.get_device() != logits.get_device():
                 raise ValueError(f"logits are on device {logits.get_device()}, this object's calls on device {status.get_device()}")
-        nbytes = N.moe_balance_workspace_size(self.E, T, n_seqs)
-        ws = _empty((nbytes,), torch.uint8, logits.device, stream)
+        nbytes = self._bytes.get((T, n_seqs))
+        if nbytes is None:
+            nbytes = self._bytes[T, n_seqs] = N.moe_balance_workspace_size(self.E, T, n_seqs)
+        ws = _empty((nbytes,), torch.uint8, logits.device, stream)       # (of the stream's memory: free again behind the call)
         N.moe_balance_loss(self._desc[bool(accumulate)], logits, _row_stride(logits, "logits"), ids, T, offsets, n_seqs, mask,
                            upstream, loss, counts, dlogits, _row_stride(dlogits, "dlogits") if dlogits is not None else 0, status,
                            ws, nbytes, stream)
