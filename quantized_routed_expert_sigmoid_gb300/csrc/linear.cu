@@ -629,6 +629,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 
                     ok = wait_warp(&accf[b], (j >> 1) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_after();
+                    // the tile's residual into L2 while the last two runs go on (a line of a row of x a lane)
+                    if (p.e.r && k0 + 2 * p.run >= p.nk && k0 + p.run < p.nk && n0 < p.e.N)
+                        for (int c = (lane & 15) + kEvery * (lane >> 4); c < n; c += 2 * kEvery)
+                            prefetch_l2(p.e.r, p.e.r_type, (tok0 + c) * p.e.r_stride + n0);
 #pragma unroll
                     for (int i = 0; i < kPairCols / kSides; i += 16)
                         if (i * kSides < n) {
