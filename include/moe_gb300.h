@@ -434,7 +434,7 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
  *   buffer, as for moe_grouped_matmul, do not).  status (device int32, nullable, never cleared by the call): raised from MOE_OK to
  *   MOE_ERR_TIMEOUT when a device-side wait ran out (y is undefined).  T <= 2^30, strides <= 2^32; T = 0 is a no-op.
  *   One launch, no workspace, nothing kept between calls; a captured call replays with the bits of the eager one.
- * Kernels (moe_linear_path): MOE_LINEAR_SPLIT, tiles of 128 outputs by up to 128 rows, the sum of a tile split over a
+ * Kernels (moe_linear_path): MOE_LINEAR_SPLIT, tiles of 128 outputs by up to 64 rows, the sum of a tile split over a
  *   cluster of up to 8 SMs where there are few tiles; MOE_LINEAR_PAIRS, tiles of 256 outputs by up to 256 rows on pairs of SMs.
  * Errors: as moe_grouped_matmul.  Pages: the parts around the experts are not printed; these are the plain definitions.
  */

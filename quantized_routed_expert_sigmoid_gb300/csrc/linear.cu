@@ -3,7 +3,7 @@
 // The weights are the M operand (a lane of TMEM holds one output channel, a column one row of x): a few rows of x
 // then cost a few columns, and the bias is one register.  Everything behind the sum happens between TMEM and
 // the one store of y, in fp32.  Two kernels:
-// - split_kernel: tiles of 128 channels by up to 128 rows of x, one CTA each; where that leaves SMs idle, a cluster
+// - split_kernel: tiles of 128 channels by up to 64 rows of x, one CTA each; where that leaves SMs idle, a cluster
 //   of up to 8 CTAs splits the sum of a tile.  Each CTA sends the columns of its part to the CTA of the cluster that finishes
 //   them (shared memory of the cluster, no workspace), which adds the parts in their order.
 // - pair_kernel: tiles of 256 channels by up to 256 rows, a pair of CTAs (cta_group::2) each, persistent, two accumulators: one
@@ -42,7 +42,7 @@ struct LinearParams {
     Epilogue e;
     int K, nk, run;              // nk: steps of the sum, run: of one run
     bool bf16;
-    int cols;                    // columns of a tile (split: 16, 32, 64 or 128; pairs: a multiple of 32)
+    int cols;                    // columns of a tile (split: 16, 32 or 64; pairs: a multiple of 32)
     int box;                     // which of tx
     int stages;
     bool vec;                    // four neighbouring channels of r and y can be read and written at once (split)
@@ -247,12 +247,16 @@ __device__ __forceinline__ void finish4(const LinearParams& p, const float (&bia
     }
 }
 
-constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128;                       // a step's weights
+// Steps of the sum that a stage of a ring holds.  A stage costs about 300 clocks of waiting, issuing and committing whatever it
+// holds (without loads and with one instruction a step still 335 of 435 clocks a step), more than the matrix instructions of a step
+// of up to 128 columns take.
+constexpr int kPer = 2;
+constexpr int kMaxStages = 6;
 
 template <bool IN_OUT, int COLS>
 __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(const __grid_constant__ LinearParams p) {
-    constexpr int kStage = kABytes + COLS * 128, kHalf = COLS / 2;
+    constexpr int kStep = kABytes + COLS * 128, kStage = kPer * kStep, kHalf = COLS / 2;
     constexpr uint32_t kTmem = 2 * COLS < 32 ? 32 : 2 * COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -311,18 +315,24 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
         const CUtensorMap* xmap = &p.tx[p.box];
         int g = 0, s = 0;
         uint32_t ph = 1;
-        for (int kb = k0; kb < k1; ++kb, ++g) {
+        for (int kb = k0; kb < k1; kb += kPer, ++g) {
             if (!wait_warp(&empty[s], ph, abort_flag, p.wait_ns)) break;
-            const uint32_t bar = full0 + 8 * s, a = stage0 + s * kStage;
+            const uint32_t bar = full0 + 8 * s, bytes = (uint32_t)min(kPer, k1 - kb) * kStep;
             if (elect_one()) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kStage) : "memory");
-                if constexpr (IN_OUT) {
-                    tma_load(a, &p.tw, mb * 128, kb * kStepK, bar);
-                    tma_load(a + 8192, &p.tw, mb * 128 + 64, kb * kStepK, bar);
-                } else {
-                    tma_load(a, &p.tw, kb * kStepK, mb * 128, bar);
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    if (kb + u >= k1) break;
+                    const uint32_t a = stage0 + s * kStage + u * kStep;
+                    const int c = (kb + u) * kStepK;
+                    if constexpr (IN_OUT) {
+                        tma_load(a, &p.tw, mb * 128, c, bar);
+                        tma_load(a + 8192, &p.tw, mb * 128 + 64, c, bar);
+                    } else {
+                        tma_load(a, &p.tw, c, mb * 128, bar);
+                    }
+                    tma_load(a + kABytes, xmap, c, tok0, bar);
                 }
-                tma_load(a + kABytes, xmap, kb * kStepK, tok0, bar);
             }
             __syncwarp();
             if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
             if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) break;
             tc_after();
             const uint32_t acc = uniform(tmem + (uint32_t)b * COLS);
-            for (int kb = r0; kb < r1; ++kb) {
+            for (int kb = r0; kb < r1; kb += kPer) {
                 const bool stalled = p.stall && !any;    // (test setting)
                 if (!wait_warp(stalled ? &never : &full[s], stalled ? 0u : ph, abort_flag, p.wait_ns)) { ok = false; break; }
                 tc_after();
@@ -350,9 +360,14 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
                 const uint64_t da = da0 + adv, db = db0 + adv;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kStepK / 16; ++kk) mma_f16(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 || kb > r0);
+                    for (int u = 0; u < kPer; ++u) {
+                        if (kb + u >= r1) break;
+#pragma unroll
+                        for (int kk = 0; kk < kStepK / 16; ++kk)
+                            mma_f16(acc, da + u * (kStep >> 4) + kk * kAdvA, db + u * (kStep >> 4) + kk * kAdvB, idesc, u > 0 || kk > 0 || kb > r0);
+                    }
                     mma_commit(&empty[s]);
-                    if (kb == r1 - 1) mma_commit(&accf[b]);
+                    if (kb + kPer >= r1) mma_commit(&accf[b]);
                 }
                 __syncwarp();
                 any = true;
@@ -484,27 +499,31 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
 }
 
 // ---------------------------------------------------------------- a pair of CTAs a tile
-constexpr int kPairStages = 6, kPairCols = 256;
-constexpr int kPairStageBytes = kABytes + 128 * 128;
+// Steps a stage, stages and bytes of one: wide tiles (more than 128 columns, which the matrix instructions bound) and narrow ones.
+constexpr int kPairCols = 256;
+template <bool WIDE> constexpr int kPairPer = WIDE ? 1 : kPer;
+template <bool WIDE> constexpr int kPairStages = WIDE ? 6 : 4;
+template <bool WIDE> constexpr int kPairStep = kABytes + (WIDE ? 128 : 64) * 128;
 constexpr uint32_t kPairTmem = 512;
 constexpr int kPairEpi0 = 2;
 // Epilogue warps: 16, or 8 that have the registers for the sums of 128 columns each.
 template <bool RUNS> constexpr int kPairEpiWarps = RUNS ? 8 : 16;
 template <bool RUNS> constexpr int kPairThreads = 32 * (kPairEpi0 + kPairEpiWarps<RUNS>);
 
-template <bool IN_OUT, bool RUNS>
+template <bool IN_OUT, bool RUNS, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 1) pair_kernel(const __grid_constant__ LinearParams p) {
-    using Ring = RingOf<kPairStages>;
+    constexpr int kStages = kPairStages<WIDE>, kP = kPairPer<WIDE>, kStep = kPairStep<WIDE>, kStage = kP * kStep;
+    using Ring = RingOf<kStages>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[kPairStages], empty[kPairStages], accf[2], accr[2], drain, never;   // full, accr: the first CTA's
+    __shared__ uint64_t full[kStages], empty[kStages], accf[2], accr[2], drain, never;   // full, accr: the first CTA's
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, issued;
     volatile int* abort_flag = &abort_word;
     const int tid = threadIdx.x, warp = uniform((int)threadIdx.x >> 5), lane = tid & 31;
     const uint32_t cta = uniform(cta_rank());
     if (tid == 0) {
-        for (int i = 0; i < kPairStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&accr[i], 2 * kPairEpiWarps<RUNS>); }
         mbar_init(&drain, 1);
         mbar_init(&never, 1);
@@ -533,33 +552,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 
     if (warp == 0) {
         // ======================= loads =======================
         const uint32_t full0 = in_leader(su32(full)), stage0 = su32(smem);
-        const uint32_t bytes = kABytes + (2048u << p.box);
+        const uint32_t step_bytes = kABytes + (2048u << p.box);
         int g = 0;
         Ring ring;
         bool ok = true;
         for (int t = first; ok && t < n_tiles; t += n_pairs) {
             const int tb = t / p.n_mb, mb = t - tb * p.n_mb;
             const int c0 = uniform(tb * p.cols + (int)cta * nh), r0 = uniform(mb * 256 + (int)cta * 128);
-            for (int kb = 0; kb < p.nk; ++kb, ++g, ring.next()) {
+            for (int kb = 0; kb < p.nk; kb += kP, ++g, ring.next()) {
                 if (!wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
-                const uint32_t bar = full0 + 8 * ring.s, a = stage0 + ring.s * kPairStageBytes;
+                const uint32_t bar = full0 + 8 * ring.s, bytes = (uint32_t)min(kP, p.nk - kb) * step_bytes;
                 if (elect_one()) {
                     arrive_tx_cluster(bar, bytes);
-                    if constexpr (IN_OUT) {
-                        tma_2d(a, &p.tw, r0, kb * kStepK, bar);
-                        tma_2d(a + 8192, &p.tw, r0 + 64, kb * kStepK, bar);
-                    } else {
-                        tma_2d(a, &p.tw, kb * kStepK, r0, bar);
+#pragma unroll
+                    for (int u = 0; u < kP; ++u) {
+                        if (kb + u >= p.nk) break;
+                        const uint32_t a = stage0 + ring.s * kStage + u * kStep;
+                        const int c = (kb + u) * kStepK;
+                        if constexpr (IN_OUT) {
+                            tma_2d(a, &p.tw, r0, c, bar);
+                            tma_2d(a + 8192, &p.tw, r0 + 64, c, bar);
+                        } else {
+                            tma_2d(a, &p.tw, c, r0, bar);
+                        }
+                        tma_2d(a + kABytes, &p.tx[p.box], c, c0, bar);
                     }
-                    tma_2d(a + kABytes, &p.tx[p.box], kb * kStepK, c0, bar);
                 }
                 __syncwarp();
             }
         }
         if (lane == 0) issued = g;
         // the last steps' arrivals on this CTA's barriers have landed before it may leave
-        if (g < kPairStages) { ring.s = 0; ring.ph = 1; }
-        for (int i = 0; ok && i < min(g, kPairStages); ++i, ring.next())
+        if (g < kStages) { ring.s = 0; ring.ph = 1; }
+        for (int i = 0; ok && i < min(g, kStages); ++i, ring.next())
             ok = wait_warp(&empty[ring.s], ring.ph ^ 1, abort_flag, p.wait_ns);
     } else if (warp == 1) {
         // ======================= MMA issue (in the first CTA) =======================
@@ -572,28 +597,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 
             int j = 0;
             bool ok = true, any = false;
             for (int t = first; ok && t < n_tiles; t += n_pairs) {
-                for (int kb = 0, start = 0, b = 0; kb < p.nk; ++kb, ring.next()) {
+                for (int kb = 0, start = 0, b = 0; kb < p.nk; kb += kP, ring.next()) {
                     if (kb == start) {                   // the first step of a run
                         b = j & 1;
                         if (j >= 2 && !wait_warp(&accr[b], ((j >> 1) - 1) & 1, abort_flag, p.wait_ns)) { ok = false; break; }
                         tc_after();
                     }
                     const uint32_t acc = uniform(tmem + (uint32_t)b * kPairCols);
-                    const bool last_step = kb == p.nk - 1 || kb - start == p.run - 1;
+                    const bool last_step = kb + kP >= p.nk || kb + kP - start >= p.run;
                     const bool stalled = p.stall && !any;            // (test setting)
                     if (!wait_warp(stalled ? &never : &full[ring.s], stalled ? 0u : ring.ph, abort_flag, p.wait_ns)) { ok = false; break; }
                     tc_after();
-                    const uint32_t adv = (uint32_t)ring.s * (kPairStageBytes >> 4);
+                    const uint32_t adv = (uint32_t)ring.s * (kStage >> 4);
                     const uint64_t da = da0 + adv, db = db0 + adv;
                     if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < kStepK / 16; ++kk)
-                            mma_pair(acc, da + kk * kAdvA, db + kk * kAdvB, idesc, kk > 0 || kb > start);
+                        for (int u = 0; u < kP; ++u) {
+                            if (kb + u >= p.nk) break;
+#pragma unroll
+                            for (int kk = 0; kk < kStepK / 16; ++kk)
+                                mma_pair(acc, da + u * (kStep >> 4) + kk * kAdvA, db + u * (kStep >> 4) + kk * kAdvB, idesc,
+                                         u > 0 || kk > 0 || kb > start);
+                        }
                         commit_pair(&empty[ring.s]);
                         if (last_step) commit_pair(&accf[b]);
                     }
                     __syncwarp();
-                    if (last_step) { start = kb + 1; ++j; }
+                    if (last_step) { start = kb + kP; ++j; }
                     any = true;
                 }
             }
@@ -696,11 +726,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other_issued) : "r"(in_peer(su32(&issued))) : "memory");
         if (*abort_flag || other_abort) {
             const int last = max(issued, other_issued);
-            for (int s = max(0, last - kPairStages); s < last; ++s) {
-                if (issued <= s) mbar_arrive(&full[s % kPairStages]);
-                if (other_issued <= s) mbar_arrive(&full[s % kPairStages]);
+            for (int s = max(0, last - kStages); s < last; ++s) {
+                if (issued <= s) mbar_arrive(&full[s % kStages]);
+                if (other_issued <= s) mbar_arrive(&full[s % kStages]);
             }
-            for (int s = max(0, last - kPairStages); s < last; ++s) drain_wait(&full[s % kPairStages], (s / kPairStages) & 1, p.wait_ns);
+            for (int s = max(0, last - kStages); s < last; ++s) drain_wait(&full[s % kStages], (s / kStages) & 1, p.wait_ns);
             if (p.status) atomicCAS(p.status, (int)MOE_OK, (int)MOE_ERR_TIMEOUT);
         }
     }
@@ -751,8 +781,9 @@ bool fill(LinearParams& p, const LinearArgs& a) {
 // Runs of even length, none longer than the output's type allows.
 int run_of(int steps, int y_type) {
     const int longest = y_type == MOE_F32 ? kRun32 : kRun16;
-    return ceil_div(steps, ceil_div(steps, longest));
+    return (ceil_div(steps, ceil_div(steps, longest)) + kPer - 1) / kPer * kPer;     // (whole stages)
 }
+static_assert(kRun32 % kPer == 0 && kRun16 % kPer == 0, "runs of whole stages");
 
 constexpr int kSplitSmem = 227 * 1024 - 1024;            // dynamic shared memory of split_kernel, at most
 
@@ -799,13 +830,14 @@ struct Shape {
 };
 // The least time by a model of both kernels, in us, fitted to graphs of calls on weights that come from HBM (512..7168 wide,
 // T = 16..1024; it is within 15 % there):
-//   split, of `cols` columns:  start[cols] + steps of the sum a CTA * step[cols] + 0.4 where CTAs share a sum
-//   pairs, of `cols` columns:  3.5 + 0.009 cols + waves * steps * pair_step(cols)
-// A step is bound by what an SM can load (18 to 32 KB); the start holds launch, first load and epilogue.  Measured, split /
-// pairs at their best: 64 rows, 2048 -> 2048: 7.2 / 9.8; 256 rows, 2048 -> 2048: 10.2 / 10.2, 768 -> 2048: 7.7 / 6.4, 7168 -> 2048:
-// 17.1 / 25.6, 2048 -> 7168: 16.8 / 12.5; 512 rows, 2048 -> 2048: 14.0 / 10.8.
-Shape shape_of(const LinearArgs& a, const void* const (&fns)[4]) {
-    static const float start[4] = {3.4f, 3.9f, 5.2f, 7.4f}, step[4] = {0.229f, 0.241f, 0.236f, 0.252f};
+//   split, of `cols` columns:  start[cols] + steps of the sum a CTA * step[cols] + 0.3 + 0.2 CTAs where they share a sum
+//   pairs, of `cols` columns:  3.4 + 0.009 cols + waves * steps * pair_step(cols)
+// The start holds launch, first load and epilogue.  Measured, split / pairs at their best: 16 rows, 2048 -> 2048: 5.6 / 8.4;
+// 64 rows, 2048 -> 2048: 6.7 / 8.4, 7168 -> 2048: 10.3 / 20.8; 128 rows, 768 -> 2048: 5.7 / 5.5; 256 rows, 2048 -> 2048: 9.1 / 8.6,
+// 768 -> 2048: 6.5 / 5.8, 7168 -> 2048: 16.2 / 20.2, 2048 -> 7168: 22.7 / 12.0; 512 rows, 2048 -> 2048: 11.3 / 9.2.
+// (The split kernel with tiles of 128 columns was slower than one or the other at each of these.)
+Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
+    static const float start[3] = {3.35f, 3.95f, 5.2f}, step[3] = {0.155f, 0.162f, 0.168f};
     const int nk = ceil_div(a.K, kStepK), sms = sm_count();
     Shape best{0, 0};
     float least = 1e30f;
@@ -815,47 +847,46 @@ Shape shape_of(const LinearArgs& a, const void* const (&fns)[4]) {
             best = Shape{cols, splits};
         }
     };
-    for (int i = 0; i < 4 && (16 << i) < 2 * a.T + 16; ++i) {
+    for (int i = 0; i < 3 && (16 << i) < 2 * a.T + 16; ++i) {
         const int64_t tiles = (int64_t)ceil_div(a.N, 128) * ceil_div(a.T, 16 << i);
         if (tiles > 4 * sms) continue;
         take(start[i] + ceil_div(tiles, sms) * nk * step[i], 16 << i, 1);
         for (int c = 2; c <= 8 && c <= nk && tiles * c <= sms; ++c)
-            if (tiles <= clusters_at_once(fns[i], c)) take(start[i] + 0.4f + ceil_div(nk, c) * step[i], 16 << i, c);
+            if (tiles <= clusters_at_once(fns[i], c)) take(start[i] + 0.3f + 0.2f * c + ceil_div(nk, c) * step[i], 16 << i, c);
     }
     // (beyond some waves, all of them full: the largest tiles)
     for (int nb = ceil_div(a.T, kPairCols), most = std::min(ceil_div(a.T, 32), nb + 64); nb <= most; ++nb) {
         const int cols = (ceil_div(a.T, nb) + 31) & ~31;
-        const float per = cols <= 128 ? 0.193f : 0.193f + (cols - 128) * 0.00053f;
+        const float per = cols <= 128 ? 0.150f + 0.00014f * cols : 0.117f + 0.00057f * cols;
         const int64_t waves = ceil_div((int64_t)ceil_div(a.N, 256) * ceil_div(a.T, cols), sms / 2);
-        take(3.5f + 0.009f * cols + waves * nk * per, cols, 0);
+        take(3.4f + 0.009f * cols + waves * nk * per, cols, 0);
     }
     return best;
 }
-const void* const kSplit[2][4] = {{(const void*)split_kernel<false, 16>, (const void*)split_kernel<false, 32>,
-                                   (const void*)split_kernel<false, 64>, (const void*)split_kernel<false, 128>},
-                                  {(const void*)split_kernel<true, 16>, (const void*)split_kernel<true, 32>,
-                                   (const void*)split_kernel<true, 64>, (const void*)split_kernel<true, 128>}};
+const void* const kSplit[2][3] = {
+    {(const void*)split_kernel<false, 16>, (const void*)split_kernel<false, 32>, (const void*)split_kernel<false, 64>},
+    {(const void*)split_kernel<true, 16>, (const void*)split_kernel<true, 32>, (const void*)split_kernel<true, 64>}};
 
 cudaError_t launch_split(const LinearArgs& a, Shape shape, cudaStream_t s) {
     LinearParams p{};
     p.cols = shape.cols;
-    p.box = p.cols > 64 ? 3 : p.cols > 32 ? 2 : p.cols > 16 ? 1 : 0;
+    p.box = p.cols > 32 ? 2 : p.cols > 16 ? 1 : 0;
     if (!fill(p, a)) return cudaErrorInvalidValue;
     p.n_mb = ceil_div(a.N, 128);
     p.n_tb = ceil_div(a.T, p.cols);
     const void* fn = kSplit[a.in_out][p.box];
-    static std::atomic<uint64_t> ready[8];
+    static std::atomic<uint64_t> ready[6];
     int sms = 0;
-    cudaError_t err = prepare_kernel(fn, kSplitSmem, ready[4 * a.in_out + p.box], &sms);
+    cudaError_t err = prepare_kernel(fn, kSplitSmem, ready[3 * a.in_out + p.box], &sms);
     if (err != cudaSuccess) return err;
-    const int steps = ceil_div(p.nk, shape.splits), stage = kABytes + p.cols * 128, sent = p.cols * 512;
+    const int steps = ceil_div(p.nk, shape.splits), stage = kPer * (kABytes + p.cols * 128), sent = p.cols * 512;
     const int parts = shape.splits > 1 ? ceil_div(p.cols, shape.splits) * shape.splits * 512 : 0;
     p.run = run_of(steps, a.y_type);
     auto fours = [](const void* q, int type, int64_t stride) {
         return !q || ((uintptr_t)q % (type == MOE_F32 ? 16 : 8) == 0 && stride % 4 == 0);
     };
     p.vec = a.N % 4 == 0 && fours(a.y, a.y_type, a.y_stride) && fours(a.r, a.r_type, a.r_stride);
-    p.stages = std::min(std::min(steps, kMaxStages), (kSplitSmem - 1024 - parts) / stage);
+    p.stages = std::min(std::min(ceil_div(steps, kPer), kMaxStages), (kSplitSmem - 1024 - parts) / stage);
     void* args[] = {&p};
     return launch_clusters(fn, dim3(p.n_mb * shape.splits, p.n_tb), shape.splits, 1024 + (size_t)std::max(p.stages * stage, sent) + parts,
                            s, args);
@@ -863,16 +894,17 @@ cudaError_t launch_split(const LinearArgs& a, Shape shape, cudaStream_t s) {
 
 cudaError_t launch_pairs(const LinearArgs& a, Shape shape, cudaStream_t s) {
     LinearParams p{};
-    static std::atomic<uint64_t> ready[4];
+    static std::atomic<uint64_t> ready[8];
     int sms = 0;
-    const bool runs = ceil_div(a.K, kStepK) > (a.y_type == MOE_F32 ? kRun32 : kRun16);
-    const int v = (a.in_out ? 2 : 0) + (runs ? 1 : 0);
-    const void* fn = v == 3   ? (const void*)pair_kernel<true, true>
-                     : v == 2 ? (const void*)pair_kernel<true, false>
-                     : v == 1 ? (const void*)pair_kernel<false, true>
-                              : (const void*)pair_kernel<false, false>;
-    constexpr size_t kSmem = 1024 + (size_t)kPairStages * kPairStageBytes;
-    cudaError_t err = prepare_kernel(fn, (int)kSmem, ready[v], &sms);
+    const bool runs = ceil_div(a.K, kStepK) > (a.y_type == MOE_F32 ? kRun32 : kRun16), wide = shape.cols > 128;
+    const int v = (a.in_out ? 4 : 0) + (runs ? 2 : 0) + (wide ? 1 : 0);
+    static const void* const fns[8] = {(const void*)pair_kernel<false, false, false>, (const void*)pair_kernel<false, false, true>,
+                                       (const void*)pair_kernel<false, true, false>,  (const void*)pair_kernel<false, true, true>,
+                                       (const void*)pair_kernel<true, false, false>,  (const void*)pair_kernel<true, false, true>,
+                                       (const void*)pair_kernel<true, true, false>,   (const void*)pair_kernel<true, true, true>};
+    const void* fn = fns[v];
+    const int smem = 1024 + (wide ? kPairStages<true> * kPairPer<true> * kPairStep<true> : kPairStages<false> * kPairPer<false> * kPairStep<false>);
+    cudaError_t err = prepare_kernel(fn, smem, ready[v], &sms);
     if (err != cudaSuccess) return err;
     p.cols = shape.cols;
     p.box = p.cols > 128 ? 3 : p.cols > 64 ? 2 : p.cols > 32 ? 1 : 0;
@@ -882,7 +914,7 @@ cudaError_t launch_pairs(const LinearArgs& a, Shape shape, cudaStream_t s) {
     p.run = run_of(p.nk, a.y_type);
     const int64_t tiles = (int64_t)p.n_mb * p.n_tb;
     void* args[] = {&p};
-    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, sms / 2)), runs ? kPairThreads<true> : kPairThreads<false>, kSmem,
+    return launch_early(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, sms / 2)), runs ? kPairThreads<true> : kPairThreads<false>, smem,
                         s, args);
 }
 
