@@ -79,7 +79,7 @@ def _compare(got, want, upstream=1.0, base=None):
         assert (bad <= 0).all(), (bad.max(), int((bad > 0).sum()))
 
 
-_SIZES = [(1, 1, 1, 0), (1, 8, 2, 0), (3, 7, 3, 0), (32, 128, 8, 0), (33, 31, 4, 1), (100, 33, 1, 0), (257, 130, 8, 4), (1000, 256, 8, 0),
+_SIZES = [(1, 1, 1, 0), (1, 8, 2, 0), (3, 7, 3, 0), (32, 128, 8, 0), (33, 31, 4, 1), (100, 33, 1, 0), (64, 256, 8, 0), (65, 256, 8, 0), (257, 130, 8, 4), (1000, 256, 8, 0),
           (4096, 128, 8, 0), (700, 255, 5, 3), (77, 500, 6, 0), (130, 512, 8, 4), (40, 1024, 32, 0), (50, 1001, 7, 0), (9000, 64, 6, 0)]
 
 
@@ -233,3 +233,16 @@ def test_balance_captured_two_at_once_and_on_another_stream(T, E):
         torch.cuda.synchronize()
         for got in outs + [eager]:
             assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_balance_of_rows_that_lie_far_apart():
+    """Strides of 2^30 + 4 elements: offsets beyond 32 bits in elements and bytes."""
+    T, E, k, far = 5, 64, 4, (1 << 30) + 4
+    logits, ids = _inputs(T, E, k)
+    op = moe.BalanceLoss(E, k)
+    want = op(logits, ids, dlogits=True)
+    buf = torch.empty(4 * far + 2 * E, device="cuda")
+    l, d = (buf[i * E:].as_strided((T, E), (far, 1)) for i in range(2))
+    l.copy_(logits)
+    got = op(l, ids, dlogits=d)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

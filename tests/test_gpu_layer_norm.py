@@ -55,6 +55,13 @@ _CASES = [
     (2, 8192, F32, F32, True, True, 0, 1), (3, 8200, BF, BF, True, True, 0, 1), (2, 16384, F32, BF, True, True, 0, 0),
     (2, 16383, BF, BF, True, False, 0, 0), (2, 32768, F32, F32, True, True, 0, 100), (2, 32767, F32, HF, False, True, 5, 0),
     (2500, 8200, BF, BF, True, True, 0, 0),
+    # more rows than two for each SM: the kernels by type, rows of all their channels and not, read 16 bytes, 8 bytes and one by one
+    (400, 512, F32, F32, True, True, 0, 100), (400, 1000, F32, BF, True, True, 0, 1), (400, 2048, F32, HF, True, True, 4, 1),
+    (400, 4096, BF, BF, True, True, 0, 1), (400, 1024, HF, HF, True, True, 8, 0), (400, 1004, BF, BF, True, True, 0, 1),
+    (400, 1024, BF, F32, True, True, 0, 1), (400, 777, HF, F32, True, False, 0, 1), (400, 777, BF, BF, False, True, 3, 1),
+    (400, 64, F32, BF, True, True, 1, 1), (400, 8192, F32, F32, True, True, 0, 1), (400, 8184, BF, BF, True, True, 0, 1),
+    (400, 7168, HF, HF, True, True, 8, 0), (400, 3, F32, F32, True, True, 0, 0), (400, 600, HF, BF, True, True, 0, 1),
+    (4000, 320, F32, BF, True, True, 0, 1), (9000, 40, BF, BF, True, True, 0, 1),
 ]
 _ID = lambda c: "-".join(str(v).replace("torch.", "") for v in c)  # noqa: E731
 
@@ -209,3 +216,21 @@ def test_layer_norm_captured_two_at_once_and_on_another_stream():
         torch.cuda.synchronize()
         for got in outs + [eager]:
             assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_layer_norm_of_rows_that_lie_far_apart():
+    """Strides of 2^31 + 8 elements: offsets beyond 32 bits in elements and bytes."""
+    T, H, far = 3, 264, (1 << 31) + 8
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    gamma = 1 + 0.1 * torch.randn(H, generator=gen, device="cuda")
+    op = moe.LayerNorm(H, gamma=gamma, beta=gamma)
+    x0, d0 = (torch.randn(T, H, generator=gen, device="cuda").to(BF) for _ in range(2))
+    want, mean, rstd = op(x0)
+    sums = op.backward(d0, x0, mean, rstd, add=d0)
+    buf = torch.empty(2 * far + 4 * H, dtype=BF, device="cuda")
+    x, y, dy, dx = (buf[i * H:].as_strided((T, H), (far, 1)) for i in range(4))
+    x.copy_(x0)
+    dy.copy_(d0)
+    op(x, out=y)
+    got = op.backward(dy, x, mean, rstd, add=dy, dx=dx)
+    assert torch.equal(y, want) and all(torch.equal(a, b) for a, b in zip(got, sums))

@@ -236,3 +236,19 @@ def test_linear_wait_that_runs_out_is_reported(T, N_, path):
 def test_linear_without_rows():
     op = moe.Linear(torch.zeros(16, 32, dtype=BF, device="cuda"))
     assert op(torch.zeros(0, 32, dtype=BF, device="cuda")).shape == (0, 16)
+
+
+@pytest.mark.parametrize("T, N_", [(3, 200), (2000, 1600)])
+def test_linear_of_rows_that_lie_far_apart(T, N_):
+    """Offsets beyond 32 bits: x, residual and y of one buffer, its rows 2^31 + 8 elements (3 rows) or 2^22 + 8 elements apart."""
+    K, far = 96, (1 << 31) + 8 if T == 3 else (1 << 22) + 8
+    gen = _gen(2)
+    op = moe.Linear(torch.randn(N_, K, generator=gen, device="cuda").to(BF), act="silu")
+    x0, r0 = torch.randn(T, K, generator=gen, device="cuda").to(BF), torch.randn(T, N_, generator=gen, device="cuda").to(BF)
+    want = op(x0, residual=r0)
+    buf = torch.empty((T - 1) * far + K + 2 * N_, dtype=BF, device="cuda")
+    x, r, y = (buf[i:].as_strided((T, w), (far, 1)) for i, w in ((0, K), (K, N_), (K + N_, N_)))
+    x.copy_(x0)
+    r.copy_(r0)
+    op(x, residual=r, out=y)
+    assert torch.equal(y, want)
