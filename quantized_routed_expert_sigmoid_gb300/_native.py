@@ -102,6 +102,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """The loaded CUDA library (built in-tree on first use when missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()

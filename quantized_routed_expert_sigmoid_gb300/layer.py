@@ -452,10 +452,20 @@ def _value_rows(t, name, T, width):
 
 
 def _given(t, name, dtypes, numel):
-    """t (or None), after checks: dense, of one of these types, numel entries, on the GPU."""
+    """Refuses a tensor (None passes) that is not dense, of one of these types, of numel entries and on the GPU."""
     if t is not None and (t.dtype not in dtypes or t.numel() != numel or not t.is_contiguous() or not t.is_cuda):
         raise ValueError(f"{name} must be a dense CUDA tensor of {numel} entries, one of {[str(d) for d in dtypes]}")
-    return t
+
+
+def _all_on(device, names, *tensors):
+    """As _on_current, without a dictionary of the tensors where nothing is wrong (about 1 us of a call)."""
+    if device == torch.cuda.current_device():
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                break
+        else:
+            return
+    _on_current(device, **dict(zip(names, tensors)))
 
 
 class Linear(_Checked):
@@ -512,7 +522,7 @@ class Linear(_Checked):
             out = _empty((T, self.n_out), self.y_dtype, x.device, stream)
         elif out.dtype is not self.y_dtype or out.shape != (T, self.n_out) or not out.is_cuda:
             raise ValueError(f"out must be a {self.y_dtype} CUDA tensor [{T}, {self.n_out}]")
-        _on_current(self.device, x=x, residual=residual, out=out, status=status)
+        _all_on(self.device, ("x", "residual", "out", "status"), x, residual, out, status)
         N.moe_linear(self.plan, x, _row_stride(x, "x"), T, residual, rt, rs, out, _row_stride(out, "out"),
                      self._status if status is None else status, stream)
         return out
@@ -538,11 +548,11 @@ class LayerNorm:
         self._keep = (gamma, beta)
         self._desc, self._bytes = {}, {}  # the call's description, by the types of its tensors; its workspace, by T
 
-    def _described(self, x, y_dtype, **tensors):
+    def _described(self, x, y_dtype, names, *tensors):
         device = x.get_device()
         if self.device is not None and device != self.device:
             raise ValueError(f"x is on device {device}, gamma / beta on device {self.device}")
-        _on_current(device, **tensors)
+        _all_on(device, names, *tensors)
         desc = self._desc.get((x.dtype, y_dtype))
         if desc is None:
             g = [t.data_ptr() if t is not None else None for t in self._keep]
@@ -569,7 +579,7 @@ class LayerNorm:
             _given(rstd, "rstd", (torch.float32,), T)
         elif stats:
             rstd = _empty((T,), torch.float32, x.device, stream)
-        desc = self._described(x, out.dtype, out=out, mean=mean, rstd=rstd)
+        desc = self._described(x, out.dtype, ("out", "mean", "rstd"), out, mean, rstd)
         N.moe_layer_norm(desc, x, xs, T, out, ys, mean, rstd, stream)
         return out, mean, rstd
 
@@ -613,7 +623,8 @@ class LayerNorm:
                 dgamma = _empty((H,), torch.float32, x.device, stream)
             if make[1]:
                 dbeta = _empty((H,), torch.float32, x.device, stream)
-        desc = self._described(x, dy.dtype, dy=dy, mean=mean, rstd=rstd, add=add, dx=dx, dgamma=dgamma, dbeta=dbeta)
+        desc = self._described(x, dy.dtype, ("dy", "mean", "rstd", "add", "dx", "dgamma", "dbeta"), dy, mean, rstd, add, dx, dgamma,
+                               dbeta)
         N.moe_layer_norm_backward(desc, dy, gs, x, xs, mean, rstd, add, as_, T, dx, ds, dgamma, dbeta, accumulate, ws, nbytes,
                                   stream)
         return dx, dgamma, dbeta
@@ -654,39 +665,52 @@ class BalanceLoss(_Checked):
         gradient, True: made; given, it is overwritten (it may be logits) or, with accumulate, added to.  Bad ids and offsets are
         reported by device_status() or in status.  Outputs that are not given are made in the order of `stream`.
         """
-        T = logits.shape[0]
-        if logits.dtype is not torch.float32 or logits.shape != (T, self.E) or not logits.is_cuda:
+        T, E = logits.shape
+        if logits.dtype is not torch.float32 or E != self.E or not logits.is_cuda:
             raise ValueError(f"logits must be an fp32 CUDA tensor [T, {self.E}]")
-        n_seqs = 1 if offsets is None else offsets.numel() - 1
-        if n_seqs < 1:
-            raise ValueError("offsets must have an entry for every sequence and one more")
-        _given(offsets, "offsets", (torch.int32,), n_seqs + 1)
-        if _given(ids, "ids", (torch.int32,), T * self.k) is None:
+        if ids is None:
             raise ValueError("ids are missing")
-        _given(mask, "mask", (torch.bool, torch.uint8), T)
-        _given(upstream, "upstream", (torch.float32,), 1)
+        _given(ids, "ids", (torch.int32,), T * self.k)
+        n_seqs = 1
+        if offsets is not None:
+            n_seqs = offsets.numel() - 1
+            if n_seqs < 1:
+                raise ValueError("offsets must have an entry for every sequence and one more")
+            _given(offsets, "offsets", (torch.int32,), n_seqs + 1)
+        if mask is not None:
+            _given(mask, "mask", (torch.bool, torch.uint8), T)
+        if upstream is not None:
+            _given(upstream, "upstream", (torch.float32,), 1)
         if status is not None and (status.dtype is not torch.int32 or status.numel() < 1 or not status.is_cuda):
             raise ValueError("status must be an int32 CUDA tensor")
+        ds = 0
         if dlogits is True or dlogits is False:
             if accumulate and dlogits:
                 raise ValueError("dlogits must be given to be added to")
-            dlogits = _empty((T, self.E), torch.float32, logits.device, stream) if dlogits else None
-        elif dlogits is not None and (dlogits.dtype is not torch.float32 or dlogits.shape != (T, self.E) or not dlogits.is_cuda):
-            raise ValueError(f"dlogits must be an fp32 CUDA tensor [{T}, {self.E}]")
-        loss = _empty((1,), torch.float32, logits.device, stream) if loss is None else _given(loss, "loss", (torch.float32,), 1)
-        counts = (_empty((n_seqs, self.E), torch.int32, logits.device, stream) if counts is None
-                  else _given(counts, "counts", (torch.int32,), n_seqs * self.E))
-        _on_current(logits.get_device(), ids=ids, offsets=offsets, mask=mask, upstream=upstream, loss=loss, counts=counts,
-                    dlogits=dlogits, status=status)
+            dlogits = _empty((T, E), torch.float32, logits.device, stream) if dlogits else None
+        if dlogits is not None:
+            if dlogits.dtype is not torch.float32 or dlogits.shape != (T, E) or not dlogits.is_cuda:
+                raise ValueError(f"dlogits must be an fp32 CUDA tensor [{T}, {E}]")
+            ds = _row_stride(dlogits, "dlogits")
+        if loss is None:
+            loss = _empty((1,), torch.float32, logits.device, stream)
+        else:
+            _given(loss, "loss", (torch.float32,), 1)
+        if counts is None:
+            counts = _empty((n_seqs, E), torch.int32, logits.device, stream)
+        else:
+            _given(counts, "counts", (torch.int32,), n_seqs * E)
+        device = logits.get_device()
+        _all_on(device, ("ids", "offsets", "mask", "upstream", "loss", "counts", "dlogits", "status"), ids, offsets, mask, upstream, loss,
+                counts, dlogits, status)
         if status is None:
             status = self._status
-            if status is not None and status.get_device() != logits.get_device():
-                raise ValueError(f"logits are on device {logits.get_device()}, this object's calls on device {status.get_device()}")
+            if status is not None and status.get_device() != device:
+                raise ValueError(f"logits are on device {device}, this object's calls on device {status.get_device()}")
         nbytes = self._bytes.get((T, n_seqs))
         if nbytes is None:
             nbytes = self._bytes[T, n_seqs] = N.moe_balance_workspace_size(self.E, T, n_seqs)
         ws = _empty((nbytes,), torch.uint8, logits.device, stream)       # (of the stream's memory: free again behind the call)
         N.moe_balance_loss(self._desc[bool(accumulate)], logits, _row_stride(logits, "logits"), ids, T, offsets, n_seqs, mask,
-                           upstream, loss, counts, dlogits, _row_stride(dlogits, "dlogits") if dlogits is not None else 0, status,
-                           ws, nbytes, stream)
+                           upstream, loss, counts, dlogits, ds, status, ws, nbytes, stream)
         return loss, counts, dlogits
