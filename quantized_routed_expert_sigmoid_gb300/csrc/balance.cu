@@ -124,6 +124,11 @@ __device__ __forceinline__ float exp2_quick(float x) {    // relative error 2^-2
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float rcp_quick(float x) {     // relative error 2^-23
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // The sum over the CTA's threads, in one order (thread 0 has it).
 __device__ __forceinline__ float cta_sum(float v, float* part) {
 #pragma unroll
@@ -247,17 +252,26 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
                     for (int j = 0; j < V; ++j) {
                         const float v = l[o][i][j];
                         if constexpr (SIGMOID) {
-                            // sigmoid = (v > 0 ? 1 : z) / (1 + z), 1 - sigmoid = (v > 0 ? z : 1) / (1 + z), z = e^-|v|; a token of negative
-                            // logits alone (its whole warp) takes e^(v - max) for z above
-                            const float z = kBack * exp2_quick(fmaf(-kLog2e, fabsf(v), 32.0f)), one = __fdividef(1.0f, 1.0f + z);
-                            float num = v > 0.f ? 1.0f : z;
-                            if (top < 0.f) num = exp2_quick(fmaf(kLog2e, v - top, 32.0f));
-                            q[o][i][j] = num * one;
-                            l[o][i][j] = (v > 0.f ? z : 1.0f) * one;
+                            // sigmoid = (v > 0 ? 1 : z) / (1 + z), 1 - sigmoid = (v > 0 ? z : 1) / (1 + z), z = e^-|v|
+                            const float z = kBack * exp2_quick(fmaf(-kLog2e, fabsf(v), 32.0f)), one = rcp_quick(1.0f + z);
+                            const bool up = v > 0.f;
+                            q[o][i][j] = (up ? 1.0f : z) * one;
+                            if (top >= 0.f) l[o][i][j] = (up ? z : 1.0f) * one;
                         } else {
                             q[o][i][j] = exp2_quick(fmaf(kLog2e, v - top, 32.0f));
                         }
                     }
+                if (SIGMOID && top < 0.f) {
+                    // negative logits alone (the token's whole warp): e^(v - max) in the place of z
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float v = l[o][i][j], one = rcp_quick(1.0f + kBack * exp2_quick(fmaf(kLog2e, v, 32.0f)));
+                            q[o][i][j] = exp2_quick(fmaf(kLog2e, v - top, 32.0f)) * one;
+                            l[o][i][j] = one;
+                        }
+                }
                 sum[o] = dot[o] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
@@ -278,7 +292,7 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
             for (int o = 0; o < TOK; ++o) {
                 const int t = tw + o;
                 const bool none = sum[o] == 0.f;
-                const float inv = none ? 0.f : __fdividef(1.0f, sum[o]);
+                const float inv = none ? 0.f : rcp_quick(sum[o]);
                 dot[o] *= inv;
                 if (!none) shares += 1.0f + dot[o];
                 if (!a.dlogits || t >= s1 || (!live[o] && a.accumulate)) continue;
