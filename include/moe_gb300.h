@@ -430,7 +430,7 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
  * The plan keeps the pointers; weights and bias must outlive it and may change between calls.
  * Call: x (device, 16-byte aligned) T rows x_stride elements apart (a multiple of 8, >= n_in); r (device, nullable) T rows of
  *   r_type, r_stride >= n_out elements apart; y (device) T rows, y_stride >= n_out; r and y aligned to their types.
- *   y may be r with r's type and stride; otherwise y must not overlap r, and never x (columns of one
+ *   y may be r with r's type and stride; otherwise y must not overlap r, and never x, w or bias (columns of one
  *   buffer, as for moe_grouped_matmul, do not).  status (device int32, nullable, never cleared by the call): raised from MOE_OK to
  *   MOE_ERR_TIMEOUT when a device-side wait ran out (y is undefined).  T <= 2^30, strides <= 2^32; T = 0 is a no-op.
  *   One launch, no workspace, nothing kept between calls; a captured call replays with the bits of the eager one.
@@ -473,13 +473,15 @@ moe_status moe_linear(const moe_linear_plan* plan, const void* x, int64_t x_stri
  *   MOE_F16; gamma (NULL: 1), beta (NULL: 0; not read by the backward call): device fp32 [H]; eps >= 0.
  * x, y, dy, add, dx (device): T rows, strides in elements, at least H; mean, rstd: device fp32 [T] (the forward call's may be
  *   NULL, as may y; not all three).  Any H, stride and element-aligned pointer is accepted; aligned rows (H and strides
- *   multiples of 8, or of 4 with fp32 among the types, pointers of 16 bytes) are read 16 bytes at a time.
+ *   multiples of 4, pointers aligned to 4 elements; with 16-bit types alone 8 of each where they allow it) are read 8 or 16
+ *   bytes at a time.
  *   y must not overlap x unless it is x, with its type and stride; dx may be add, x or dy itself (same type and
  *   stride; none of the others overlaps it).  dx, dgamma, dbeta: nullable, not all.
  * dgamma, dbeta (device fp32 [H]): overwritten, or added to with accumulate = 1; the sums over the rows have one order (the
  *   bits are those of every run).  They need a workspace (device, 256-byte aligned) of moe_layer_norm_backward_workspace_size
  *   bytes, which is free again when the call is done; calls that may overlap need one each.  dx alone needs none.
- * T <= 2^30; T = 0: nothing but dgamma = dbeta = 0 (unless accumulate).  The backward call launches two kernels.
+ * T <= 2^30; T = 0: nothing but dgamma = dbeta = 0 (unless accumulate).  The backward call launches two kernels,
+ *   one for dx alone.
  */
 typedef struct {
     int H;
@@ -520,7 +522,7 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_desc* desc, const void* 
  *   may overlap need one each.  status (device int32, nullable, never cleared by the call): raised to MOE_ERR_DEVICE_CHECK when
  *   an id of a counted token leaves 0..E-1 (it is not counted) or an offset leaves 0..T or decreases (the outputs are undefined).
  * T*k <= 2^30, n_seqs 1..65535; T = 0: loss = 0, counts = 0.  All sums have one order: the same bits each time.
- * Up to three launches.
+ * One launch up to 64 tokens, two beyond.
  */
 typedef struct {
     moe_route_mode mode;

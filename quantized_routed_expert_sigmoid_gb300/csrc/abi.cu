@@ -834,6 +834,11 @@ moe_status moe_linear(const moe_linear_plan* plan, const void* x, int64_t x_stri
     const bool in_place = r == y && (int)r_type == a.y_type && (r_stride == y_stride || T == 1);
     if (meet(sx, sy)) return fail(MOE_ERR_INVALID_ARG, "y overlaps x");
     if (!in_place && meet(sr, sy)) return fail(MOE_ERR_INVALID_ARG, "y overlaps r without being it");
+    const uint64_t wide = a.in_out ? a.N : a.K, bias_bytes = a.bias ? value_bytes(a.bias_type) * (uint64_t)a.N : 0;
+    const RowSpan sw{(uintptr_t)a.w, 2 * wide, 2 * (uint64_t)a.w_stride, a.in_out ? a.K : a.N};
+    const RowSpan sb{(uintptr_t)a.bias, bias_bytes, bias_bytes, a.bias ? 1 : 0}, ss{(uintptr_t)status, 4, 4, status ? 1 : 0};
+    if (meet(sw, sy) || meet(sb, sy)) return fail(MOE_ERR_INVALID_ARG, "y overlaps w or bias");
+    if (meet(ss, sy) || meet(ss, sx) || meet(ss, sr)) return fail(MOE_ERR_INVALID_ARG, "status overlaps x, r or y");
     a.T = T;
     a.x = x; a.x_stride = x_stride;
     a.r = r; a.r_type = r_type; a.r_stride = r_stride;

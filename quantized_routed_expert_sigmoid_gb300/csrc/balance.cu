@@ -13,6 +13,10 @@
 // (the only atomics are on whole numbers).
 // f - 1 = (E c - k n) / (k n) takes the place of f in the gradient (the p sum to 1): nothing cancels where the load is balanced.
 // No 64-bit floating point: its rate is a 64th of fp32's, and a handful of divisions took longer than the rest of a small call.
+// Measured, loss, counts and gradient: 32 tokens of 128 experts, top 8, 4.8 us; 4096 of them 11.2 us (bytes alone 0.6): two launches,
+// each with a chain of dependent reads; 32768 tokens of 256 experts in 16 sequences, sigmoid, masked: 27.4 us (bytes alone 10.1), of
+// which the counts take 8 and the pass 19, there bound by its instructions (60 % of the issue
+// slots: an exponential and a reciprocal an element are among them).
 #include <algorithm>
 
 #include "block_ops.cuh"

@@ -2,12 +2,19 @@
 //   y[t, n] = res_scale * r[t, n] + scale * act(sum_c W[n, c] x[t, c] + bias[n])
 // The weights are the M operand (a lane of TMEM holds one output channel, a column one row of x): a few rows of x
 // then cost a few columns, and the bias is one register.  Everything behind the sum happens between TMEM and
-// the one store of y, in fp32.  Two kernels:
+// the one store of y, in fp32.  Two kernels; which one, and how a product is cut, is shape_of's model of their times:
 // - split_kernel: tiles of 128 channels by up to 64 rows of x, one CTA each; where that leaves SMs idle, a cluster
 //   of up to 8 CTAs splits the sum of a tile.  Each CTA sends the columns of its part to the CTA of the cluster that finishes
 //   them (shared memory of the cluster, no workspace), which adds the parts in their order.
+//   Bound: latency.  1 x 2048 -> 2048 with bias and residual, bf16: 5.3 us, 32 x 2048 -> 7168 with bias and GELU: 9.7 us, on
+//   weights from HBM (their bytes alone take 1.2 and 4.4 us): 3 us are the launch, the first load and the closing code, the rest
+//   is steps of the sum at 0.16 us each.
 // - pair_kernel: tiles of 256 channels by up to 256 rows, a pair of CTAs (cta_group::2) each, persistent, two accumulators: one
 //   is read out while the next tile runs.  A weight is read from L2 once per 256 rows.
+//   Bound: the matrix instructions (81 % of the pipe's time).  4096 x 2048 -> 7168, bf16 with bias and GELU: 66.7 us, 1.80 PFLOP/s
+//   (without an epilogue 65.6; the floor at cuBLAS's best rate 62.3); 4096 x 7168 -> 2048 with bias and residual, fp32 outputs, sums
+//   in runs: 75.2 us, 1.60 PFLOP/s (without residual 68.5, bf16 outputs 70.2).  Columns are dealt evenly to as few waves of tiles as
+//   there can be: the last wave is what large products lose.
 // The tensor cores cut a sum off after each instruction instead of rounding it, an error that grows with the
 // sum's length; so long sums are made of runs (768 elements for fp32 outputs, 8192 for 16-bit ones), which the epilogue
 // adds with rounding in its registers.
@@ -38,12 +45,12 @@ struct Epilogue {
 
 struct LinearParams {
     CUtensorMap tw;              // W: boxes of 64 x 128, or 64 x 64 of [K][N]
-    CUtensorMap tx[4];           // x: boxes of 64 x 16, 32, 64, 128
+    CUtensorMap tx;              // x: boxes of 64 x (16 << box)
     Epilogue e;
-    int K, nk, run;              // nk: steps of the sum, run: of one run
+    int nk, run;                 // nk: steps of the sum, run: of one run
     bool bf16;
     int cols;                    // columns of a tile (split: 16, 32 or 64; pairs: a multiple of 32)
-    int box;                     // which of tx
+    int box;                     // rows of a box of x: 16 << box
     int stages;
     bool vec;                    // four neighbouring channels of r and y can be read and written at once (split)
     int n_mb, n_tb;              // tiles along the channels and along the rows of x
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 64) prefetch_map(&p.tw);
-    if (tid == 96) prefetch_map(&p.tx[p.box]);
+    if (tid == 96) prefetch_map(&p.tx);
     __syncwarp();
     tc_before();
     __syncthreads();
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 ? 2 : 1) split_kernel(con
         // ======================= loads =======================
         // (the whole warp keeps step, so that what one lane issues lies in uniform registers)
         const uint32_t stage0 = su32(smem), full0 = su32(full);
-        const CUtensorMap* xmap = &p.tx[p.box];
+        const CUtensorMap* xmap = &p.tx;
         int g = 0, s = 0;
         uint32_t ph = 1;
         for (int kb = k0; kb < k1; kb += kPer, ++g) {
@@ -531,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 
         issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tw);
-        prefetch_map(&p.tx[p.box]);
+        prefetch_map(&p.tx);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)), "n"(kPairTmem)
@@ -575,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<RUNS>, 
                         } else {
                             tma_2d(a, &p.tw, c, r0, bar);
                         }
-                        tma_2d(a + kABytes, &p.tx[p.box], c, c0, bar);
+                        tma_2d(a + kABytes, &p.tx, c, c0, bar);
                     }
                 }
                 __syncwarp();
@@ -767,9 +774,8 @@ bool fill(LinearParams& p, const LinearArgs& a) {
     const cuuint64_t xs[2] = {(cuuint64_t)a.x_stride * 2, 0};
     const CUtensorMapDataType type = a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (!encode_map(&p.tw, type, 2, a.w, wd, ws, 64, a.in_out ? 64 : 128)) return false;
-    if (!encode_map(&p.tx[p.box], type, 2, a.x, xd, xs, 64, 16 << p.box)) return false;
+    if (!encode_map(&p.tx, type, 2, a.x, xd, xs, 64, 16 << p.box)) return false;
     p.e = Epilogue{a.bias, a.r, a.y, a.bias_type, a.r_type, a.y_type, a.act, a.r_stride, a.y_stride, a.scale, a.res_scale, a.T, a.N};
-    p.K = a.K;
     p.nk = ceil_div(a.K, kStepK);
     p.bf16 = a.bf16;
     p.status = a.status;

@@ -7,6 +7,7 @@ and calls moe_layer.  All arithmetic runs in the CUDA library.
 """
 from __future__ import annotations
 
+import functools
 import threading
 
 import torch
@@ -528,6 +529,11 @@ class Linear(_Checked):
         return out
 
 
+# Bytes of the workspaces (the queries take 1 us).
+_norm_bytes = functools.lru_cache(4096)(lambda H, T: N.moe_layer_norm_backward_workspace_size(H, T))
+_balance_bytes = functools.lru_cache(4096)(lambda E, T, n_seqs: N.moe_balance_workspace_size(E, T, n_seqs))
+
+
 class LayerNorm:
     """Layer norm over rows of H and its gradient (moe_layer_norm, moe_layer_norm_backward).
 
@@ -546,7 +552,7 @@ class LayerNorm:
                 _given(g, name, (torch.float32,), H)
         self.H, self.eps, self.y_dtype = H, eps, y_dtype
         self._keep = (gamma, beta)
-        self._desc, self._bytes = {}, {}  # the call's description, by the types of its tensors; its workspace, by T
+        self._desc = {}                  # the call's description, by the types of its tensors
 
     def _described(self, x, y_dtype, names, *tensors):
         device = x.get_device()
@@ -617,7 +623,7 @@ class LayerNorm:
         ws, nbytes = None, 0
         if dgamma is not None or dbeta is not None or any(make):
             # (of the stream's memory: free again behind the call)
-            nbytes = self._workspace(T)
+            nbytes = _norm_bytes(H, T)
             ws = _empty((nbytes,), torch.uint8, x.device, stream) if nbytes else None
             if make[0]:
                 dgamma = _empty((H,), torch.float32, x.device, stream)
@@ -628,13 +634,6 @@ class LayerNorm:
         N.moe_layer_norm_backward(desc, dy, gs, x, xs, mean, rstd, add, as_, T, dx, ds, dgamma, dbeta, accumulate, ws, nbytes,
                                   stream)
         return dx, dgamma, dbeta
-
-    def _workspace(self, T):
-        """Bytes of the backward call's workspace for T rows (by T: the query takes 1 us)."""
-        nbytes = self._bytes.get(T)
-        if nbytes is None:
-            nbytes = self._bytes[T] = N.moe_layer_norm_backward_workspace_size(self.H, T)
-        return nbytes
 
 
 class BalanceLoss(_Checked):
@@ -648,7 +647,6 @@ class BalanceLoss(_Checked):
         if mode not in ("softmax", "sigmoid"):
             raise ValueError(f"mode must be 'softmax' or 'sigmoid', not {mode!r}")
         self.E, self.k = E, k
-        self._bytes = {}                 # of the workspace, by T and sequences
         self._desc = [N.moe_balance_desc(N.MOE_ROUTE_SIGMOID_GROUP if mode == "sigmoid" else N.MOE_ROUTE_SOFTMAX, E, k, coef, a)
                       for a in (0, 1)]
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -707,9 +705,7 @@ class BalanceLoss(_Checked):
             status = self._status
             if status is not None and status.get_device() != device:
                 raise ValueError(f"logits are on device {device}, this object's calls on device {status.get_device()}")
-        nbytes = self._bytes.get((T, n_seqs))
-        if nbytes is None:
-            nbytes = self._bytes[T, n_seqs] = N.moe_balance_workspace_size(self.E, T, n_seqs)
+        nbytes = _balance_bytes(E, T, n_seqs)
         ws = _empty((nbytes,), torch.uint8, logits.device, stream)       # (of the stream's memory: free again behind the call)
         N.moe_balance_loss(self._desc[bool(accumulate)], logits, _row_stride(logits, "logits"), ids, T, offsets, n_seqs, mask,
                            upstream, loss, counts, dlogits, ds, status, ws, nbytes, stream)

@@ -50,6 +50,8 @@ _LINEAR = dict(x=FAKE, x_stride=64, T=3, r=2 * FAR, r_type=N.MOE_F32, r_stride=4
     (dict(x_stride=68), BAD, "x_stride"), (dict(y_stride=47), BAD, "y_stride"), (dict(r_stride=47), BAD, "r_stride"),
     (dict(y_stride=(1 << 32) + 1), BAD, "y_stride"), (dict(y=FAKE + 256), BAD, "overlaps x"), (dict(r=FAR + 192), BAD, "overlaps r"),
     (dict(r=FAR, r_stride=64), BAD, "overlaps r"), (dict(r=FAR, r_type=N.MOE_BF16), BAD, "overlaps r"),
+    (dict(x=3 * FAR, y=FAKE + 48 * 128 - 4), BAD, "overlaps w"), (dict(status=FAR + 3 * 192 - 4), BAD, "status overlaps"),
+    (dict(status=FAKE + 8), BAD, "status overlaps"), (dict(status=2 * FAR), BAD, "status overlaps"),
 ])
 def test_linear_call_refusals(kw, status, word):
     plan = moe.moe_linear_plan_create(N.moe_linear_desc(*_PLAN.values()))
