@@ -13,8 +13,8 @@
 // (the only atomics are on whole numbers).
 // f - 1 = (E c - k n) / (k n) takes the place of f in the gradient (the p sum to 1): nothing cancels where the load is balanced.
 // No 64-bit floating point: its rate is a 64th of fp32's, and a handful of divisions took longer than the rest of a small call.
-// Measured, loss, counts and gradient: 32 tokens of 128 experts, top 8, 4.8 us; 4096 of them 11.2 us (bytes alone 0.6): two launches,
-// each with a chain of dependent reads; 32768 tokens of 256 experts in 16 sequences, sigmoid, masked: 27.4 us (bytes alone 10.1), of
+// Measured, loss, counts and gradient: 32 tokens of 128 experts, top 8, 4.7 us; 4096 of them, masked, 11.3 us (bytes alone 0.6): two launches,
+// each with a chain of dependent reads; 32768 tokens of 256 experts in 16 sequences, sigmoid: 27.4 us (bytes alone 10.1), of
 // which the counts take 8 and the pass 19, there bound by its instructions (60 % of the issue
 // slots: an exponential and a reciprocal an element are among them).
 #include <algorithm>
@@ -26,7 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMostChunks = 1024, kMostCounts = 128;
+constexpr int kMostChunks = 1024, kMostCounts = 128, kFewSeqs = 2;
 constexpr float kInf = __builtin_huge_valf();
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -38,6 +38,7 @@ struct BalanceParams {
     int32_t* counts;             // [chunks1 + n_seqs][row]
     float* losses;               // [chunks2] shares of the loss
     uint32_t* ticket;
+    int32_t* used;               // [chunks1] sequences whose first counted token lies in the chunk
 };
 
 // First token of sequence b (b <= n_seqs), clamped into 0..T.
@@ -62,20 +63,11 @@ __device__ __forceinline__ int tokens_of(const BalanceParams& p, int b) {
     for (int c = t0 / p.len1 + (threadIdx.x & 31); c <= (t1 - 1) / p.len1; c += 32) n += p.counts[(int64_t)(c + b) * p.row + p.a.E];
     return __reduce_add_sync(kAll, n);
 }
-// Sequences with a counted token (the whole CTA asks).  word: shared.
-__device__ __forceinline__ int used_sequences(const BalanceParams& p, int* word) {
-    if (p.a.n_seqs == 1) return tokens_of(p, 0) > 0;
-    if (threadIdx.x == 0) *word = 0;
-    __syncthreads();
-    if (!p.a.mask) {
-        for (int b = threadIdx.x; b < p.a.n_seqs; b += kThreads)
-            if (start_of(p.a, b + 1) > start_of(p.a, b)) atomicAdd(word, 1);
-    } else {
-        for (int b = threadIdx.x >> 5; b < p.a.n_seqs; b += kWarps)
-            if (tokens_of(p, b) > 0 && (threadIdx.x & 31) == 0) atomicAdd(word, 1);
-    }
-    __syncthreads();
-    return *word;
+// Sequences with a counted token (a whole warp asks).
+__device__ __forceinline__ int used_sequences(const BalanceParams& p) {
+    int n = 0;
+    for (int c = threadIdx.x & 31; c < p.chunks1; c += 32) n += p.used[c];
+    return min(__reduce_add_sync(kAll, n), p.a.n_seqs);
 }
 
 // ---------------------------------------------------------------- counts
@@ -84,6 +76,7 @@ __device__ __forceinline__ void count_chunk(const BalanceParams& p, int c, int* 
     const BalanceArgs& a = p.a;
     const int tid = threadIdx.x, t0 = c * p.len1, t1 = min(t0 + p.len1, a.T);
     bool bad = false;
+    int used = 0;
     if (c == 0) {
         if (tid == 0) *p.ticket = 0;
         if (a.seq_offsets)
@@ -96,6 +89,16 @@ __device__ __forceinline__ void count_chunk(const BalanceParams& p, int c, int* 
         const int s0 = max(start_of(a, b), t0), s1 = min(start_of(a, b + 1), t1);
         if (start_of(a, b) >= t1) break;
         if (s1 <= s0) continue;
+        bool before = false;                             // a token of the sequence counts in a chunk ahead
+        if (!a.mask) before = start_of(a, b) < t0;
+        else if (a.n_seqs > 1)                           // (one alone is used by as many chunks as it likes)
+            for (int t = start_of(a, b) + tid; t - tid < t0 && !before; t += 4 * kThreads) {
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t + i * kThreads < t0) any |= a.mask[t + i * kThreads] != 0;
+                before = __syncthreads_or(any);
+            }
         for (int e = tid; e <= a.E; e += kThreads) hist[e] = 0;
         __syncthreads();
         if (a.mask)
@@ -103,17 +106,19 @@ __device__ __forceinline__ void count_chunk(const BalanceParams& p, int c, int* 
                 if (a.mask[t]) atomicAdd(&hist[a.E], 1);
 #pragma unroll 4
         for (int i = s0 * a.k + tid; i < s1 * a.k; i += kThreads) {      // (T k <= 2^30)
+            const int e = __ldg(a.ids + i);              // (beside the mask, not behind it)
             if (a.mask && !a.mask[(unsigned)i / (unsigned)a.k]) continue;
-            const int e = __ldg(a.ids + i);
             if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
             else bad = true;
         }
         __syncthreads();
+        used += !before && (!a.mask || hist[a.E] > 0);
         int32_t* out = p.counts + (int64_t)(c + b) * p.row;
         for (int e = tid; e <= a.E; e += kThreads) out[e] = hist[e];
         __syncthreads();
     }
-    if (bad && a.status) atomicCAS(a.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
+    if (tid == 0) p.used[c] = used;
+    if (__any_sync(kAll, bad) && (tid & 31) == 0 && a.status) atomicCAS(a.status, (int)MOE_OK, (int)MOE_ERR_DEVICE_CHECK);
 }
 __global__ void __launch_bounds__(kThreads) count_kernel(const __grid_constant__ BalanceParams p) {
     extern __shared__ int hist[];
@@ -147,16 +152,16 @@ __device__ __forceinline__ float cta_sum(float v, float* part) {
 }
 template <int EPL> constexpr int kResident = EPL <= 8 ? 2 : 1;     // CTAs an SM
 // Chunk c of the tokens; the chunk's share of the loss (thread 0 has it).  A warp takes TOK tokens at a time; lane l holds
-// experts (32 i + l) V + j of each, EPL in all.  fsm: shared, [E]; part: shared; word: shared.
+// experts (32 i + l) V + j of each, EPL in all.  fsm: shared, [E]; part: shared.
 template <int EPL, int V, int TOK, bool SIGMOID>
-__device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float* fsm, float* part, int* word) {
+__device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float* fsm, float* part) {
     constexpr int NC = EPL / V;
     constexpr float kLog2e = 1.4426950408889634f, kBack = 2.3283064365386963e-10f;      // 2^-32
     const BalanceArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto expert = [&](int i) { return (i * 32 + lane) * V; };
     const bool logits = a.loss || a.dlogits;
-    const int used = logits ? used_sequences(p, word) : 0;
+    const int used = logits ? used_sequences(p) : 0;
     const float up = a.upstream ? __ldg(a.upstream) : 1.0f;
     const int t0 = c * p.len2, t1 = min(t0 + p.len2, a.T);
     float loss = 0.f;
@@ -176,6 +181,17 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
         const int b0 = start_of(a, b), b1 = start_of(a, b + 1), s0 = max(b0, t0), s1 = min(b1, t1);
         if (b0 >= t1) break;
         if (s1 <= s0) continue;
+        // the mask of this warp's next 32 steps, a bit each: read step by step it held up the logits behind it (32768 tokens of 128
+        // experts in 64 sequences 24.3 us, 18.9 without a mask)
+        uint32_t seen[TOK];
+        auto look = [&](int t) {
+#pragma unroll
+            for (int o = 0; o < TOK; ++o) {
+                const int at = t + o + lane * kWarps * TOK;
+                seen[o] = __ballot_sync(kAll, at < s1 && (!a.mask || a.mask[at]));
+            }
+        };
+        look(s0 + warp * TOK);
         int* cnt = reinterpret_cast<int*>(fsm);
         for (int e = tid; e < a.E; e += kThreads) cnt[e] = 0;
         __syncthreads();
@@ -218,13 +234,18 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) f[i][j] = expert(i) + j < a.E ? fsm[expert(i) + j] : 0.f;
-        for (int tw = logits ? s0 + warp * TOK : s1; tw < s1; tw += kWarps * TOK) {
+        int step = 0;
+        for (int tw = logits ? s0 + warp * TOK : s1; tw < s1; tw += kWarps * TOK, ++step) {
+            if (step == 32) {
+                look(tw);
+                step = 0;
+            }
             float l[TOK][NC][V], q[TOK][NC][V], m[TOK], sum[TOK], dot[TOK];
             bool live[TOK];
 #pragma unroll
             for (int o = 0; o < TOK; ++o) {
                 const int t = tw + o;
-                live[o] = t < s1 && (!a.mask || a.mask[t]);
+                live[o] = (seen[o] >> step) & 1;
                 const float* row = a.logits + t * a.stride;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
@@ -329,13 +350,12 @@ template <int EPL, int V, int TOK, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, kResident<EPL>) pass_kernel(const __grid_constant__ BalanceParams p) {
     extern __shared__ float fsm[];
     __shared__ float part[kWarps];
-    __shared__ int word;
     __shared__ bool last;
     const BalanceArgs& a = p.a;
     const int tid = threadIdx.x;
     wait_for_previous();
     allow_next();
-    float v = pass_chunk<EPL, V, TOK, SIGMOID>(p, blockIdx.x, fsm, part, &word);
+    float v = pass_chunk<EPL, V, TOK, SIGMOID>(p, blockIdx.x, fsm, part);
     if (!a.loss) return;
     if (tid == 0) {
         p.losses[blockIdx.x] = v;
@@ -356,12 +376,11 @@ template <int EPL, int V, int TOK, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ BalanceParams p) {
     extern __shared__ float fsm[];
     __shared__ float part[kWarps];
-    __shared__ int word;
     wait_for_previous();
     allow_next();
     count_chunk(p, 0, reinterpret_cast<int*>(fsm));
     __syncthreads();
-    const float v = pass_chunk<EPL, V, TOK, SIGMOID>(p, 0, fsm, part, &word);
+    const float v = pass_chunk<EPL, V, TOK, SIGMOID>(p, 0, fsm, part);
     if (p.a.loss && threadIdx.x == 0) *p.a.loss = v;
 }
 
@@ -371,6 +390,7 @@ int count_chunks(int k, int T, int n_seqs) {
     const int64_t want = std::max<int64_t>((int64_t)T * k / 1024, n_seqs / 4);
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, T), kMostCounts));
 }
+constexpr size_t kUsedAt = 256;                          // (in front of it: the ticket)
 struct Layout {
     size_t counts, losses, total;
     int row;
@@ -378,7 +398,7 @@ struct Layout {
 Layout layout(int E, int n_seqs, int chunks1, int chunks2) {
     Layout l;
     l.row = (E + 4) & ~3;
-    l.counts = 256;
+    l.counts = kUsedAt + kMostCounts * 4;
     l.losses = align_up(l.counts + (size_t)(chunks1 + n_seqs) * l.row * 4, 256);
     l.total = align_up(l.losses + (size_t)chunks2 * 4, 256);
     return l;
@@ -391,8 +411,9 @@ cudaError_t launch_pass(BalanceParams& p, bool small, cudaStream_t s) {
     const void* fn = small ? (const void*)small_kernel<EPL, V, TOK, SIGMOID> : (const void*)pass_kernel<EPL, V, TOK, SIGMOID>;
     cudaError_t err = prepare_kernel(fn, 32 * EPL * 4 + 16, ready[small], &sms);
     if (err != cudaSuccess) return err;
-    // even chunks, one for each CTA that runs at a time, of a token a warp at least
-    p.len2 = small ? std::max(p.a.T, 1) : std::max(kWarps, ceil_div(p.a.T, std::min(kResident<EPL> * sms, kMostChunks)));
+    // even chunks, one for each CTA that runs at a time, of a token a warp or a sequence's tokens at least
+    p.len2 = small ? std::max(p.a.T, 1)
+                   : std::max(std::min(kWarps, ceil_div(p.a.T, p.a.n_seqs)), ceil_div(p.a.T, std::min(kResident<EPL> * sms, kMostChunks)));
     p.chunks2 = std::max(1, ceil_div(p.a.T, p.len2));
     void* args[] = {&p};
     return launch_early(fn, dim3(p.chunks2), kThreads, (size_t)p.a.E * 4 + 16, s, args);
@@ -426,13 +447,17 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     BalanceParams p{};
     p.a = a;
-    const bool small = a.T <= 64;                        // (a chunk of 16 warps, 4 tokens each at most)
+    // One launch where one CTA is not what takes the time: a few tokens in one or two sequences (it takes them one after another).
+    // 128 experts, one launch / two: 64 tokens 5.7 / 6.9 us, in two sequences 8.5 / 8.7, in 8 23 / 9.2; 384 experts: 10 tokens
+    // 5.0 / 7.4, 32 in two sequences 9.4 / 9.3, 64 8.5 / 7.6.
+    const bool small = a.T <= 64 && a.T * a.E <= 16384 && std::min(a.T, a.n_seqs) <= kFewSeqs;
     p.len1 = small ? std::max(a.T, 1) : ceil_div(a.T, count_chunks(a.k, a.T, a.n_seqs));
     p.chunks1 = std::max(1, ceil_div(a.T, p.len1));
     const Layout l = layout(a.E, a.n_seqs, p.chunks1, 0);
     char* ws = static_cast<char*>(a.ws);
     p.row = l.row;
     p.ticket = reinterpret_cast<uint32_t*>(ws);
+    p.used = reinterpret_cast<int32_t*>(ws + kUsedAt);
     p.counts = reinterpret_cast<int32_t*>(ws + l.counts);
     p.losses = reinterpret_cast<float*>(ws + l.losses);
     if (small) return a.sigmoid ? launch_pass_of<true>(p, true, s) : launch_pass_of<false>(p, true, s);

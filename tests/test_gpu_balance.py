@@ -138,6 +138,29 @@ def test_balance_of_sequences(T, E, k, off, mode, masked):
 
 
 @pytest.mark.parametrize("mode", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T, E, k, off, live", [
+    (100000, 300, 2, [0, 100000], None), (100000, 300, 2, [7, 60000, 99990], None),      # more steps a warp than bits of a word
+    (20000, 64, 8, [0, 15000, 20000], [(14990, 15000), (15001, 15002)]),                 # what counts lies many chunks behind the start
+    (20000, 64, 8, [0, 9000, 9000, 20000], [(9000, 20000)]), (20000, 64, 8, [0, 20000], [(19999, 20000)]),
+    (20000, 64, 8, [0, 10000, 20000], [(0, 1), (5000, 9000), (19999, 20000)]), (20000, 64, 8, [0, 20000], []),
+    (64, 256, 8, [0, 30, 64], [(0, 10), (50, 64)]), (64, 260, 8, [0, 30, 64], [(0, 10), (50, 64)]), (64, 128, 8, [0, 30, 60, 64], [(31, 64)]),
+])
+def test_balance_of_masked_stretches(T, E, k, off, live, mode):
+    logits, ids = _inputs(T, E, k, seed=4)
+    if live is None:
+        mask = torch.rand(T, device="cuda", generator=torch.Generator(device="cuda").manual_seed(T)) < 0.5
+    else:
+        mask = torch.zeros(T, dtype=torch.bool, device="cuda")
+        for a, b in live:
+            mask[a:b] = True
+    logits[~mask] = float("nan")
+    op = moe.BalanceLoss(E, k, mode=mode)
+    got = op(logits, ids, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), mask=mask, dlogits=True)
+    _compare(got, _want(logits, ids, k, mode, 1.0, off, mask))
+    assert bool((got[2][~mask] == 0).all()) and op.device_status() == N.MOE_OK
+
+
+@pytest.mark.parametrize("mode", ["softmax", "sigmoid"])
 def test_balance_of_far_logits_and_infinities(mode):
     T, E, k = 64, 40, 4
     logits, ids = _inputs(T, E, k, seed=2, spread=30.0)
