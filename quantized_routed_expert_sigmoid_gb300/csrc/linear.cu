@@ -7,13 +7,13 @@
 //   of up to 8 CTAs splits the sum of a tile.  Each CTA sends the columns of its part to the CTA of the cluster that finishes
 //   them (shared memory of the cluster, no workspace), which adds the parts in their order.
 //   Bound: latency.  1 x 2048 -> 2048 with bias and residual, bf16: 5.3 us, 32 x 2048 -> 7168 with bias and GELU: 9.7 us, on
-//   weights from HBM (their bytes alone take 1.2 and 4.4 us): 3 us are the launch, the first load and the closing code, the rest
+//   weights from HBM (their bytes alone: 1.2 and 4.4): 3 us are the launch, the first load and the closing code, the rest
 //   is steps of the sum at 0.16 us each.
 // - pair_kernel: tiles of 256 channels by up to 256 rows, a pair of CTAs (cta_group::2) each, persistent, two accumulators: one
 //   is read out while the next tile runs.  A weight is read from L2 once per 256 rows.
-//   Bound: the matrix instructions (81 % of the pipe's time).  4096 x 2048 -> 7168, bf16 with bias and GELU: 66.7 us, 1.80 PFLOP/s
-//   (without an epilogue 65.6; the floor at cuBLAS's best rate 62.3); 4096 x 7168 -> 2048 with bias and residual, fp32 outputs, sums
-//   in runs: 75.2 us, 1.60 PFLOP/s (without residual 68.5, bf16 outputs 70.2).  Columns are dealt evenly to as few waves of tiles as
+//   Bound: the matrix instructions (81 % of the pipe's time).  4096 x 2048 -> 7168, bf16 with bias and GELU: 67 us, 1.79 PFLOP/s
+//   (1 less without an epilogue); 4096 x 7168 -> 2048 with bias and residual, fp32 outputs, sums in runs: 75 to 79 us, 1.6 PFLOP/s
+//   (without residual 68.5).  Columns are dealt evenly to as few waves of tiles as
 //   there can be: the last wave is what large products lose.
 // The tensor cores cut a sum off after each instruction instead of rounding it, an error that grows with the
 // sum's length; so long sums are made of runs (768 elements for fp32 outputs, 8192 for 16-bit ones), which the epilogue
