@@ -419,7 +419,8 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
  *     y[t, n] = res_scale * r[t, n] + scale * act(sum_c W[n, c] * x[t, c] + bias[n])
  *   act: MOE_ACT_NONE; RELU max(z, 0) (NaN stays); GELU z * Phi(z), Phi the normal distribution function;
  *   GELU_TANH z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))); SILU z / (1 + exp(-z)).
- *   Products exact, sums in fp32 in a fixed order, one rounding to y_type at the end.  Long sums are made of runs of at
+ *   Products exact, sums in fp32 in a fixed order, one rounding to y_type at the end; the activation of a 16-bit output is within
+ *   2e-5 of its value (of an fp32 one within a few units of the last place).  Long sums are made of runs of at
  *   most 768 elements with y_type MOE_F32 and 8192 with a 16-bit one, added with rounding, as those of moe_grouped_matmul.
  * The projections in front of and behind the routed experts, and dense blocks: an up half with its activation, a down
  * half that adds to the residual stream (r the stream; y may be r itself).
@@ -638,12 +639,12 @@ moe_status moe_permute_read_device_status(int T, int k, int E, void* workspace, 
  * moe_debug_set_waits -- test hook for the bounded device-side waits; off by
  * default.  Every wait of the library's kernels on a copy or an MMA gives up
  * after limit_ns nanoseconds (0 restores the default of 2 s), records
- * MOE_ERR_TIMEOUT in the workspace status word (the call's status argument for the grouped and
- * 4-bit products), waits (within the same limit)
+ * MOE_ERR_TIMEOUT in the workspace status word (the call's status argument for the grouped,
+ * 4-bit and dense products), waits (within the same limit)
  * for the copies its CTA still has in flight, releases what it holds and
  * returns; the call's outputs are then undefined and moe_read_device_status
  * reports the code.  stall = 1 makes the first wait of the chained decode,
- * segmented GEMV, tensor-core, grouped and 4-bit kernels wait on a barrier that nothing
+ * segmented GEMV, tensor-core, grouped, 4-bit and dense-product kernels wait on a barrier that nothing
  * completes, so that a test can run this path without a faulty input.
  * Applies to calls launched after it, from any host thread (a graph keeps the
  * setting it was captured with).  The failure reporting follows the pages'
