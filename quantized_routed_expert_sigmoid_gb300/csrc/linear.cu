@@ -851,14 +851,17 @@ struct Shape {
 };
 // The least time by a model of both kernels, in us, fitted to graphs of calls on weights that come from HBM (512..7168 wide,
 // T = 16..1024; it is within 15 % there):
-//   split, of `cols` columns:  start[cols] + steps of the sum a CTA * step[cols] + 0.3 + 0.2 CTAs where they share a sum
-//   pairs, of `cols` columns:  3.4 + 0.009 cols + waves * steps * pair_step(cols)
-// The start holds launch, first load and epilogue.  Measured, split / pairs at their best: 16 rows, 2048 -> 2048: 5.6 / 8.4;
+//   split, of `cols` columns:  start[cols] + (waves - 1) wave[cols] + waves * steps of the sum a CTA * step[cols]
+//                              + 0.3 + 0.2 CTAs where they share a sum
+//   pairs, of `cols` columns:  3.4 + 0.009 cols + s + (waves - 1) max(s, 0.6 + 0.0063 cols),  s = steps * pair_step(cols)
+// The start holds launch, first load and epilogue; what a further wave costs besides its steps is the set-up and epilogue of a CTA
+// (pairs: an epilogue longer than the steps that it overlaps; 5521 x 32 -> 3320 in tiles of 32, 64, 128 and 256: 25.3, 17.0, 14.2 and
+// 12.3 us; 1000 x 64 -> 1000: split by 16 in 4 waves 8.4, pairs of 64 in one 4.2).  Measured, split / pairs at their best: 16 rows, 2048 -> 2048: 5.6 / 8.4;
 // 64 rows, 2048 -> 2048: 6.7 / 8.4, 7168 -> 2048: 10.3 / 20.8; 128 rows, 768 -> 2048: 5.7 / 5.5; 256 rows, 2048 -> 2048: 9.1 / 8.6,
 // 768 -> 2048: 6.5 / 5.8, 7168 -> 2048: 16.2 / 20.2, 2048 -> 7168: 22.7 / 12.0; 512 rows, 2048 -> 2048: 11.3 / 9.2.
 // (The split kernel with tiles of 128 columns was slower than one or the other at each of these.)
 Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
-    static const float start[3] = {3.35f, 3.95f, 5.2f}, step[3] = {0.155f, 0.162f, 0.168f};
+    static const float start[3] = {3.35f, 3.95f, 5.2f}, step[3] = {0.155f, 0.162f, 0.168f}, wave[3] = {2.0f, 2.3f, 5.0f};
     const int nk = ceil_div(a.K, kStepK), sms = sm_count();
     Shape best{0, 0};
     float least = 1e30f;
@@ -871,7 +874,8 @@ Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
     for (int i = 0; i < 3 && (16 << i) < 2 * a.T + 16; ++i) {
         const int64_t tiles = (int64_t)ceil_div(a.N, 128) * ceil_div(a.T, 16 << i);
         if (tiles > 4 * sms) continue;
-        take(start[i] + ceil_div(tiles, sms) * nk * step[i], 16 << i, 1);
+        const int waves = ceil_div(tiles, sms);
+        take(start[i] + (waves - 1) * wave[i] + waves * nk * step[i], 16 << i, 1);
         for (int c = 2; c <= 8 && c <= nk && tiles * c <= sms; ++c)
             if (tiles <= clusters_at_once(fns[i], c)) take(start[i] + 0.3f + 0.2f * c + ceil_div(nk, c) * step[i], 16 << i, c);
     }
@@ -880,7 +884,7 @@ Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
         const int cols = (ceil_div(a.T, nb) + 31) & ~31;
         const float per = cols <= 128 ? 0.150f + 0.00014f * cols : 0.117f + 0.00057f * cols;
         const int64_t waves = ceil_div((int64_t)ceil_div(a.N, 256) * ceil_div(a.T, cols), sms / 2);
-        take(3.4f + 0.009f * cols + waves * nk * per, cols, 0);
+        take(3.4f + 0.009f * cols + nk * per + (waves - 1) * std::max(nk * per, 0.6f + 0.0063f * cols), cols, 0);
     }
     return best;
 }
