@@ -420,7 +420,8 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
  *   act: MOE_ACT_NONE; RELU max(z, 0) (NaN stays); GELU z * Phi(z), Phi the normal distribution function;
  *   GELU_TANH z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))); SILU z / (1 + exp(-z)).
  *   Products exact, sums in fp32 in a fixed order, one rounding to y_type at the end; the activation of a 16-bit output is within
- *   2e-5 of its value (of an fp32 one within a few units of the last place).  Long sums are made of runs of at
+ *   2e-5 of its value (of an fp32 one within 2^-20, of the tanh form far below 0 within
+ *   2^-15: its exponent is a rounded number).  Long sums are made of runs of at
  *   most 768 elements with y_type MOE_F32 and 8192 with a 16-bit one, added with rounding, as those of moe_grouped_matmul.
  * The projections in front of and behind the routed experts, and dense blocks: an up half with its activation, a down
  * half that adds to the residual stream (r the stream; y may be r itself).
