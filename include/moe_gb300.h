@@ -510,7 +510,8 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_desc* desc, const void* 
  *     loss = coef / B' * sum_b sum_e f_be * P_be        (B': sequences with a counted token; 0 without any)
  *     dlogits_te = upstream * d loss / d logits_te      (counts held constant)
  *               = upstream * coef / (B' n_b) * p_te * (f_be - sum_j f_bj p_tj)  [sigmoid: * (1 - sigmoid(logits_te))]
- *   coef for a perfectly even load.  A logit of -inf has p = 0 and no gradient; a token of nothing else has p = 0 throughout.
+ *   coef for a perfectly even load.  A logit of -inf has p = 0 and no gradient (the formula's upstream * 0: NaN with an upstream that
+ *   is not finite); a token of nothing else has p = 0 throughout and a gradient of 0.
  * desc (host, read during the call): mode; n_experts 1..1024, top_k 1..min(E, 32); coef finite; accumulate.
  * logits (device, fp32): T rows, stride elements apart (>= E), as moe_route's logits_out;  ids (device, int32 [T][k]):
  *   its topk_ids;  seq_offsets (device int32 [n_seqs + 1], nullable with n_seqs = 1: one sequence of all T tokens):
@@ -519,7 +520,7 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_desc* desc, const void* 
  *   nullable: 1): the gradient of what the loss goes into.
  * Outputs (device, nullable, not all): loss fp32 [1];  counts int32 [n_seqs][E];  dlogits fp32, T rows dstride apart
  *   (may be logits itself, with its stride, unless accumulating): overwritten, with 0 for tokens that do not count or that
- *   no sequence has; with accumulate added to, those tokens' rows left as they were.
+ *   no sequence has, whatever upstream is; with accumulate added to, those tokens' rows left as they were.
  * workspace (device, 256-byte aligned): moe_balance_workspace_size bytes; it is free again when the call is done, calls that
  *   may overlap need one each.  status (device int32, nullable, never cleared by the call): raised to MOE_ERR_DEVICE_CHECK when
  *   an id of a counted token leaves 0..E-1 (it is not counted) or an offset leaves 0..T or decreases (the outputs are undefined).

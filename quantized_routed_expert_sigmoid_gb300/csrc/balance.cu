@@ -322,7 +322,7 @@ __device__ __forceinline__ float pass_chunk(const BalanceParams& p, int c, float
                 if (!none) shares += 1.0f + dot[o];
                 if (!a.dlogits || t >= s1 || (!live[o] && a.accumulate)) continue;
                 float* row = a.dlogits + t * a.dstride;
-                const float by = inv * scale;
+                const float by = none ? 0.f : inv * scale;     // (0 whatever the upstream gradient: 0 * inf is no 0)
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
 #pragma unroll
