@@ -802,6 +802,7 @@ moe_status moe_linear_plan_destroy(moe_linear_plan* plan) {
 moe_status moe_linear_path(const moe_linear_plan* plan, int T, int* path) {
     if (!plan || !path) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
     if (T < 1) return fail(MOE_ERR_INVALID_ARG, "T = %d", T);
+    if (T > 1 << 30) return fail(MOE_ERR_INVALID_ARG, "T = %d too large", T);
     LinearArgs a = plan->a;
     a.T = T;
     *path = linear_pairs(a) ? MOE_LINEAR_PAIRS : MOE_LINEAR_SPLIT;

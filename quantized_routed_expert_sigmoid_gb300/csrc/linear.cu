@@ -871,7 +871,7 @@ Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
             best = Shape{cols, splits};
         }
     };
-    for (int i = 0; i < 3 && (16 << i) < 2 * a.T + 16; ++i) {
+    for (int i = 0; i < 3 && (16 << i) < 2 * (int64_t)a.T + 16; ++i) {
         const int64_t tiles = (int64_t)ceil_div(a.N, 128) * ceil_div(a.T, 16 << i);
         if (tiles > 4 * sms) continue;
         const int waves = ceil_div(tiles, sms);
