@@ -808,22 +808,39 @@ static_assert(kRun32 % kPer == 0 && kRun16 % kPer == 0, "runs of whole stages");
 
 constexpr int kSplitSmem = 227 * 1024 - 1024;            // dynamic shared memory of split_kernel, at most
 
-int sm_count() {
-    static std::atomic<int> known{0};
-    int n = known.load(std::memory_order_relaxed), dev = 0;
-    if (n) return n;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+// What the choice knows of a GPU is kept for each of the first kDevices of them (others are asked every time): how many clusters
+// fit at a time depends on the GPU's own groups of SMs.
+constexpr int kDevices = 64;
+struct Gpu {
+    int device;                                          // -1: none (moe_linear_path answers for a GB300)
+    int sms;
+};
+Gpu current_gpu() {
+    static std::atomic<int> known[kDevices];
+    Gpu g{-1, 152};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
-        return 152;                                      // (no device: moe_linear_path answers for a GB300)
+        return g;
     }
-    known.store(n, std::memory_order_relaxed);
-    return n;
+    if (dev < kDevices) n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return g;
+        }
+        if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+    }
+    return Gpu{dev, n};
 }
 // Clusters of c CTAs of the split kernel, one an SM, that run at one time.  A cluster lies within one of the GPU's groups
 // of SMs, which are not multiples of it: of 8 CTAs 15 fit 152 SMs, of 6 23, of 4 36.  (One more than fit takes twice the time.)
-int clusters_at_once(const void* fn, int c) {
-    static std::atomic<int> known[9];                    // (the same for every form of the kernel: its shared memory decides)
-    int n = known[c].load(std::memory_order_relaxed);
+int clusters_at_once(const Gpu& gpu, const void* fn, int c) {
+    static std::atomic<int> known[kDevices][9];          // (the same for every form of the kernel: its shared memory decides)
+    static const int gb300[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    if (gpu.device < 0) return gb300[c];
+    const bool kept = gpu.device < kDevices;
+    int n = kept ? known[gpu.device][c].load(std::memory_order_relaxed) : 0;
     if (n > 0) return n - 1;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -838,10 +855,9 @@ int clusters_at_once(const void* fn, int c) {
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
         cudaGetLastError();
-        static const int gb300[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
         return gb300[c];
     }
-    known[c].store(n + 1, std::memory_order_relaxed);
+    if (kept) known[gpu.device][c].store(n + 1, std::memory_order_relaxed);
     return n;
 }
 
@@ -862,7 +878,8 @@ struct Shape {
 // (The split kernel with tiles of 128 columns was slower than one or the other at each of these.)
 Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
     static const float start[3] = {3.35f, 3.95f, 5.2f}, step[3] = {0.155f, 0.162f, 0.168f}, wave[3] = {2.0f, 2.3f, 5.0f};
-    const int nk = ceil_div(a.K, kStepK), sms = sm_count();
+    const Gpu gpu = current_gpu();
+    const int nk = ceil_div(a.K, kStepK), sms = gpu.sms;
     Shape best{0, 0};
     float least = 1e30f;
     auto take = [&](float t, int cols, int splits) {
@@ -877,7 +894,7 @@ Shape shape_of(const LinearArgs& a, const void* const (&fns)[3]) {
         const int waves = ceil_div(tiles, sms);
         take(start[i] + (waves - 1) * wave[i] + waves * nk * step[i], 16 << i, 1);
         for (int c = 2; c <= 8 && c <= nk && tiles * c <= sms; ++c)
-            if (tiles <= clusters_at_once(fns[i], c)) take(start[i] + 0.3f + 0.2f * c + ceil_div(nk, c) * step[i], 16 << i, c);
+            if (tiles <= clusters_at_once(gpu, fns[i], c)) take(start[i] + 0.3f + 0.2f * c + ceil_div(nk, c) * step[i], 16 << i, c);
     }
     // (beyond some waves, all of them full: the largest tiles)
     for (int nb = ceil_div(a.T, kPairCols), most = std::min(ceil_div(a.T, 32), nb + 64); nb <= most; ++nb) {
