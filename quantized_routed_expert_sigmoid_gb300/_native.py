@@ -75,18 +75,36 @@ class moe_norm_desc(ctypes.Structure):
                 ("res_scale", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
-class moe_linear_desc(ctypes.Structure):
+def _c_int(v, name):
+    """v as it is, if it is a C int: ctypes would cut off what lies above 32 bits without a word."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name} = {v} too large")
+    return v
+
+
+class _Desc(ctypes.Structure):
+    """A description whose whole numbers fit their fields."""
+
+    def __init__(self, *values, **named):
+        super().__init__(*values, **named)
+        given = {**dict(zip((name for name, _ in self._fields_), values)), **named}
+        for name, kind in self._fields_:
+            if kind is ctypes.c_int and name in given:
+                _c_int(given[name], name)
+
+
+class moe_linear_desc(_Desc):
     _fields_ = [("type", ctypes.c_int), ("y_type", ctypes.c_int), ("order", ctypes.c_int), ("n_out", ctypes.c_int),
                 ("n_in", ctypes.c_int), ("w", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("bias", ctypes.c_void_p),
                 ("bias_type", ctypes.c_int), ("act", ctypes.c_int), ("scale", ctypes.c_float), ("res_scale", ctypes.c_float)]
 
 
-class moe_layer_norm_desc(ctypes.Structure):
+class moe_layer_norm_desc(_Desc):
     _fields_ = [("H", ctypes.c_int), ("x_type", ctypes.c_int), ("y_type", ctypes.c_int), ("gamma", ctypes.c_void_p),
                 ("beta", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
-class moe_balance_desc(ctypes.Structure):
+class moe_balance_desc(_Desc):
     _fields_ = [("mode", ctypes.c_int), ("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("coef", ctypes.c_float),
                 ("accumulate", ctypes.c_int)]
 
@@ -331,42 +349,44 @@ def moe_linear_plan_destroy(plan: int):
 def moe_linear_path(plan, T) -> int:
     """Which kernel moe_linear runs for T rows: a MOE_LINEAR_* value."""
     v = ctypes.c_int(-1)
-    _check(load().moe_linear_path(plan, T, ctypes.byref(v)))
+    _check(load().moe_linear_path(plan, _c_int(T, "T"), ctypes.byref(v)))
     return v.value
 
 
 def moe_linear(plan, x, x_stride, T, r, r_type, r_stride, y, y_stride, status=None, stream=None):
-    _check(load().moe_linear(plan, _p(x), x_stride, T, _p(r), r_type, r_stride, _p(y), y_stride, _p(status), _stream(stream)))
+    _check(load().moe_linear(plan, _p(x), x_stride, _c_int(T, "T"), _p(r), r_type, r_stride, _p(y), y_stride, _p(status),
+                             _stream(stream)))
 
 
 def moe_layer_norm(desc: moe_layer_norm_desc, x, x_stride, T, y, y_stride, mean, rstd, stream=None):
-    _check(load().moe_layer_norm(ctypes.byref(desc), _p(x), x_stride, T, _p(y), y_stride, _p(mean), _p(rstd), _stream(stream)))
+    _check(load().moe_layer_norm(ctypes.byref(desc), _p(x), x_stride, _c_int(T, "T"), _p(y), y_stride, _p(mean), _p(rstd),
+                                 _stream(stream)))
 
 
 def moe_layer_norm_backward_workspace_size(H, T) -> int:
     n = ctypes.c_size_t(0)
-    _check(load().moe_layer_norm_backward_workspace_size(H, T, ctypes.byref(n)))
+    _check(load().moe_layer_norm_backward_workspace_size(_c_int(H, "H"), _c_int(T, "T"), ctypes.byref(n)))
     return n.value
 
 
 def moe_layer_norm_backward(desc: moe_layer_norm_desc, dy, dy_stride, x, x_stride, mean, rstd, add, add_stride, T, dx, dx_stride,
                             dgamma, dbeta, accumulate, workspace, ws_bytes, stream=None):
     _check(load().moe_layer_norm_backward(ctypes.byref(desc), _p(dy), dy_stride, _p(x), x_stride, _p(mean), _p(rstd), _p(add),
-                                          add_stride, T, _p(dx), dx_stride, _p(dgamma), _p(dbeta), int(accumulate),
+                                          add_stride, _c_int(T, "T"), _p(dx), dx_stride, _p(dgamma), _p(dbeta), int(accumulate),
                                           _p(workspace), ws_bytes, _stream(stream)))
 
 
 def moe_balance_workspace_size(E, T, n_seqs=1) -> int:
     n = ctypes.c_size_t(0)
-    _check(load().moe_balance_workspace_size(E, T, n_seqs, ctypes.byref(n)))
+    _check(load().moe_balance_workspace_size(_c_int(E, "n_experts"), _c_int(T, "T"), _c_int(n_seqs, "n_seqs"), ctypes.byref(n)))
     return n.value
 
 
 def moe_balance_loss(desc: moe_balance_desc, logits, stride, ids, T, seq_offsets, n_seqs, mask, upstream, loss, counts, dlogits,
                      dstride, status, workspace, ws_bytes, stream=None):
-    _check(load().moe_balance_loss(ctypes.byref(desc), _p(logits), stride, _p(ids), T, _p(seq_offsets), n_seqs, _p(mask),
-                                   _p(upstream), _p(loss), _p(counts), _p(dlogits), dstride, _p(status), _p(workspace),
-                                   ws_bytes, _stream(stream)))
+    _check(load().moe_balance_loss(ctypes.byref(desc), _p(logits), stride, _p(ids), _c_int(T, "T"), _p(seq_offsets),
+                                   _c_int(n_seqs, "n_seqs"), _p(mask), _p(upstream), _p(loss), _p(counts),
+                                   _p(dlogits), dstride, _p(status), _p(workspace), ws_bytes, _stream(stream)))
 
 
 def moe_layer_plan_create(desc: moe_layer_desc) -> int:
