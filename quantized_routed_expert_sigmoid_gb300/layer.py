@@ -669,6 +669,8 @@ class BalanceLoss(_Checked):
         if ids is None:
             raise ValueError("ids are missing")
         _given(ids, "ids", (torch.int32,), T * self.k)
+        if ids.dim() > 1 and ids.shape[-1] != self.k > 1:
+            raise ValueError(f"ids must be [T, {self.k}], not {list(ids.shape)}")
         n_seqs = 1
         if offsets is not None:
             n_seqs = offsets.numel() - 1
@@ -698,6 +700,8 @@ class BalanceLoss(_Checked):
             counts = _empty((n_seqs, E), torch.int32, logits.device, stream)
         else:
             _given(counts, "counts", (torch.int32,), n_seqs * E)
+            if counts.dim() > 1 and counts.shape[-1] != E > 1 and n_seqs > 1:
+                raise ValueError(f"counts must be [{n_seqs}, {E}], not {list(counts.shape)}")
         device = logits.get_device()
         _all_on(device, ("ids", "offsets", "mask", "upstream", "loss", "counts", "dlogits", "status"), ids, offsets, mask, upstream, loss,
                 counts, dlogits, status)
