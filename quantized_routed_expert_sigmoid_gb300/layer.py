@@ -385,7 +385,7 @@ class NormResidual:
         self.H = H
         self._keep = (gamma_post, gamma_pre)
         self._scales = (eps, res_scale, scale)
-        self._desc = {}                  # the call's description, by the types of its tensors
+        self._desc = {}                  # the call's description, by the types of its tensors and gamma's and beta's memory
 
     def __call__(self, x: torch.Tensor | None, y: torch.Tensor, gate: torch.Tensor | None = None,
                  x_out: torch.Tensor | None = None, u: torch.Tensor | None = None, stream=None):
@@ -552,17 +552,25 @@ class LayerNorm:
                 _given(g, name, (torch.float32,), H)
         self.H, self.eps, self.y_dtype = H, eps, y_dtype
         self._keep = (gamma, beta)
-        self._desc = {}                  # the call's description, by the types of its tensors
+        self._desc = {}                  # the call's description, by the types of its tensors and gamma's and beta's memory
 
     def _described(self, x, y_dtype, names, *tensors):
         device = x.get_device()
         if self.device is not None and device != self.device:
             raise ValueError(f"x is on device {device}, gamma / beta on device {self.device}")
         _all_on(device, names, *tensors)
-        desc = self._desc.get((x.dtype, y_dtype))
+        gamma, beta = self._keep
+        # (where they lie now: a parameter's memory may have been replaced since the last call)
+        key = (x.dtype, y_dtype, None if gamma is None else gamma.data_ptr(), None if beta is None else beta.data_ptr())
+        desc = self._desc.get(key)
         if desc is None:
-            g = [t.data_ptr() if t is not None else None for t in self._keep]
-            desc = self._desc[x.dtype, y_dtype] = N.moe_layer_norm_desc(self.H, _VT[x.dtype], _VT[y_dtype], *g, self.eps)
+            for name, g in (("gamma", gamma), ("beta", beta)):
+                if g is not None:
+                    _given(g, name, (torch.float32,), self.H)
+                    _cuda(g, name, None, 1, device)
+            if len(self._desc) >= 64:
+                self._desc.clear()
+            desc = self._desc[key] = N.moe_layer_norm_desc(self.H, _VT[x.dtype], _VT[y_dtype], *key[2:], self.eps)
         return desc
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
