@@ -475,6 +475,7 @@ class Linear(_Checked):
     w: bf16 or fp16 [n_out, n_in] (order "out_in") or [n_in, n_out] ("in_out") on the GPU, last dimension dense, the
     row stride a multiple of 8 elements; bias: [n_out], fp32, bf16 or fp16, or None; act: "none", "relu", "gelu" (of
     the normal distribution function), "gelu_tanh" or "silu"; y_dtype: fp32, bf16 or fp16 (None: w's type).
+    w and bias may be written between calls, but not laid elsewhere: a call then raises.
     """
 
     _destroy = staticmethod(N.moe_linear_plan_destroy)
@@ -495,11 +496,16 @@ class Linear(_Checked):
             _given(bias, "bias", tuple(_VT), self.n_out)
         self.x_dtype, self.y_dtype, self.device = w.dtype, y_dtype, w.get_device()
         self._keep = (w, bias)
+        self._at = self._addresses()
         self._status = _status_word(w.device)
         self.plan = N.moe_linear_plan_create(N.moe_linear_desc(
             _VT[w.dtype], _VT[y_dtype], N.MOE_W_OUT_IN if order == "out_in" else N.MOE_W_IN_OUT, self.n_out, self.n_in,
             w.data_ptr(), _row_stride(w, "w"), bias.data_ptr() if bias is not None else None,
             _VT[bias.dtype] if bias is not None else N.MOE_F32, _ACTS[act], scale, res_scale))
+
+    def _addresses(self):
+        w, bias = self._keep
+        return w.data_ptr(), None if bias is None else bias.data_ptr()
 
     def path(self, T: int) -> str:
         """Which kernel a call with T rows runs: "split" or "pairs"."""
@@ -514,6 +520,8 @@ class Linear(_Checked):
         T, width = x.shape
         if x.dtype is not self.x_dtype or width != self.n_in or not x.is_cuda:
             raise ValueError(f"x must be a {self.x_dtype} CUDA tensor [T, {self.n_in}]")
+        if self._addresses() != self._at:
+            raise ValueError("the memory of w or bias has been replaced since this object was made: make another one")
         rs, rt = 0, N.MOE_F32
         if residual is not None:
             rs, rt = _value_rows(residual, "residual", T, self.n_out), _VT[residual.dtype]
