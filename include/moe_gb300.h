@@ -420,9 +420,11 @@ moe_status moe_norm_residual(const moe_norm_desc* desc, const void* x, int64_t x
  *   act: MOE_ACT_NONE; RELU max(z, 0) (NaN stays); GELU z * Phi(z), Phi the normal distribution function;
  *   GELU_TANH z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))); SILU z / (1 + exp(-z)).
  *   Products exact, sums in fp32 in a fixed order, one rounding to y_type at the end; the activation of a 16-bit output is within
- *   2e-5 of its value (of an fp32 one within 2^-20, of the tanh form far below 0 within
- *   2^-15: its exponent is a rounded number).  Long sums are made of runs of at
- *   most 768 elements with y_type MOE_F32 and 8192 with a 16-bit one, added with rounding, as those of moe_grouped_matmul.
+ *   2e-5 of its value, of an fp32 one within 2^-20; the tanh form of an fp32 z < 0 within 2^-20 + 5.1 w 2^-24, w = 2 sqrt(2 / pi)
+ *   |z + 0.044715 z^3| its exponent, a rounded number (2^-15 where the value is not subnormal).  Long sums are made of runs of at
+ *   most 768 elements with y_type MOE_F32 and 8192 with a 16-bit one, added with rounding, as those of moe_grouped_matmul; within
+ *   a run the matrix instructions cut their sums off instead of rounding them (one row of 2048 elements, fp32 output: off by
+ *   3.4e-7 in norm where a sum with rounding is by 7e-8; 4096 rows of 7168: 5.3e-7 and 6.4e-7).
  * The projections in front of and behind the routed experts, and dense blocks: an up half with its activation, a down
  * half that adds to the residual stream (r the stream; y may be r itself).
  * desc (host, read by plan_create):
@@ -525,7 +527,7 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_desc* desc, const void* 
  *   may overlap need one each.  status (device int32, nullable, never cleared by the call): raised to MOE_ERR_DEVICE_CHECK when
  *   an id of a counted token leaves 0..E-1 (it is not counted) or an offset leaves 0..T or decreases (the outputs are undefined).
  * T*k <= 2^30, n_seqs 1..65535; T = 0: loss = 0, counts = 0.  All sums have one order: the same bits each time.
- * One launch up to 64 tokens, two beyond.
+ * One launch for up to 64 tokens in one or two sequences whose T * n_experts is at most 16384, two for all others.
  */
 typedef struct {
     moe_route_mode mode;

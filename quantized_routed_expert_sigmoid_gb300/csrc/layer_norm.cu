@@ -16,10 +16,12 @@
 //   4096 rows, fp32 to bf16: forward 12.2 us, 4.1 TB/s (bytes alone: 7.4); backward with the residual's gradient 26.3 us,
 //   4.5 TB/s (17.3).  512 rows of 7168, bf16: 15.7 us (3.3), 9.4 without the sums over the rows: two launches, four rows one after another.
 //   1024 threads leave too few registers for rows, sums and gamma: slower.  Forward with gamma and beta in shared memory and two CTAs an
-//   SM: 4096 rows of fp32 12.1 -> 11.8, of bf16 10.2 -> 12.7.
+//   SM: 4096 rows of fp32 12.1 -> 11.8, of bf16 (bytes alone 4.9) 10.2 -> 12.7.
 // - row_kernel: forward, a few rows (which leave most SMs without any): more threads a row, no ring to fill; and what the others
-//   do not take: rows above 8192 elements, bf16 with fp16.  One row: 2.1 us, a launch and three trips to memory.
-// - wide_backward_kernel: the gradient of those.
+//   do not take: rows above 8192 elements, bf16 with fp16.  One row: 2.1 us, a launch and three trips to memory; 2048 rows of 12288,
+//   fp32 to bf16: 50.8 us (22.3), 1024 of 16384, bf16: 33.6 (9.9).
+// - wide_backward_kernel: the gradient of those, in the simplest form: element by element, types looked up, sums for gamma and beta
+//   in memory.  2048 rows of 12288: 262 us (37), 1024 of 16384, bf16: 218 (15).
 // - sums_kernel: dgamma and dbeta of the CTAs' partial sums.
 #include <algorithm>
 

@@ -6,9 +6,9 @@
 // - split_kernel: tiles of 128 channels by up to 64 rows of x, one CTA each; where that leaves SMs idle, a cluster
 //   of up to 8 CTAs splits the sum of a tile.  Each CTA sends the columns of its part to the CTA of the cluster that finishes
 //   them (shared memory of the cluster, no workspace), which adds the parts in their order.
-//   Bound: latency.  1 x 2048 -> 2048 with bias and residual, bf16: 5.3 us, 32 x 2048 -> 7168 with bias and GELU: 9.7 us, on
+//   Bound: latency.  1 x 2048 -> 2048 with bias and residual, bf16: 5.2 us, 32 x 7168 -> 2048 with bias and GELU: 9.6 us, on
 //   weights from HBM (their bytes alone: 1.2 and 4.4): 3 us are the launch, the first load and the closing code, the rest
-//   is steps of the sum at 0.16 us each.
+//   is steps of the sum at 0.16 us each (8 and 19 of them a CTA).
 // - pair_kernel: tiles of 256 channels by up to 256 rows, a pair of CTAs (cta_group::2) each, persistent, two accumulators: one
 //   is read out while the next tile runs.  A weight is read from L2 once per 256 rows.
 //   Bound: the matrix instructions (81 % of the pipe's time).  4096 x 2048 -> 7168, bf16 with bias and GELU: 67 us, 1.79 PFLOP/s
@@ -72,7 +72,7 @@ __device__ __forceinline__ float rcp_quick(float x) {
     return r;
 }
 // e^-(w + more), w from 0 to 200, as value * back: 2^32 times too large where it would be subnormal.  `more` is what w lacks of the
-// number that it stands for.  The product with log2(e) is taken in two parts and the second one's power as 1 + x: relative error 2^-22 of
+// number that it stands for.  (Argument reduction in two parts, after Cody and Waite.)  The product with log2(e) is taken in two parts and the second one's power as 1 + x: relative error 2^-22 of
 // the instruction and 2^-24.
 __device__ __forceinline__ float exp_minus(float w, float more, float& back) {
     constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911266175e-8f;     // (log2(e) - kLog2e)
@@ -866,7 +866,8 @@ struct Shape {
     int cols, splits;
 };
 // The least time by a model of both kernels, in us, fitted to graphs of calls on weights that come from HBM (512..7168 wide,
-// T = 16..1024; it is within 15 % there):
+// T = 16..1024; it is within 15 % there).  Outside it is a guide, no more: where x is what streams from memory a step takes longer than
+// its constants say (6225 x 4920 -> 328 in tiles of 192: 23 us by the model, 37 measured; of 128 30 and 50):
 //   split, of `cols` columns:  start[cols] + (waves - 1) wave[cols] + waves * steps of the sum a CTA * step[cols]
 //                              + 0.3 + 0.2 CTAs where they share a sum
 //   pairs, of `cols` columns:  3.4 + 0.009 cols + s + (waves - 1) max(s, 0.6 + 0.0063 cols),  s = steps * pair_step(cols)

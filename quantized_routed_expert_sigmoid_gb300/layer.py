@@ -476,6 +476,7 @@ class Linear(_Checked):
     row stride a multiple of 8 elements; bias: [n_out], fp32, bf16 or fp16, or None; act: "none", "relu", "gelu" (of
     the normal distribution function), "gelu_tanh" or "silu"; y_dtype: fp32, bf16 or fp16 (None: w's type).
     w and bias may be written between calls, but not laid elsewhere: a call then raises.
+    Not recorded by autograd, and without a gradient of its own.
     """
 
     _destroy = staticmethod(N.moe_linear_plan_destroy)
@@ -546,6 +547,7 @@ class LayerNorm:
     """Layer norm over rows of H and its gradient (moe_layer_norm, moe_layer_norm_backward).
 
     gamma, beta: fp32 [H] on the GPU (None: 1 and 0).  y_dtype: the type of outputs that a call makes.
+    Not recorded by autograd: outputs require no gradient whatever the inputs do; backward() is called by hand.
     """
 
     def __init__(self, H: int, *, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None, eps: float = 1e-5,
@@ -656,7 +658,7 @@ class BalanceLoss(_Checked):
     """The auxiliary loss that keeps a router's load even, with its counts and its gradient (moe_balance_loss).
 
     E experts, k a token; mode: "softmax" or "sigmoid" (what makes a token's scores of its logits); coef: the loss's weight.
-    device: of the calls (None: the current one).
+    device: of the calls (None: the current one).  Not recorded by autograd: dlogits is the gradient.
     """
 
     def __init__(self, E: int, k: int, *, mode: str = "softmax", coef: float = 1.0, device=None):
